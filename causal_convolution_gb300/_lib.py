@@ -54,6 +54,14 @@ SIGNATURES = {
     "cc_head_out": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _Z, _P]),
     "cc_head_out_noalloc": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "cc_head_out_fused": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "cc_group_norm_workspace_bytes": (_Z, [_I, _I, _I, _I]),
+    "cc_group_norm_act": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _Z, _P]),
+    "cc_group_norm_act_fp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _Z, _P]),
+    "cc_rms_norm_act": (_I, [_P, _P, _P, _I, _I, _L, _F, _I, _P]),
+    "cc_rms_norm_act_fp8": (_I, [_P, _P, _P, _P, _I, _I, _L, _F, _I, _P]),
+    "cc_fp8_quantize": (_I, [_P, _P, _P, _I, _I, _L, _P]),
+    "cc_gemm_fp8_prepare": (_I, [_P, _P, _P, _I, _I, _P]),
+    "cc_gemm_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _L, _L, _P]),
     "cc_copy_to_host": (_I, [_P, _P, _Z, _I, _P]),
     "cc_debug_im2col_tile": (_I, [_P, _P] + [_I] * 19 + [_P]),
     "cc_debug_wait_timeout": (_I, [_L, _P]),

@@ -25,6 +25,9 @@ __all__ = [
     "cc_head_prepare", "cc_head_workspace_bytes", "cc_head_temporal", "cc_head_stencil", "cc_head_out",
     "cc_attn_scores_stats", "cc_attn_fused_workspace_bytes", "cc_attn_frame_fused",
     "cc_head_out_fused", "cc_head_out_noalloc", "HEAD_NOALLOC_SCRATCH_BYTES", "cc_copy_to_host",
+    "cc_group_norm_workspace_bytes", "cc_group_norm_act", "cc_group_norm_act_fp8",
+    "cc_rms_norm_act", "cc_rms_norm_act_fp8",
+    "cc_fp8_quantize", "cc_gemm_fp8_prepare", "cc_gemm_fp8",
     "cc_debug_im2col_tile", "cc_debug_wait_timeout", "cc_debug_conv_bad_tile_order",
     "HEAD_COUT", "HEAD_G_CH",
 ]
@@ -376,6 +379,162 @@ def cc_head_out_noalloc(x, wp, bias, out, hist: int = 0, stream=None) -> None:
         raise ValueError("head_out_noalloc: out must be [N,D,H,W,12] of x [N,D+hist,H,W,Cin]")
     _check(_lib.load().cc_head_out_noalloc(_ptr(x, name="x"), _ptr(wp, name="wp"), _ptr(bias, name="bias"),
                                            _ptr(out, name="out"), n, d, h, w, cin, hist, _stream(stream)))
+
+
+# ------------------------------------------------- norms with an activation --
+
+ACTS = {"none": 0, "silu": 1}  # CC_ACT_*
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act: expected one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _on_current(tensors: dict) -> None:
+    """Every tensor given is on the current CUDA device, whose stream the call uses."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+
+
+def _last_rows(t: torch.Tensor, dtype, name: str):
+    """(rows, C, ld) of a [..., C] tensor whose rows are C channels next to each other at one stride `ld`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() == 0:
+        raise ValueError(f"{name}: expected [..., C]")
+    c = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // c if c else 0), c, c
+    if t.stride(-1) != 1 and c > 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    rows, ld = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != ld * rows:
+            raise ValueError(f"{name}: rows must lie at one stride")
+        rows *= size
+    return rows, c, c if ld is None else ld
+
+
+def _scale_blocks(c: int) -> int:
+    return (c + 127) // 128
+
+
+def cc_group_norm_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
+    return _lib.load().cc_group_norm_workspace_bytes(n, p, c, groups)
+
+
+def _group_norm_sizes(x, gamma, beta, y):
+    if x.dim() < 2 or x.shape != y.shape:
+        raise ValueError(f"group_norm_act: x and y must share [N,...,C], got {tuple(x.shape)} and {tuple(y.shape)}")
+    n, c = x.shape[0], x.shape[-1]
+    if (gamma is not None and gamma.numel() != c) or (beta is not None and beta.numel() != c):
+        raise ValueError("group_norm_act: gamma and beta must hold C elements")
+    p = 1
+    for s in x.shape[1:-1]:
+        p *= s
+    return n, p, c
+
+
+def cc_group_norm_act(x, gamma, beta, y, groups: int, ws, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
+    """Group norm of x [N, ..., C] over everything but N (view [N, D, H, W, C] as [N*D, H, W, C] for a norm per
+    frame) and an activation ("silu" or "none"). gamma, beta: [C] or None."""
+    n, p, c = _group_norm_sizes(x, gamma, beta, y)
+    px, pg, pb, py = _ptr(x, name="x"), _ptr(gamma, name="gamma"), _ptr(beta, name="beta"), _ptr(y, name="y")
+    pw = _ptr(ws, torch.uint8, "ws")
+    _on_current({"x": x, "gamma": gamma, "beta": beta, "y": y, "ws": ws})
+    _check(_lib.load().cc_group_norm_act(px, pg, pb, py, n, p, c, groups, eps, _act(act), pw,
+                                         0 if ws is None else ws.numel(), _stream(stream)))
+
+
+def cc_group_norm_act_fp8(x, gamma, beta, y, scales, groups: int, ws, eps: float = 1e-6, act: str = "silu",
+                          stream=None) -> None:
+    """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [N, ..., ceil(C/128)]."""
+    n, p, c = _group_norm_sizes(x, gamma, beta, y)
+    if tuple(scales.shape) != (*x.shape[:-1], _scale_blocks(c)):
+        raise ValueError("group_norm_act_fp8: scales must be [N,...,ceil(C/128)]")
+    px, pg, pb = _ptr(x, name="x"), _ptr(gamma, name="gamma"), _ptr(beta, name="beta")
+    py, ps, pw = _ptr(y, torch.float8_e4m3fn, "y"), _ptr(scales, torch.float32, "scales"), _ptr(ws, torch.uint8, "ws")
+    _on_current({"x": x, "gamma": gamma, "beta": beta, "y": y, "scales": scales, "ws": ws})
+    _check(_lib.load().cc_group_norm_act_fp8(px, pg, pb, py, ps, n, p, c, groups, eps, _act(act), pw,
+                                             0 if ws is None else ws.numel(), _stream(stream)))
+
+
+def cc_rms_norm_act(x, gamma, y, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
+    """RMS norm over the channels of x [..., C] (rows may be strided) and an activation. gamma: [C] or None."""
+    rows, c, ld = _last_rows(x, torch.bfloat16, "x")
+    if x.shape != y.shape or (gamma is not None and gamma.numel() != c):
+        raise ValueError("rms_norm_act: x and y must share [...,C] and gamma hold C elements")
+    pg, py = _ptr(gamma, name="gamma"), _ptr(y, name="y")
+    _on_current({"x": x, "gamma": gamma, "y": y})
+    _check(_lib.load().cc_rms_norm_act(x.data_ptr(), pg, py, rows, c, ld, eps, _act(act), _stream(stream)))
+
+
+def cc_rms_norm_act_fp8(x, gamma, y, scales, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
+    """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [..., ceil(C/128)]."""
+    rows, c, ld = _last_rows(x, torch.bfloat16, "x")
+    if x.shape != y.shape or tuple(scales.shape) != (*x.shape[:-1], _scale_blocks(c)) \
+            or (gamma is not None and gamma.numel() != c):
+        raise ValueError("rms_norm_act_fp8: y must be [...,C], scales [...,ceil(C/128)] and gamma [C] of x [...,C]")
+    pg, py = _ptr(gamma, name="gamma"), _ptr(y, torch.float8_e4m3fn, "y")
+    ps = _ptr(scales, torch.float32, "scales")
+    _on_current({"x": x, "gamma": gamma, "y": y, "scales": scales})
+    _check(_lib.load().cc_rms_norm_act_fp8(x.data_ptr(), pg, py, ps, rows, c, ld, eps, _act(act), _stream(stream)))
+
+
+# ------------------------------------- product in 8 bits with block scales --
+
+def cc_fp8_quantize(x, y, scales, stream=None) -> None:
+    """bf16 rows x [..., C] (rows may be strided) to e4m3 y with scales [..., ceil(C/128)]."""
+    rows, c, ld = _last_rows(x, torch.bfloat16, "x")
+    if x.shape != y.shape or tuple(scales.shape) != (*x.shape[:-1], _scale_blocks(c)):
+        raise ValueError("fp8_quantize: y must be [...,C] and scales [...,ceil(C/128)] of x [...,C]")
+    py, ps = _ptr(y, torch.float8_e4m3fn, "y"), _ptr(scales, torch.float32, "scales")
+    _on_current({"x": x, "y": y, "scales": scales})
+    _check(_lib.load().cc_fp8_quantize(x.data_ptr(), py, ps, rows, c, ld, _stream(stream)))
+
+
+def cc_gemm_fp8_prepare(w, wq, sw, stream=None) -> None:
+    """Weights w [N, K] (a 1x1x1 convolution's [Cout, Cin]) to e4m3 wq with scales sw [ceil(N/128), ceil(K/128)]."""
+    if w.dim() != 2 or w.shape != wq.shape or tuple(sw.shape) != (_scale_blocks(w.shape[0]), _scale_blocks(w.shape[1])):
+        raise ValueError("gemm_fp8_prepare: wq must be [N,K] and sw [ceil(N/128),ceil(K/128)] of w [N,K]")
+    pw, pq, ps = _ptr(w, name="w"), _ptr(wq, torch.float8_e4m3fn, "wq"), _ptr(sw, torch.float32, "sw")
+    _on_current({"w": w, "wq": wq, "sw": sw})
+    _check(_lib.load().cc_gemm_fp8_prepare(pw, pq, ps, w.shape[0], w.shape[1], _stream(stream)))
+
+
+def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
+    """out [..., N] = a [..., K] wq^T with the block scales, plus bias [N] and res [..., N] (or None). out and res
+    may be rows at a stride (a slice of packed qkv)."""
+    k = a.shape[-1]
+    m, n, ld_out = _last_rows(out, torch.bfloat16, "out")
+    ld_res = n
+    if a.shape[:-1] != out.shape[:-1] or tuple(sa.shape) != (*a.shape[:-1], _scale_blocks(k)):
+        raise ValueError("gemm_fp8: a must be [...,K] and sa [...,ceil(K/128)] of out [...,N]")
+    if tuple(wq.shape) != (n, k) or tuple(sw.shape) != (_scale_blocks(n), _scale_blocks(k)):
+        raise ValueError("gemm_fp8: wq must be [N,K] and sw [ceil(N/128),ceil(K/128)]")
+    if bias is not None and bias.numel() != n:
+        raise ValueError("gemm_fp8: bias must hold N elements")
+    if res is not None:
+        if res.shape != out.shape:
+            raise ValueError("gemm_fp8: res must have out's shape")
+        ld_res = _last_rows(res, torch.bfloat16, "res")[2]
+    pa, ps = _ptr(a, torch.float8_e4m3fn, "a"), _ptr(sa, torch.float32, "sa")
+    pw, pt, pb = _ptr(wq, torch.float8_e4m3fn, "wq"), _ptr(sw, torch.float32, "sw"), _ptr(bias, name="bias")
+    _on_current({"a": a, "sa": sa, "wq": wq, "sw": sw, "bias": bias, "res": res, "out": out})
+    _check(_lib.load().cc_gemm_fp8(pa, ps, pw, pt, pb, None if res is None else res.data_ptr(), out.data_ptr(), m, n,
+                                   k, ld_res, ld_out, _stream(stream)))
 
 
 # -------------------------------------------------------- result read-back --

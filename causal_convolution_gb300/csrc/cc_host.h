@@ -65,6 +65,9 @@ cc_status encode_im2col_5d(CUtensorMap* map, const void* base, int n, int d, int
                            int lo_d, int up_w, int up_h, int up_d, int pixels, int channels);
 cc_status encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                           uint32_t box_inner, uint32_t box_outer);
+// The same over 8-bit elements (box_inner = 128 bytes).
+cc_status encode_tiled_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                             uint32_t box_inner, uint32_t box_outer);
 cc_status encode_tiled_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                           uint64_t stride2, uint32_t box0, uint32_t box1);
 // Rank-3 fp32 map with 128-byte swizzle, box {box0, box1, 1} (box0 * 4 <= 128).

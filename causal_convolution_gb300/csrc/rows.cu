@@ -1,0 +1,215 @@
+// Passes over independent rows of channels: RMS norm with an activation, and
+// the quantisation of bf16 rows and weights to e4m3 with block scales.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cc.h"
+#include "cc_host.h"
+#include "cc_ptx.cuh"
+#include "cc_rows.cuh"
+
+namespace cc {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxRowChannels = 16384;
+
+struct RowArgs {
+  const uint4* x;
+  const uint4* gamma;  // nullptr: ones
+  void* y;
+  float* scales;
+  long long rows;
+  long long ld_x;  // in vectors of eight channels
+  int vecs;        // C / 8
+  int blocks;      // ceil(C / 128)
+  float inv_c;
+  float eps;
+};
+
+// One row per block.
+template <bool NORM, bool SILU, bool FP8>
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int kMaxVec = kMaxRowChannels / 8 / kRowThreads;
+  __shared__ float red[kRowThreads / 32];
+  const int tid = threadIdx.x;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    uint4 raw[kMaxVec];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxVec; ++i) {
+      const int v = tid + i * kRowThreads;
+      raw[i] = v < a.vecs ? a.x[r * a.ld_x + v] : make_uint4(0, 0, 0, 0);
+      if (NORM) {
+        float f[8];
+        unpack8(raw[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+      }
+    }
+    float rs = 1.f;
+    if (NORM) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncthreads();
+      if ((tid & 31) == 0) red[tid >> 5] = sum;
+      __syncthreads();
+      sum = 0.f;
+      for (int i = 0; i < kRowThreads / 32; ++i) sum += red[i];
+      rs = 1.f / sqrtf(fmaf(sum, a.inv_c, a.eps));
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxVec; ++i) {
+      const int v = tid + i * kRowThreads;
+      if (i * kRowThreads >= a.vecs) break;
+      float f[8];
+      unpack8(raw[i], f);
+      if (NORM) {
+        if (a.gamma && v < a.vecs) {
+          float g[8];
+          unpack8(a.gamma[v], g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= rs * g[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= rs;
+        }
+        activate8<SILU>(f);
+      }
+      if (FP8) {
+        if (v >= a.vecs) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = 0.f;
+        }
+        float scale;
+        const uint2 q = quantize_block(f, scale);
+        if (v < a.vecs) {
+          static_cast<uint2*>(a.y)[r * a.vecs + v] = q;
+          if ((tid & 15) == 0) a.scales[r * a.blocks + (v >> 4)] = scale;
+        }
+      } else if (v < a.vecs) {
+        static_cast<uint4*>(a.y)[r * a.vecs + v] = pack8(f);
+      }
+    }
+  }
+}
+
+cc_status run_rows(const char* what, bool norm, const cc_bf16* x, const cc_bf16* gamma, void* y, float* scales,
+                   int rows, int c, int64_t ld_x, float eps, int act, void* stream) {
+  cc_status st;
+  if (empty_request(what, {rows}, &st)) return st;
+  if (!x || !y) return fail(CC_ERR_INVALID, "%s: null pointer", what);
+  if (!aligned16(x) || !aligned16(gamma) || !aligned16(y) || !aligned16(scales))
+    return fail(CC_ERR_INVALID, "%s: pointers must be 16-byte aligned", what);
+  if (c <= 0) return fail(CC_ERR_INVALID, "%s: channel counts must be positive", what);
+  if (c % 8 != 0) return fail(CC_ERR_UNSUPPORTED, "%s: C must be a multiple of 8 (got %d)", what, c);
+  if (c > kMaxRowChannels)
+    return fail(CC_ERR_UNSUPPORTED, "%s: C must be at most %d (got %d)", what, kMaxRowChannels, c);
+  if (ld_x < c || ld_x % 8 != 0)
+    return fail(CC_ERR_INVALID, "%s: ld_x must be at least C and a multiple of 8", what);
+  if (act != CC_ACT_NONE && act != CC_ACT_SILU) return fail(CC_ERR_INVALID, "%s: unknown activation %d", what, act);
+  if (norm && !(eps > 0.f && eps <= 1e30f)) return fail(CC_ERR_INVALID, "%s: eps must be positive and finite", what);
+  DeviceInfo di;
+  if ((st = device_info(&di)) != CC_OK) return st;
+  RowArgs a = {};
+  a.x = reinterpret_cast<const uint4*>(x);
+  a.gamma = reinterpret_cast<const uint4*>(gamma);
+  a.y = y;
+  a.scales = scales;
+  a.rows = rows;
+  a.ld_x = ld_x / 8;
+  a.vecs = c / 8;
+  a.blocks = (c + kScaleBlock - 1) / kScaleBlock;
+  a.inv_c = 1.f / static_cast<float>(c);
+  a.eps = eps;
+  auto kern = !norm    ? row_kernel<false, false, true>
+              : scales ? (act == CC_ACT_SILU ? row_kernel<true, true, true> : row_kernel<true, false, true>)
+                       : (act == CC_ACT_SILU ? row_kernel<true, true, false> : row_kernel<true, false, false>);
+  const int grid = std::min(rows, di.sm_count * 8);
+  kern<<<grid, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launch_status(what);
+}
+
+// One CTA per 128 x 128 block of the weights: the block's largest |w|, then
+// its e4m3 values. Run once per layer when weights are loaded.
+__global__ void __launch_bounds__(256) fp8_weights_kernel(const uint4* __restrict__ w, uint2* __restrict__ wq,
+                                                          float* __restrict__ sw, int n, int kv, int kblocks) {
+  __shared__ uint32_t red[8];
+  const int tid = threadIdx.x;
+  const int v = blockIdx.x * 16 + (tid & 15);
+  const int row0 = blockIdx.y * kScaleBlock + (tid >> 4);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
+    if (row < n && v < kv) {
+      float f[8];
+      unpack8(w[static_cast<long long>(row) * kv + v], f);
+      m = max(m, absmax8_bits(f));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+  const float scale = block_scale(m);
+  const float inv = 1.f / scale;
+  if (tid == 0) sw[static_cast<long long>(blockIdx.y) * kblocks + blockIdx.x] = scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
+    if (row < n && v < kv) {
+      float f[8];
+      unpack8(w[static_cast<long long>(row) * kv + v], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= inv;
+      wq[static_cast<long long>(row) * kv + v] = pack8_e4m3(f);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace cc
+
+using namespace cc;
+
+extern "C" cc_status cc_rms_norm_act(const cc_bf16* x, const cc_bf16* gamma, cc_bf16* y, int rows, int c,
+                                     int64_t ld_x, float eps, int act, void* stream) {
+  return run_rows("rms_norm_act", true, x, gamma, y, nullptr, rows, c, ld_x, eps, act, stream);
+}
+
+extern "C" cc_status cc_rms_norm_act_fp8(const cc_bf16* x, const cc_bf16* gamma, cc_fp8* y, float* scales, int rows,
+                                         int c, int64_t ld_x, float eps, int act, void* stream) {
+  cc_status st;
+  if (empty_request("rms_norm_act_fp8", {rows}, &st)) return st;
+  if (!scales) return fail(CC_ERR_INVALID, "rms_norm_act_fp8: null pointer");
+  return run_rows("rms_norm_act_fp8", true, x, gamma, y, scales, rows, c, ld_x, eps, act, stream);
+}
+
+extern "C" cc_status cc_fp8_quantize(const cc_bf16* x, cc_fp8* y, float* scales, int rows, int c, int64_t ld_x,
+                                     void* stream) {
+  cc_status st;
+  if (empty_request("fp8_quantize", {rows}, &st)) return st;
+  if (!scales) return fail(CC_ERR_INVALID, "fp8_quantize: null pointer");
+  return run_rows("fp8_quantize", false, x, nullptr, y, scales, rows, c, ld_x, 1.f, CC_ACT_NONE, stream);
+}
+
+extern "C" cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, int k, void* stream) {
+  if (!w || !wq || !sw) return fail(CC_ERR_INVALID, "gemm_fp8_prepare: null pointer");
+  if (!aligned16(w) || !aligned16(wq) || !aligned16(sw))
+    return fail(CC_ERR_INVALID, "gemm_fp8_prepare: pointers must be 16-byte aligned");
+  if (n <= 0 || k <= 0) return fail(CC_ERR_INVALID, "gemm_fp8_prepare: sizes must be positive");
+  if (k % 16 != 0) return fail(CC_ERR_UNSUPPORTED, "gemm_fp8_prepare: K must be a multiple of 16 (got %d)", k);
+  const int nb = (n - 1) / kScaleBlock + 1, kb = (k - 1) / kScaleBlock + 1;
+  if (nb > 65535) return fail(CC_ERR_UNSUPPORTED, "gemm_fp8_prepare: N must be at most %d", 65535 * kScaleBlock);
+  DeviceInfo di;
+  cc_status st = device_info(&di);
+  if (st != CC_OK) return st;
+  fp8_weights_kernel<<<dim3(kb, nb), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<const uint4*>(w), reinterpret_cast<uint2*>(wq), sw, n, k / 8, kb);
+  return launch_status("gemm_fp8_prepare");
+}

@@ -12,7 +12,9 @@
  *  - Pointers are DEVICE pointers owned by the caller. The library allocates
  *    no device memory: intermediates live in a caller-provided workspace
  *    whose size the matching *_workspace_bytes() function returns.
- *  - bf16 tensors are passed as raw 16-bit patterns (cc_bf16 = uint16_t).
+ *  - bf16 tensors are passed as raw 16-bit patterns (cc_bf16 = uint16_t), e4m3
+ *    ones (4 exponent bits, 3 mantissa bits, largest value 448, no infinity) as
+ *    raw bytes (cc_fp8 = uint8_t).
  *  - Activations are channels-last: [N, D, H, W, C] contiguous, C fastest.
  *    Convolution weights keep the PyTorch Conv3d order [C_out, C_in, 3, 3, 3]
  *    until a *_prepare() call repacks them.
@@ -48,6 +50,9 @@
  *         a 3x3 stencil, bias and clamp) and head_stencil_kernel.
  *  [STACK] the stack's definition: causal 3x3x3 conv with two history frames,
  *         zeros before frame 0, spatial zero padding 1, fp32 accumulation.
+ *  [NORM], [FP8] no page: the norms in front of the convolutions and the
+ *         attention, and the 1x1x1 products around the attention and in the
+ *         shortcuts, in 8 bits.
  *  [HOST] no page: a transfer helper for the chunk-by-chunk decode loop.
  */
 #ifndef CC_H_
@@ -61,6 +66,7 @@ extern "C" {
 #endif
 
 typedef uint16_t cc_bf16;
+typedef uint8_t cc_fp8;
 
 typedef enum cc_status {
   CC_OK = 0,
@@ -333,6 +339,73 @@ cc_status cc_head_out_fused(const cc_bf16* x, const cc_bf16* wp, const cc_bf16* 
  * Other arguments, layouts and errors as cc_head_out. */
 cc_status cc_head_out_noalloc(const cc_bf16* x, const cc_bf16* wp, const cc_bf16* bias, cc_bf16* out, int n, int d,
                               int h, int w, int cin, int hist, void* stream);
+
+/* ----------------------------------- norms with an activation [NORM] */
+
+/* What follows the affine part of a norm: nothing, or v * sigmoid(v). */
+typedef enum cc_act { CC_ACT_NONE = 0, CC_ACT_SILU = 1 } cc_act;
+
+/* e4m3 outputs (the *_fp8 functions here and cc_fp8_quantize): for each row of
+ * C channels and block b of 128 of them (the last one may be shorter),
+ *   scales[row][b] = max(max |v| / 448, 2^-126),  y = e4m3(v / scales[row][b])
+ * from the unrounded fp32 v, rounded to nearest even; y [rows, C], scales
+ * [rows, ceil(C / 128)]. A block that holds a NaN gets a NaN scale and NaN
+ * values; one with an infinity gets an infinite scale, zeros for its finite
+ * values and NaN for the infinite ones. */
+
+/* Bytes of workspace a group norm of these sizes needs (0 for empty or
+ * invalid sizes). The contents need no preparation and nothing in them is
+ * kept between calls; calls whose GPU work overlaps need one each. */
+size_t cc_group_norm_workspace_bytes(int n, int p, int c, int groups);
+
+/* Group norm of N instances (frames, for a causal decoder) of P positions,
+ * channels last, C / groups neighbouring channels to a group:
+ *   y[n,i,c] = act((x[n,i,c] - m) / sqrt(v + eps) * gamma[c] + beta[c])
+ * with m and v the mean and the (biased) variance of the instance's group,
+ * held in fp32 and merged without cancellation; one rounding to bf16. x and
+ * y: [N, P, C], not overlapping; gamma, beta: [C] or NULL (ones, zeros).
+ * Needs C % 8 == 0, C <= 4096, groups dividing C, N <= 65535, eps > 0. Results
+ * do not change from run to run. */
+cc_status cc_group_norm_act(const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, cc_bf16* y, int n, int p,
+                            int c, int groups, float eps, int act, void* ws, size_t ws_bytes, void* stream);
+cc_status cc_group_norm_act_fp8(const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, cc_fp8* y, float* scales,
+                                int n, int p, int c, int groups, float eps, int act, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* RMS norm of each row: y[r,c] = act(x[r,c] / sqrt(mean_c x[r,c]^2 + eps) * gamma[c]),
+ * the mean in fp32, one rounding to bf16. x: row stride ld_x elements
+ * (ld_x >= C, % 8 == 0); gamma: [C] or NULL (ones); y: [rows, C] contiguous,
+ * not overlapping x. Needs C % 8 == 0, C <= 16384, eps > 0. */
+cc_status cc_rms_norm_act(const cc_bf16* x, const cc_bf16* gamma, cc_bf16* y, int rows, int c, int64_t ld_x,
+                          float eps, int act, void* stream);
+cc_status cc_rms_norm_act_fp8(const cc_bf16* x, const cc_bf16* gamma, cc_fp8* y, float* scales, int rows, int c,
+                              int64_t ld_x, float eps, int act, void* stream);
+
+/* ------------------------------ product in 8 bits with block scales [FP8] */
+
+/* bf16 rows to e4m3 with a scale per row and block of 128 channels, as
+ * above. x: row stride ld_x elements (ld_x >= C, % 8 == 0). Needs C % 8 == 0,
+ * C <= 16384. */
+cc_status cc_fp8_quantize(const cc_bf16* x, cc_fp8* y, float* scales, int rows, int c, int64_t ld_x, void* stream);
+
+/* Weights w [N, K] to e4m3 with one scale per 128 x 128 block (blocks at the
+ * right and lower edges may be smaller): wq [N, K], sw [ceil(N / 128)][ceil(K / 128)],
+ * each scale max(max |w| / 448, 2^-126). Needs K % 16 == 0. */
+cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, int k, void* stream);
+
+/* out[m,n] = bf16( sum_b sa[m,b] sw[n/128,b] sum_{k in block b} a[m,k] wq[n,k]
+ *                  + bias[n] + res[m,n] ),
+ * b over the blocks of 128 of K; products and sums in fp32, one rounding. a:
+ * [M, K] e4m3, sa: [M, ceil(K / 128)] (any fp32 values), wq, sw as written by
+ * cc_gemm_fp8_prepare; bias: [N] or NULL; res: bf16 rows of stride ld_res
+ * elements or NULL (ld_res is then ignored); out: bf16 rows of stride ld_out
+ * elements, columns N .. ld_out-1 untouched; out may be res when their strides
+ * are the same. Needs K % 16 == 0, N % 8 == 0, ld_out and ld_res >= N and
+ * % 8 == 0. ld_out lets q, k and v land in the packed rows that cc_attn_frame
+ * reads. */
+cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8* wq, const float* sw, const cc_bf16* bias,
+                      const cc_bf16* res, cc_bf16* out, int m, int n, int k, int64_t ld_res, int64_t ld_out,
+                      void* stream);
 
 /* ------------------------------------------------- result read-back [HOST] */
 
