@@ -10,6 +10,8 @@ message.
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _lib
@@ -392,22 +394,38 @@ def _act(act: str) -> int:
     return ACTS[act]
 
 
-def _on_current(tensors: dict) -> None:
-    """Every tensor given is on the current CUDA device, whose stream the call uses."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+def _arg(t, dtype, name: str, dev: int) -> int | None:
+    """_ptr for a tensor on the current device `dev`, whose stream the call uses (one quick test: a call's host time
+    counts where its tensors are small)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    ptr = _ptr(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    return ptr
 
 
-def _last_rows(t: torch.Tensor, dtype, name: str):
-    """(rows, C, ld) of a [..., C] tensor whose rows are C channels next to each other at one stride `ld`."""
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _last_rows(t, dtype, name: str, dev: int):
+    """(pointer, rows, C, ld) of a [..., C] tensor whose rows are C channels next to each other at one stride `ld`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    return (t.data_ptr(), *_row_layout(t, name))
+
+
+def _row_layout(t, name: str):
+    """(rows, C, ld)"""
     if t.dim() == 0:
         raise ValueError(f"{name}: expected [..., C]")
     c = t.shape[-1]
@@ -427,8 +445,11 @@ def _last_rows(t: torch.Tensor, dtype, name: str):
     return rows, c, c if ld is None else ld
 
 
-def _scale_blocks(c: int) -> int:
-    return (c + 127) // 128
+def _scales_of(scales, t, name: str) -> None:
+    """`scales` has a value for each row and 128 channels of t [..., C]."""
+    if scales.shape[:-1] != t.shape[:-1] or scales.shape[-1] != (t.shape[-1] + 127) // 128:
+        raise ValueError(f"{name} must be [..., ceil(C/128)] of [..., C], got {tuple(scales.shape)} for "
+                         f"{tuple(t.shape)}")
 
 
 def cc_group_norm_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
@@ -441,100 +462,99 @@ def _group_norm_sizes(x, gamma, beta, y):
     n, c = x.shape[0], x.shape[-1]
     if (gamma is not None and gamma.numel() != c) or (beta is not None and beta.numel() != c):
         raise ValueError("group_norm_act: gamma and beta must hold C elements")
-    p = 1
-    for s in x.shape[1:-1]:
-        p *= s
-    return n, p, c
+    return n, math.prod(x.shape[1:-1]), c
 
 
 def cc_group_norm_act(x, gamma, beta, y, groups: int, ws, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
     """Group norm of x [N, ..., C] over everything but N (view [N, D, H, W, C] as [N*D, H, W, C] for a norm per
     frame) and an activation ("silu" or "none"). gamma, beta: [C] or None."""
     n, p, c = _group_norm_sizes(x, gamma, beta, y)
-    px, pg, pb, py = _ptr(x, name="x"), _ptr(gamma, name="gamma"), _ptr(beta, name="beta"), _ptr(y, name="y")
-    pw = _ptr(ws, torch.uint8, "ws")
-    _on_current({"x": x, "gamma": gamma, "beta": beta, "y": y, "ws": ws})
-    _check(_lib.load().cc_group_norm_act(px, pg, pb, py, n, p, c, groups, eps, _act(act), pw,
-                                         0 if ws is None else ws.numel(), _stream(stream)))
+    dev, bf16 = torch.cuda.current_device(), torch.bfloat16
+    _check(_lib.load().cc_group_norm_act(
+        _arg(x, bf16, "x", dev), _arg(gamma, bf16, "gamma", dev), _arg(beta, bf16, "beta", dev),
+        _arg(y, bf16, "y", dev), n, p, c, groups, eps, _act(act), _arg(ws, torch.uint8, "ws", dev),
+        0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
 
 
 def cc_group_norm_act_fp8(x, gamma, beta, y, scales, groups: int, ws, eps: float = 1e-6, act: str = "silu",
                           stream=None) -> None:
     """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [N, ..., ceil(C/128)]."""
     n, p, c = _group_norm_sizes(x, gamma, beta, y)
-    if tuple(scales.shape) != (*x.shape[:-1], _scale_blocks(c)):
-        raise ValueError("group_norm_act_fp8: scales must be [N,...,ceil(C/128)]")
-    px, pg, pb = _ptr(x, name="x"), _ptr(gamma, name="gamma"), _ptr(beta, name="beta")
-    py, ps, pw = _ptr(y, torch.float8_e4m3fn, "y"), _ptr(scales, torch.float32, "scales"), _ptr(ws, torch.uint8, "ws")
-    _on_current({"x": x, "gamma": gamma, "beta": beta, "y": y, "scales": scales, "ws": ws})
-    _check(_lib.load().cc_group_norm_act_fp8(px, pg, pb, py, ps, n, p, c, groups, eps, _act(act), pw,
-                                             0 if ws is None else ws.numel(), _stream(stream)))
+    _scales_of(scales, x, "group_norm_act_fp8: scales")
+    dev, bf16 = torch.cuda.current_device(), torch.bfloat16
+    _check(_lib.load().cc_group_norm_act_fp8(
+        _arg(x, bf16, "x", dev), _arg(gamma, bf16, "gamma", dev), _arg(beta, bf16, "beta", dev),
+        _arg(y, torch.float8_e4m3fn, "y", dev), _arg(scales, torch.float32, "scales", dev), n, p, c, groups, eps,
+        _act(act), _arg(ws, torch.uint8, "ws", dev), 0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
 
 
 def cc_rms_norm_act(x, gamma, y, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
     """RMS norm over the channels of x [..., C] (rows may be strided) and an activation. gamma: [C] or None."""
-    rows, c, ld = _last_rows(x, torch.bfloat16, "x")
+    dev, bf16 = torch.cuda.current_device(), torch.bfloat16
+    px, rows, c, ld = _last_rows(x, bf16, "x", dev)
     if x.shape != y.shape or (gamma is not None and gamma.numel() != c):
         raise ValueError("rms_norm_act: x and y must share [...,C] and gamma hold C elements")
-    pg, py = _ptr(gamma, name="gamma"), _ptr(y, name="y")
-    _on_current({"x": x, "gamma": gamma, "y": y})
-    _check(_lib.load().cc_rms_norm_act(x.data_ptr(), pg, py, rows, c, ld, eps, _act(act), _stream(stream)))
+    _check(_lib.load().cc_rms_norm_act(px, _arg(gamma, bf16, "gamma", dev), _arg(y, bf16, "y", dev), rows, c, ld, eps,
+                                       _act(act), _raw_stream(stream, dev)))
 
 
 def cc_rms_norm_act_fp8(x, gamma, y, scales, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
     """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [..., ceil(C/128)]."""
-    rows, c, ld = _last_rows(x, torch.bfloat16, "x")
-    if x.shape != y.shape or tuple(scales.shape) != (*x.shape[:-1], _scale_blocks(c)) \
-            or (gamma is not None and gamma.numel() != c):
-        raise ValueError("rms_norm_act_fp8: y must be [...,C], scales [...,ceil(C/128)] and gamma [C] of x [...,C]")
-    pg, py = _ptr(gamma, name="gamma"), _ptr(y, torch.float8_e4m3fn, "y")
-    ps = _ptr(scales, torch.float32, "scales")
-    _on_current({"x": x, "gamma": gamma, "y": y, "scales": scales})
-    _check(_lib.load().cc_rms_norm_act_fp8(x.data_ptr(), pg, py, ps, rows, c, ld, eps, _act(act), _stream(stream)))
+    dev, bf16 = torch.cuda.current_device(), torch.bfloat16
+    px, rows, c, ld = _last_rows(x, bf16, "x", dev)
+    if x.shape != y.shape or (gamma is not None and gamma.numel() != c):
+        raise ValueError("rms_norm_act_fp8: x and y must share [...,C] and gamma hold C elements")
+    _scales_of(scales, x, "rms_norm_act_fp8: scales")
+    _check(_lib.load().cc_rms_norm_act_fp8(
+        px, _arg(gamma, bf16, "gamma", dev), _arg(y, torch.float8_e4m3fn, "y", dev),
+        _arg(scales, torch.float32, "scales", dev), rows, c, ld, eps, _act(act), _raw_stream(stream, dev)))
 
 
 # ------------------------------------- product in 8 bits with block scales --
 
 def cc_fp8_quantize(x, y, scales, stream=None) -> None:
     """bf16 rows x [..., C] (rows may be strided) to e4m3 y with scales [..., ceil(C/128)]."""
-    rows, c, ld = _last_rows(x, torch.bfloat16, "x")
-    if x.shape != y.shape or tuple(scales.shape) != (*x.shape[:-1], _scale_blocks(c)):
-        raise ValueError("fp8_quantize: y must be [...,C] and scales [...,ceil(C/128)] of x [...,C]")
-    py, ps = _ptr(y, torch.float8_e4m3fn, "y"), _ptr(scales, torch.float32, "scales")
-    _on_current({"x": x, "y": y, "scales": scales})
-    _check(_lib.load().cc_fp8_quantize(x.data_ptr(), py, ps, rows, c, ld, _stream(stream)))
+    dev = torch.cuda.current_device()
+    px, rows, c, ld = _last_rows(x, torch.bfloat16, "x", dev)
+    if x.shape != y.shape:
+        raise ValueError("fp8_quantize: x and y must share [...,C]")
+    _scales_of(scales, x, "fp8_quantize: scales")
+    _check(_lib.load().cc_fp8_quantize(px, _arg(y, torch.float8_e4m3fn, "y", dev),
+                                       _arg(scales, torch.float32, "scales", dev), rows, c, ld,
+                                       _raw_stream(stream, dev)))
 
 
 def cc_gemm_fp8_prepare(w, wq, sw, stream=None) -> None:
     """Weights w [N, K] (a 1x1x1 convolution's [Cout, Cin]) to e4m3 wq with scales sw [ceil(N/128), ceil(K/128)]."""
-    if w.dim() != 2 or w.shape != wq.shape or tuple(sw.shape) != (_scale_blocks(w.shape[0]), _scale_blocks(w.shape[1])):
+    if w.dim() != 2 or w.shape != wq.shape or tuple(sw.shape) != tuple((s + 127) // 128 for s in w.shape):
         raise ValueError("gemm_fp8_prepare: wq must be [N,K] and sw [ceil(N/128),ceil(K/128)] of w [N,K]")
-    pw, pq, ps = _ptr(w, name="w"), _ptr(wq, torch.float8_e4m3fn, "wq"), _ptr(sw, torch.float32, "sw")
-    _on_current({"w": w, "wq": wq, "sw": sw})
-    _check(_lib.load().cc_gemm_fp8_prepare(pw, pq, ps, w.shape[0], w.shape[1], _stream(stream)))
+    dev = torch.cuda.current_device()
+    _check(_lib.load().cc_gemm_fp8_prepare(
+        _arg(w, torch.bfloat16, "w", dev), _arg(wq, torch.float8_e4m3fn, "wq", dev),
+        _arg(sw, torch.float32, "sw", dev), w.shape[0], w.shape[1], _raw_stream(stream, dev)))
 
 
 def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
     """out [..., N] = a [..., K] wq^T with the block scales, plus bias [N] and res [..., N] (or None). out and res
     may be rows at a stride (a slice of packed qkv)."""
+    dev, bf16, f8, f32 = torch.cuda.current_device(), torch.bfloat16, torch.float8_e4m3fn, torch.float32
+    po, m, n, ld_out = _last_rows(out, bf16, "out", dev)
     k = a.shape[-1]
-    m, n, ld_out = _last_rows(out, torch.bfloat16, "out")
-    ld_res = n
-    if a.shape[:-1] != out.shape[:-1] or tuple(sa.shape) != (*a.shape[:-1], _scale_blocks(k)):
-        raise ValueError("gemm_fp8: a must be [...,K] and sa [...,ceil(K/128)] of out [...,N]")
-    if tuple(wq.shape) != (n, k) or tuple(sw.shape) != (_scale_blocks(n), _scale_blocks(k)):
-        raise ValueError("gemm_fp8: wq must be [N,K] and sw [ceil(N/128),ceil(K/128)]")
+    if a.shape[:-1] != out.shape[:-1] or wq.dim() != 2 or wq.shape[0] != n or wq.shape[1] != k:
+        raise ValueError("gemm_fp8: a must be [...,K] and wq [N,K] of out [...,N]")
+    _scales_of(sa, a, "gemm_fp8: sa")
+    if sw.dim() != 2 or sw.shape[0] != (n + 127) // 128 or sw.shape[1] != (k + 127) // 128:
+        raise ValueError("gemm_fp8: sw must be [ceil(N/128),ceil(K/128)]")
     if bias is not None and bias.numel() != n:
         raise ValueError("gemm_fp8: bias must hold N elements")
+    pr, ld_res = None, n
     if res is not None:
         if res.shape != out.shape:
             raise ValueError("gemm_fp8: res must have out's shape")
-        ld_res = _last_rows(res, torch.bfloat16, "res")[2]
-    pa, ps = _ptr(a, torch.float8_e4m3fn, "a"), _ptr(sa, torch.float32, "sa")
-    pw, pt, pb = _ptr(wq, torch.float8_e4m3fn, "wq"), _ptr(sw, torch.float32, "sw"), _ptr(bias, name="bias")
-    _on_current({"a": a, "sa": sa, "wq": wq, "sw": sw, "bias": bias, "res": res, "out": out})
-    _check(_lib.load().cc_gemm_fp8(pa, ps, pw, pt, pb, None if res is None else res.data_ptr(), out.data_ptr(), m, n,
-                                   k, ld_res, ld_out, _stream(stream)))
+        pr, _, _, ld_res = _last_rows(res, bf16, "res", dev)
+    _check(_lib.load().cc_gemm_fp8(_arg(a, f8, "a", dev), _arg(sa, f32, "sa", dev), _arg(wq, f8, "wq", dev),
+                                   _arg(sw, f32, "sw", dev), _arg(bias, bf16, "bias", dev), pr, po, m, n, k, ld_res,
+                                   ld_out, _raw_stream(stream, dev)))
 
 
 # -------------------------------------------------------- result read-back --

@@ -29,71 +29,155 @@ struct RowArgs {
   float eps;
 };
 
-// One row per block.
+// What follows the load: norm factor, activation, output. `on`: the lane has a
+// vector of the row. Whole warps call it, with the lanes of a half warp on one
+// block of 128 channels.
 template <bool NORM, bool SILU, bool FP8>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int kMaxVec = kMaxRowChannels / 8 / kRowThreads;
-  __shared__ float red[kRowThreads / 32];
-  const int tid = threadIdx.x;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    uint4 raw[kMaxVec];
-    float sum = 0.f;
+__device__ __forceinline__ void finish_vector(const RowArgs& a, const uint4& raw, const uint4& gamma, float rs,
+                                              long long r, int v, bool on) {
+  float f[8];
+  unpack8(raw, f);
+  if (NORM) {
+    float g[8];
+    unpack8(gamma, g);
 #pragma unroll
-    for (int i = 0; i < kMaxVec; ++i) {
-      const int v = tid + i * kRowThreads;
-      raw[i] = v < a.vecs ? a.x[r * a.ld_x + v] : make_uint4(0, 0, 0, 0);
-      if (NORM) {
-        float f[8];
-        unpack8(raw[i], f);
+    for (int e = 0; e < 8; ++e) f[e] *= rs * g[e];
+    activate8<SILU>(f);
+  }
+  if (FP8) {
+    float scale;
+    const uint2 q = quantize_block(f, scale);  // lanes without a vector hold zeros
+    if (on) {
+      static_cast<uint2*>(a.y)[r * a.vecs + v] = q;
+      if ((threadIdx.x & 15) == 0) a.scales[r * a.blocks + (v >> 4)] = scale;
+    }
+  } else if (on) {
+    static_cast<uint4*>(a.y)[r * a.vecs + v] = pack8(f);
+  }
+}
+
+__device__ __forceinline__ float sum_squares(const uint4& raw, float sum) {
+  float f[8];
+  unpack8(raw, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+  for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+  return sum;
+}
+
+// Rows of up to 8 * TPR * V channels, TPR lanes each with V vectors of a row in
+// registers, so a row is read once and its sum costs shuffles only. A warp
+// loads R rows (about four 16-byte loads a lane) before it uses the first, and
+// walks the rows in steps of the grid; gamma stays in registers. Neighbouring
+// rows go to different CTAs, so few rows spread over the SMs.
+template <int TPR, int V, bool NORM, bool SILU, bool FP8>
+__global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int R = V >= 4 ? 1 : 4 / V;
+  const int lane = threadIdx.x % TPR;
+  const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / TPR);
+  const long long first = static_cast<long long>(threadIdx.x / TPR) * gridDim.x + blockIdx.x;
+  uint4 gamma[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = lane + i * TPR;
+    gamma[i] = NORM && a.gamma && v < a.vecs ? a.gamma[v]
+                                             : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+  }
+  // every lane of a warp runs the same number of rounds (they share shuffles)
+  const long long warp_first = TPR == 32 ? first : static_cast<long long>(threadIdx.x / 32 * 2) * gridDim.x + blockIdx.x;
+  for (long long off = 0; warp_first + off < a.rows; off += R * step) {
+    uint4 raw[R][V];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const long long r = first + off + j * step;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int v = lane + i * TPR;
+        raw[j][i] = r < a.rows && v < a.vecs ? __ldcs(a.x + r * a.ld_x + v) : make_uint4(0, 0, 0, 0);
       }
     }
-    float rs = 1.f;
+    float rs[R];
     if (NORM) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      __syncthreads();
-      if ((tid & 31) == 0) red[tid >> 5] = sum;
-      __syncthreads();
-      sum = 0.f;
-      for (int i = 0; i < kRowThreads / 32; ++i) sum += red[i];
-      rs = 1.f / sqrtf(fmaf(sum, a.inv_c, a.eps));
+      for (int j = 0; j < R; ++j) {
+        rs[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) rs[j] = sum_squares(raw[j][i], rs[j]);
+      }
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) rs[j] += __shfl_xor_sync(0xffffffffu, rs[j], o);
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j) rs[j] = 1.f / sqrtf(fmaf(rs[j], a.inv_c, a.eps));
     }
 #pragma unroll
-    for (int i = 0; i < kMaxVec; ++i) {
-      const int v = tid + i * kRowThreads;
-      if (i * kRowThreads >= a.vecs) break;
-      float f[8];
-      unpack8(raw[i], f);
-      if (NORM) {
-        if (a.gamma && v < a.vecs) {
-          float g[8];
-          unpack8(a.gamma[v], g);
+    for (int j = 0; j < R; ++j) {
+      const long long r = first + off + j * step;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= rs * g[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= rs;
-        }
-        activate8<SILU>(f);
-      }
-      if (FP8) {
-        if (v >= a.vecs) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = 0.f;
-        }
-        float scale;
-        const uint2 q = quantize_block(f, scale);
-        if (v < a.vecs) {
-          static_cast<uint2*>(a.y)[r * a.vecs + v] = q;
-          if ((tid & 15) == 0) a.scales[r * a.blocks + (v >> 4)] = scale;
-        }
-      } else if (v < a.vecs) {
-        static_cast<uint4*>(a.y)[r * a.vecs + v] = pack8(f);
+      for (int i = 0; i < V; ++i) {
+        const int v = lane + i * TPR;
+        finish_vector<NORM, SILU, FP8>(a, raw[j][i], gamma[i], NORM ? rs[j] : 1.f, r, v, r < a.rows && v < a.vecs);
       }
     }
   }
+}
+
+// Longer rows: one per CTA, up to four vectors a thread.
+template <bool NORM, bool SILU, bool FP8>
+__global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __grid_constant__ RowArgs a) {
+  __shared__ float red[2][16];
+  const int tid = threadIdx.x;
+  int turn = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+    uint4 raw[4];
+    float rs = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = tid + i * blockDim.x;
+      raw[i] = v < a.vecs ? __ldcs(a.x + r * a.ld_x + v) : make_uint4(0, 0, 0, 0);
+    }
+    if (NORM) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rs = sum_squares(raw[i], rs);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
+      if ((tid & 31) == 0) red[turn][tid >> 5] = rs;
+      __syncthreads();  // one per row: the two halves of `red` take turns
+      rs = 0.f;
+      for (int i = 0; i < blockDim.x / 32; ++i) rs += red[turn][i];
+      rs = 1.f / sqrtf(fmaf(rs, a.inv_c, a.eps));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = tid + i * blockDim.x;
+      const uint4 gamma = NORM && a.gamma && v < a.vecs
+                              ? a.gamma[v]
+                              : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+      finish_vector<NORM, SILU, FP8>(a, raw[i], gamma, rs, r, v, v < a.vecs);
+    }
+  }
+}
+
+template <bool NORM, bool SILU, bool FP8>
+cc_status launch_rows(const char* what, const RowArgs& a, int sms, cudaStream_t stream) {
+  const int lanes = a.vecs <= 16 ? 16 : 32;
+  const int v = (a.vecs + lanes - 1) / lanes;
+  if (v > 8) {
+    const int threads = (a.vecs + 127) / 128 * 32;
+    const int grid = static_cast<int>(std::min<long long>(a.rows, static_cast<long long>(sms) * (2048 / threads)));
+    long_row_kernel<NORM, SILU, FP8><<<grid, threads, 0, stream>>>(a);
+    return launch_status(what);
+  }
+  auto kern = lanes == 16 ? row_kernel<16, 1, NORM, SILU, FP8>
+              : v == 1    ? row_kernel<32, 1, NORM, SILU, FP8>
+              : v == 2    ? row_kernel<32, 2, NORM, SILU, FP8>
+              : v <= 4    ? row_kernel<32, 4, NORM, SILU, FP8>
+                          : row_kernel<32, 8, NORM, SILU, FP8>;
+  // as many CTAs as fit, walking the rows
+  const int grid = static_cast<int>(std::min<long long>(a.rows, static_cast<long long>(sms) * (v > 4 ? 2 : 4)));
+  kern<<<grid, kRowThreads, 0, stream>>>(a);
+  return launch_status(what);
 }
 
 cc_status run_rows(const char* what, bool norm, const cc_bf16* x, const cc_bf16* gamma, void* y, float* scales,
@@ -124,12 +208,13 @@ cc_status run_rows(const char* what, bool norm, const cc_bf16* x, const cc_bf16*
   a.blocks = (c + kScaleBlock - 1) / kScaleBlock;
   a.inv_c = 1.f / static_cast<float>(c);
   a.eps = eps;
-  auto kern = !norm    ? row_kernel<false, false, true>
-              : scales ? (act == CC_ACT_SILU ? row_kernel<true, true, true> : row_kernel<true, false, true>)
-                       : (act == CC_ACT_SILU ? row_kernel<true, true, false> : row_kernel<true, false, false>);
-  const int grid = std::min(rows, di.sm_count * 8);
-  kern<<<grid, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status(what);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (!norm) return launch_rows<false, false, true>(what, a, di.sm_count, cs);
+  if (scales)
+    return act == CC_ACT_SILU ? launch_rows<true, true, true>(what, a, di.sm_count, cs)
+                              : launch_rows<true, false, true>(what, a, di.sm_count, cs);
+  return act == CC_ACT_SILU ? launch_rows<true, true, false>(what, a, di.sm_count, cs)
+                            : launch_rows<true, false, false>(what, a, di.sm_count, cs);
 }
 
 // One CTA per 128 x 128 block of the weights: the block's largest |w|, then

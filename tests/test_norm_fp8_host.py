@@ -103,9 +103,11 @@ def test_empty_requests(lib):
     assert lib.cc_gemm_fp8(None, None, None, None, None, None, None, 0, 64, 128, 64, 64, None) == 0
 
 
-def test_the_binding_refuses_what_it_cannot_pass_on():
+def test_the_binding_refuses_what_it_cannot_pass_on(lib, monkeypatch):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     f8 = torch.zeros(4, 64).to(torch.float8_e4m3fn)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(api, "_raw_stream", lambda stream, dev: 0)
     with pytest.raises(ValueError, match="CUDA"):
         api.cc_rms_norm_act(x, None, torch.empty_like(x))
     with pytest.raises(ValueError, match="CUDA"):
@@ -121,15 +123,10 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
 
 
 def test_rows_at_one_stride():
-    rows = api._last_rows
-    t = torch.zeros(2, 5, 48, dtype=torch.bfloat16, device="meta")
-
-    class Cuda(torch.Tensor):  # a layout to look at: the device check is the only thing that needs CUDA
-        device = torch.device("cuda")
+    t = torch.zeros(2, 5, 48, dtype=torch.bfloat16)
 
     def layout(v):
-        return rows(torch.empty_strided(v.shape, v.stride(), dtype=v.dtype, device="meta").as_subclass(Cuda),
-                    torch.bfloat16, "t")
+        return api._row_layout(v, "t")
 
     assert layout(t) == (10, 48, 48)
     assert layout(t[..., 16:32]) == (10, 16, 48)
@@ -140,3 +137,19 @@ def test_rows_at_one_stride():
         layout(t[:, :3, :8])
     with pytest.raises(ValueError, match="contiguous"):
         layout(t.transpose(1, 2))
+
+
+def test_tensors_on_another_device_are_refused():
+    class Elsewhere(torch.Tensor):  # a CPU tensor that says it lives on cuda:1
+        is_cuda = True
+        device = torch.device("cuda:1")
+
+        def get_device(self):
+            return 1
+
+    t = torch.zeros(4, 64, dtype=torch.bfloat16).as_subclass(Elsewhere)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        api._arg(t, torch.bfloat16, "x", 0)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        api._last_rows(t, torch.bfloat16, "x", 0)
+    assert api._arg(t, torch.bfloat16, "x", 1) == t.data_ptr()
