@@ -171,19 +171,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kTile; c += 8) {
         const int n = n0 + c;
         if (n < args.n) {
-          float v[8];
+          Vec8 v;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = acc[c + e];
-          float t[8];
+          for (int e = 0; e < 4; ++e) v.p[e] = pair(acc[c + 2 * e], acc[c + 2 * e + 1]);
           if (args.bias) {
-            unpack8(args.bias[n >> 3], t);
+            const Vec8 t = unpack8(args.bias[n >> 3]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += t[e];
+            for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
           }
           if (args.res) {
-            unpack8(*reinterpret_cast<const uint4*>(args.res + m * args.ld_res + n), t);
+            const Vec8 t = unpack8(*reinterpret_cast<const uint4*>(args.res + m * args.ld_res + n));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += t[e];
+            for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
           }
           *reinterpret_cast<uint4*>(args.out + m * args.ld_out + n) = pack8(v);
         }

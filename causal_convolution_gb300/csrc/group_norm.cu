@@ -1,9 +1,25 @@
 // Group norm over channels-last instances with an optional SiLU, written as
 // bf16 or as e4m3 with a scale per position and block of 128 channels.
+//
+// The channels of an instance are cut into slabs of whole groups (64 channels
+// where the groups allow it, so that a position's piece is 128 bytes). A slab
+// is independent of the others, and two kernels take it:
+//
+//  - gn_cluster_kernel: a cluster of up to 16 CTAs holds the slab in its
+//    shared memory, exchanges the groups' moments through it and writes the
+//    result. x is read once; no workspace.
+//  - gn_stream_kernel, for slabs that a cluster cannot hold: CTAs take tiles
+//    in an order in which a slab's second reading (to normalise) follows its
+//    first (for the moments) closely enough to find the slab in L2.
+//
+// Both sum a thread's values around a pivot, its first value, so that nothing
+// cancels where the mean is large against the deviation, and merge the
+// threads' means and squared deviations in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "cc.h"
 #include "cc_host.h"
@@ -13,9 +29,7 @@
 namespace cc {
 namespace {
 
-constexpr int kGnThreads = 512;
-constexpr int kGnMaxChannels = 8 * kGnThreads;
-constexpr int kChunkVecs = 16;  // vectors per thread and statistics chunk
+constexpr int kGnMaxChannels = 4096;
 
 // Mean and sum of squared deviations of `n` values; two of them merge exactly
 // (in real arithmetic) into that of their union, without the cancellation
@@ -25,31 +39,29 @@ struct Moments {
 };
 
 __device__ __forceinline__ void merge(Moments& a, const Moments& b) {
-  if (b.n == 0.f) return;
-  const float n = a.n + b.n;
-  const float d = b.mean - a.mean;
-  const float f = b.n / n;
-  a.mean = fmaf(d, f, a.mean);
-  a.m2 += b.m2 + d * d * a.n * f;
-  a.n = n;
+  if (a.n == 0.f) {
+    a = b;
+  } else if (b.n != 0.f) {
+    const float n = a.n + b.n;
+    const float d = b.mean - a.mean;
+    const float f = __fdividef(b.n, n);
+    a.mean = fmaf(d, f, a.mean);
+    a.m2 += fmaf(d * d, a.n * f, b.m2);
+    a.n = n;
+  }
 }
 
 __device__ __forceinline__ Moments warp_merge(Moments m) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    // the lower lane's moments come first on both sides, so all lanes agree
     Moments b = {__shfl_xor_sync(0xffffffffu, m.n, o), __shfl_xor_sync(0xffffffffu, m.mean, o),
                  __shfl_xor_sync(0xffffffffu, m.m2, o)};
-    if ((threadIdx.x & o) != 0) {
+    if ((threadIdx.x & o) != 0) {  // the lower lane's moments come first on both sides: all lanes agree
       const Moments t = m;
       m = b;
       b = t;
     }
-    if (m.n == 0.f) {
-      m = b;
-    } else {
-      merge(m, b);
-    }
+    merge(m, b);
   }
   return m;
 }
@@ -60,175 +72,551 @@ struct GnArgs {
   const uint4* beta;   // nullptr: zeros
   void* y;
   float* scales;
-  float2* part;  // [N][chunks][G]
-  float2* stat;  // [N][G] (mean, 1 / standard deviation)
   int p;
-  int vecs;   // C / 8
-  int slots;  // vecs, rounded up to whole half warps for e4m3
-  int groups;
-  int cpg;
-  int gw;  // channels of a vector part that always share a group: gcd(C / G, 8)
-  int chunks;
-  int chunk_rows;
-  int blocks;
+  int vecs;        // C / 8
+  int blocks;      // ceil(C / 128)
+  int slabs;       // per instance
+  int slab_vecs;   // of every slab but, perhaps, the last
+  int cpg;         // C / groups
+  int gw;          // channels of a vector that always share a group: gcd(C / groups, 8)
   float eps;
+  // cluster kernel
+  int rows_per_cta;
+  int rounds;      // vectors a thread keeps
+  int scratch_at, keep_at;  // bytes into shared memory
+  // stream kernel
+  int tiles;       // per slab
+  int lead;        // tiles between a tile's first and second reading, at least `tiles`
+  long long all_tiles;
+  unsigned long long* ticket;
+  unsigned int* done;   // [units] tiles whose moments are written
+  unsigned int* ready;  // [units] 1: stat is written
+  float2* part;         // [units][tiles][groups of a slab]
+  float2* stat;         // [units][groups of a slab]: mean, 1 / deviation
+  int slab_groups;
+  unsigned int* err;
+  unsigned long long timeout_ns;
 };
 
-// The moments of each group over a CTA's positions, from each thread's sums
-// of its eight channels around a pivot of their own.
-__device__ __forceinline__ void block_moments(const GnArgs& a, float2* red, float* cnt, const float (&pivot)[8],
-                                              const float (&s1)[8], const float (&s2)[8], int n, float2* out) {
+// Where a thread of T stands in its slab: positions `lane`, lane + lanes, ...,
+// and vector v of them. For e4m3 the vectors take whole half warps, so that the
+// 16 lanes of a block of 128 channels are neighbours.
+template <bool FP8, int T>
+struct Place {
+  int vecs, slots, lanes, lane, v;
+  bool on;
+  __device__ __forceinline__ Place(const GnArgs& a, int slab) {
+    vecs = min(a.slab_vecs, a.vecs - slab * a.slab_vecs);
+    slots = FP8 ? (vecs + 15) & ~15 : vecs;
+    lanes = T / slots;
+    lane = threadIdx.x / slots;
+    v = threadIdx.x - lane * slots;
+    on = lane < lanes && v < vecs;
+  }
+  // positions below `rows` that are this thread's
+  __device__ __forceinline__ int count(int rows) const { return on && lane < rows ? (rows - lane - 1) / lanes + 1 : 0; }
+};
+
+// A thread's sums around its pivots: one for its vector where all eight
+// channels share a group (ONE), one for each channel otherwise. `first` is the
+// thread's first vector.
+template <bool ONE>
+struct Sums {
+  static constexpr int K = ONE ? 1 : 4;
+  f32x2 neg[K], s1[K], s2[K];
+  __device__ __forceinline__ void start(const uint4& first) {
+    const Vec8 f = unpack8(first);
+#pragma unroll
+    for (int e = 0; e < K; ++e) {
+      neg[e] = ONE ? pair(-f[0], -f[0]) : pair(-f[2 * e], -f[2 * e + 1]);
+      s1[e] = s2[e] = pair(0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void add(const uint4& raw) {
+    const Vec8 f = unpack8(raw);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = ONE ? 0 : e;
+      const f32x2 d = add2(f.p[e], neg[k]);
+      s1[k] = add2(s1[k], d);
+      s2[k] = fma2(d, d, s2[k]);
+    }
+  }
+};
+
+// Shared scratch of block_moments: an entry (moments of each part of a vector,
+// count) per thread, or per warp and slot where a warp's lanes of the same
+// slot can be merged by shuffles.
+__host__ __device__ constexpr bool gn_shuffles(int slots) { return slots <= 16 && (slots & (slots - 1)) == 0; }
+__host__ __device__ constexpr int gn_entries(int slots, int threads) {
+  return gn_shuffles(slots) ? threads / 32 * slots : threads;
+}
+__host__ __device__ constexpr int gn_entry_bytes(int gw) { return 8 / gw * 8 + 4; }
+
+// The moments of the slab's groups over the CTA's positions, merged from the
+// threads' sums (of n positions each) in a fixed order; `out(group, moments)`
+// runs on one lane.
+template <bool ONE, bool FP8, int T, typename Out>
+__device__ __forceinline__ void block_moments(const GnArgs& a, const Place<FP8, T>& at, const Sums<ONE>& s, int n,
+                                              void* scratch, Out out) {
+  constexpr int K = ONE ? 1 : 8;
   const int tid = threadIdx.x;
-  float mean[8], m2[8];
-  const float inv = n > 0 ? 1.f / n : 0.f;
+  const int entries = gn_entries(at.slots, T);
+  float2* red = static_cast<float2*>(scratch);
+  float* cnt = reinterpret_cast<float*>(red + (ONE ? 1 : 8 / a.gw) * entries);
+  Moments m[K];
+  if (ONE) {
+    const float c = 8.f * n, sum = lo(s.s1[0]) + hi(s.s1[0]);
+    const float d = n > 0 ? __fdividef(sum, c) : 0.f;
+    m[0] = {c, d - lo(s.neg[0]), lo(s.s2[0]) + hi(s.s2[0]) - sum * d};
+  } else {
+    const float inv = n > 0 ? 1.f / n : 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float d = s1[e] * inv;
-    mean[e] = pivot[e] + d;
-    m2[e] = s2[e] - s1[e] * d;
-    m2[e] = m2[e] < 0.f ? 0.f : m2[e];  // keeps a NaN
+    for (int e = 0; e < K; ++e) {
+      const int k = (e >> 1) % Sums<ONE>::K;
+      const float sum = (e & 1) ? hi(s.s1[k]) : lo(s.s1[k]);
+      const float d = sum * inv;
+      m[e] = {static_cast<float>(n), d - ((e & 1) ? hi(s.neg[k]) : lo(s.neg[k])),
+              ((e & 1) ? hi(s.s2[k]) : lo(s.s2[k])) - sum * d};
+    }
   }
+#pragma unroll
+  for (int e = 0; e < K; ++e) m[e].m2 = m[e].m2 < 0.f ? 0.f : m[e].m2;  // keeps a NaN
   int w = 1;
-  float half = 0.5f * n;
+  if (!ONE) {
 #pragma unroll
-  for (int l = 1; l < 8; l <<= 1) {
-    if (a.gw > l) {  // uniform
+    for (int l = 1; l < 8; l <<= 1) {
+      if (a.gw > l) {  // neighbours of the same group
 #pragma unroll
-      for (int e = 0; e < 8; e += 2 * l) {
-        const float d = mean[e + l] - mean[e];
-        m2[e] += m2[e + l] + d * d * half;
-        mean[e] = 0.5f * (mean[e] + mean[e + l]);
+        for (int e = 0; e < 8; e += 2 * l) merge(m[e % K], m[(e + l) % K]);
+        w = 2 * l;
       }
-      w = 2 * l;
-      half *= 2.f;
     }
   }
+  int entry = tid;
+  bool writes = true;
+  if (gn_shuffles(at.slots)) {  // uniform
+    for (int o = at.slots; o < 32; o <<= 1) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e % w == 0) red[(e / w) * kGnThreads + tid] = make_float2(mean[e], m2[e]);
-  cnt[tid] = static_cast<float>(n * w);
+      for (int e = 0; e < K; ++e) {
+        if (e % w == 0) {
+          Moments b = {__shfl_xor_sync(0xffffffffu, m[e].n, o), __shfl_xor_sync(0xffffffffu, m[e].mean, o),
+                       __shfl_xor_sync(0xffffffffu, m[e].m2, o)};
+          merge(m[e], b);  // only the lowest lanes' results are used
+        }
+      }
+    }
+    entry = (tid >> 5) * at.slots + (tid & 31);
+    writes = (tid & 31) < at.slots;
+  }
+  if (writes) {
+#pragma unroll
+    for (int e = 0; e < K; ++e)
+      if (e % w == 0) red[(e / w) * entries + entry] = make_float2(m[e].mean, m[e].m2);
+    cnt[entry] = m[0].n;
+  }
   __syncthreads();
-  const int per = a.cpg / a.gw;           // vector parts per group and position
-  const int lanes = kGnThreads / a.slots;  // positions side by side
-  const int parts = 8 / a.gw;
-  for (int g = tid >> 5; g < a.groups; g += kGnThreads / 32) {
-    Moments m = {0.f, 0.f, 0.f};
-    for (int i = tid & 31; i < per * lanes; i += 32) {
-      const int j = g * per + i % per;
-      const int t = (i / per) * a.slots + j / parts;
-      const float2 v = red[(j % parts) * kGnThreads + t];
-      const Moments b = {cnt[t], v.x, v.y};
-      if (m.n == 0.f) {
-        m = b;
-      } else {
-        merge(m, b);
-      }
+  const int parts = ONE ? 1 : 8 / a.gw;      // of a vector
+  const int per = ONE ? a.cpg >> 3 : a.cpg / a.gw;  // parts in a group
+  const int side = gn_shuffles(at.slots) ? T / 32 : at.lanes;  // entries of a slot
+  for (int g = tid >> 5; g < at.vecs * 8 / a.cpg; g += T / 32) {
+    Moments t = {0.f, 0.f, 0.f};
+    for (int i = tid & 31; i < per * side; i += 32) {
+      const int q = i / per;
+      const int j = g * per + (i - q * per);
+      const int at_entry = q * at.slots + (ONE ? j : j / parts);
+      const float2 v = red[(ONE ? 0 : j % parts) * entries + at_entry];
+      merge(t, Moments{cnt[at_entry], v.x, v.y});
     }
-    m = warp_merge(m);
-    if ((tid & 31) == 0) out[g] = make_float2(m.mean, m.m2);
+    t = warp_merge(t);
+    if ((tid & 31) == 0) out(g, t);
   }
 }
 
-__global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(const __grid_constant__ GnArgs a) {
-  extern __shared__ float2 red[];
-  __shared__ float cnt[kGnThreads];
-  const int lanes = kGnThreads / a.slots;
-  const int lane = threadIdx.x / a.slots;
-  const int v = threadIdx.x - lane * a.slots;
-  const int r0 = blockIdx.x * a.chunk_rows;
-  const int r1 = min(r0 + a.chunk_rows, a.p);
-  const uint4* x = a.x + static_cast<long long>(blockIdx.y) * a.p * a.vecs + v;
-  float pivot[8] = {}, s1[8] = {}, s2[8] = {};
-  int n = 0;
-  if (lane < lanes && v < a.vecs) {
-    for (int r = r0 + lane; r < r1; r += lanes) {
-      float f[8];
-      unpack8(x[static_cast<long long>(r) * a.vecs], f);
+__device__ __forceinline__ float2 mean_and_factor(const Moments& m, float eps) {
+  return make_float2(m.mean, 1.f / sqrtf(m.m2 / m.n + eps));
+}
+
+// A thread's eight channels: act((x - mean) * k + beta). The mean is taken off
+// first: folded into beta it would cost digits where it is large.
+template <bool ONE, bool SILU, bool FP8, int T>
+struct Affine {
+  f32x2 neg[Sums<ONE>::K];
+  Vec8 k, b;
+  __device__ __forceinline__ void load_params(const GnArgs& a, const Place<FP8, T>& at, int slab) {
+    k = splat8(1.f);
+    b = splat8(0.f);
+    if (at.on && a.gamma) k = unpack8(__ldg(a.gamma + slab * a.slab_vecs + at.v));
+    if (at.on && a.beta) b = unpack8(__ldg(a.beta + slab * a.slab_vecs + at.v));
+  }
+  template <typename Stat>
+  __device__ __forceinline__ void load_stat(const GnArgs& a, const Place<FP8, T>& at, Stat stat) {
+    if (ONE) {
+      const float2 s = at.on ? stat(8 * at.v / a.cpg) : make_float2(0.f, 0.f);
+      neg[0] = pair(-s.x, -s.x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (n == 0) pivot[e] = f[e];
-        const float d = f[e] - pivot[e];
-        s1[e] += d;
-        s2[e] = fmaf(d, d, s2[e]);
-      }
-      ++n;
-    }
-  }
-  block_moments(a, red, cnt, pivot, s1, s2, n,
-                a.part + (static_cast<long long>(blockIdx.y) * a.chunks + blockIdx.x) * a.groups);
-}
-
-__global__ void __launch_bounds__(128) gn_finish_kernel(const __grid_constant__ GnArgs a) {
-  const int g = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (g >= a.groups) return;
-  const long long n = blockIdx.y;
-  Moments m = {0.f, 0.f, 0.f};
-  for (int i = threadIdx.x & 31; i < a.chunks; i += 32) {
-    const float2 v = a.part[(n * a.chunks + i) * a.groups + g];
-    const int rows = min(a.chunk_rows, a.p - i * a.chunk_rows);
-    const Moments b = {static_cast<float>(rows) * a.cpg, v.x, v.y};
-    if (m.n == 0.f) {
-      m = b;
+      for (int i = 0; i < 4; ++i) k.p[i] = mul2(k.p[i], pair(s.y, s.y));
     } else {
-      merge(m, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * at.v + 2 * i;
+        const float2 s = at.on ? stat(c / a.cpg) : make_float2(0.f, 0.f);
+        const float2 t = at.on ? stat((c + 1) / a.cpg) : make_float2(0.f, 0.f);
+        neg[i % Sums<ONE>::K] = pair(-s.x, -t.x);
+        k.p[i] = mul2(k.p[i], pair(s.y, t.y));
+      }
     }
   }
-  m = warp_merge(m);
-  if ((threadIdx.x & 31) == 0) a.stat[n * a.groups + g] = make_float2(m.mean, 1.f / sqrtf(m.m2 / m.n + a.eps));
-}
-
-template <bool SILU, bool FP8>
-__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(const __grid_constant__ GnArgs a) {
-  const int lanes = kGnThreads / a.slots;
-  const int lane = threadIdx.x / a.slots;
-  const int v = threadIdx.x - lane * a.slots;
-  const int r0 = blockIdx.x * a.chunk_rows;
-  const int r1 = min(r0 + a.chunk_rows, a.p);
-  const bool used = lane < lanes && v < a.vecs;
-  // (x - mean) * k + beta, the mean taken off first: folded into beta it would
-  // cost digits where it is large against the deviation
-  float mean[8], k[8], b[8];
+  // y and scales: of the vector, and of the row's first block of the slab
+  __device__ __forceinline__ void write(const Place<FP8, T>& at, const uint4& raw, void* y, float* scales,
+                                        bool on) const {
+    Vec8 f = unpack8(raw);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) k[e] = 1.f, b[e] = 0.f, mean[e] = 0.f;
-  if (used) {
-    if (a.gamma) unpack8(a.gamma[v], k);
-    if (a.beta) unpack8(a.beta[v], b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 st = a.stat[static_cast<long long>(blockIdx.y) * a.groups + (8 * v + e) / a.cpg];
-      mean[e] = st.x;
-      k[e] *= st.y;
-    }
-  }
-  for (int rr = r0; rr < r1; rr += lanes) {
-    const int r = rr + lane;
-    const bool on = used && r < r1;
-    const long long at = (static_cast<long long>(blockIdx.y) * a.p + r) * a.vecs + v;
-    float f[8] = {};
-    if (on) {
-      unpack8(a.x[at], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e] - mean[e], k[e], b[e]);
-      activate8<SILU>(f);
-    }
+    for (int i = 0; i < 4; ++i) f.p[i] = fma2(add2(f.p[i], neg[ONE ? 0 : i]), k.p[i], b.p[i]);
+    activate8<SILU>(f);
     if (FP8) {
+      if (!at.on) f = splat8(0.f);
       float scale;
       const uint2 q = quantize_block(f, scale);
       if (on) {
-        static_cast<uint2*>(a.y)[at] = q;
-        if ((v & 15) == 0) a.scales[(static_cast<long long>(blockIdx.y) * a.p + r) * a.blocks + (v >> 4)] = scale;
+        *static_cast<uint2*>(y) = q;
+        if ((at.v & 15) == 0) scales[at.v >> 4] = scale;
       }
     } else if (on) {
-      static_cast<uint4*>(a.y)[at] = pack8(f);
+      *static_cast<uint4*>(y) = pack8(f);
     }
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// ---------------------------------------------------------------- on chip --
+
+// One cluster per (instance, slab); its CTAs take the positions in equal runs.
+// A thread copies its own vectors to shared memory and is the only one to read
+// them back, so the copies need no barrier; they are waited for in quarters,
+// the moments of one while the next are on their way.
+template <bool ONE, bool SILU, bool FP8, int T>
+__global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_constant__ GnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint32_t ranks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const uint32_t rank = cluster_ctarank();
+  const int unit = blockIdx.x / ranks;
+  const int instance = unit / a.slabs;
+  const int slab = unit - instance * a.slabs;
+  const Place<FP8, T> at(a, slab);
+  float2* mom = reinterpret_cast<float2*>(smem);
+  float2* stat = mom + a.slab_groups;
+  uint8_t* scratch = smem + a.scratch_at;
+  const int stride = at.lanes * at.slots;
+  uint4* keep = reinterpret_cast<uint4*>(smem + a.keep_at) + threadIdx.x;
+  const int r0 = rank * a.rows_per_cta;
+  const int rows = max(0, min(a.rows_per_cta, a.p - r0));
+  const int n = at.count(rows);
+  const long long row0 = static_cast<long long>(instance) * a.p + r0;
+  const uint4* x = a.x + (row0 + at.lane) * a.vecs + slab * a.slab_vecs + at.v;
+  const int step = at.lanes * a.vecs;
+  const int quarter = (a.rounds + 3) / 4;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int end = min((q + 1) * quarter, n);
+    for (int i = q * quarter; i < end; ++i)
+      cp_async16(smem_u32(keep + i * stride), x + static_cast<long long>(i) * step);
+    cp_async_commit();
+  }
+  Affine<ONE, SILU, FP8, T> affine;
+  affine.load_params(a, at, slab);
+  Sums<ONE> sums;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (q == 0) cp_async_wait<3>();
+    if (q == 1) cp_async_wait<2>();
+    if (q == 2) cp_async_wait<1>();
+    if (q == 3) cp_async_wait<0>();
+    if (q == 0) sums.start(n > 0 ? keep[0] : make_uint4(0, 0, 0, 0));
+    const int end = min((q + 1) * quarter, n);
+    for (int i = q * quarter; i < end; ++i) sums.add(keep[i * stride]);
+  }
+  block_moments<ONE>(a, at, sums, n, scratch,
+                     [&](int g, const Moments& m) { mom[g] = make_float2(m.mean, m.m2); });
+  __syncwarp();
+  cluster_sync_all();
+  for (int g = threadIdx.x; g < at.vecs * 8 / a.cpg; g += T) {
+    Moments m = {0.f, 0.f, 0.f};
+    for (uint32_t k = 0; k < ranks; ++k) {
+      const float2 v = ld_cluster_f2(mapa_shared(smem_u32(&mom[g]), k));
+      const int c = max(0, min(a.rows_per_cta, a.p - static_cast<int>(k) * a.rows_per_cta));
+      merge(m, Moments{static_cast<float>(c) * a.cpg, v.x, v.y});
+    }
+    stat[g] = mean_and_factor(m, a.eps);
+  }
+  __syncthreads();
+  // nobody reads this CTA's moments any more once all have arrived here
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  affine.load_stat(a, at, [&](int g) { return stat[g]; });
+  const long long at_y = (row0 + at.lane) * a.vecs + slab * a.slab_vecs + at.v;
+  uint8_t* y = static_cast<uint8_t*>(a.y) + at_y * (FP8 ? 8 : 16);
+  float* scales = FP8 ? a.scales + (row0 + at.lane) * a.blocks + slab * a.slab_vecs / 16 : nullptr;
+  // e4m3: whole warps stay together, for the shuffles
+  const int end = FP8 ? (rows + at.lanes - 1) / at.lanes : n;
+#pragma unroll 2
+  for (int i = 0; i < end; ++i) {
+    const bool on = i < n;
+    affine.write(at, on ? keep[i * stride] : make_uint4(0, 0, 0, 0), y, scales, on);
+    y += static_cast<long long>(step) * (FP8 ? 8 : 16);
+    if (FP8) scales += at.lanes * a.blocks;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// -------------------------------------------------------------- through L2 --
+
+constexpr int kTileVecs = 4;   // vectors a thread has in flight
+constexpr int kTileTurns = 2;  // times that makes a tile
+
+__device__ __forceinline__ unsigned int ld_acquire(const unsigned int* p) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(unsigned int* p, unsigned int v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Tiles are numbered through the units (instance, slab) in order. Tickets hand
+// out first readings `lead` tiles ahead of second readings and alternate
+// between them; a second reading waits until its unit's statistics are there,
+// which takes first readings with smaller tickets only, so the smallest open
+// ticket never waits for one that nobody holds, however few CTAs run at once.
+template <bool ONE, bool SILU, bool FP8, int T>
+__global__ void __launch_bounds__(T, 1024 / T) gn_stream_kernel(const __grid_constant__ GnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ unsigned long long next;
+  __shared__ unsigned int word;
+  const int tid = threadIdx.x;
+  if (tid == 0) next = atomicAdd(a.ticket, 1ull);
+  __syncthreads();
+  for (;;) {
+    const long long t = static_cast<long long>(next);
+    if (t >= 2 * a.all_tiles) return;
+    bool second;
+    long long tile;
+    if (t < a.lead) {
+      second = false, tile = t;
+    } else if (t < 2 * a.all_tiles - a.lead) {
+      second = (t - a.lead) & 1;
+      tile = (t - a.lead) / 2 + (second ? 0 : a.lead);
+    } else {
+      second = true, tile = t - a.all_tiles;
+    }
+    const int unit = static_cast<int>(tile / a.tiles);
+    const int i0 = static_cast<int>(tile - static_cast<long long>(unit) * a.tiles);
+    const int instance = unit / a.slabs;
+    const int slab = unit - instance * a.slabs;
+    const Place<FP8, T> at(a, slab);
+    const int tile_rows = at.lanes * kTileVecs * kTileTurns;
+    const int r0 = i0 * tile_rows;
+    const int rows = max(0, min(tile_rows, a.p - r0));  // a narrower last slab has fewer tiles than the others
+    const int n = at.count(rows);
+    const long long row0 = static_cast<long long>(instance) * a.p + r0 + at.lane;
+    const uint4* x = a.x + row0 * a.vecs + slab * a.slab_vecs + at.v;
+    const int step = at.lanes * a.vecs;
+    __syncthreads();  // `next` is read
+    if (tid == 0) next = atomicAdd(a.ticket, 1ull);
+    uint4 raw[kTileVecs];
+    if (!second) {
+      Sums<ONE> sums;
+#pragma unroll
+      for (int turn = 0; turn < kTileTurns; ++turn) {
+#pragma unroll
+        for (int i = 0; i < kTileVecs; ++i)
+          if (turn * kTileVecs + i < n) raw[i] = __ldg(x + static_cast<long long>(turn * kTileVecs + i) * step);
+        if (turn == 0) sums.start(n > 0 ? raw[0] : make_uint4(0, 0, 0, 0));
+#pragma unroll
+        for (int i = 0; i < kTileVecs; ++i)
+          if (turn * kTileVecs + i < n) sums.add(raw[i]);
+      }
+      float2* part = a.part + (static_cast<long long>(unit) * a.tiles + i0) * a.slab_groups;
+      block_moments<ONE>(a, at, sums, n, smem, [&](int g, const Moments& m) {
+        part[g] = make_float2(m.mean, m.m2);
+        __threadfence();
+      });
+      __syncthreads();
+      if (tid == 0) word = atomicAdd(a.done + unit, 1u);
+      __syncthreads();
+      if (word == static_cast<unsigned int>(a.tiles - 1)) {  // the unit's last: merge in the tiles' order
+        __threadfence();
+        const float2* all = a.part + static_cast<long long>(unit) * a.tiles * a.slab_groups;
+        for (int g = tid >> 5; g < at.vecs * 8 / a.cpg; g += T / 32) {
+          Moments m = {0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int i = tid & 31; i < a.tiles; i += 32) {
+            const float2 v = __ldcg(all + static_cast<long long>(i) * a.slab_groups + g);
+            const int c = max(0, min(tile_rows, a.p - i * tile_rows));
+            merge(m, Moments{static_cast<float>(c) * a.cpg, v.x, v.y});
+          }
+          m = warp_merge(m);
+          if ((tid & 31) == 0) {
+            a.stat[static_cast<long long>(unit) * a.slab_groups + g] = mean_and_factor(m, a.eps);
+            __threadfence();
+          }
+        }
+        __syncthreads();
+        if (tid == 0) st_release(a.ready + unit, 1u);
+      }
+    } else {
+      Affine<ONE, SILU, FP8, T> affine;
+#pragma unroll
+      for (int i = 0; i < kTileVecs; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (i < n) raw[i] = __ldcs(x + static_cast<long long>(i) * step);
+      }
+      affine.load_params(a, at, slab);
+      if (tid == 0) {
+        unsigned int ok = ld_acquire(a.ready + unit);
+        if (!ok) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!ok && globaltimer_ns() - t0 < a.timeout_ns) ok = ld_acquire(a.ready + unit);
+          if (!ok) atomicOr(a.err, DEVERR_TIMEOUT);
+        }
+        word = ok;
+      }
+      __syncthreads();
+      if (!word) return;
+      const float2* stat = a.stat + static_cast<long long>(unit) * a.slab_groups;
+      affine.load_stat(a, at, [&](int g) { return __ldcg(stat + g); });
+      uint8_t* y = static_cast<uint8_t*>(a.y) + (row0 * a.vecs + slab * a.slab_vecs + at.v) * (FP8 ? 8 : 16);
+      float* scales = FP8 ? a.scales + row0 * a.blocks + slab * a.slab_vecs / 16 : nullptr;
+#pragma unroll
+      for (int turn = 0; turn < kTileTurns; ++turn) {
+        if (turn > 0) {
+#pragma unroll
+          for (int i = 0; i < kTileVecs; ++i)
+            if (turn * kTileVecs + i < n) raw[i] = __ldcs(x + static_cast<long long>(turn * kTileVecs + i) * step);
+        }
+#pragma unroll
+        for (int i = 0; i < kTileVecs; ++i) {
+          const int j = turn * kTileVecs + i;
+          affine.write(at, raw[i], y + static_cast<long long>(j) * step * (FP8 ? 8 : 16),
+                       FP8 ? scales + static_cast<long long>(j) * at.lanes * a.blocks : nullptr, j < n);
+        }
+      }
+    }
+    __syncthreads();  // the next ticket is there, `word` and the scratch are free
   }
 }
 
-int gn_chunk_rows(int c) { return std::max(1, kGnThreads / (c / 8)) * kChunkVecs; }
+// -------------------------------------------------------------------- host --
 
-size_t gn_bytes(int n, int p, int c, int groups) {
-  const size_t chunks = (static_cast<size_t>(p) + gn_chunk_rows(c) - 1) / gn_chunk_rows(c);
-  return (chunks + 1) * n * groups * sizeof(float2);
+// Channels of a slab: whole groups, whole vectors (whole blocks of 128 for
+// e4m3), at least 64 of them. At most 128 groups: below 64 channels the least
+// common multiple of C / groups and 8 has 8 groups at most, and that with 128
+// has 128.
+int slab_channels(int c, int groups, bool fp8) {
+  const int unit = std::lcm(c / groups, fp8 ? kScaleBlock : 8);
+  if (unit >= c) return c;
+  return std::min(c, unit * std::max(1, 64 / unit));
+}
+
+struct GnPlan {
+  bool cluster;
+  int threads;
+  int slab_c, slabs, slab_groups, scratch;
+  int ranks, rows, rounds, scratch_at, keep_at;  // cluster
+  size_t smem;
+  int tiles;  // stream
+  long long units;
+  size_t ws_bytes;
+};
+
+constexpr size_t kMaxSmem = 232448;
+
+GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
+  GnPlan g = {};
+  g.slab_c = slab_channels(c, groups, fp8);
+  g.slabs = (c + g.slab_c - 1) / g.slab_c;
+  g.slab_groups = g.slab_c / (c / groups);
+  g.units = static_cast<long long>(n) * g.slabs;
+  const int gw = std::gcd(c / groups, 8);
+  // the widest slab has the fewest positions side by side
+  const int slots = fp8 ? (g.slab_c / 8 + 15) / 16 * 16 : g.slab_c / 8;
+  const int last_c = c - (g.slabs - 1) * g.slab_c;
+  const int last = fp8 ? (last_c / 8 + 15) / 16 * 16 : last_c / 8;
+  g.threads = slots > 256 ? 512 : 256;
+  const int lanes = g.threads / slots;
+  g.scratch = std::max(gn_entries(slots, g.threads), gn_entries(last, g.threads)) * gn_entry_bytes(gw);
+  g.scratch_at = (2 * g.slab_groups * static_cast<int>(sizeof(float2)) + 15) / 16 * 16;
+  g.keep_at = g.scratch_at + (g.scratch + 15) / 16 * 16;
+  auto cut = [&](int ranks) {
+    g.ranks = ranks;
+    g.rows = (p + ranks - 1) / ranks;
+    g.rounds = (g.rows + lanes - 1) / lanes;
+    g.smem = g.keep_at + static_cast<size_t>(g.rows) * slots * 16;
+  };
+  for (int ranks = 1; ranks <= 16; ranks *= 2) {
+    cut(ranks);
+    if (g.smem <= kMaxSmem) break;
+  }
+  g.cluster = g.smem <= kMaxSmem;
+  if (g.cluster) {
+    // two CTAs to an SM where eight of them hold the slab, and more CTAs while
+    // SMs are idle and a thread still has several vectors
+    while (g.ranks < 8 && (g.smem > kMaxSmem / 2 - 1024 || (g.units * g.ranks < 152 && g.rounds > 2))) cut(g.ranks * 2);
+    return g;
+  }
+  const int tile_rows = lanes * kTileVecs * kTileTurns;
+  g.tiles = (p + tile_rows - 1) / tile_rows;
+  g.ws_bytes = 16 + (g.units * 8 + 15) / 16 * 16 +
+               static_cast<size_t>(g.units) * (g.tiles + 1) * g.slab_groups * sizeof(float2);
+  return g;
+}
+
+template <bool ONE, bool SILU, bool FP8, int T>
+cc_status launch_group_norm(const char* what, GnArgs& a, const GnPlan& g, int sms, cudaStream_t s) {
+  if (g.cluster) {
+    auto kern = gn_cluster_kernel<ONE, SILU, FP8, T>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess && g.ranks > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: kernel attributes: %s", what, cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(g.units * g.ranks));
+    cfg.blockDim = dim3(T);
+    cfg.dynamicSmemBytes = g.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = g.ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+    return launch_status(what);
+  }
+  auto kern = gn_stream_kernel<ONE, SILU, FP8, T>;
+  const long long grid = std::min<long long>(1024LL / T * sms, 2 * a.all_tiles);
+  kern<<<static_cast<unsigned>(grid), T, g.scratch, s>>>(a);
+  return launch_status(what);
+}
+
+template <bool ONE, bool SILU, bool FP8>
+cc_status launch_group_norm(const char* what, GnArgs& a, const GnPlan& g, int sms, cudaStream_t s) {
+  return g.threads == 512 ? launch_group_norm<ONE, SILU, FP8, 512>(what, a, g, sms, s)
+                          : launch_group_norm<ONE, SILU, FP8, 256>(what, a, g, sms, s);
 }
 
 cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, void* y,
@@ -247,9 +635,9 @@ cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamm
   if (p > (1 << 30)) return fail(CC_ERR_UNSUPPORTED, "%s: too many positions", what);
   if (!(eps > 0.f && eps <= 1e30f)) return fail(CC_ERR_INVALID, "%s: eps must be positive and finite", what);
   if (act != CC_ACT_NONE && act != CC_ACT_SILU) return fail(CC_ERR_INVALID, "%s: unknown activation %d", what, act);
-  const size_t need = gn_bytes(n, p, c, groups);
-  if (!ws || ws_bytes < need)
-    return fail(CC_ERR_INVALID, "%s: workspace of %zu bytes needed (got %zu)", what, need, ws ? ws_bytes : 0);
+  const GnPlan g = gn_plan(n, p, c, groups, fp8);
+  if (g.ws_bytes > 0 && (!ws || ws_bytes < g.ws_bytes))
+    return fail(CC_ERR_INVALID, "%s: workspace of %zu bytes needed (got %zu)", what, g.ws_bytes, ws ? ws_bytes : 0);
   DeviceInfo di;
   if ((st = device_info(&di)) != CC_OK) return st;
   GnArgs a = {};
@@ -260,26 +648,47 @@ cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamm
   a.scales = scales;
   a.p = p;
   a.vecs = c / 8;
-  a.groups = groups;
-  a.cpg = c / groups;
-  a.gw = a.cpg % 8 == 0 ? 8 : a.cpg % 4 == 0 ? 4 : a.cpg % 2 == 0 ? 2 : 1;
-  a.chunk_rows = gn_chunk_rows(c);
-  a.chunks = (p + a.chunk_rows - 1) / a.chunk_rows;
   a.blocks = (c + kScaleBlock - 1) / kScaleBlock;
+  a.slabs = g.slabs;
+  a.slab_vecs = g.slab_c / 8;
+  a.cpg = c / groups;
+  a.gw = std::gcd(a.cpg, 8);
   a.eps = eps;
-  a.stat = static_cast<float2*>(ws);
-  a.part = a.stat + static_cast<size_t>(n) * groups;
+  a.slab_groups = g.slab_groups;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  a.slots = a.vecs;
-  gn_stats_kernel<<<dim3(a.chunks, n), kGnThreads, 8 / a.gw * kGnThreads * sizeof(float2), s>>>(a);
-  if ((st = launch_status(what)) != CC_OK) return st;
-  gn_finish_kernel<<<dim3((groups + 3) / 4, n), 128, 0, s>>>(a);
-  if ((st = launch_status(what)) != CC_OK) return st;
-  if (fp8) a.slots = (a.vecs + 15) / 16 * 16;
-  auto kern = fp8 ? (act == CC_ACT_SILU ? gn_apply_kernel<true, true> : gn_apply_kernel<false, true>)
-                  : (act == CC_ACT_SILU ? gn_apply_kernel<true, false> : gn_apply_kernel<false, false>);
-  kern<<<dim3(a.chunks, n), kGnThreads, 0, s>>>(a);
-  return launch_status(what);
+  if (g.cluster) {
+    a.rows_per_cta = g.rows;
+    a.rounds = g.rounds;
+    a.scratch_at = g.scratch_at;
+    a.keep_at = g.keep_at;
+  } else {
+    a.tiles = g.tiles;
+    a.all_tiles = g.units * g.tiles;
+    a.lead = static_cast<int>(std::min<long long>(a.all_tiles, g.tiles + std::min(g.tiles, 1200)));
+    a.err = di.err_word;
+    a.timeout_ns = kWaitLimitNs;
+    a.ticket = static_cast<unsigned long long*>(ws);
+    a.done = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + 16);
+    a.ready = a.done + g.units;
+    const size_t head = 16 + (g.units * 8 + 15) / 16 * 16;
+    a.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + head);
+    a.part = a.stat + g.units * a.slab_groups;
+    const cudaError_t e = cudaMemsetAsync(ws, 0, head, s);
+    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: workspace: %s", what, cudaGetErrorString(e));
+  }
+  const bool silu = act == CC_ACT_SILU;
+  if (a.gw == 8) {
+    if (fp8)
+      return silu ? launch_group_norm<true, true, true>(what, a, g, di.sm_count, s)
+                  : launch_group_norm<true, false, true>(what, a, g, di.sm_count, s);
+    return silu ? launch_group_norm<true, true, false>(what, a, g, di.sm_count, s)
+                : launch_group_norm<true, false, false>(what, a, g, di.sm_count, s);
+  }
+  if (fp8)
+    return silu ? launch_group_norm<false, true, true>(what, a, g, di.sm_count, s)
+                : launch_group_norm<false, false, true>(what, a, g, di.sm_count, s);
+  return silu ? launch_group_norm<false, true, false>(what, a, g, di.sm_count, s)
+              : launch_group_norm<false, false, false>(what, a, g, di.sm_count, s);
 }
 
 }  // namespace
@@ -288,8 +697,8 @@ cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamm
 using namespace cc;
 
 extern "C" size_t cc_group_norm_workspace_bytes(int n, int p, int c, int groups) {
-  if (n <= 0 || p <= 0 || c < 8 || groups <= 0) return 0;
-  return gn_bytes(n, p, c, groups);
+  if (n <= 0 || p <= 0 || c < 8 || c > kGnMaxChannels || c % 8 != 0 || groups <= 0 || c % groups != 0) return 0;
+  return std::max(gn_plan(n, p, c, groups, false).ws_bytes, gn_plan(n, p, c, groups, true).ws_bytes);
 }
 
 extern "C" cc_status cc_group_norm_act(const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, cc_bf16* y, int n,

@@ -35,13 +35,11 @@ struct RowArgs {
 template <bool NORM, bool SILU, bool FP8>
 __device__ __forceinline__ void finish_vector(const RowArgs& a, const uint4& raw, const uint4& gamma, float rs,
                                               long long r, int v, bool on) {
-  float f[8];
-  unpack8(raw, f);
+  Vec8 f = unpack8(raw);
   if (NORM) {
-    float g[8];
-    unpack8(gamma, g);
+    const Vec8 g = unpack8(gamma);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= rs * g[e];
+    for (int i = 0; i < 4; ++i) f.p[i] = mul2(f.p[i], mul2(g.p[i], pair(rs, rs)));
     activate8<SILU>(f);
   }
   if (FP8) {
@@ -56,11 +54,10 @@ __device__ __forceinline__ void finish_vector(const RowArgs& a, const uint4& raw
   }
 }
 
-__device__ __forceinline__ float sum_squares(const uint4& raw, float sum) {
-  float f[8];
-  unpack8(raw, f);
+__device__ __forceinline__ f32x2 sum_squares(const uint4& raw, f32x2 sum) {
+  const Vec8 f = unpack8(raw);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+  for (int i = 0; i < 4; ++i) sum = fma2(f.p[i], f.p[i], sum);
   return sum;
 }
 
@@ -99,9 +96,10 @@ __global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const 
     if (NORM) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        rs[j] = 0.f;
+        f32x2 sum = pair(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) rs[j] = sum_squares(raw[j][i], rs[j]);
+        for (int i = 0; i < V; ++i) sum = sum_squares(raw[j][i], sum);
+        rs[j] = lo(sum) + hi(sum);
       }
 #pragma unroll
       for (int o = TPR / 2; o > 0; o >>= 1) {
@@ -138,8 +136,10 @@ __global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __
       raw[i] = v < a.vecs ? __ldcs(a.x + r * a.ld_x + v) : make_uint4(0, 0, 0, 0);
     }
     if (NORM) {
+      f32x2 sum = pair(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rs = sum_squares(raw[i], rs);
+      for (int i = 0; i < 4; ++i) sum = sum_squares(raw[i], sum);
+      rs = lo(sum) + hi(sum);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
       if ((tid & 31) == 0) red[turn][tid >> 5] = rs;
@@ -221,26 +221,22 @@ cc_status run_rows(const char* what, bool norm, const cc_bf16* x, const cc_bf16*
 // its e4m3 values. Run once per layer when weights are loaded.
 __global__ void __launch_bounds__(256) fp8_weights_kernel(const uint4* __restrict__ w, uint2* __restrict__ wq,
                                                           float* __restrict__ sw, int n, int kv, int kblocks) {
-  __shared__ uint32_t red[8];
+  __shared__ float red[8];
   const int tid = threadIdx.x;
   const int v = blockIdx.x * 16 + (tid & 15);
   const int row0 = blockIdx.y * kScaleBlock + (tid >> 4);
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = row0 + 16 * i;
-    if (row < n && v < kv) {
-      float f[8];
-      unpack8(w[static_cast<long long>(row) * kv + v], f);
-      m = max(m, absmax8_bits(f));
-    }
+    if (row < n && v < kv) m = max_nan(m, absmax8(unpack8(w[static_cast<long long>(row) * kv + v])));
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((tid & 31) == 0) red[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+  for (int i = 0; i < 8; ++i) m = max_nan(m, red[i]);
   const float scale = block_scale(m);
   const float inv = 1.f / scale;
   if (tid == 0) sw[static_cast<long long>(blockIdx.y) * kblocks + blockIdx.x] = scale;
@@ -248,10 +244,9 @@ __global__ void __launch_bounds__(256) fp8_weights_kernel(const uint4* __restric
   for (int i = 0; i < 8; ++i) {
     const int row = row0 + 16 * i;
     if (row < n && v < kv) {
-      float f[8];
-      unpack8(w[static_cast<long long>(row) * kv + v], f);
+      Vec8 f = unpack8(w[static_cast<long long>(row) * kv + v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= inv;
+      for (int e = 0; e < 4; ++e) f.p[e] = mul2(f.p[e], pair(inv, inv));
       wq[static_cast<long long>(row) * kv + v] = pack8_e4m3(f);
     }
   }

@@ -98,6 +98,13 @@ def test_group_norm_large_instances(fp8):
     check_group_norm(x, rnd((256,), 6), rnd((256,), 7), 32, "silu", fp8, "large")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,p,c,groups", [(2, 60001, 136, 17), (1, 70000, 200, 100), (1, 33000, 1000, 8)])
+def test_group_norm_large_instances_with_uneven_slabs(n, p, c, groups, fp8):
+    x = rnd((n, p, c), 24, 1.0, 0.5)
+    check_group_norm(x, rnd((c,), 25), rnd((c,), 26), groups, "silu", fp8, f"{(n, p, c, groups)}")
+
+
 def test_group_norm_without_gamma_and_beta():
     x = rnd((2, 50, 64), 8)
     check_group_norm(x, None, None, 4, "none", False, "plain")
