@@ -8,6 +8,9 @@
 // and adds them, times sa[row][block] * sw[column block][block], to fp32
 // accumulators in its registers. Two accumulator buffers in tensor memory let
 // the MMAs of one block run while the previous one is read.
+//
+// Two kernels: CTA pairs with 256 x 256 tiles for many rows, and, for few, the
+// weights as the tensor core's 128-row side with K split over a cluster.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,35 +31,583 @@ struct Fp8GemmArgs {
   const cc_bf16* res;
   cc_bf16* out;
   int m, n, kblocks;
+  int n_tiles, tiles;   // pair kernel
+  int kb_split;         // few-rows kernel: blocks of K per CTA
   long long ld_res, ld_out;
   unsigned int* err;
   unsigned long long timeout_ns;
 };
 
-constexpr int kTile = 128;
-constexpr int kStageBytes = 2 * kTile * kTile;
-constexpr int kStages = 6;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
-constexpr int kThreads = 192;
+constexpr int kKBytes = 128;  // bytes of K per stage: one scale block, one swizzle row
 
-__global__ void __launch_bounds__(kThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+// ------------------------------------------------------- CTA pairs, many rows --
+
+// Persistent pairs on 256 x 256 tiles (128 rows of a per CTA, the weights'
+// rows in halves), two 256-column accumulators in tensor memory. An epilogue
+// thread keeps 128 columns of its row -- one scale block of the weights -- in
+// registers, which takes half of the register file; eight warps with 128
+// columns each measured faster than sixteen with 64.
+constexpr int kPairRows = 128;     // of A, per CTA
+constexpr int kPairCols = 256;     // of the tile; each CTA loads half of them
+constexpr int kHalfCols = 128;     // of an accumulator; each CTA loads 64 of its weight rows
+constexpr int kPairABytes = kPairRows * kKBytes;
+constexpr int kPairBBytes = kPairCols / 2 * kKBytes;
+constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
+constexpr int kPairStages = 5;
+constexpr int kEpiWarps = 8;       // one per half of the columns and quarter of the rows
+constexpr int kEpiCols = kHalfCols;
+constexpr int kStageOutBytes = 32 * kEpiCols * 2;  // a warp's 32 rows, two pieces of 64 columns
+constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + kEpiWarps * kStageOutBytes + 256;
+constexpr int kPairThreads = 128 + 32 * kEpiWarps;  // a warpgroup to load and issue, two for the epilogue
+// registers a thread: 128 * 72 + 256 * 216 = 384 * 168, what the launch has
+constexpr int kIssueRegs = 72, kEpiRegs = 216;
+static_assert(kPairSmem <= 232448, "shared memory budget");
+
+// acc += 64 sums of this thread's tensor memory lane times `scale`. In one
+// statement, so that the sums are used where the load puts them: as separate
+// ones they were moved first, which took longer than adding them.
+__device__ __forceinline__ void add_sums64(uint32_t taddr, f32x2* acc, f32x2 scale) {
+  asm volatile("{\n\t"
+      ".reg .b32 t<64>;\n\t"
+      ".reg .b64 p<32>;\n\t"
+      ".reg .b32 a<4>;\n\t"
+      "add.u32 a0, %32, 0;\n\t"
+      "add.u32 a1, %32, 16;\n\t"
+      "add.u32 a2, %32, 32;\n\t"
+      "add.u32 a3, %32, 48;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [a0];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [a1];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47}, [a2];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [a3];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 p0, {t0, t1};\n\t"
+      "fma.rn.f32x2 %0, p0, %33, %0;\n\t"
+      "mov.b64 p1, {t2, t3};\n\t"
+      "fma.rn.f32x2 %1, p1, %33, %1;\n\t"
+      "mov.b64 p2, {t4, t5};\n\t"
+      "fma.rn.f32x2 %2, p2, %33, %2;\n\t"
+      "mov.b64 p3, {t6, t7};\n\t"
+      "fma.rn.f32x2 %3, p3, %33, %3;\n\t"
+      "mov.b64 p4, {t8, t9};\n\t"
+      "fma.rn.f32x2 %4, p4, %33, %4;\n\t"
+      "mov.b64 p5, {t10, t11};\n\t"
+      "fma.rn.f32x2 %5, p5, %33, %5;\n\t"
+      "mov.b64 p6, {t12, t13};\n\t"
+      "fma.rn.f32x2 %6, p6, %33, %6;\n\t"
+      "mov.b64 p7, {t14, t15};\n\t"
+      "fma.rn.f32x2 %7, p7, %33, %7;\n\t"
+      "mov.b64 p8, {t16, t17};\n\t"
+      "fma.rn.f32x2 %8, p8, %33, %8;\n\t"
+      "mov.b64 p9, {t18, t19};\n\t"
+      "fma.rn.f32x2 %9, p9, %33, %9;\n\t"
+      "mov.b64 p10, {t20, t21};\n\t"
+      "fma.rn.f32x2 %10, p10, %33, %10;\n\t"
+      "mov.b64 p11, {t22, t23};\n\t"
+      "fma.rn.f32x2 %11, p11, %33, %11;\n\t"
+      "mov.b64 p12, {t24, t25};\n\t"
+      "fma.rn.f32x2 %12, p12, %33, %12;\n\t"
+      "mov.b64 p13, {t26, t27};\n\t"
+      "fma.rn.f32x2 %13, p13, %33, %13;\n\t"
+      "mov.b64 p14, {t28, t29};\n\t"
+      "fma.rn.f32x2 %14, p14, %33, %14;\n\t"
+      "mov.b64 p15, {t30, t31};\n\t"
+      "fma.rn.f32x2 %15, p15, %33, %15;\n\t"
+      "mov.b64 p16, {t32, t33};\n\t"
+      "fma.rn.f32x2 %16, p16, %33, %16;\n\t"
+      "mov.b64 p17, {t34, t35};\n\t"
+      "fma.rn.f32x2 %17, p17, %33, %17;\n\t"
+      "mov.b64 p18, {t36, t37};\n\t"
+      "fma.rn.f32x2 %18, p18, %33, %18;\n\t"
+      "mov.b64 p19, {t38, t39};\n\t"
+      "fma.rn.f32x2 %19, p19, %33, %19;\n\t"
+      "mov.b64 p20, {t40, t41};\n\t"
+      "fma.rn.f32x2 %20, p20, %33, %20;\n\t"
+      "mov.b64 p21, {t42, t43};\n\t"
+      "fma.rn.f32x2 %21, p21, %33, %21;\n\t"
+      "mov.b64 p22, {t44, t45};\n\t"
+      "fma.rn.f32x2 %22, p22, %33, %22;\n\t"
+      "mov.b64 p23, {t46, t47};\n\t"
+      "fma.rn.f32x2 %23, p23, %33, %23;\n\t"
+      "mov.b64 p24, {t48, t49};\n\t"
+      "fma.rn.f32x2 %24, p24, %33, %24;\n\t"
+      "mov.b64 p25, {t50, t51};\n\t"
+      "fma.rn.f32x2 %25, p25, %33, %25;\n\t"
+      "mov.b64 p26, {t52, t53};\n\t"
+      "fma.rn.f32x2 %26, p26, %33, %26;\n\t"
+      "mov.b64 p27, {t54, t55};\n\t"
+      "fma.rn.f32x2 %27, p27, %33, %27;\n\t"
+      "mov.b64 p28, {t56, t57};\n\t"
+      "fma.rn.f32x2 %28, p28, %33, %28;\n\t"
+      "mov.b64 p29, {t58, t59};\n\t"
+      "fma.rn.f32x2 %29, p29, %33, %29;\n\t"
+      "mov.b64 p30, {t60, t61};\n\t"
+      "fma.rn.f32x2 %30, p30, %33, %30;\n\t"
+      "mov.b64 p31, {t62, t63};\n\t"
+      "fma.rn.f32x2 %31, p31, %33, %31;\n\t"
+      "}"
+      : "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]),
+        "+l"(acc[6]), "+l"(acc[7]), "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]),
+        "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15]), "+l"(acc[16]), "+l"(acc[17]),
+        "+l"(acc[18]), "+l"(acc[19]), "+l"(acc[20]), "+l"(acc[21]), "+l"(acc[22]), "+l"(acc[23]),
+        "+l"(acc[24]), "+l"(acc[25]), "+l"(acc[26]), "+l"(acc[27]), "+l"(acc[28]), "+l"(acc[29]),
+        "+l"(acc[30]), "+l"(acc[31])
+      : "r"(taddr), "l"(scale)
+      : "memory");
+}
+
+// The same for the last 64 sums of an accumulator buffer: once they are in
+// registers the warp's first lane releases the buffer (`tempty`, in the even
+// CTA), and the next buffer's barrier is asked for its phase, both before the
+// additions that hide them. Returns whether that phase is complete.
+__device__ __forceinline__ bool add_sums64_release(uint32_t taddr, f32x2* acc, f32x2 scale, uint32_t tempty,
+                                                   uint32_t first, uint32_t next_bar, uint32_t next_parity) {
+  uint32_t ready;
+  asm volatile("{\n\t"
+      ".reg .b32 t<64>;\n\t"
+      ".reg .b64 p<32>;\n\t"
+      ".reg .b32 a<4>;\n\t"
+      ".reg .pred first, ready;\n\t"
+      "add.u32 a0, %33, 0;\n\t"
+      "add.u32 a1, %33, 16;\n\t"
+      "add.u32 a2, %33, 32;\n\t"
+      "add.u32 a3, %33, 48;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [a0];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [a1];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47}, [a2];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [a3];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "tcgen05.fence::before_thread_sync;\n\t"
+      "bar.warp.sync 0xffffffff;\n\t"
+      "setp.ne.b32 first, %36, 0;\n\t"
+      "@first mbarrier.arrive.shared::cluster.b64 _, [%35];\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 ready, [%37], %38;\n\t"
+      "selp.u32 %32, 1, 0, ready;\n\t"
+      "mov.b64 p0, {t0, t1};\n\t"
+      "fma.rn.f32x2 %0, p0, %34, %0;\n\t"
+      "mov.b64 p1, {t2, t3};\n\t"
+      "fma.rn.f32x2 %1, p1, %34, %1;\n\t"
+      "mov.b64 p2, {t4, t5};\n\t"
+      "fma.rn.f32x2 %2, p2, %34, %2;\n\t"
+      "mov.b64 p3, {t6, t7};\n\t"
+      "fma.rn.f32x2 %3, p3, %34, %3;\n\t"
+      "mov.b64 p4, {t8, t9};\n\t"
+      "fma.rn.f32x2 %4, p4, %34, %4;\n\t"
+      "mov.b64 p5, {t10, t11};\n\t"
+      "fma.rn.f32x2 %5, p5, %34, %5;\n\t"
+      "mov.b64 p6, {t12, t13};\n\t"
+      "fma.rn.f32x2 %6, p6, %34, %6;\n\t"
+      "mov.b64 p7, {t14, t15};\n\t"
+      "fma.rn.f32x2 %7, p7, %34, %7;\n\t"
+      "mov.b64 p8, {t16, t17};\n\t"
+      "fma.rn.f32x2 %8, p8, %34, %8;\n\t"
+      "mov.b64 p9, {t18, t19};\n\t"
+      "fma.rn.f32x2 %9, p9, %34, %9;\n\t"
+      "mov.b64 p10, {t20, t21};\n\t"
+      "fma.rn.f32x2 %10, p10, %34, %10;\n\t"
+      "mov.b64 p11, {t22, t23};\n\t"
+      "fma.rn.f32x2 %11, p11, %34, %11;\n\t"
+      "mov.b64 p12, {t24, t25};\n\t"
+      "fma.rn.f32x2 %12, p12, %34, %12;\n\t"
+      "mov.b64 p13, {t26, t27};\n\t"
+      "fma.rn.f32x2 %13, p13, %34, %13;\n\t"
+      "mov.b64 p14, {t28, t29};\n\t"
+      "fma.rn.f32x2 %14, p14, %34, %14;\n\t"
+      "mov.b64 p15, {t30, t31};\n\t"
+      "fma.rn.f32x2 %15, p15, %34, %15;\n\t"
+      "mov.b64 p16, {t32, t33};\n\t"
+      "fma.rn.f32x2 %16, p16, %34, %16;\n\t"
+      "mov.b64 p17, {t34, t35};\n\t"
+      "fma.rn.f32x2 %17, p17, %34, %17;\n\t"
+      "mov.b64 p18, {t36, t37};\n\t"
+      "fma.rn.f32x2 %18, p18, %34, %18;\n\t"
+      "mov.b64 p19, {t38, t39};\n\t"
+      "fma.rn.f32x2 %19, p19, %34, %19;\n\t"
+      "mov.b64 p20, {t40, t41};\n\t"
+      "fma.rn.f32x2 %20, p20, %34, %20;\n\t"
+      "mov.b64 p21, {t42, t43};\n\t"
+      "fma.rn.f32x2 %21, p21, %34, %21;\n\t"
+      "mov.b64 p22, {t44, t45};\n\t"
+      "fma.rn.f32x2 %22, p22, %34, %22;\n\t"
+      "mov.b64 p23, {t46, t47};\n\t"
+      "fma.rn.f32x2 %23, p23, %34, %23;\n\t"
+      "mov.b64 p24, {t48, t49};\n\t"
+      "fma.rn.f32x2 %24, p24, %34, %24;\n\t"
+      "mov.b64 p25, {t50, t51};\n\t"
+      "fma.rn.f32x2 %25, p25, %34, %25;\n\t"
+      "mov.b64 p26, {t52, t53};\n\t"
+      "fma.rn.f32x2 %26, p26, %34, %26;\n\t"
+      "mov.b64 p27, {t54, t55};\n\t"
+      "fma.rn.f32x2 %27, p27, %34, %27;\n\t"
+      "mov.b64 p28, {t56, t57};\n\t"
+      "fma.rn.f32x2 %28, p28, %34, %28;\n\t"
+      "mov.b64 p29, {t58, t59};\n\t"
+      "fma.rn.f32x2 %29, p29, %34, %29;\n\t"
+      "mov.b64 p30, {t60, t61};\n\t"
+      "fma.rn.f32x2 %30, p30, %34, %30;\n\t"
+      "mov.b64 p31, {t62, t63};\n\t"
+      "fma.rn.f32x2 %31, p31, %34, %31;\n\t"
+      "}"
+      : "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]),
+        "+l"(acc[6]), "+l"(acc[7]), "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]),
+        "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15]), "+l"(acc[16]), "+l"(acc[17]),
+        "+l"(acc[18]), "+l"(acc[19]), "+l"(acc[20]), "+l"(acc[21]), "+l"(acc[22]), "+l"(acc[23]),
+        "+l"(acc[24]), "+l"(acc[25]), "+l"(acc[26]), "+l"(acc[27]), "+l"(acc[28]), "+l"(acc[29]),
+        "+l"(acc[30]), "+l"(acc[31]), "=r"(ready)
+      : "r"(taddr), "l"(scale), "r"(tempty), "r"(first), "r"(next_bar), "r"(next_parity)
+      : "memory");
+  return ready != 0;
+}
+
+// Four blocks' scales of a row of a, or of a block row of the weights.
+__device__ __forceinline__ float4 load_scales(const float* p, int kb, int kblocks, bool on) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (on) {
+    if ((kblocks & 3) == 0) {  // rows of scales start on 16-byte boundaries
+      v = __ldg(reinterpret_cast<const float4*>(p + kb));
+    } else {
+      v.x = __ldg(p + kb);
+      if (kb + 1 < kblocks) v.y = __ldg(p + kb + 1);
+      if (kb + 2 < kblocks) v.z = __ldg(p + kb + 2);
+      if (kb + 3 < kblocks) v.w = __ldg(p + kb + 3);
+    }
+  }
+  return v;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmRes, const __grid_constant__ CUtensorMap tmOut,
                     const __grid_constant__ Fp8GemmArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* done = tempty + 2;
+  uint8_t* s_out = smem + kPairStages * kPairStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + kEpiWarps * kStageOutBytes);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* tfull = empty + kPairStages;  // [half][buffer]
+  uint64_t* tempty = tfull + 4;
+  uint64_t* rfull = tempty + 4;  // [kEpiWarps] residual pieces
+  uint64_t* done = rfull + kEpiWarps;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  const int warp = threadIdx.x >> 5;
+  static_assert((2 * kPairStages + 8 + kEpiWarps + 1) * 8 + 4 <= 256, "barriers");
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // known to be uniform: a fifth of the time
   const int lane = threadIdx.x & 31;
-  const int m0 = blockIdx.y * kTile;
-  const int n0 = blockIdx.x * kTile;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair_id = blockIdx.x >> 1;
+  const int pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&tfull[i]), 1);
+      mbar_init(smem_u32(&tempty[i]), kEpiWarps);  // the half's four warps of both CTAs
+    }
+    mbar_init(smem_u32(done), 1);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(&rfull[i]), 1);
+    fence_mbar_init();
+    tma_prefetch_map(&tmA);
+    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&tmOut);
+    if (args.res) tma_prefetch_map(&tmRes);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 2 * kPairCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint64_t tlim = args.timeout_ns;
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
+        const int m0 = (2 * (tile / args.n_tiles) + static_cast<int>(rank)) * kPairRows;
+        const int n0 = tile % args.n_tiles * kPairCols + static_cast<int>(rank) * (kHalfCols / 2);
+        for (int kb = 0; kb < args.kblocks; ++kb) {
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, args.err, tlim)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = smem_u32(&full[stage]);
+          const uint32_t fb = mapa_shared(fb_local, 0);
+          if (leader) mbar_arrive_expect_tx(fb_local, 2 * kPairStageBytes);
+          const uint32_t dst = smem_u32(smem + stage * kPairStageBytes);
+          tma_load_2d_pair(dst, &tmA, fb, kb * kKBytes, m0);
+          tma_load_2d_pair(dst + kPairABytes, &tmB, fb, kb * kKBytes, n0);
+          tma_load_2d_pair(dst + kPairABytes + kPairBBytes / 2, &tmB, fb, kb * kKBytes, n0 + kHalfCols);
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) {
+        // copies of both CTAs complete on the even CTA's barriers; let the
+        // armed ones land (200 ms each at most) before the pair winds down
+        for (int s = 0; s < kPairStages; ++s)
+          (void)mbar_wait(smem_u32(&full[s]), (s < stage) ? phase : (phase ^ 1u), args.err, 200000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------- MMA issuer (even CTA only) --
+    if (leader) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kPairRows, kHalfCols);
+      int stage = 0;
+      uint32_t phase = 0;
+      int buf = 0;
+      uint32_t buf_phase = 0;
+      bool ok = true;
+      const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t b_desc0 = sdesc_sw128(smem_u32(smem + kPairABytes), 16, 1024);
+      for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
+        for (int kb = 0; ok && kb < args.kblocks; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, args.err, tlim))) {
+            ok = false;
+            break;
+          }
+          const uint64_t off = static_cast<uint64_t>(stage) * (kPairStageBytes >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int acc = 2 * h + buf;
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc]), buf_phase ^ 1u, args.err, tlim)))
+              ok = false;
+            if (ok) {
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // 32 channels, 32 bytes on inside the swizzle row
+                  mma_f8_pair(tmem_base + acc * kHalfCols, a_desc0 + off + 2 * k,
+                              b_desc0 + off + h * (kPairBBytes / 2 >> 4) + 2 * k, idesc, k != 0 ? 1u : 0u);
+                mma_commit_pair_both(smem_u32(&tfull[acc]));
+                if (h == 1) mma_commit_pair_both(smem_u32(&empty[stage]));
+              }
+              __syncwarp();
+            }
+          }
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          buf ^= 1;
+          buf_phase ^= buf == 0 ? 1u : 0u;
+        }
+      }
+      // no MMA may still be running when tensor memory is released
+      if (elect_one()) mma_commit_pair_both(smem_u32(done));
+      __syncwarp();
+      (void)mbar_wait(smem_u32(done), 0, args.err, tlim);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------- epilogue (both CTAs) --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int quarter = warp & 3;  // tensor memory lanes this warp may read
+    const int half = (warp - 4) >> 2;
+    uint8_t* stage_out = s_out + (warp - 4) * kStageOutBytes;
+    const uint32_t rbar = smem_u32(&rfull[warp - 4]);
+    uint32_t rphase = 0;
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 2 * kHalfCols;
+    const uint32_t tfull0 = smem_u32(&tfull[2 * half]);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[2 * half]), 0);
+    uint32_t it = 0;  // blocks of K so far: buffer it & 1, its phase (it >> 1) & 1
+    bool ready = false;
+    bool ok = true;
+    // The scales come in fours and a group ahead, and are multiplied when their
+    // turn comes: a product at once would wait for the loads.
+    const float *row_scales, *col_scales;
+    bool row_on;
+    float4 ahead_a, ahead_w;
+    auto scales_of = [&](int tile, int mt, int nt) {
+      const int m = (2 * mt + static_cast<int>(rank)) * kPairRows + quarter * 32 + lane;
+      const int nb = 2 * nt + half;
+      row_on = tile < args.tiles && m < args.m && nb * kHalfCols < args.n;
+      row_scales = args.sa + static_cast<long long>(row_on ? m : 0) * args.kblocks;
+      col_scales = args.sw + static_cast<long long>(row_on ? nb : 0) * args.kblocks;
+    };
+    auto load_ahead = [&](int kb) {
+      ahead_a = load_scales(row_scales, kb, args.kblocks, row_on);
+      ahead_w = load_scales(col_scales, kb, args.kblocks, row_on);
+    };
+    int mt = pair_id / args.n_tiles, nt = pair_id % args.n_tiles;
+    const int mt_step = pairs / args.n_tiles, nt_step = pairs % args.n_tiles;
+    scales_of(pair_id, mt, nt);
+    load_ahead(0);
+    for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
+      const int m0 = (2 * mt + static_cast<int>(rank)) * kPairRows + quarter * 32;
+      const int n0 = nt * kPairCols + half * kEpiCols;
+      const bool any = m0 < args.m && n0 < args.n;  // uniform
+      mt += mt_step;
+      nt += nt_step;
+      if (nt >= args.n_tiles) {
+        nt -= args.n_tiles;
+        ++mt;
+      }
+      f32x2 acc[kEpiCols / 2];
+#pragma unroll
+      for (int j = 0; j < kEpiCols / 2; ++j) acc[j] = 0;
+      float4 now = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int kb = 0; kb < args.kblocks; ++kb) {
+        if ((kb & 3) == 0) {
+          now = make_float4(ahead_a.x * ahead_w.x, ahead_a.y * ahead_w.y, ahead_a.z * ahead_w.z, ahead_a.w * ahead_w.w);
+          if (kb + 4 < args.kblocks) {
+            load_ahead(kb + 4);
+          } else {
+            scales_of(tile + pairs, mt, nt);
+            load_ahead(0);
+          }
+        }
+        const uint32_t buf = it & 1;
+        if (!__all_sync(0xffffffffu, ready) &&
+            !__all_sync(0xffffffffu, mbar_wait(tfull0 + buf * 8, (it >> 1) & 1, args.err, tlim))) {
+          ok = false;
+          break;
+        }
+        ++it;
+        tc_fence_after();
+        const f32x2 ss = pair(now.x, now.x);
+        now = make_float4(now.y, now.z, now.w, 0.f);
+        const uint32_t from = tbase + buf * kHalfCols;
+        add_sums64(from, acc, ss);
+        ready = add_sums64_release(from + 64, acc + 32, ss, tempty0 + buf * 8, lane == 0, tfull0 + (it & 1) * 8,
+                                   (it >> 1) & 1);
+        // the staging rows are free once the previous tile's stores have read
+        // them, which they have by now; asked for at the tile's start, it took
+        // a thousand cycles
+        if (kb == 0 && lane == 0 && any) {
+          bulk_wait_read_all();
+          if (args.res) {
+            mbar_arrive_expect_tx(rbar, kStageOutBytes);
+            tma_load_2d(smem_u32(stage_out), &tmRes, rbar, n0, m0);
+            tma_load_2d(smem_u32(stage_out + kStageOutBytes / 2), &tmRes, rbar, n0 + 64, m0);
+          }
+        }
+      }
+      __syncwarp();
+      if (!any) continue;
+      if (args.res && !__all_sync(0xffffffffu, mbar_wait(rbar, rphase, args.err, tlim))) ok = false;
+      rphase ^= 1u;
+      if (!ok) break;
+      // 64 columns at a time, all loads in front of the first store
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint8_t* row = stage_out + g * (kStageOutBytes / 2) + lane * 128;
+        uint4 extra[8];
+        if (args.bias) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            extra[j] = n0 + 64 * g + 8 * j < args.n ? __ldg(args.bias + (n0 >> 3) + 8 * g + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const Vec8 t = unpack8(extra[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[32 * g + 4 * j + e] = add2(acc[32 * g + 4 * j + e], t.p[e]);
+          }
+        }
+        if (args.res) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) extra[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (lane & 7)) << 4));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const Vec8 t = unpack8(extra[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[32 * g + 4 * j + e] = add2(acc[32 * g + 4 * j + e], t.p[e]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          Vec8 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v.p[e] = acc[32 * g + 4 * j + e];
+          *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = pack8(v);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&tmOut, smem_u32(stage_out), n0, m0);
+        if (n0 + 64 < args.n) tma_store_2d(&tmOut, smem_u32(stage_out + kStageOutBytes / 2), n0 + 64, m0);
+        bulk_commit();
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer no longer reads this CTA's shared memory or signals its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kPairCols);
+  }
+}
+
+// ------------------------------------------------------------------ few rows --
+
+// The weights' 128 rows take the tensor core's M side and up to MT rows of a
+// its N side, so a call with one row moves the weights and nothing but padding
+// of the tensor core's time. K is split over the CTAs of a cluster, whose
+// partial sums meet in shared memory, in rank order: the weights stream
+// through all SMs although there are few output tiles.
+constexpr int kFewThreads = 192;
+constexpr int kFewMax = 64;       // rows
+constexpr int kFewScales = 4096;  // staged scales of a: MT x blocks of K per CTA
+constexpr int kFewStages = 6;
+
+template <int MT>
+struct FewShape {
+  static constexpr int kWBytes = 128 * kKBytes;
+  static constexpr int kABytes = MT * kKBytes;
+  static constexpr int kStageBytes = kWBytes + kABytes;
+  static constexpr uint32_t kTmemCols = 2 * MT;
+  static constexpr int kPartBytes = MT * 128 * 4;  // partial sums, over the stages when all are used up
+  static int smem(int stages, int scales) {
+    return 1024 + std::max(stages * kStageBytes, kPartBytes) + scales * 4 + 256;
+  }
+};
+
+template <int MT>
+__global__ void __launch_bounds__(kFewThreads)
+    fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ Fp8GemmArgs args, const int stages) {
+  using S = FewShape<MT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t bars[2 * kFewStages + 5];
+  __shared__ uint32_t tmem_slot;
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kFewStages;
+  uint64_t* tfull = empty + kFewStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  float* part = reinterpret_cast<float*>(smem);
+  float* ssa = reinterpret_cast<float*>(smem + (stages * S::kStageBytes > S::kPartBytes ? stages * S::kStageBytes
+                                                                                        : S::kPartBytes));
+  uint32_t ranks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const uint32_t rank = cluster_ctarank();
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int nt = blockIdx.x / ranks;
+  const int kb0 = rank * args.kb_split;
+  const int kbs = max(0, min(args.kb_split, args.kblocks - kb0));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
@@ -67,135 +618,220 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(done), 1);
     fence_mbar_init();
     tma_prefetch_map(&tmA);
-    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&tmW);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 2 * kTile);
+    tmem_alloc(smem_u32(&tmem_slot), S::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
   const uint64_t tlim = args.timeout_ns;
 
+  bool ok = true;
+  f32x2 acc[MT / 2];
+#pragma unroll
+  for (int j = 0; j < MT / 2; ++j) acc[j] = 0;
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = 0; kb < args.kblocks; ++kb) {
+      for (int kb = 0; kb < kbs; ++kb) {
         if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, args.err, tlim)) {
           ok = false;
           break;
         }
         const uint32_t fb = smem_u32(&full[stage]);
-        const uint32_t dst = smem_u32(smem + stage * kStageBytes);
-        mbar_arrive_expect_tx(fb, kStageBytes);
-        tma_load_2d(dst, &tmA, fb, kb * kTile, m0);
-        tma_load_2d(dst + kTile * kTile, &tmB, fb, kb * kTile, n0);
-        if (++stage == kStages) {
+        const uint32_t dst = smem_u32(smem + stage * S::kStageBytes);
+        mbar_arrive_expect_tx(fb, S::kStageBytes);
+        tma_load_2d(dst, &tmW, fb, (kb0 + kb) * kKBytes, nt * 128);
+        tma_load_2d(dst + S::kWBytes, &tmA, fb, (kb0 + kb) * kKBytes, 0);
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) {
         // copies already issued land before the CTA can exit
-        for (int s = 0; s < kStages; ++s)
+        for (int s = 0; s < stages; ++s)
           (void)mbar_wait(smem_u32(&full[s]), (s < stage) ? phase : (phase ^ 1u), args.err, 200000000ull);
       }
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_e4m3_f32(kTile, kTile);
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, MT);
     int stage = 0;
     uint32_t phase = 0;
-    const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t b_desc0 = sdesc_sw128(smem_u32(smem + kTile * kTile), 16, 1024);
-    for (int kb = 0; kb < args.kblocks; ++kb) {
-      const int acc = kb & 1;
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(smem_u32(&tempty[acc]), ((kb >> 1) & 1) ^ 1u, args.err, tlim) &&
-                          mbar_wait(smem_u32(&full[stage]), phase, args.err, tlim)))
+    const uint64_t w_desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem + S::kWBytes), 16, 1024);
+    for (int kb = 0; kb < kbs; ++kb) {
+      const int buf = kb & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[buf]), ((kb >> 1) & 1) ^ 1u, args.err, tlim) &&
+                                       mbar_wait(smem_u32(&full[stage]), phase, args.err, tlim)))
         break;
       tc_fence_after();
-      const uint64_t off = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
+      const uint64_t off = static_cast<uint64_t>(stage) * (S::kStageBytes >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f8(tmem_base + acc * kTile, a_desc0 + off + 2 * k, b_desc0 + off + 2 * k, idesc, k != 0 ? 1u : 0u);
+          mma_f8(tmem_base + buf * MT, w_desc0 + off + 2 * k, a_desc0 + off + 2 * k, idesc, k != 0 ? 1u : 0u);
         mma_commit(smem_u32(&empty[stage]));
-        mma_commit(smem_u32(&tfull[acc]));
+        mma_commit(smem_u32(&tfull[buf]));
       }
       __syncwarp();
-      if (++stage == kStages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
     }
-    // no MMA may still be running when tensor memory is released
     if (elect_one()) mma_commit(smem_u32(done));
     __syncwarp();
     (void)mbar_wait(smem_u32(done), 0, args.err, tlim);
   } else {
     const int quarter = warp & 3;
-    const int m = m0 + quarter * 32 + lane;
-    const bool row_ok = m < args.m;
-    const float* sa = args.sa + static_cast<long long>(row_ok ? m : 0) * args.kblocks;
-    const float* sw = args.sw + static_cast<long long>(blockIdx.x) * args.kblocks;
+    const int tid = threadIdx.x - 64;
+    // ssa[kb][row]: the rows' scales times the weights'
+    for (int i = tid; i < MT * kbs; i += 128) {
+      const int kb = i / MT, r = i % MT;
+      ssa[i] = r < args.m ? __ldg(args.sa + static_cast<long long>(r) * args.kblocks + kb0 + kb) *
+                                     __ldg(args.sw + static_cast<long long>(nt) * args.kblocks + kb0 + kb)
+                               : 0.f;
+    }
+    named_barrier_sync(1, 128);
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    float acc[kTile];
-#pragma unroll
-    for (int j = 0; j < kTile; ++j) acc[j] = 0.f;
-    bool ok = true;
-    for (int kb = 0; kb < args.kblocks; ++kb) {
+    for (int kb = 0; kb < kbs; ++kb) {
       const int buf = kb & 1;
-      const float s = row_ok ? sa[kb] * sw[kb] : 0.f;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[buf]), (kb >> 1) & 1, args.err, tlim))) {
         ok = false;
         break;
       }
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t r[32];
-        tmem_ld32_wait(tbase + buf * kTile + c, r);
+      for (int c = 0; c < MT; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tbase + buf * MT + c, r);
+        tmem_wait16(r);
+        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(ssa + kb * MT + c);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(r[j]), s, acc[c + j]);
+        for (int j = 0; j < 4; ++j) {
+          const ulonglong2 s = sc[j];
+          acc[c / 2 + 2 * j] = fma2(pair(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), s.x,
+                                    acc[c / 2 + 2 * j]);
+          acc[c / 2 + 2 * j + 1] = fma2(pair(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), s.y,
+                                        acc[c / 2 + 2 * j + 1]);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
     }
-    if (ok && row_ok) {
-#pragma unroll
-      for (int c = 0; c < kTile; c += 8) {
-        const int n = n0 + c;
-        if (n < args.n) {
-          Vec8 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v.p[e] = pair(acc[c + 2 * e], acc[c + 2 * e + 1]);
-          if (args.bias) {
-            const Vec8 t = unpack8(args.bias[n >> 3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
-          }
-          if (args.res) {
-            const Vec8 t = unpack8(*reinterpret_cast<const uint4*>(args.res + m * args.ld_res + n));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
-          }
-          *reinterpret_cast<uint4*>(args.out + m * args.ld_out + n) = pack8(v);
-        }
-      }
-    }
   }
-
+  // every copy has landed and every MMA has read it before the stages become
+  // the partial sums (the MMA warp waited for `done`)
   tc_fence_before();
   __syncthreads();
+  if (warp >= 2) {
+    const int n = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < MT / 2; ++j) {
+      part[(2 * j) * 128 + n] = lo(acc[j]);
+      part[(2 * j + 1) * 128 + n] = hi(acc[j]);
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();
+  // each rank finishes its share of the rows, two columns to a thread
+  const int share = (MT + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
+  for (int i = threadIdx.x; i < share * 64; i += kFewThreads) {
+    const int m = static_cast<int>(rank) * share + (i >> 6);
+    const int c = (i & 63) * 2;
+    const int n = nt * 128 + c;
+    if (m < args.m && n < args.n) {
+      const uint32_t at = smem_u32(part + m * 128 + c);
+      float2 v = make_float2(0.f, 0.f);
+      for (uint32_t k = 0; k < ranks; ++k) {
+        float2 t;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(t.x), "=f"(t.y) : "r"(mapa_shared(at, k)));
+        v.x += t.x;
+        v.y += t.y;
+      }
+      if (args.bias) {
+        const float2 t = __bfloat1622float2(__ldg(reinterpret_cast<const __nv_bfloat162*>(args.bias) + (n >> 1)));
+        v.x += t.x;
+        v.y += t.y;
+      }
+      if (args.res) {
+        const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(args.res + m * args.ld_res + n));
+        v.x += t.x;
+        v.y += t.y;
+      }
+      *reinterpret_cast<__nv_bfloat162*>(args.out + m * args.ld_out + n) = __floats2bfloat162_rn(v.x, v.y);
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // the peers have read this CTA's partial sums
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 2 * kTile);
+    tmem_dealloc(tmem_base, S::kTmemCols);
   }
+}
+
+// -------------------------------------------------------------------- launch --
+
+template <int MT>
+cc_status launch_few(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const cc_fp8* wq, int k, int ranks,
+                     cudaStream_t stream) {
+  using S = FewShape<MT>;
+  CUtensorMap ta, tw;
+  cc_status st;
+  if ((st = encode_tiled_2d_u8(&ta, a, k, args.m, k, kKBytes, MT)) != CC_OK) return st;
+  if ((st = encode_tiled_2d_u8(&tw, wq, k, args.n, k, kKBytes, 128)) != CC_OK) return st;
+  const int stages = std::min(kFewStages, args.kb_split);
+  const int smem = S::smem(stages, MT * args.kb_split);
+  auto kern = fp8_few_kernel<MT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       S::smem(kFewStages, kFewScales));
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(((args.n - 1) / 128 + 1) * ranks);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tw, args, stages);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+  return launch_status(what);
+}
+
+cc_status launch_pair(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const cc_fp8* wq, int k, int sms,
+                      cudaStream_t stream) {
+  CUtensorMap ta, tb, to, tr;
+  cc_status st;
+  if ((st = encode_tiled_2d_u8(&ta, a, k, args.m, k, kKBytes, kPairRows)) != CC_OK) return st;
+  if ((st = encode_tiled_2d_u8(&tb, wq, k, args.n, k, kKBytes, kHalfCols / 2)) != CC_OK) return st;
+  if ((st = encode_tiled_2d(&to, args.out, args.n, args.m, args.ld_out * 2, 64, 32)) != CC_OK) return st;
+  tr = to;
+  if (args.res && (st = encode_tiled_2d(&tr, args.res, args.n, args.m, args.ld_res * 2, 64, 32)) != CC_OK) return st;
+  const long long m_tiles = (args.m - 1) / (2 * kPairRows) + 1;
+  args.n_tiles = (args.n - 1) / kPairCols + 1;
+  if (m_tiles * args.n_tiles > 0x7fffffffLL - 1024) return fail(CC_ERR_UNSUPPORTED, "%s: too many output tiles", what);
+  args.tiles = static_cast<int>(m_tiles * args.n_tiles);
+  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
+  e = launch_pdl(fp8_pair_kernel, dim3(2 * std::min(args.tiles, sms / 2)), dim3(kPairThreads), kPairSmem, stream, ta,
+                 tb, tr, to, args);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+  return launch_status(what);
 }
 
 }  // namespace
@@ -218,13 +854,8 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   if (n % 8 != 0) return fail(CC_ERR_UNSUPPORTED, "%s: N must be a multiple of 8 (got %d)", what, n);
   if (ld_out < n || ld_out % 8 != 0 || (res && (ld_res < n || ld_res % 8 != 0)))
     return fail(CC_ERR_INVALID, "%s: ld_out and ld_res must be at least N and multiples of 8", what);
-  const int m_tiles = (m - 1) / kTile + 1, n_tiles = (n - 1) / kTile + 1;
-  if (m_tiles > 65535) return fail(CC_ERR_UNSUPPORTED, "%s: too many output tiles", what);
   DeviceInfo di;
   if ((st = device_info(&di)) != CC_OK) return st;
-  CUtensorMap ta, tb;
-  if ((st = encode_tiled_2d_u8(&ta, a, k, m, k, kTile, kTile)) != CC_OK) return st;
-  if ((st = encode_tiled_2d_u8(&tb, wq, k, n, k, kTile, kTile)) != CC_OK) return st;
   Fp8GemmArgs args = {};
   args.sa = sa;
   args.sw = sw;
@@ -238,8 +869,21 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   args.ld_out = ld_out;
   args.err = di.err_word;
   args.timeout_ns = kWaitLimitNs;
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
-  fp8_gemm_kernel<<<dim3(n_tiles, m_tiles), kThreads, kSmemBytes, static_cast<cudaStream_t>(stream)>>>(ta, tb, args);
-  return launch_status(what);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  // Few rows: one N-side tile of the tensor core. At 64 rows x 4096 x 4096 it
+  // takes 8.3 us against the pairs' 14; with 128 rows it would take 24.
+  if (m <= kFewMax) {
+    const int mt = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+    const int n_tiles = (n - 1) / 128 + 1;
+    int ranks = 1;
+    while (ranks < 8 && 2 * ranks <= args.kblocks && static_cast<long long>(n_tiles) * ranks < di.sm_count) ranks *= 2;
+    args.kb_split = (args.kblocks - 1) / ranks + 1;
+    if (static_cast<long long>(mt) * args.kb_split <= kFewScales) {
+      if (mt == 16) return launch_few<16>(what, args, a, wq, k, ranks, s);
+      if (mt == 32) return launch_few<32>(what, args, a, wq, k, ranks, s);
+      return launch_few<64>(what, args, a, wq, k, ranks, s);
+    }
+  }
+  return launch_pair(what, args, a, wq, k, di.sm_count, s);
 }
