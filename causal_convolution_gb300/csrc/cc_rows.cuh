@@ -132,14 +132,25 @@ __device__ __forceinline__ float block_scale(float absmax) {
 
 // Quantises the eight values of each lane of a half warp, whose 16 lanes hold
 // one block of 128 channels (lanes past the row hold zeros). The values are
-// multiplied by the scale's correctly rounded reciprocal rather than divided:
-// at most two roundings of 2^-24 in front of the one to e4m3 (2^-4).
+// multiplied by the scale's reciprocal rather than divided: a few roundings of
+// 2^-24 in front of the one to e4m3 (2^-4). EXACT: scale and reciprocal are
+// correctly rounded quotients, so that a quantised tensor can be told bit by
+// bit; behind a norm, whose values are rounded already, they may be a step of
+// 2^-23 off and cost a quarter of the instructions.
+template <bool EXACT>
 __device__ __forceinline__ uint2 quantize_block(Vec8& v, float& scale) {
   float m = absmax8(v);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  scale = block_scale(m);
-  const float inv = 1.f / scale;
+  float inv;
+  if (EXACT) {
+    scale = block_scale(m);
+    inv = 1.f / scale;
+  } else {
+    scale = m * (1.f / kE4m3Max);
+    scale = scale < kMinScale ? kMinScale : scale;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) v.p[i] = mul2(v.p[i], pair(inv, inv));
   return pack8_e4m3(v);

@@ -486,13 +486,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // the staging rows are free once the previous tile's stores have read
         // them, which they have by now; asked for at the tile's start, it took
         // a thousand cycles
-        if (kb == 0 && lane == 0 && any) {
-          bulk_wait_read_all();
-          if (args.res) {
-            mbar_arrive_expect_tx(rbar, kStageOutBytes);
-            tma_load_2d(smem_u32(stage_out), &tmRes, rbar, n0, m0);
-            tma_load_2d(smem_u32(stage_out + kStageOutBytes / 2), &tmRes, rbar, n0 + 64, m0);
+        if (kb == 0 && any) {
+          if (lane == 0) {
+            bulk_wait_read_all();
+            if (args.res) {
+              mbar_arrive_expect_tx(rbar, kStageOutBytes);
+              tma_load_2d(smem_u32(stage_out), &tmRes, rbar, n0, m0);
+              tma_load_2d(smem_u32(stage_out + kStageOutBytes / 2), &tmRes, rbar, n0 + 64, m0);
+            }
           }
+          __syncwarp();
         }
       }
       __syncwarp();
@@ -700,6 +703,7 @@ __global__ void __launch_bounds__(kFewThreads)
                                      __ldg(args.sw + static_cast<long long>(nt) * args.kblocks + kb0 + kb)
                                : 0.f;
     }
+    __syncwarp();
     named_barrier_sync(1, 128);
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     for (int kb = 0; kb < kbs; ++kb) {

@@ -3,18 +3,23 @@
 //
 // The channels of an instance are cut into slabs of whole groups (64 channels
 // where the groups allow it, so that a position's piece is 128 bytes). A slab
-// is independent of the others, and two kernels take it:
+// is independent of the others, and one of two ways takes it:
 //
-//  - gn_cluster_kernel: a cluster of up to 16 CTAs holds the slab in its
+//  - gn_cluster_kernel: a cluster of up to 16 CTAs keeps the slab in its
 //    shared memory, exchanges the groups' moments through it and writes the
 //    result. x is read once; no workspace.
-//  - gn_stream_kernel, for slabs that a cluster cannot hold: CTAs take tiles
-//    in an order in which a slab's second reading (to normalise) follows its
-//    first (for the moments) closely enough to find the slab in L2.
+//  - gn_moments_kernel, gn_merge_kernel, gn_apply_kernel: x is read twice.
 //
-// Both sum a thread's values around a pivot, its first value, so that nothing
-// cancels where the mean is large against the deviation, and merge the
-// threads' means and squared deviations in a fixed order.
+// (One kernel that keeps slabs of up to 15 MB on all SMs and meets in global
+// memory, and one that reads a slab a second time out of L2, took 1.1 ms for
+// 16 frames of 219,648 x 256 where these three take 0.81 ms: 1.02 of the time
+// that copying 3 x 1.8 GB takes. Their CTAs spent their time meeting.)
+//
+// A thread sums its values around a pivot, its first value, so that nothing
+// cancels where the mean is large against the deviation. The CTA then adds up
+// the threads' sums to the groups' means q, and after that each thread's
+// squared deviations from its own mean plus n (mean - q)^2: two plain sums in a
+// fixed order, of terms that are not negative in the second.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -78,24 +83,16 @@ struct GnArgs {
   int slabs;       // per instance
   int slab_vecs;   // of every slab but, perhaps, the last
   int cpg;         // C / groups
-  int gw;          // channels of a vector that always share a group: gcd(C / groups, 8)
+  int gw_shift;    // log2 of gw = gcd(C / groups, 8): channels of a vector that always share a group
+  int per;         // C / groups / gw: parts of gw channels in a group
   float eps;
-  // cluster kernel
   int rows_per_cta;
-  int rounds;      // vectors a thread keeps
-  int scratch_at, keep_at;  // bytes into shared memory
-  // stream kernel
-  int tiles;       // per slab
-  int lead;        // tiles between a tile's first and second reading, at least `tiles`
-  long long all_tiles;
-  unsigned long long* ticket;
-  unsigned int* done;   // [units] tiles whose moments are written
-  unsigned int* ready;  // [units] 1: stat is written
-  float2* part;         // [units][tiles][groups of a slab]
-  float2* stat;         // [units][groups of a slab]: mean, 1 / deviation
-  int slab_groups;
-  unsigned int* err;
-  unsigned long long timeout_ns;
+  int rounds;       // vectors a thread keeps (cluster kernel)
+  int slab_groups;  // of the widest slab
+  int cols_at, red_at, keep_at;  // bytes into shared memory (cluster kernel)
+  int runs;         // per instance (two readings)
+  float2* part;     // moments of each CTA's positions (two readings)
+  float2* stat;     // mean, 1 / deviation (two readings)
 };
 
 // Where a thread of T stands in its slab: positions `lane`, lane + lanes, ...,
@@ -144,97 +141,135 @@ struct Sums {
   }
 };
 
-// Shared scratch of block_moments: an entry (moments of each part of a vector,
-// count) per thread, or per warp and slot where a warp's lanes of the same
-// slot can be merged by shuffles.
+// Columns are the parts of gw channels of a position's slab, slots * 8 / gw of
+// them. A warp's lanes of the same slot can be added up by shuffles where their
+// number divides 32.
 __host__ __device__ constexpr bool gn_shuffles(int slots) { return slots <= 16 && (slots & (slots - 1)) == 0; }
-__host__ __device__ constexpr int gn_entries(int slots, int threads) {
-  return gn_shuffles(slots) ? threads / 32 * slots : threads;
+// Rows of `red` in block_sums, one value per column each.
+__host__ __device__ constexpr int gn_red_rows(int slots, int threads) {
+  return gn_shuffles(slots) ? threads / 32 : threads / slots;
 }
-__host__ __device__ constexpr int gn_entry_bytes(int gw) { return 8 / gw * 8 + 4; }
 
-// The moments of the slab's groups over the CTA's positions, merged from the
-// threads' sums (of n positions each) in a fixed order; `out(group, moments)`
-// runs on one lane.
-template <bool ONE, bool FP8, int T, typename Out>
-__device__ __forceinline__ void block_moments(const GnArgs& a, const Place<FP8, T>& at, const Sums<ONE>& s, int n,
-                                              void* scratch, Out out) {
+// The sums over the CTA's positions of val[0 .. parts), each thread's value for
+// its parts, added up per group: `of(sum)` of a group's sum goes to all of the
+// group's columns in `cols` and to out(group, value). red: [red rows][columns].
+template <int K, bool FP8, int T, typename Of, typename Out>
+__device__ __forceinline__ void block_sums(const GnArgs& a, const Place<FP8, T>& at, int parts, int groups,
+                                           float (&val)[K], float* red, float* cols, Of of, Out out) {
+  const int n_cols = at.slots * parts;
+  int row = at.lane;
+  bool writes = at.lane < at.lanes;
+  if (gn_shuffles(at.slots)) {  // the same for every thread
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      if (o >= at.slots) {
+#pragma unroll
+        for (int e = 0; e < K; ++e) val[e] += __shfl_xor_sync(0xffffffffu, val[e], o);
+      }
+    }
+    row = threadIdx.x >> 5;
+    writes = (threadIdx.x & 31) < at.slots;
+  }
+  if (writes) {
+    float* to = red + row * n_cols + at.v * parts;
+#pragma unroll
+    for (int e = 0; e < K; ++e)
+      if (e < parts) to[e] = val[e];
+  }
+  __syncthreads();
+  const int rows = gn_shuffles(at.slots) ? T / 32 : at.lanes;
+  for (int c = threadIdx.x; c < n_cols; c += T) {
+    float t = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) t += red[r * n_cols + c];
+    cols[c] = t;
+  }
+  __syncthreads();
+  if (a.per < 32) {  // a thread to a group
+    for (int g = threadIdx.x; g < groups; g += T) {
+      float t = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < a.per; ++j) t += cols[g * a.per + j];
+      t = of(t);
+#pragma unroll 4
+      for (int j = 0; j < a.per; ++j) cols[g * a.per + j] = t;
+      out(g, t);
+    }
+  } else {  // a warp to a group
+    for (int g = threadIdx.x >> 5; g < groups; g += T / 32) {
+      float t = 0.f;
+      for (int j = threadIdx.x & 31; j < a.per; j += 32) t += cols[g * a.per + j];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      t = of(t);
+      for (int j = threadIdx.x & 31; j < a.per; j += 32) cols[g * a.per + j] = t;
+      if ((threadIdx.x & 31) == 0) out(g, t);
+    }
+  }
+  __syncthreads();
+}
+
+// mom[group] = mean and summed squared deviations over the CTA's `rows`
+// positions, of which this thread has n. red, cols: scratch of block_sums.
+template <bool ONE, bool FP8, int T>
+__device__ __forceinline__ void block_moments(const GnArgs& a, const Place<FP8, T>& at, int groups, const Sums<ONE>& s,
+                                              int n, int rows, float* red, float* cols, float2* mom) {
   constexpr int K = ONE ? 1 : 8;
-  const int tid = threadIdx.x;
-  const int entries = gn_entries(at.slots, T);
-  float2* red = static_cast<float2*>(scratch);
-  float* cnt = reinterpret_cast<float*>(red + (ONE ? 1 : 8 / a.gw) * entries);
-  Moments m[K];
+  const int parts = ONE ? 1 : 8 >> a.gw_shift;
+  // each part's mean and squared deviations; parts of several channels in
+  // their lowest elements
+  float mean[K], m2[K], val[K];
+  float count = static_cast<float>(ONE ? 8 * n : n);
+  const float inv = n > 0 ? __fdividef(1.f, count) : 0.f;
   if (ONE) {
-    const float c = 8.f * n, sum = lo(s.s1[0]) + hi(s.s1[0]);
-    const float d = n > 0 ? __fdividef(sum, c) : 0.f;
-    m[0] = {c, d - lo(s.neg[0]), lo(s.s2[0]) + hi(s.s2[0]) - sum * d};
+    const float sum = lo(s.s1[0]) + hi(s.s1[0]);
+    const float d = sum * inv;
+    mean[0] = d - lo(s.neg[0]);
+    m2[0] = lo(s.s2[0]) + hi(s.s2[0]) - sum * d;
   } else {
-    const float inv = n > 0 ? 1.f / n : 0.f;
 #pragma unroll
     for (int e = 0; e < K; ++e) {
       const int k = (e >> 1) % Sums<ONE>::K;
       const float sum = (e & 1) ? hi(s.s1[k]) : lo(s.s1[k]);
       const float d = sum * inv;
-      m[e] = {static_cast<float>(n), d - ((e & 1) ? hi(s.neg[k]) : lo(s.neg[k])),
-              ((e & 1) ? hi(s.s2[k]) : lo(s.s2[k])) - sum * d};
+      mean[e] = d - ((e & 1) ? hi(s.neg[k]) : lo(s.neg[k]));
+      m2[e] = ((e & 1) ? hi(s.s2[k]) : lo(s.s2[k])) - sum * d;
     }
   }
 #pragma unroll
-  for (int e = 0; e < K; ++e) m[e].m2 = m[e].m2 < 0.f ? 0.f : m[e].m2;  // keeps a NaN
-  int w = 1;
+  for (int e = 0; e < K; ++e) m2[e] = m2[e] < 0.f ? 0.f : m2[e];  // keeps a NaN
   if (!ONE) {
 #pragma unroll
-    for (int l = 1; l < 8; l <<= 1) {
-      if (a.gw > l) {  // neighbours of the same group
+    for (int l = 0; l < 2; ++l) {
+      if (a.gw_shift > l) {  // the same for every thread: neighbours of one group, with equal counts
 #pragma unroll
-        for (int e = 0; e < 8; e += 2 * l) merge(m[e % K], m[(e + l) % K]);
-        w = 2 * l;
-      }
-    }
-  }
-  int entry = tid;
-  bool writes = true;
-  if (gn_shuffles(at.slots)) {  // uniform
-    for (int o = at.slots; o < 32; o <<= 1) {
-#pragma unroll
-      for (int e = 0; e < K; ++e) {
-        if (e % w == 0) {
-          Moments b = {__shfl_xor_sync(0xffffffffu, m[e].n, o), __shfl_xor_sync(0xffffffffu, m[e].mean, o),
-                       __shfl_xor_sync(0xffffffffu, m[e].m2, o)};
-          merge(m[e], b);  // only the lowest lanes' results are used
+        for (int e = 0; e < (8 >> (l + 1)); ++e) {
+          const int u = 2 * e % K, v = (2 * e + 1) % K;
+          const float d = mean[v] - mean[u];
+          const float q = m2[u] + m2[v] + 0.5f * count * d * d;
+          mean[e % K] = mean[u] + 0.5f * d;
+          m2[e % K] = q;
         }
+        count *= 2.f;
       }
     }
-    entry = (tid >> 5) * at.slots + (tid & 31);
-    writes = (tid & 31) < at.slots;
   }
-  if (writes) {
 #pragma unroll
-    for (int e = 0; e < K; ++e)
-      if (e % w == 0) red[(e / w) * entries + entry] = make_float2(m[e].mean, m[e].m2);
-    cnt[entry] = m[0].n;
+  for (int e = 0; e < K; ++e) val[e] = count * mean[e];
+  const float all = static_cast<float>(rows) * a.cpg;
+  block_sums(a, at, parts, groups, val, red, cols, [&](float t) { return rows > 0 ? t / all : 0.f; },
+             [&](int g, float t) { mom[g].x = t; });
+#pragma unroll
+  for (int e = 0; e < K; ++e) {
+    const float d = at.on && e < parts ? mean[e] - cols[at.v * parts + e] : 0.f;
+    val[e] = at.on && e < parts ? fmaf(count * d, d, m2[e]) : 0.f;
   }
-  __syncthreads();
-  const int parts = ONE ? 1 : 8 / a.gw;      // of a vector
-  const int per = ONE ? a.cpg >> 3 : a.cpg / a.gw;  // parts in a group
-  const int side = gn_shuffles(at.slots) ? T / 32 : at.lanes;  // entries of a slot
-  for (int g = tid >> 5; g < at.vecs * 8 / a.cpg; g += T / 32) {
-    Moments t = {0.f, 0.f, 0.f};
-    for (int i = tid & 31; i < per * side; i += 32) {
-      const int q = i / per;
-      const int j = g * per + (i - q * per);
-      const int at_entry = q * at.slots + (ONE ? j : j / parts);
-      const float2 v = red[(ONE ? 0 : j % parts) * entries + at_entry];
-      merge(t, Moments{cnt[at_entry], v.x, v.y});
-    }
-    t = warp_merge(t);
-    if ((tid & 31) == 0) out(g, t);
-  }
+  __syncthreads();  // the columns' means are read
+  block_sums(a, at, parts, groups, val, red, cols, [](float t) { return t; }, [&](int g, float t) { mom[g].y = t; });
 }
 
 __device__ __forceinline__ float2 mean_and_factor(const Moments& m, float eps) {
-  return make_float2(m.mean, 1.f / sqrtf(m.m2 / m.n + eps));
+  return make_float2(m.mean, rsqrtf(m.m2 / m.n + eps));
 }
 
 // A thread's eight channels: act((x - mean) * k + beta). The mean is taken off
@@ -244,27 +279,22 @@ struct Affine {
   f32x2 neg[Sums<ONE>::K];
   Vec8 k, b;
   __device__ __forceinline__ void load_params(const GnArgs& a, const Place<FP8, T>& at, int slab) {
-    k = splat8(1.f);
+    // a thread without a vector computes zeros
+    k = splat8(at.on ? 1.f : 0.f);
     b = splat8(0.f);
     if (at.on && a.gamma) k = unpack8(__ldg(a.gamma + slab * a.slab_vecs + at.v));
     if (at.on && a.beta) b = unpack8(__ldg(a.beta + slab * a.slab_vecs + at.v));
   }
+  // stat(e): mean and factor of the thread's channel e
   template <typename Stat>
-  __device__ __forceinline__ void load_stat(const GnArgs& a, const Place<FP8, T>& at, Stat stat) {
-    if (ONE) {
-      const float2 s = at.on ? stat(8 * at.v / a.cpg) : make_float2(0.f, 0.f);
-      neg[0] = pair(-s.x, -s.x);
+  __device__ __forceinline__ void load_stat(const Place<FP8, T>& at, Stat stat) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k.p[i] = mul2(k.p[i], pair(s.y, s.y));
-    } else {
+    for (int i = 0; i < Sums<ONE>::K; ++i) {
+      const float2 s = at.on ? stat(2 * i) : make_float2(0.f, 0.f);
+      const float2 t = ONE ? s : at.on ? stat(2 * i + 1) : make_float2(0.f, 0.f);
+      neg[i] = pair(-s.x, -t.x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 8 * at.v + 2 * i;
-        const float2 s = at.on ? stat(c / a.cpg) : make_float2(0.f, 0.f);
-        const float2 t = at.on ? stat((c + 1) / a.cpg) : make_float2(0.f, 0.f);
-        neg[i % Sums<ONE>::K] = pair(-s.x, -t.x);
-        k.p[i] = mul2(k.p[i], pair(s.y, t.y));
-      }
+      for (int j = 0; j < (ONE ? 4 : 1); ++j) k.p[ONE ? j : i] = mul2(k.p[ONE ? j : i], pair(s.y, t.y));
     }
   }
   // y and scales: of the vector, and of the row's first block of the slab
@@ -275,9 +305,8 @@ struct Affine {
     for (int i = 0; i < 4; ++i) f.p[i] = fma2(add2(f.p[i], neg[ONE ? 0 : i]), k.p[i], b.p[i]);
     activate8<SILU>(f);
     if (FP8) {
-      if (!at.on) f = splat8(0.f);
       float scale;
-      const uint2 q = quantize_block(f, scale);
+      const uint2 q = quantize_block<false>(f, scale);
       if (on) {
         *static_cast<uint2*>(y) = q;
         if ((at.v & 15) == 0) scales[at.v >> 4] = scale;
@@ -311,16 +340,11 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 template <bool ONE, bool SILU, bool FP8, int T>
 __global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  uint32_t ranks;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  const uint32_t rank = cluster_ctarank();
-  const int unit = blockIdx.x / ranks;
-  const int instance = unit / a.slabs;
-  const int slab = unit - instance * a.slabs;
+  const int ranks = gridDim.x, rank = blockIdx.x, slab = blockIdx.y, instance = blockIdx.z;
   const Place<FP8, T> at(a, slab);
   float2* mom = reinterpret_cast<float2*>(smem);
-  float2* stat = mom + a.slab_groups;
-  uint8_t* scratch = smem + a.scratch_at;
+  float* cols = reinterpret_cast<float*>(smem + a.cols_at);  // later the columns' statistics
+  float* red = reinterpret_cast<float*>(smem + a.red_at);
   const int stride = at.lanes * at.slots;
   uint4* keep = reinterpret_cast<uint4*>(smem + a.keep_at) + threadIdx.x;
   const int r0 = rank * a.rows_per_cta;
@@ -330,6 +354,11 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_co
   const uint4* x = a.x + (row0 + at.lane) * a.vecs + slab * a.slab_vecs + at.v;
   const int step = at.lanes * a.vecs;
   const int quarter = (a.rounds + 3) / 4;
+  const int parts = ONE ? 1 : 8 >> a.gw_shift;
+  const int groups = at.vecs * 8 / a.cpg;
+  // set up: the next kernel may be scheduled, the previous one has to be done
+  pdl_launch_dependents();
+  pdl_wait();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int end = min((q + 1) * quarter, n);
@@ -350,23 +379,44 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_co
     const int end = min((q + 1) * quarter, n);
     for (int i = q * quarter; i < end; ++i) sums.add(keep[i * stride]);
   }
-  block_moments<ONE>(a, at, sums, n, scratch,
-                     [&](int g, const Moments& m) { mom[g] = make_float2(m.mean, m.m2); });
+  block_moments<ONE>(a, at, groups, sums, n, rows, red, cols, mom);
   __syncwarp();
   cluster_sync_all();
-  for (int g = threadIdx.x; g < at.vecs * 8 / a.cpg; g += T) {
-    Moments m = {0.f, 0.f, 0.f};
-    for (uint32_t k = 0; k < ranks; ++k) {
-      const float2 v = ld_cluster_f2(mapa_shared(smem_u32(&mom[g]), k));
-      const int c = max(0, min(a.rows_per_cta, a.p - static_cast<int>(k) * a.rows_per_cta));
-      merge(m, Moments{static_cast<float>(c) * a.cpg, v.x, v.y});
+  // The ranks' moments in their order, around the first one's mean (which
+  // takes at most four bits if that rank is the odd one out of sixteen).
+  float2* col_stat = reinterpret_cast<float2*>(cols);
+  const float count = static_cast<float>(a.p) * a.cpg;
+  for (int g = threadIdx.x; g < groups; g += T) {
+    float pivot = 0.f, sum = 0.f, m2 = 0.f;
+    for (int k0 = 0; k0 < ranks; k0 += 8) {
+      float2 of[8];  // eight trips to the other CTAs at once
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < ranks) of[k] = ld_cluster_f2(mapa_shared(smem_u32(&mom[g]), k0 + k));
+      if (k0 == 0) pivot = of[0].x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k0 + k < ranks) {
+          const float c = static_cast<float>(max(0, min(a.rows_per_cta, a.p - (k0 + k) * a.rows_per_cta))) * a.cpg;
+          const float d = of[k].x - pivot;
+          sum = fmaf(c, d, sum);
+          m2 += fmaf(c * d, d, of[k].y);
+        }
+      }
     }
-    stat[g] = mean_and_factor(m, a.eps);
+    const float shift = sum / count;
+    m2 -= sum * shift;
+    m2 = m2 < 0.f ? 0.f : m2;  // keeps a NaN
+    // for all of the group's columns, so that a thread finds its own without a division
+    const float2 st = mean_and_factor(Moments{count, pivot + shift, m2}, a.eps);
+#pragma unroll 4
+    for (int j = 0; j < a.per; ++j) col_stat[g * a.per + j] = st;
   }
   __syncthreads();
+  __syncwarp();
   // nobody reads this CTA's moments any more once all have arrived here
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  affine.load_stat(a, at, [&](int g) { return stat[g]; });
+  affine.load_stat(at, [&](int e) { return col_stat[at.v * parts + (ONE ? 0 : e >> a.gw_shift)]; });
   const long long at_y = (row0 + at.lane) * a.vecs + slab * a.slab_vecs + at.v;
   uint8_t* y = static_cast<uint8_t*>(a.y) + at_y * (FP8 ? 8 : 16);
   float* scales = FP8 ? a.scales + (row0 + at.lane) * a.blocks + slab * a.slab_vecs / 16 : nullptr;
@@ -383,149 +433,91 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_co
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// -------------------------------------------------------------- through L2 --
+// ------------------------------------------------------------- twice from memory --
 
-constexpr int kTileVecs = 4;   // vectors a thread has in flight
-constexpr int kTileTurns = 2;  // times that makes a tile
-
-__device__ __forceinline__ unsigned int ld_acquire(const unsigned int* p) {
-  unsigned int v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_release(unsigned int* p, unsigned int v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// Tiles are numbered through the units (instance, slab) in order. Tickets hand
-// out first readings `lead` tiles ahead of second readings and alternate
-// between them; a second reading waits until its unit's statistics are there,
-// which takes first readings with smaller tickets only, so the smallest open
-// ticket never waits for one that nobody holds, however few CTAs run at once.
-template <bool ONE, bool SILU, bool FP8, int T>
-__global__ void __launch_bounds__(T, 1024 / T) gn_stream_kernel(const __grid_constant__ GnArgs a) {
+// What does not fit on chip: the moments of runs of positions, their merging,
+// and a second reading that normalises.
+template <bool ONE, int T>
+__global__ void __launch_bounds__(T, 1024 / T) gn_moments_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ unsigned long long next;
-  __shared__ unsigned int word;
-  const int tid = threadIdx.x;
-  if (tid == 0) next = atomicAdd(a.ticket, 1ull);
-  __syncthreads();
-  for (;;) {
-    const long long t = static_cast<long long>(next);
-    if (t >= 2 * a.all_tiles) return;
-    bool second;
-    long long tile;
-    if (t < a.lead) {
-      second = false, tile = t;
-    } else if (t < 2 * a.all_tiles - a.lead) {
-      second = (t - a.lead) & 1;
-      tile = (t - a.lead) / 2 + (second ? 0 : a.lead);
-    } else {
-      second = true, tile = t - a.all_tiles;
+  const Place<false, T> at(a, 0);
+  const int r0 = blockIdx.x * a.rows_per_cta;
+  const int rows = min(a.rows_per_cta, a.p - r0);
+  const int n = at.count(rows);
+  const int step = at.lanes * a.vecs;
+  const uint4* x = a.x + (static_cast<long long>(blockIdx.y) * a.p + r0 + at.lane) * a.vecs + at.v;
+  pdl_launch_dependents();
+  pdl_wait();
+  Sums<ONE> sums;
+  sums.start(n > 0 ? __ldg(x) : make_uint4(0, 0, 0, 0));
+  int i = 0;
+  for (; i + 8 <= n; i += 8) {
+    uint4 raw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) raw[j] = __ldg(x + static_cast<long long>(i + j) * step);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums.add(raw[j]);
+  }
+  for (; i < n; ++i) sums.add(__ldg(x + static_cast<long long>(i) * step));
+  block_moments<ONE>(a, at, at.vecs * 8 / a.cpg, sums, n, rows, reinterpret_cast<float*>(smem),
+                     reinterpret_cast<float*>(smem + a.cols_at),
+                     a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * a.slab_groups);
+}
+
+__global__ void __launch_bounds__(128) gn_merge_kernel(const __grid_constant__ GnArgs a) {
+  const int g = blockIdx.x * 4 + (threadIdx.x >> 5);
+  pdl_launch_dependents();
+  pdl_wait();
+  if (g >= a.slab_groups) return;
+  const float2* part = a.part + static_cast<long long>(blockIdx.y) * a.runs * a.slab_groups + g;
+  Moments m = {0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = threadIdx.x & 31; i < a.runs; i += 32) {
+    const float2 v = part[static_cast<long long>(i) * a.slab_groups];
+    const int c = min(a.rows_per_cta, a.p - i * a.rows_per_cta);
+    merge(m, Moments{static_cast<float>(c) * a.cpg, v.x, v.y});
+  }
+  m = warp_merge(m);
+  if ((threadIdx.x & 31) == 0)
+    a.stat[static_cast<long long>(blockIdx.y) * a.slab_groups + g] = mean_and_factor(m, a.eps);
+}
+
+template <bool ONE, bool SILU, bool FP8, int T>
+__global__ void __launch_bounds__(T, 1024 / T) gn_apply_kernel(const __grid_constant__ GnArgs a) {
+  const Place<FP8, T> at(a, 0);
+  const int r0 = blockIdx.x * a.rows_per_cta;
+  const int rows = min(a.rows_per_cta, a.p - r0);
+  const int n = at.count(rows);
+  const int step = at.lanes * a.vecs;
+  const long long row0 = static_cast<long long>(blockIdx.y) * a.p + r0 + at.lane;
+  const uint4* x = a.x + row0 * a.vecs + at.v;
+  pdl_launch_dependents();
+  pdl_wait();
+  Affine<ONE, SILU, FP8, T> affine;
+  affine.load_params(a, at, 0);
+  const float2* stat = a.stat + static_cast<long long>(blockIdx.y) * a.slab_groups;
+  affine.load_stat(at, [&](int e) { return stat[(8 * at.v + e) / a.cpg]; });
+  uint8_t* y = static_cast<uint8_t*>(a.y) + (row0 * a.vecs + at.v) * (FP8 ? 8 : 16);
+  float* scales = FP8 ? a.scales + row0 * a.blocks : nullptr;
+  const int end = FP8 ? (rows + at.lanes - 1) / at.lanes : n;
+  for (int i = 0; i < end; i += 4) {
+    uint4 raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      raw[j] = i + j < n ? __ldcs(x + static_cast<long long>(i + j) * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i + j < end)
+        affine.write(at, raw[j], y + static_cast<long long>(i + j) * step * (FP8 ? 8 : 16),
+                     FP8 ? scales + static_cast<long long>(i + j) * at.lanes * a.blocks : nullptr, i + j < n);
     }
-    const int unit = static_cast<int>(tile / a.tiles);
-    const int i0 = static_cast<int>(tile - static_cast<long long>(unit) * a.tiles);
-    const int instance = unit / a.slabs;
-    const int slab = unit - instance * a.slabs;
-    const Place<FP8, T> at(a, slab);
-    const int tile_rows = at.lanes * kTileVecs * kTileTurns;
-    const int r0 = i0 * tile_rows;
-    const int rows = max(0, min(tile_rows, a.p - r0));  // a narrower last slab has fewer tiles than the others
-    const int n = at.count(rows);
-    const long long row0 = static_cast<long long>(instance) * a.p + r0 + at.lane;
-    const uint4* x = a.x + row0 * a.vecs + slab * a.slab_vecs + at.v;
-    const int step = at.lanes * a.vecs;
-    __syncthreads();  // `next` is read
-    if (tid == 0) next = atomicAdd(a.ticket, 1ull);
-    uint4 raw[kTileVecs];
-    if (!second) {
-      Sums<ONE> sums;
-#pragma unroll
-      for (int turn = 0; turn < kTileTurns; ++turn) {
-#pragma unroll
-        for (int i = 0; i < kTileVecs; ++i)
-          if (turn * kTileVecs + i < n) raw[i] = __ldg(x + static_cast<long long>(turn * kTileVecs + i) * step);
-        if (turn == 0) sums.start(n > 0 ? raw[0] : make_uint4(0, 0, 0, 0));
-#pragma unroll
-        for (int i = 0; i < kTileVecs; ++i)
-          if (turn * kTileVecs + i < n) sums.add(raw[i]);
-      }
-      float2* part = a.part + (static_cast<long long>(unit) * a.tiles + i0) * a.slab_groups;
-      block_moments<ONE>(a, at, sums, n, smem, [&](int g, const Moments& m) {
-        part[g] = make_float2(m.mean, m.m2);
-        __threadfence();
-      });
-      __syncthreads();
-      if (tid == 0) word = atomicAdd(a.done + unit, 1u);
-      __syncthreads();
-      if (word == static_cast<unsigned int>(a.tiles - 1)) {  // the unit's last: merge in the tiles' order
-        __threadfence();
-        const float2* all = a.part + static_cast<long long>(unit) * a.tiles * a.slab_groups;
-        for (int g = tid >> 5; g < at.vecs * 8 / a.cpg; g += T / 32) {
-          Moments m = {0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int i = tid & 31; i < a.tiles; i += 32) {
-            const float2 v = __ldcg(all + static_cast<long long>(i) * a.slab_groups + g);
-            const int c = max(0, min(tile_rows, a.p - i * tile_rows));
-            merge(m, Moments{static_cast<float>(c) * a.cpg, v.x, v.y});
-          }
-          m = warp_merge(m);
-          if ((tid & 31) == 0) {
-            a.stat[static_cast<long long>(unit) * a.slab_groups + g] = mean_and_factor(m, a.eps);
-            __threadfence();
-          }
-        }
-        __syncthreads();
-        if (tid == 0) st_release(a.ready + unit, 1u);
-      }
-    } else {
-      Affine<ONE, SILU, FP8, T> affine;
-#pragma unroll
-      for (int i = 0; i < kTileVecs; ++i) {
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (i < n) raw[i] = __ldcs(x + static_cast<long long>(i) * step);
-      }
-      affine.load_params(a, at, slab);
-      if (tid == 0) {
-        unsigned int ok = ld_acquire(a.ready + unit);
-        if (!ok) {
-          const uint64_t t0 = globaltimer_ns();
-          while (!ok && globaltimer_ns() - t0 < a.timeout_ns) ok = ld_acquire(a.ready + unit);
-          if (!ok) atomicOr(a.err, DEVERR_TIMEOUT);
-        }
-        word = ok;
-      }
-      __syncthreads();
-      if (!word) return;
-      const float2* stat = a.stat + static_cast<long long>(unit) * a.slab_groups;
-      affine.load_stat(a, at, [&](int g) { return __ldcg(stat + g); });
-      uint8_t* y = static_cast<uint8_t*>(a.y) + (row0 * a.vecs + slab * a.slab_vecs + at.v) * (FP8 ? 8 : 16);
-      float* scales = FP8 ? a.scales + row0 * a.blocks + slab * a.slab_vecs / 16 : nullptr;
-#pragma unroll
-      for (int turn = 0; turn < kTileTurns; ++turn) {
-        if (turn > 0) {
-#pragma unroll
-          for (int i = 0; i < kTileVecs; ++i)
-            if (turn * kTileVecs + i < n) raw[i] = __ldcs(x + static_cast<long long>(turn * kTileVecs + i) * step);
-        }
-#pragma unroll
-        for (int i = 0; i < kTileVecs; ++i) {
-          const int j = turn * kTileVecs + i;
-          affine.write(at, raw[i], y + static_cast<long long>(j) * step * (FP8 ? 8 : 16),
-                       FP8 ? scales + static_cast<long long>(j) * at.lanes * a.blocks : nullptr, j < n);
-        }
-      }
-    }
-    __syncthreads();  // the next ticket is there, `word` and the scratch are free
   }
 }
 
 // -------------------------------------------------------------------- host --
 
 // Channels of a slab: whole groups, whole vectors (whole blocks of 128 for
-// e4m3), at least 64 of them. At most 128 groups: below 64 channels the least
-// common multiple of C / groups and 8 has 8 groups at most, and that with 128
-// has 128.
+// e4m3), at least 64 of them where there are that many.
 int slab_channels(int c, int groups, bool fp8) {
   const int unit = std::lcm(c / groups, fp8 ? kScaleBlock : 8);
   if (unit >= c) return c;
@@ -535,88 +527,126 @@ int slab_channels(int c, int groups, bool fp8) {
 struct GnPlan {
   bool cluster;
   int threads;
-  int slab_c, slabs, slab_groups, scratch;
-  int ranks, rows, rounds, scratch_at, keep_at;  // cluster
+  int slab_c, slabs, slab_groups;
+  int ranks, rows, rounds;
+  int cols_at, red_at, keep_at;
   size_t smem;
-  int tiles;  // stream
+  int runs;
   long long units;
   size_t ws_bytes;
 };
 
 constexpr size_t kMaxSmem = 232448;
 
+int align16(int v) { return (v + 15) / 16 * 16; }
+
 GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
   GnPlan g = {};
+  const int cpg = c / groups;
+  const int parts = 8 / std::gcd(cpg, 8);
   g.slab_c = slab_channels(c, groups, fp8);
   g.slabs = (c + g.slab_c - 1) / g.slab_c;
-  g.slab_groups = g.slab_c / (c / groups);
+  g.slab_groups = g.slab_c / cpg;
   g.units = static_cast<long long>(n) * g.slabs;
-  const int gw = std::gcd(c / groups, 8);
   // the widest slab has the fewest positions side by side
   const int slots = fp8 ? (g.slab_c / 8 + 15) / 16 * 16 : g.slab_c / 8;
   const int last_c = c - (g.slabs - 1) * g.slab_c;
   const int last = fp8 ? (last_c / 8 + 15) / 16 * 16 : last_c / 8;
-  g.threads = slots > 256 ? 512 : 256;
-  const int lanes = g.threads / slots;
-  g.scratch = std::max(gn_entries(slots, g.threads), gn_entries(last, g.threads)) * gn_entry_bytes(gw);
-  g.scratch_at = (2 * g.slab_groups * static_cast<int>(sizeof(float2)) + 15) / 16 * 16;
-  g.keep_at = g.scratch_at + (g.scratch + 15) / 16 * 16;
-  auto cut = [&](int ranks) {
+  auto red_bytes = [&](int sl) { return gn_red_rows(sl, g.threads) * sl * parts * 4; };
+  auto cut = [&](int ranks, int threads) {
+    g.threads = std::max(threads, slots > 256 ? 512 : 256);
+    const int lanes = g.threads / slots;
+    g.cols_at = align16(g.slab_groups * 8);
+    g.red_at = g.cols_at + align16(slots * parts * 8);
+    g.keep_at = g.red_at + align16(std::max(red_bytes(slots), red_bytes(last)));
     g.ranks = ranks;
-    g.rows = (p + ranks - 1) / ranks;
+    g.rows = (p - 1) / ranks + 1;
     g.rounds = (g.rows + lanes - 1) / lanes;
     g.smem = g.keep_at + static_cast<size_t>(g.rows) * slots * 16;
   };
   for (int ranks = 1; ranks <= 16; ranks *= 2) {
-    cut(ranks);
+    cut(ranks, 256);
     if (g.smem <= kMaxSmem) break;
   }
-  g.cluster = g.smem <= kMaxSmem;
-  if (g.cluster) {
+  if (g.smem <= kMaxSmem) {
+    g.cluster = true;
     // two CTAs to an SM where eight of them hold the slab, and more CTAs while
     // SMs are idle and a thread still has several vectors
-    while (g.ranks < 8 && (g.smem > kMaxSmem / 2 - 1024 || (g.units * g.ranks < 152 && g.rounds > 2))) cut(g.ranks * 2);
+    while (g.ranks < 8 && (g.smem > kMaxSmem / 2 - 1024 || (g.units * g.ranks < 152 && g.rounds > 2)))
+      cut(g.ranks * 2, 256);
+    // 512 threads where each still has eight vectors and only one partial sum
+    // to hand over: 4 x 3432 x 1024 (32 groups) takes 12.8 us against 13.5 with
+    // 256; with eight partial sums, 3 x 3555 x 480 takes 12.5 against 11.5
+    const size_t room = g.smem > kMaxSmem / 2 - 1024 ? kMaxSmem : kMaxSmem / 2 - 1024;
+    if (parts == 1 && g.rounds >= 16) {
+      cut(g.ranks, 512);
+      if (g.smem > room) cut(g.ranks, 256);
+    }
     return g;
   }
-  const int tile_rows = lanes * kTileVecs * kTileTurns;
-  g.tiles = (p + tile_rows - 1) / tile_rows;
-  g.ws_bytes = 16 + (g.units * 8 + 15) / 16 * 16 +
-               static_cast<size_t>(g.units) * (g.tiles + 1) * g.slab_groups * sizeof(float2);
+  g.slab_c = c;
+  g.slabs = 1;
+  g.slab_groups = groups;
+  g.units = n;
+  g.threads = c > 2048 ? 512 : 256;
+  // runs of up to 64 vectors a thread, shorter ones while they would not fill
+  // the SMs (four CTAs of 256 threads to one)
+  const int lanes = g.threads / (c / 8);
+  const long long vecs = static_cast<long long>(n) * ((p - 1) / lanes + 1);
+  g.rows = lanes * static_cast<int>(std::min(64LL, std::max(8LL, vecs / 608)));
+  g.runs = (p - 1) / g.rows + 1;
+  g.cols_at = align16(red_bytes(c / 8));
+  g.smem = g.cols_at + static_cast<size_t>(c / 8) * parts * 4;
+  g.ws_bytes = static_cast<size_t>(n) * (g.runs + 1) * groups * sizeof(float2);
   return g;
 }
 
 template <bool ONE, bool SILU, bool FP8, int T>
-cc_status launch_group_norm(const char* what, GnArgs& a, const GnPlan& g, int sms, cudaStream_t s) {
-  if (g.cluster) {
-    auto kern = gn_cluster_kernel<ONE, SILU, FP8, T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess && g.ranks > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cc_status launch_cluster(const char* what, GnArgs& a, const GnPlan& g, cudaStream_t s) {
+  auto kern = gn_cluster_kernel<ONE, SILU, FP8, T>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess && g.ranks > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: kernel attributes: %s", what, cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(g.ranks, g.slabs, static_cast<unsigned>(g.units / g.slabs));
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = g.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = g.ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+  return launch_status(what);
+}
+
+template <bool ONE, bool SILU, bool FP8, int T>
+cc_status launch_twice(const char* what, GnArgs& a, const GnPlan& g, int n, cudaStream_t s) {
+  auto moments = gn_moments_kernel<ONE, T>;
+  if (g.smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(moments, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(g.smem));
     if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: kernel attributes: %s", what, cudaGetErrorString(e));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(g.units * g.ranks));
-    cfg.blockDim = dim3(T);
-    cfg.dynamicSmemBytes = g.smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = g.ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, a);
-    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
-    return launch_status(what);
   }
-  auto kern = gn_stream_kernel<ONE, SILU, FP8, T>;
-  const long long grid = std::min<long long>(1024LL / T * sms, 2 * a.all_tiles);
-  kern<<<static_cast<unsigned>(grid), T, g.scratch, s>>>(a);
+  cudaError_t e = launch_pdl(moments, dim3(g.runs, n), dim3(T), g.smem, s, a);
+  if (e == cudaSuccess) e = launch_pdl(gn_merge_kernel, dim3((a.slab_groups + 3) / 4, n), dim3(128), 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(gn_apply_kernel<ONE, SILU, FP8, T>, dim3(g.runs, n), dim3(T), 0, s, a);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
 }
 
 template <bool ONE, bool SILU, bool FP8>
-cc_status launch_group_norm(const char* what, GnArgs& a, const GnPlan& g, int sms, cudaStream_t s) {
-  return g.threads == 512 ? launch_group_norm<ONE, SILU, FP8, 512>(what, a, g, sms, s)
-                          : launch_group_norm<ONE, SILU, FP8, 256>(what, a, g, sms, s);
+cc_status launch_group_norm(const char* what, GnArgs& a, const GnPlan& g, int n, cudaStream_t s) {
+  if (!g.cluster)
+    return g.threads == 512 ? launch_twice<ONE, SILU, FP8, 512>(what, a, g, n, s)
+                            : launch_twice<ONE, SILU, FP8, 256>(what, a, g, n, s);
+  return g.threads == 512 ? launch_cluster<ONE, SILU, FP8, 512>(what, a, g, s)
+                          : launch_cluster<ONE, SILU, FP8, 256>(what, a, g, s);
 }
 
 cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, void* y,
@@ -652,43 +682,35 @@ cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamm
   a.slabs = g.slabs;
   a.slab_vecs = g.slab_c / 8;
   a.cpg = c / groups;
-  a.gw = std::gcd(a.cpg, 8);
+  const int gw = std::gcd(a.cpg, 8);
+  a.gw_shift = gw == 8 ? 3 : gw == 4 ? 2 : gw == 2 ? 1 : 0;
+  a.per = a.cpg / gw;
   a.eps = eps;
   a.slab_groups = g.slab_groups;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (g.cluster) {
-    a.rows_per_cta = g.rows;
-    a.rounds = g.rounds;
-    a.scratch_at = g.scratch_at;
-    a.keep_at = g.keep_at;
-  } else {
-    a.tiles = g.tiles;
-    a.all_tiles = g.units * g.tiles;
-    a.lead = static_cast<int>(std::min<long long>(a.all_tiles, g.tiles + std::min(g.tiles, 1200)));
-    a.err = di.err_word;
-    a.timeout_ns = kWaitLimitNs;
-    a.ticket = static_cast<unsigned long long*>(ws);
-    a.done = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + 16);
-    a.ready = a.done + g.units;
-    const size_t head = 16 + (g.units * 8 + 15) / 16 * 16;
-    a.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + head);
-    a.part = a.stat + g.units * a.slab_groups;
-    const cudaError_t e = cudaMemsetAsync(ws, 0, head, s);
-    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: workspace: %s", what, cudaGetErrorString(e));
+  a.rows_per_cta = g.rows;
+  a.rounds = g.rounds;
+  a.cols_at = g.cols_at;
+  a.red_at = g.red_at;
+  a.keep_at = g.keep_at;
+  a.runs = g.runs;
+  if (!g.cluster) {
+    a.stat = static_cast<float2*>(ws);
+    a.part = a.stat + static_cast<size_t>(n) * groups;
   }
   const bool silu = act == CC_ACT_SILU;
-  if (a.gw == 8) {
+  if (gw == 8) {
     if (fp8)
-      return silu ? launch_group_norm<true, true, true>(what, a, g, di.sm_count, s)
-                  : launch_group_norm<true, false, true>(what, a, g, di.sm_count, s);
-    return silu ? launch_group_norm<true, true, false>(what, a, g, di.sm_count, s)
-                : launch_group_norm<true, false, false>(what, a, g, di.sm_count, s);
+      return silu ? launch_group_norm<true, true, true>(what, a, g, n, s)
+                  : launch_group_norm<true, false, true>(what, a, g, n, s);
+    return silu ? launch_group_norm<true, true, false>(what, a, g, n, s)
+                : launch_group_norm<true, false, false>(what, a, g, n, s);
   }
   if (fp8)
-    return silu ? launch_group_norm<false, true, true>(what, a, g, di.sm_count, s)
-                : launch_group_norm<false, false, true>(what, a, g, di.sm_count, s);
-  return silu ? launch_group_norm<false, true, false>(what, a, g, di.sm_count, s)
-              : launch_group_norm<false, false, false>(what, a, g, di.sm_count, s);
+    return silu ? launch_group_norm<false, true, true>(what, a, g, n, s)
+                : launch_group_norm<false, false, true>(what, a, g, n, s);
+  return silu ? launch_group_norm<false, true, false>(what, a, g, n, s)
+              : launch_group_norm<false, false, false>(what, a, g, n, s);
 }
 
 }  // namespace

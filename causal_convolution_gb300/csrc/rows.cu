@@ -44,7 +44,7 @@ __device__ __forceinline__ void finish_vector(const RowArgs& a, const uint4& raw
   }
   if (FP8) {
     float scale;
-    const uint2 q = quantize_block(f, scale);  // lanes without a vector hold zeros
+    const uint2 q = quantize_block<!NORM>(f, scale);  // lanes without a vector hold zeros
     if (on) {
       static_cast<uint2*>(a.y)[r * a.vecs + v] = q;
       if ((threadIdx.x & 15) == 0) a.scales[r * a.blocks + (v >> 4)] = scale;
@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const 
   const int lane = threadIdx.x % TPR;
   const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / TPR);
   const long long first = static_cast<long long>(threadIdx.x / TPR) * gridDim.x + blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   uint4 gamma[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -127,6 +129,8 @@ __global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __
   __shared__ float red[2][16];
   const int tid = threadIdx.x;
   int turn = 0;
+  pdl_launch_dependents();
+  pdl_wait();
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     uint4 raw[4];
     float rs = 0.f;
@@ -166,7 +170,8 @@ cc_status launch_rows(const char* what, const RowArgs& a, int sms, cudaStream_t 
   if (v > 8) {
     const int threads = (a.vecs + 127) / 128 * 32;
     const int grid = static_cast<int>(std::min<long long>(a.rows, static_cast<long long>(sms) * (2048 / threads)));
-    long_row_kernel<NORM, SILU, FP8><<<grid, threads, 0, stream>>>(a);
+    const cudaError_t e = launch_pdl(long_row_kernel<NORM, SILU, FP8>, dim3(grid), dim3(threads), 0, stream, a);
+    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
     return launch_status(what);
   }
   auto kern = lanes == 16 ? row_kernel<16, 1, NORM, SILU, FP8>
@@ -176,7 +181,8 @@ cc_status launch_rows(const char* what, const RowArgs& a, int sms, cudaStream_t 
                           : row_kernel<32, 8, NORM, SILU, FP8>;
   // as many CTAs as fit, walking the rows
   const int grid = static_cast<int>(std::min<long long>(a.rows, static_cast<long long>(sms) * (v > 4 ? 2 : 4)));
-  kern<<<grid, kRowThreads, 0, stream>>>(a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kRowThreads), 0, stream, a);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
 }
 

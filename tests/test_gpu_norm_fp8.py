@@ -105,6 +105,61 @@ def test_group_norm_large_instances_with_uneven_slabs(n, p, c, groups, fp8):
     check_group_norm(x, rnd((c,), 25), rnd((c,), 26), groups, "silu", fp8, f"{(n, p, c, groups)}")
 
 
+@pytest.mark.parametrize("n,p,c,groups,fp8", [
+    (2, 219648, 64, 8, False),   # 32 channels to a slab on all SMs
+    (1, 120000, 192, 3, True),   # two readings: 128 channels are too many for the SMs
+    (2, 60007, 264, 1, False),   # two readings, one group of everything
+    (1, 100003, 72, 9, True),    # a slab of 72 channels, padded to 128
+    (3, 40009, 328, 41, False),  # the last slab is narrower
+    (1, 600000, 64, 32, False),  # a frame beyond the SMs' shared memory
+    (1, 3001, 4096, 1, True), (1, 70001, 8, 2, False), (1, 300000, 8, 8, False),
+])
+def test_group_norm_of_large_frames(n, p, c, groups, fp8):
+    x = rnd((n, p, c), 27, 1.0, -0.5)
+    check_group_norm(x, rnd((c,), 28), rnd((c,), 29), groups, "silu", fp8, f"{(n, p, c, groups)}")
+
+
+def test_group_norm_of_large_frames_replays_from_a_graph():
+    for n, p, c, groups in ((3, 60000, 128, 16), (1, 200000, 256, 1)):
+        x, y = rnd((n, p, c), 30), torch.empty((n, p, c), dtype=BF16, device=DEV)
+        ws = torch.empty(api.cc_group_norm_workspace_bytes(n, p, c, groups), dtype=torch.uint8, device=DEV)
+        api.cc_group_norm_act(x, None, None, y, groups, ws)
+        torch.cuda.synchronize()
+        eager = y.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(2):
+                api.cc_group_norm_act(x, None, None, y, groups, ws)
+        for _ in range(3):
+            y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, eager)
+        api.cc_check_device()
+
+
+def test_large_group_norms_on_two_streams_at_once():
+    # both want every SM: the second waits for the first, neither for parts of the other
+    x = [rnd((4, 60000, 128), 31 + i) for i in range(2)]
+    ws = [torch.empty(api.cc_group_norm_workspace_bytes(4, 60000, 128, 16), dtype=torch.uint8, device=DEV)
+          for _ in range(2)]
+    y = [torch.empty_like(v) for v in x]
+    for i in range(2):
+        api.cc_group_norm_act(x[i], None, None, y[i], 16, ws[i])
+    torch.cuda.synchronize()
+    want = [v.clone() for v in y]
+    for v in y:
+        v.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            api.cc_group_norm_act(x[i], None, None, y[i], 16, ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    api.cc_check_device()
+    assert all(torch.equal(v, w) for v, w in zip(y, want))
+
+
 def test_group_norm_without_gamma_and_beta():
     x = rnd((2, 50, 64), 8)
     check_group_norm(x, None, None, 4, "none", False, "plain")
