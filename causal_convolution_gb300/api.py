@@ -421,7 +421,8 @@ def _last_rows(t, dtype, name: str, dev: int):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
-    return (t.data_ptr(), *_row_layout(t, name))
+    rows, c, ld = _row_layout(t, name)
+    return t.data_ptr(), rows, c, ld
 
 
 def _row_layout(t, name: str):
@@ -445,11 +446,11 @@ def _row_layout(t, name: str):
     return rows, c, c if ld is None else ld
 
 
-def _scales_of(scales, t, name: str) -> None:
-    """`scales` has a value for each row and 128 channels of t [..., C]."""
-    if scales.shape[:-1] != t.shape[:-1] or scales.shape[-1] != (t.shape[-1] + 127) // 128:
-        raise ValueError(f"{name} must be [..., ceil(C/128)] of [..., C], got {tuple(scales.shape)} for "
-                         f"{tuple(t.shape)}")
+def _scales_of(scales, dims: int, rows: int, c: int, name: str) -> None:
+    """`scales` has a value for each row and 128 channels of a [..., C] tensor of `dims` dimensions."""
+    blocks = (c + 127) // 128
+    if scales.dim() != dims or scales.shape[-1] != blocks or scales.numel() != rows * blocks:
+        raise ValueError(f"{name} must be [..., {blocks}] for {rows} rows of {c} channels, got {tuple(scales.shape)}")
 
 
 def cc_group_norm_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
@@ -457,12 +458,13 @@ def cc_group_norm_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
 
 
 def _group_norm_sizes(x, gamma, beta, y):
-    if x.dim() < 2 or x.shape != y.shape:
-        raise ValueError(f"group_norm_act: x and y must share [N,...,C], got {tuple(x.shape)} and {tuple(y.shape)}")
-    n, c = x.shape[0], x.shape[-1]
+    shape = x.shape
+    if len(shape) < 2 or shape != y.shape:
+        raise ValueError(f"group_norm_act: x and y must share [N,...,C], got {tuple(shape)} and {tuple(y.shape)}")
+    n, c = shape[0], shape[-1]
     if (gamma is not None and gamma.numel() != c) or (beta is not None and beta.numel() != c):
         raise ValueError("group_norm_act: gamma and beta must hold C elements")
-    return n, math.prod(x.shape[1:-1]), c
+    return n, shape[1] if len(shape) == 3 else math.prod(shape[1:-1]), c
 
 
 def cc_group_norm_act(x, gamma, beta, y, groups: int, ws, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
@@ -480,7 +482,7 @@ def cc_group_norm_act_fp8(x, gamma, beta, y, scales, groups: int, ws, eps: float
                           stream=None) -> None:
     """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [N, ..., ceil(C/128)]."""
     n, p, c = _group_norm_sizes(x, gamma, beta, y)
-    _scales_of(scales, x, "group_norm_act_fp8: scales")
+    _scales_of(scales, x.dim(), n * p, c, "group_norm_act_fp8: scales")
     dev, bf16 = torch.cuda.current_device(), torch.bfloat16
     _check(_lib.load().cc_group_norm_act_fp8(
         _arg(x, bf16, "x", dev), _arg(gamma, bf16, "gamma", dev), _arg(beta, bf16, "beta", dev),
@@ -504,7 +506,7 @@ def cc_rms_norm_act_fp8(x, gamma, y, scales, eps: float = 1e-6, act: str = "silu
     px, rows, c, ld = _last_rows(x, bf16, "x", dev)
     if x.shape != y.shape or (gamma is not None and gamma.numel() != c):
         raise ValueError("rms_norm_act_fp8: x and y must share [...,C] and gamma hold C elements")
-    _scales_of(scales, x, "rms_norm_act_fp8: scales")
+    _scales_of(scales, x.dim(), rows, c, "rms_norm_act_fp8: scales")
     _check(_lib.load().cc_rms_norm_act_fp8(
         px, _arg(gamma, bf16, "gamma", dev), _arg(y, torch.float8_e4m3fn, "y", dev),
         _arg(scales, torch.float32, "scales", dev), rows, c, ld, eps, _act(act), _raw_stream(stream, dev)))
@@ -518,7 +520,7 @@ def cc_fp8_quantize(x, y, scales, stream=None) -> None:
     px, rows, c, ld = _last_rows(x, torch.bfloat16, "x", dev)
     if x.shape != y.shape:
         raise ValueError("fp8_quantize: x and y must share [...,C]")
-    _scales_of(scales, x, "fp8_quantize: scales")
+    _scales_of(scales, x.dim(), rows, c, "fp8_quantize: scales")
     _check(_lib.load().cc_fp8_quantize(px, _arg(y, torch.float8_e4m3fn, "y", dev),
                                        _arg(scales, torch.float32, "scales", dev), rows, c, ld,
                                        _raw_stream(stream, dev)))
@@ -540,10 +542,10 @@ def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
     dev, bf16, f8, f32 = torch.cuda.current_device(), torch.bfloat16, torch.float8_e4m3fn, torch.float32
     po, m, n, ld_out = _last_rows(out, bf16, "out", dev)
     k = a.shape[-1]
-    if a.shape[:-1] != out.shape[:-1] or wq.dim() != 2 or wq.shape[0] != n or wq.shape[1] != k:
+    if a.shape[:-1] != out.shape[:-1] or wq.shape != (n, k):
         raise ValueError("gemm_fp8: a must be [...,K] and wq [N,K] of out [...,N]")
-    _scales_of(sa, a, "gemm_fp8: sa")
-    if sw.dim() != 2 or sw.shape[0] != (n + 127) // 128 or sw.shape[1] != (k + 127) // 128:
+    _scales_of(sa, a.dim(), m, k, "gemm_fp8: sa")
+    if sw.shape != ((n + 127) // 128, (k + 127) // 128):
         raise ValueError("gemm_fp8: sw must be [ceil(N/128),ceil(K/128)]")
     if bias is not None and bias.numel() != n:
         raise ValueError("gemm_fp8: bias must hold N elements")
