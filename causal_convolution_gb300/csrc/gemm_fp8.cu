@@ -456,7 +456,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       f32x2 acc[kEpiCols / 2];
 #pragma unroll
-      for (int j = 0; j < kEpiCols / 2; ++j) acc[j] = 0;
+      for (int j = 0; j < kEpiCols / 8; ++j) {
+        const bool on = args.bias && n0 + 8 * j < args.n;
+        const Vec8 t = unpack8(on ? __ldg(args.bias + (n0 >> 3) + j) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[4 * j + e] = t.p[e];
+      }
       float4 now = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int kb = 0; kb < args.kblocks; ++kb) {
@@ -483,43 +488,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         add_sums64(from, acc, ss);
         ready = add_sums64_release(from + 64, acc + 32, ss, tempty0 + buf * 8, lane == 0, tfull0 + (it & 1) * 8,
                                    (it >> 1) & 1);
-        // the staging rows are free once the previous tile's stores have read
-        // them, which they have by now; asked for at the tile's start, it took
-        // a thousand cycles
-        if (kb == 0 && any) {
+        if (kb == 0 && args.res && any) {
+          // the residual's piece, into staging rows that the previous tile's
+          // stores have read by now (at the tile's start they had not)
           if (lane == 0) {
             bulk_wait_read_all();
-            if (args.res) {
-              mbar_arrive_expect_tx(rbar, kStageOutBytes);
-              tma_load_2d(smem_u32(stage_out), &tmRes, rbar, n0, m0);
-              tma_load_2d(smem_u32(stage_out + kStageOutBytes / 2), &tmRes, rbar, n0 + 64, m0);
-            }
+            mbar_arrive_expect_tx(rbar, kStageOutBytes);
+            tma_load_2d(smem_u32(stage_out), &tmRes, rbar, n0, m0);
+            tma_load_2d(smem_u32(stage_out + kStageOutBytes / 2), &tmRes, rbar, n0 + 64, m0);
           }
           __syncwarp();
         }
       }
       __syncwarp();
       if (!any) continue;
-      if (args.res && !__all_sync(0xffffffffu, mbar_wait(rbar, rphase, args.err, tlim))) ok = false;
-      rphase ^= 1u;
+      if (args.res) {
+        if (!__all_sync(0xffffffffu, mbar_wait(rbar, rphase, args.err, tlim))) ok = false;
+        rphase ^= 1u;
+      } else {
+        if (lane == 0) bulk_wait_read_all();  // the previous tile's stores have read the staging rows
+        __syncwarp();
+      }
       if (!ok) break;
       // 64 columns at a time, all loads in front of the first store
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint8_t* row = stage_out + g * (kStageOutBytes / 2) + lane * 128;
-        uint4 extra[8];
-        if (args.bias) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            extra[j] = n0 + 64 * g + 8 * j < args.n ? __ldg(args.bias + (n0 >> 3) + 8 * g + j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const Vec8 t = unpack8(extra[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[32 * g + 4 * j + e] = add2(acc[32 * g + 4 * j + e], t.p[e]);
-          }
-        }
         if (args.res) {
+          uint4 extra[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) extra[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (lane & 7)) << 4));
 #pragma unroll
