@@ -437,6 +437,8 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_co
 
 // What does not fit on chip: the moments of runs of positions, their merging,
 // and a second reading that normalises.
+constexpr int kMergeThreads = 256;
+
 template <bool ONE, int T>
 __global__ void __launch_bounds__(T, 1024 / T) gn_moments_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -464,22 +466,27 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_moments_kernel(const __grid_co
                      a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * a.slab_groups);
 }
 
-__global__ void __launch_bounds__(128) gn_merge_kernel(const __grid_constant__ GnArgs a) {
-  const int g = blockIdx.x * 4 + (threadIdx.x >> 5);
+// A CTA to a group, so that few trips to memory follow one another.
+__global__ void __launch_bounds__(kMergeThreads) gn_merge_kernel(const __grid_constant__ GnArgs a) {
+  __shared__ Moments of[kMergeThreads / 32];
+  const int g = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
-  if (g >= a.slab_groups) return;
   const float2* part = a.part + static_cast<long long>(blockIdx.y) * a.runs * a.slab_groups + g;
   Moments m = {0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = threadIdx.x & 31; i < a.runs; i += 32) {
+#pragma unroll 4
+  for (int i = threadIdx.x; i < a.runs; i += kMergeThreads) {
     const float2 v = part[static_cast<long long>(i) * a.slab_groups];
     const int c = min(a.rows_per_cta, a.p - i * a.rows_per_cta);
     merge(m, Moments{static_cast<float>(c) * a.cpg, v.x, v.y});
   }
   m = warp_merge(m);
-  if ((threadIdx.x & 31) == 0)
+  if ((threadIdx.x & 31) == 0) of[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kMergeThreads / 32; ++i) merge(m, of[i]);
     a.stat[static_cast<long long>(blockIdx.y) * a.slab_groups + g] = mean_and_factor(m, a.eps);
+  }
 }
 
 template <bool ONE, bool SILU, bool FP8, int T>
@@ -589,11 +596,13 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
   g.slab_groups = groups;
   g.units = n;
   g.threads = c > 2048 ? 512 : 256;
-  // runs of up to 64 vectors a thread, shorter ones while they would not fill
-  // the SMs (four CTAs of 256 threads to one)
+  // runs of up to 32 vectors a thread, shorter ones while they would not fill
+  // the SMs (four CTAs of 256 threads to one): 16 x 219648 x 256 takes 790 us
+  // with 32, 794 with 64; 3 x 30000 x 1024 e4m3 104 and 113. (Launching a frame
+  // at a time, to find it in L2 the second time, took 1.0-1.1 ms.)
   const int lanes = g.threads / (c / 8);
   const long long vecs = static_cast<long long>(n) * ((p - 1) / lanes + 1);
-  g.rows = lanes * static_cast<int>(std::min(64LL, std::max(8LL, vecs / 608)));
+  g.rows = lanes * static_cast<int>(std::min(32LL, std::max(8LL, vecs / 608)));
   g.runs = (p - 1) / g.rows + 1;
   g.cols_at = align16(red_bytes(c / 8));
   g.smem = g.cols_at + static_cast<size_t>(c / 8) * parts * 4;
@@ -634,7 +643,7 @@ cc_status launch_twice(const char* what, GnArgs& a, const GnPlan& g, int n, cuda
     if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: kernel attributes: %s", what, cudaGetErrorString(e));
   }
   cudaError_t e = launch_pdl(moments, dim3(g.runs, n), dim3(T), g.smem, s, a);
-  if (e == cudaSuccess) e = launch_pdl(gn_merge_kernel, dim3((a.slab_groups + 3) / 4, n), dim3(128), 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(gn_merge_kernel, dim3(a.slab_groups, n), dim3(kMergeThreads), 0, s, a);
   if (e == cudaSuccess) e = launch_pdl(gn_apply_kernel<ONE, SILU, FP8, T>, dim3(g.runs, n), dim3(T), 0, s, a);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
