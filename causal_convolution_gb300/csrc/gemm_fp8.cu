@@ -6,8 +6,7 @@
 // from row to row and block to block, so the sum leaves tensor memory before
 // the next block's is added: each epilogue thread owns a row, reads its sums
 // and adds them, times sa[row][block] * sw[column block][block], to fp32
-// accumulators in its registers. Two accumulator buffers in tensor memory let
-// the MMAs of one block run while the previous one is read.
+// accumulators in its registers.
 //
 // Two kernels: CTA pairs with 256 x 256 tiles for many rows, and, for few, the
 // weights as the tensor core's 128-row side with K split over a cluster.
@@ -38,15 +37,29 @@ struct Fp8GemmArgs {
   unsigned long long timeout_ns;
 };
 
+// Tile coordinates stay in 32 bits.
+constexpr int kMaxRows = 0x7fffffff - 1024;
+constexpr int kMaxChannels = 1 << 24;
+
 constexpr int kKBytes = 128;  // bytes of K per stage: one scale block, one swizzle row
 
 // ------------------------------------------------------- CTA pairs, many rows --
 
 // Persistent pairs on 256 x 256 tiles (128 rows of a per CTA, the weights'
-// rows in halves), two 256-column accumulators in tensor memory. An epilogue
-// thread keeps 128 columns of its row -- one scale block of the weights -- in
-// registers, which takes half of the register file; eight warps with 128
-// columns each measured faster than sixteen with 64.
+// rows in halves). A tile's sums are two halves of 128 columns, each a scale
+// block of the weights, and each half has two accumulators in tensor memory
+// (4 x 128 columns, all of it), so that the MMAs of one run while the other is
+// read. An epilogue thread keeps 128 columns of its row in registers, which
+// takes half of the register file; eight warps with 128 columns each measured
+// faster than sixteen with 64.
+//
+// What bounds it: the epilogue. A block of K takes the tensor core 512 cycles,
+// and a warp about 620 to read and add its 128 columns (two trips to tensor
+// memory, 64 paired multiply-adds that the two warps of a scheduler share, and
+// what the loop around them costs); a tile's end takes 2000 more, of which the
+// accumulators in reserve hide two blocks. Measured: 16384 x 4096 x 4096 in 178
+// us (3.1 PFLOP/s; 139 us with the epilogue left out), 13728 x 1024 x 1024 with
+// bias and residual 19 us, 439296 x 256 x 512 79 us (5.7 TB/s).
 constexpr int kPairRows = 128;     // of A, per CTA
 constexpr int kPairCols = 256;     // of the tile; each CTA loads half of them
 constexpr int kHalfCols = 128;     // of an accumulator; each CTA loads 64 of its weight rows
@@ -63,96 +76,53 @@ constexpr int kPairThreads = 128 + 32 * kEpiWarps;  // a warpgroup to load and i
 constexpr int kIssueRegs = 72, kEpiRegs = 216;
 static_assert(kPairSmem <= 232448, "shared memory budget");
 
-// acc += 64 sums of this thread's tensor memory lane times `scale`. In one
-// statement, so that the sums are used where the load puts them: as separate
-// ones they were moved first, which took longer than adding them.
+// 64 sums of this thread's tensor memory lane, at %33 and on, into t0 .. t63;
+// then each pair of them, times %34, added to the accumulators %0 .. %31.
+#define CC_LOAD_SUMS \
+  ".reg .b32 t<64>, a<4>;\n\t.reg .b64 p<32>;\n\t" \
+  "add.u32 a0, %33, 0;\n\t" \
+  "add.u32 a1, %33, 16;\n\t" \
+  "add.u32 a2, %33, 32;\n\t" \
+  "add.u32 a3, %33, 48;\n\t" \
+  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, " \
+  "t8, t9, t10, t11, t12, t13, t14, t15}, [a0];\n\t" \
+  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t16, t17, t18, t19, t20, t21, t22, t23, " \
+  "t24, t25, t26, t27, t28, t29, t30, t31}, [a1];\n\t" \
+  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t32, t33, t34, t35, t36, t37, t38, t39, " \
+  "t40, t41, t42, t43, t44, t45, t46, t47}, [a2];\n\t" \
+  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t48, t49, t50, t51, t52, t53, t54, t55, " \
+  "t56, t57, t58, t59, t60, t61, t62, t63}, [a3];\n\t" \
+  "tcgen05.wait::ld.sync.aligned;\n\t"
+#define CC_ADD(k, lo, hi) \
+  "mov.b64 p" #k ", {t" #lo ", t" #hi "};\n\tfma.rn.f32x2 %" #k ", p" #k ", %34, %" #k ";\n\t"
+#define CC_ADD_SUMS \
+  CC_ADD(0, 0, 1) CC_ADD(1, 2, 3) CC_ADD(2, 4, 5) CC_ADD(3, 6, 7) \
+  CC_ADD(4, 8, 9) CC_ADD(5, 10, 11) CC_ADD(6, 12, 13) CC_ADD(7, 14, 15) \
+  CC_ADD(8, 16, 17) CC_ADD(9, 18, 19) CC_ADD(10, 20, 21) CC_ADD(11, 22, 23) \
+  CC_ADD(12, 24, 25) CC_ADD(13, 26, 27) CC_ADD(14, 28, 29) CC_ADD(15, 30, 31) \
+  CC_ADD(16, 32, 33) CC_ADD(17, 34, 35) CC_ADD(18, 36, 37) CC_ADD(19, 38, 39) \
+  CC_ADD(20, 40, 41) CC_ADD(21, 42, 43) CC_ADD(22, 44, 45) CC_ADD(23, 46, 47) \
+  CC_ADD(24, 48, 49) CC_ADD(25, 50, 51) CC_ADD(26, 52, 53) CC_ADD(27, 54, 55) \
+  CC_ADD(28, 56, 57) CC_ADD(29, 58, 59) CC_ADD(30, 60, 61) CC_ADD(31, 62, 63)
+#define CC_ACCUMULATORS \
+  "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), \
+  "+l"(acc[4]), "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7]), \
+  "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]), \
+  "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15]), \
+  "+l"(acc[16]), "+l"(acc[17]), "+l"(acc[18]), "+l"(acc[19]), \
+  "+l"(acc[20]), "+l"(acc[21]), "+l"(acc[22]), "+l"(acc[23]), \
+  "+l"(acc[24]), "+l"(acc[25]), "+l"(acc[26]), "+l"(acc[27]), \
+  "+l"(acc[28]), "+l"(acc[29]), "+l"(acc[30]), "+l"(acc[31])
+
+// acc += 64 sums times `scale`. In one statement, so that the sums are used
+// where the load puts them: as separate ones they were moved first, which took
+// a third of the time that adding them takes.
 __device__ __forceinline__ void add_sums64(uint32_t taddr, f32x2* acc, f32x2 scale) {
-  asm volatile("{\n\t"
-      ".reg .b32 t<64>;\n\t"
-      ".reg .b64 p<32>;\n\t"
-      ".reg .b32 a<4>;\n\t"
-      "add.u32 a0, %32, 0;\n\t"
-      "add.u32 a1, %32, 16;\n\t"
-      "add.u32 a2, %32, 32;\n\t"
-      "add.u32 a3, %32, 48;\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [a0];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [a1];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47}, [a2];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [a3];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t"
-      "mov.b64 p0, {t0, t1};\n\t"
-      "fma.rn.f32x2 %0, p0, %33, %0;\n\t"
-      "mov.b64 p1, {t2, t3};\n\t"
-      "fma.rn.f32x2 %1, p1, %33, %1;\n\t"
-      "mov.b64 p2, {t4, t5};\n\t"
-      "fma.rn.f32x2 %2, p2, %33, %2;\n\t"
-      "mov.b64 p3, {t6, t7};\n\t"
-      "fma.rn.f32x2 %3, p3, %33, %3;\n\t"
-      "mov.b64 p4, {t8, t9};\n\t"
-      "fma.rn.f32x2 %4, p4, %33, %4;\n\t"
-      "mov.b64 p5, {t10, t11};\n\t"
-      "fma.rn.f32x2 %5, p5, %33, %5;\n\t"
-      "mov.b64 p6, {t12, t13};\n\t"
-      "fma.rn.f32x2 %6, p6, %33, %6;\n\t"
-      "mov.b64 p7, {t14, t15};\n\t"
-      "fma.rn.f32x2 %7, p7, %33, %7;\n\t"
-      "mov.b64 p8, {t16, t17};\n\t"
-      "fma.rn.f32x2 %8, p8, %33, %8;\n\t"
-      "mov.b64 p9, {t18, t19};\n\t"
-      "fma.rn.f32x2 %9, p9, %33, %9;\n\t"
-      "mov.b64 p10, {t20, t21};\n\t"
-      "fma.rn.f32x2 %10, p10, %33, %10;\n\t"
-      "mov.b64 p11, {t22, t23};\n\t"
-      "fma.rn.f32x2 %11, p11, %33, %11;\n\t"
-      "mov.b64 p12, {t24, t25};\n\t"
-      "fma.rn.f32x2 %12, p12, %33, %12;\n\t"
-      "mov.b64 p13, {t26, t27};\n\t"
-      "fma.rn.f32x2 %13, p13, %33, %13;\n\t"
-      "mov.b64 p14, {t28, t29};\n\t"
-      "fma.rn.f32x2 %14, p14, %33, %14;\n\t"
-      "mov.b64 p15, {t30, t31};\n\t"
-      "fma.rn.f32x2 %15, p15, %33, %15;\n\t"
-      "mov.b64 p16, {t32, t33};\n\t"
-      "fma.rn.f32x2 %16, p16, %33, %16;\n\t"
-      "mov.b64 p17, {t34, t35};\n\t"
-      "fma.rn.f32x2 %17, p17, %33, %17;\n\t"
-      "mov.b64 p18, {t36, t37};\n\t"
-      "fma.rn.f32x2 %18, p18, %33, %18;\n\t"
-      "mov.b64 p19, {t38, t39};\n\t"
-      "fma.rn.f32x2 %19, p19, %33, %19;\n\t"
-      "mov.b64 p20, {t40, t41};\n\t"
-      "fma.rn.f32x2 %20, p20, %33, %20;\n\t"
-      "mov.b64 p21, {t42, t43};\n\t"
-      "fma.rn.f32x2 %21, p21, %33, %21;\n\t"
-      "mov.b64 p22, {t44, t45};\n\t"
-      "fma.rn.f32x2 %22, p22, %33, %22;\n\t"
-      "mov.b64 p23, {t46, t47};\n\t"
-      "fma.rn.f32x2 %23, p23, %33, %23;\n\t"
-      "mov.b64 p24, {t48, t49};\n\t"
-      "fma.rn.f32x2 %24, p24, %33, %24;\n\t"
-      "mov.b64 p25, {t50, t51};\n\t"
-      "fma.rn.f32x2 %25, p25, %33, %25;\n\t"
-      "mov.b64 p26, {t52, t53};\n\t"
-      "fma.rn.f32x2 %26, p26, %33, %26;\n\t"
-      "mov.b64 p27, {t54, t55};\n\t"
-      "fma.rn.f32x2 %27, p27, %33, %27;\n\t"
-      "mov.b64 p28, {t56, t57};\n\t"
-      "fma.rn.f32x2 %28, p28, %33, %28;\n\t"
-      "mov.b64 p29, {t58, t59};\n\t"
-      "fma.rn.f32x2 %29, p29, %33, %29;\n\t"
-      "mov.b64 p30, {t60, t61};\n\t"
-      "fma.rn.f32x2 %30, p30, %33, %30;\n\t"
-      "mov.b64 p31, {t62, t63};\n\t"
-      "fma.rn.f32x2 %31, p31, %33, %31;\n\t"
-      "}"
-      : "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]),
-        "+l"(acc[6]), "+l"(acc[7]), "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]),
-        "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15]), "+l"(acc[16]), "+l"(acc[17]),
-        "+l"(acc[18]), "+l"(acc[19]), "+l"(acc[20]), "+l"(acc[21]), "+l"(acc[22]), "+l"(acc[23]),
-        "+l"(acc[24]), "+l"(acc[25]), "+l"(acc[26]), "+l"(acc[27]), "+l"(acc[28]), "+l"(acc[29]),
-        "+l"(acc[30]), "+l"(acc[31])
-      : "r"(taddr), "l"(scale)
-      : "memory");
+  uint32_t unused = 0;
+  asm volatile("{\n\t" CC_LOAD_SUMS CC_ADD_SUMS "}"
+               : CC_ACCUMULATORS, "+r"(unused)
+               : "r"(taddr), "l"(scale)
+               : "memory");
 }
 
 // The same for the last 64 sums of an accumulator buffer: once they are in
@@ -161,102 +131,23 @@ __device__ __forceinline__ void add_sums64(uint32_t taddr, f32x2* acc, f32x2 sca
 // additions that hide them. Returns whether that phase is complete.
 __device__ __forceinline__ bool add_sums64_release(uint32_t taddr, f32x2* acc, f32x2 scale, uint32_t tempty,
                                                    uint32_t first, uint32_t next_bar, uint32_t next_parity) {
-  uint32_t ready;
-  asm volatile("{\n\t"
-      ".reg .b32 t<64>;\n\t"
-      ".reg .b64 p<32>;\n\t"
-      ".reg .b32 a<4>;\n\t"
-      ".reg .pred first, ready;\n\t"
-      "add.u32 a0, %33, 0;\n\t"
-      "add.u32 a1, %33, 16;\n\t"
-      "add.u32 a2, %33, 32;\n\t"
-      "add.u32 a3, %33, 48;\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [a0];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [a1];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47}, [a2];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [a3];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t"
-      "tcgen05.fence::before_thread_sync;\n\t"
-      "bar.warp.sync 0xffffffff;\n\t"
-      "setp.ne.b32 first, %36, 0;\n\t"
-      "@first mbarrier.arrive.shared::cluster.b64 _, [%35];\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 ready, [%37], %38;\n\t"
-      "selp.u32 %32, 1, 0, ready;\n\t"
-      "mov.b64 p0, {t0, t1};\n\t"
-      "fma.rn.f32x2 %0, p0, %34, %0;\n\t"
-      "mov.b64 p1, {t2, t3};\n\t"
-      "fma.rn.f32x2 %1, p1, %34, %1;\n\t"
-      "mov.b64 p2, {t4, t5};\n\t"
-      "fma.rn.f32x2 %2, p2, %34, %2;\n\t"
-      "mov.b64 p3, {t6, t7};\n\t"
-      "fma.rn.f32x2 %3, p3, %34, %3;\n\t"
-      "mov.b64 p4, {t8, t9};\n\t"
-      "fma.rn.f32x2 %4, p4, %34, %4;\n\t"
-      "mov.b64 p5, {t10, t11};\n\t"
-      "fma.rn.f32x2 %5, p5, %34, %5;\n\t"
-      "mov.b64 p6, {t12, t13};\n\t"
-      "fma.rn.f32x2 %6, p6, %34, %6;\n\t"
-      "mov.b64 p7, {t14, t15};\n\t"
-      "fma.rn.f32x2 %7, p7, %34, %7;\n\t"
-      "mov.b64 p8, {t16, t17};\n\t"
-      "fma.rn.f32x2 %8, p8, %34, %8;\n\t"
-      "mov.b64 p9, {t18, t19};\n\t"
-      "fma.rn.f32x2 %9, p9, %34, %9;\n\t"
-      "mov.b64 p10, {t20, t21};\n\t"
-      "fma.rn.f32x2 %10, p10, %34, %10;\n\t"
-      "mov.b64 p11, {t22, t23};\n\t"
-      "fma.rn.f32x2 %11, p11, %34, %11;\n\t"
-      "mov.b64 p12, {t24, t25};\n\t"
-      "fma.rn.f32x2 %12, p12, %34, %12;\n\t"
-      "mov.b64 p13, {t26, t27};\n\t"
-      "fma.rn.f32x2 %13, p13, %34, %13;\n\t"
-      "mov.b64 p14, {t28, t29};\n\t"
-      "fma.rn.f32x2 %14, p14, %34, %14;\n\t"
-      "mov.b64 p15, {t30, t31};\n\t"
-      "fma.rn.f32x2 %15, p15, %34, %15;\n\t"
-      "mov.b64 p16, {t32, t33};\n\t"
-      "fma.rn.f32x2 %16, p16, %34, %16;\n\t"
-      "mov.b64 p17, {t34, t35};\n\t"
-      "fma.rn.f32x2 %17, p17, %34, %17;\n\t"
-      "mov.b64 p18, {t36, t37};\n\t"
-      "fma.rn.f32x2 %18, p18, %34, %18;\n\t"
-      "mov.b64 p19, {t38, t39};\n\t"
-      "fma.rn.f32x2 %19, p19, %34, %19;\n\t"
-      "mov.b64 p20, {t40, t41};\n\t"
-      "fma.rn.f32x2 %20, p20, %34, %20;\n\t"
-      "mov.b64 p21, {t42, t43};\n\t"
-      "fma.rn.f32x2 %21, p21, %34, %21;\n\t"
-      "mov.b64 p22, {t44, t45};\n\t"
-      "fma.rn.f32x2 %22, p22, %34, %22;\n\t"
-      "mov.b64 p23, {t46, t47};\n\t"
-      "fma.rn.f32x2 %23, p23, %34, %23;\n\t"
-      "mov.b64 p24, {t48, t49};\n\t"
-      "fma.rn.f32x2 %24, p24, %34, %24;\n\t"
-      "mov.b64 p25, {t50, t51};\n\t"
-      "fma.rn.f32x2 %25, p25, %34, %25;\n\t"
-      "mov.b64 p26, {t52, t53};\n\t"
-      "fma.rn.f32x2 %26, p26, %34, %26;\n\t"
-      "mov.b64 p27, {t54, t55};\n\t"
-      "fma.rn.f32x2 %27, p27, %34, %27;\n\t"
-      "mov.b64 p28, {t56, t57};\n\t"
-      "fma.rn.f32x2 %28, p28, %34, %28;\n\t"
-      "mov.b64 p29, {t58, t59};\n\t"
-      "fma.rn.f32x2 %29, p29, %34, %29;\n\t"
-      "mov.b64 p30, {t60, t61};\n\t"
-      "fma.rn.f32x2 %30, p30, %34, %30;\n\t"
-      "mov.b64 p31, {t62, t63};\n\t"
-      "fma.rn.f32x2 %31, p31, %34, %31;\n\t"
-      "}"
-      : "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]),
-        "+l"(acc[6]), "+l"(acc[7]), "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]),
-        "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15]), "+l"(acc[16]), "+l"(acc[17]),
-        "+l"(acc[18]), "+l"(acc[19]), "+l"(acc[20]), "+l"(acc[21]), "+l"(acc[22]), "+l"(acc[23]),
-        "+l"(acc[24]), "+l"(acc[25]), "+l"(acc[26]), "+l"(acc[27]), "+l"(acc[28]), "+l"(acc[29]),
-        "+l"(acc[30]), "+l"(acc[31]), "=r"(ready)
-      : "r"(taddr), "l"(scale), "r"(tempty), "r"(first), "r"(next_bar), "r"(next_parity)
-      : "memory");
+  uint32_t ready = 0;
+  asm volatile("{\n\t.reg .pred first, ready;\n\t" CC_LOAD_SUMS
+               "tcgen05.fence::before_thread_sync;\n\t"
+               "bar.warp.sync 0xffffffff;\n\t"
+               "setp.ne.b32 first, %36, 0;\n\t"
+               "@first mbarrier.arrive.shared::cluster.b64 _, [%35];\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 ready, [%37], %38;\n\t"
+               "selp.u32 %32, 1, 0, ready;\n\t" CC_ADD_SUMS "}"
+               : CC_ACCUMULATORS, "+r"(ready)
+               : "r"(taddr), "l"(scale), "r"(tempty), "r"(first), "r"(next_bar), "r"(next_parity)
+               : "memory");
   return ready != 0;
 }
+#undef CC_LOAD_SUMS
+#undef CC_ADD
+#undef CC_ADD_SUMS
+#undef CC_ACCUMULATORS
 
 // Four blocks' scales of a row of a, or of a block row of the weights.
 __device__ __forceinline__ float4 load_scales(const float* p, int kb, int kblocks, bool on) {
@@ -290,7 +181,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   static_assert((2 * kPairStages + 8 + kEpiWarps + 1) * 8 + 4 <= 256, "barriers");
 
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // known to be uniform: a fifth of the time
+  // from a shuffle, so that the roles' branches are known to be uniform: without
+  // it the whole kernel took a fifth longer
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -558,10 +451,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ------------------------------------------------------------------ few rows --
 
 // The weights' 128 rows take the tensor core's M side and up to MT rows of a
-// its N side, so a call with one row moves the weights and nothing but padding
-// of the tensor core's time. K is split over the CTAs of a cluster, whose
-// partial sums meet in shared memory, in rank order: the weights stream
-// through all SMs although there are few output tiles.
+// its N side, so a call with one row moves the weights and wastes nothing but
+// tensor core time. K is split over the CTAs of a cluster, whose partial sums
+// meet in shared memory, in rank order: the weights stream through all SMs
+// although there are few output tiles. One row x 4096 x 4096: 5.6 us (3 TB/s,
+// of which half is the launch and the exchange); 64 rows: 8.3 us.
 constexpr int kFewThreads = 192;
 constexpr int kFewMax = 64;       // rows
 constexpr int kFewScales = 4096;  // staged scales of a: MT x blocks of K per CTA
@@ -852,6 +746,8 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   if (n <= 0 || k <= 0) return fail(CC_ERR_INVALID, "%s: channel counts must be positive", what);
   if (k % 16 != 0) return fail(CC_ERR_UNSUPPORTED, "%s: K must be a multiple of 16 (got %d)", what, k);
   if (n % 8 != 0) return fail(CC_ERR_UNSUPPORTED, "%s: N must be a multiple of 8 (got %d)", what, n);
+  if (m > kMaxRows || n > kMaxChannels || k > kMaxChannels)
+    return fail(CC_ERR_UNSUPPORTED, "%s: too many rows or channels", what);
   if (ld_out < n || ld_out % 8 != 0 || (res && (ld_res < n || ld_res % 8 != 0)))
     return fail(CC_ERR_INVALID, "%s: ld_out and ld_res must be at least N and multiples of 8", what);
   DeviceInfo di;

@@ -728,7 +728,7 @@ cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamm
 using namespace cc;
 
 extern "C" size_t cc_group_norm_workspace_bytes(int n, int p, int c, int groups) {
-  if (n <= 0 || p <= 0 || c < 8 || c > kGnMaxChannels || c % 8 != 0 || groups <= 0 || c % groups != 0) return 0;
+  if (n <= 0 || n > 65535 || p <= 0 || p > (1 << 30) || c < 8 || c > kGnMaxChannels || c % 8 != 0 || groups <= 0 || c % groups != 0) return 0;
   return std::max(gn_plan(n, p, c, groups, false).ws_bytes, gn_plan(n, p, c, groups, true).ws_bytes);
 }
 

@@ -291,7 +291,8 @@ extern "C" cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw
   if (n <= 0 || k <= 0) return fail(CC_ERR_INVALID, "gemm_fp8_prepare: sizes must be positive");
   if (k % 16 != 0) return fail(CC_ERR_UNSUPPORTED, "gemm_fp8_prepare: K must be a multiple of 16 (got %d)", k);
   const int nb = (n - 1) / kScaleBlock + 1, kb = (k - 1) / kScaleBlock + 1;
-  if (nb > 65535) return fail(CC_ERR_UNSUPPORTED, "gemm_fp8_prepare: N must be at most %d", 65535 * kScaleBlock);
+  if (nb > 65535 || k > (1 << 24))
+    return fail(CC_ERR_UNSUPPORTED, "gemm_fp8_prepare: N must be at most %d and K %d", 65535 * kScaleBlock, 1 << 24);
   DeviceInfo di;
   cc_status st = device_info(&di);
   if (st != CC_OK) return st;

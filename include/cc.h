@@ -349,7 +349,8 @@ typedef enum cc_act { CC_ACT_NONE = 0, CC_ACT_SILU = 1 } cc_act;
  * C channels and block b of 128 of them (the last one may be shorter),
  *   scales[row][b] = max(max |v| / 448, 2^-126),  y = e4m3(v / scales[row][b])
  * from the unrounded fp32 v, rounded to nearest even; y [rows, C], scales
- * [rows, ceil(C / 128)]. A block that holds a NaN gets a NaN scale and NaN
+ * [rows, ceil(C / 128)]. cc_fp8_quantize's scales are correctly rounded
+ * quotients; behind a norm they may be one step of 2^-23 off. A block that holds a NaN gets a NaN scale and NaN
  * values; one with an infinity gets an infinite scale, zeros for its finite
  * values and NaN for the infinite ones. */
 
@@ -390,7 +391,8 @@ cc_status cc_fp8_quantize(const cc_bf16* x, cc_fp8* y, float* scales, int rows, 
 
 /* Weights w [N, K] to e4m3 with one scale per 128 x 128 block (blocks at the
  * right and lower edges may be smaller): wq [N, K], sw [ceil(N / 128)][ceil(K / 128)],
- * each scale max(max |w| / 448, 2^-126). Needs K % 16 == 0. */
+ * each scale max(max |w| / 448, 2^-126). Needs K % 16 == 0, N <= 8388480 and
+ * K <= 2^24. */
 cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, int k, void* stream);
 
 /* out[m,n] = bf16( sum_b sa[m,b] sw[n/128,b] sum_{k in block b} a[m,k] wq[n,k]
@@ -400,8 +402,8 @@ cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, in
  * cc_gemm_fp8_prepare; bias: [N] or NULL; res: bf16 rows of stride ld_res
  * elements or NULL (ld_res is then ignored); out: bf16 rows of stride ld_out
  * elements, columns N .. ld_out-1 untouched; out may be res when their strides
- * are the same. Needs K % 16 == 0, N % 8 == 0, ld_out and ld_res >= N and
- * % 8 == 0. ld_out lets q, k and v land in the packed rows that cc_attn_frame
+ * are the same. Needs K % 16 == 0, N % 8 == 0, N and K <= 2^24, ld_out and
+ * ld_res >= N and % 8 == 0. ld_out lets q, k and v land in the packed rows that cc_attn_frame
  * reads. */
 cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8* wq, const float* sw, const cc_bf16* bias,
                       const cc_bf16* res, cc_bf16* out, int m, int n, int k, int64_t ld_res, int64_t ld_out,

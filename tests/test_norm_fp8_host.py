@@ -92,6 +92,17 @@ def test_gemm_refusals(lib, p):
     assert prep(p, p, p + 4, 64, 64, None) == 1 and prep(p, p, p, 64, 72, None) == 2
 
 
+def test_sizes_beyond_the_kernels_indexes(lib, p):
+    g, prep = lib.cc_gemm_fp8, lib.cc_gemm_fp8_prepare
+    big = (1 << 24) + 16
+    assert g(p, p, p, p, p, p, p, (1 << 31) - 1, 64, 128, 64, 64, None) == 2 and b"too many" in lib.cc_last_error()
+    assert g(p, p, p, p, p, p, p, 4, big, 128, big, big, None) == 2
+    assert g(p, p, p, p, p, p, p, 4, 64, big, 64, 64, None) == 2
+    assert prep(p, p, p, 8388481, 64, None) == 2 and prep(p, p, p, 64, big, None) == 2
+    assert lib.cc_group_norm_act(p, p, p, p, 1, (1 << 30) + 1, 64, 8, F(1e-6), 0, p, 1 << 60, None) == 2
+    assert lib.cc_group_norm_workspace_bytes(65536, 5, 64, 8) == 0
+
+
 def test_empty_requests(lib):
     e = F(1e-6)
     assert lib.cc_group_norm_act(None, None, None, None, 0, 4, 64, 8, e, 0, None, 0, None) == 0
