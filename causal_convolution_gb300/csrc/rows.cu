@@ -66,6 +66,13 @@ __device__ __forceinline__ f32x2 sum_squares(const uint4& raw, f32x2 sum) {
 // loads R rows (about four 16-byte loads a lane) before it uses the first, and
 // walks the rows in steps of the grid; gamma stays in registers. Neighbouring
 // rows go to different CTAs, so few rows spread over the SMs.
+//
+// Bound by memory where there are many rows: RMS norm + SiLU of 439296 x 512 in
+// 145 us (6.2 TB/s, 0.92 of a copy; a block per row took 1.6 ms), quantising
+// 13728 x 1024 in 5.9 us (7.2 TB/s, part of it out of L2). Few rows cost a
+// launch and a trip to memory: 17 x 2048 2.7 us, 5 x 1000 1.6 us, less than the
+// call on the host. 64 registers a thread (two more CTAs to an SM) are worth a
+// few spilled ones: 166 us became 145 with the paired arithmetic.
 template <int TPR, int V, bool NORM, bool SILU, bool FP8>
 __global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const __grid_constant__ RowArgs a) {
   constexpr int R = V >= 4 ? 1 : 4 / V;
@@ -123,7 +130,8 @@ __global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const 
   }
 }
 
-// Longer rows: one per CTA, up to four vectors a thread.
+// Longer rows: one per CTA, up to four vectors a thread. (Longer than a warp
+// can keep in registers; a CTA sums them with one barrier a row.)
 template <bool NORM, bool SILU, bool FP8>
 __global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __grid_constant__ RowArgs a) {
   __shared__ float red[2][16];
