@@ -210,6 +210,33 @@ def test_group_norm_is_the_same_every_time():
         assert torch.equal(group_norm(x, g, b, 32, "silu", False)[0], first)
 
 
+def test_group_norm_of_many_small_instances():
+    x = rnd((3001, 5, 72), 24, 2.0, 1.0)
+    check_group_norm(x, rnd((72,), 25), rnd((72,), 26), 9, "silu", False, "3001 instances")
+    check_group_norm(x, rnd((72,), 25), rnd((72,), 26), 3, "none", True, "3001 instances, e4m3")
+
+
+def test_group_norm_one_value_to_a_group():
+    # the variance of one value is 0: everything is beta
+    x, beta = rnd((4, 1, 64), 27), rnd((64,), 28)
+    (y,) = group_norm(x, rnd((64,), 29), beta, 64, "none", False)
+    assert torch.equal(y, beta.expand(4, 1, 64))
+
+
+def test_empty_tensors():
+    e = torch.empty
+    api.cc_group_norm_act(e((0, 5, 64), dtype=BF16, device=DEV), None, None, e((0, 5, 64), dtype=BF16, device=DEV), 8,
+                          None)
+    api.cc_group_norm_act_fp8(e((2, 0, 64), dtype=BF16, device=DEV), None, None, e((2, 0, 64), dtype=F8, device=DEV),
+                              e((2, 0, 1), device=DEV), 8, None)
+    api.cc_rms_norm_act(e((0, 64), dtype=BF16, device=DEV), None, e((0, 64), dtype=BF16, device=DEV))
+    api.cc_fp8_quantize(e((0, 3, 64), dtype=BF16, device=DEV), e((0, 3, 64), dtype=F8, device=DEV),
+                        e((0, 3, 1), device=DEV))
+    api.cc_gemm_fp8(e((0, 64), dtype=F8, device=DEV), e((0, 1), device=DEV), rnd_f8((128, 64), 30),
+                    rnd_scales((1, 1), 31), None, None, e((0, 128), dtype=BF16, device=DEV))
+    api.cc_check_device()
+
+
 def test_group_norm_of_video_frames():
     # [N, D, H, W, C] normalised per frame
     x = rnd((2, 3, 6, 7, 64), 23)
@@ -352,6 +379,24 @@ def test_gemm_matches_64_bits(m, n, k, extras):
     check_gemm(gemm(a, sa, wq, sw, bias, res), a, sa, wq, sw, bias, res, f"{m}x{n}x{k} {extras}")
 
 
+@pytest.mark.parametrize("m,n,k", [
+    (20001, 520, 272),   # several tiles to a CTA pair, an odd number of blocks of K
+    (19999, 264, 1280),  # ten blocks: fours and a rest
+    (30000, 136, 16),    # one block, half of every tile empty
+    (3, 128, 16384),     # few rows, more blocks of K than stages
+    (40, 136, 66000),    # few rows, too many scales to stage: the pairs' kernel
+    (64, 1000, 16), (33, 8, 5008),
+])
+def test_gemm_walks_many_tiles_and_blocks(m, n, k):
+    a, sa = rnd_f8((m, k), 160 + m), rnd_scales((m, ref.blocks(k)), 161)
+    wq, sw = rnd_f8((n, k), 162 + n), rnd_scales((ref.blocks(n), ref.blocks(k)), 163)
+    bias, res = rnd((n,), 164, 20.0), rnd((m, n), 165, 20.0)
+    first = gemm(a, sa, wq, sw, bias, res).clone()
+    check_gemm(first, a, sa, wq, sw, bias, res, f"{m}x{n}x{k}")
+    for _ in range(3):
+        assert torch.equal(gemm(a, sa, wq, sw, bias, res), first)  # the sums' order is fixed
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_gemm_with_strided_rows(m):
     # out and res as column slices of wider rows (packed q, k, v)
@@ -470,6 +515,50 @@ def test_attention_block_replays_from_a_graph_bit_by_bit():
     step()
     api.cc_check_device()
     assert torch.equal(out, replayed) and not torch.equal(out, eager)
+
+
+def test_graphs_with_one_workspace_one_after_the_other():
+    # the workspace needs no preparation and keeps nothing: two graphs may share it while they do not overlap
+    x = [rnd((1, 200000, 128), 190), rnd((2, 90000, 256), 191)]
+    y = [torch.empty_like(v) for v in x]
+    need = max(api.cc_group_norm_workspace_bytes(v.shape[0], v.shape[1], v.shape[2], 8) for v in x)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    want, graphs = [], []
+    for v, o in zip(x, y):
+        api.cc_group_norm_act(v, None, None, o, 8, ws)
+        torch.cuda.synchronize()
+        want.append(o.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            api.cc_group_norm_act(v, None, None, o, 8, ws)
+        graphs.append(g)
+    for _ in range(3):
+        ws.fill_(0xFF)
+        for o in y:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(y, want))
+    api.cc_check_device()
+
+
+def test_packed_rows_of_a_chunk():
+    # q, k and v normalised and quantised out of, and projected into, packed rows
+    t, hw, c = 2, 77, 128
+    qkv = rnd((t, hw, 3 * c), 192)
+    q8, s8 = torch.empty((t, hw, c), dtype=F8, device=DEV), torch.empty((t, hw, 1), device=DEV)
+    out = torch.zeros((t, hw, 3 * c), dtype=BF16, device=DEV)
+    wq, sw = rnd_f8((c, c), 193), rnd_scales((1, 1), 194)
+    for i in range(3):
+        part = qkv[..., i * c:(i + 1) * c]
+        api.cc_rms_norm_act_fp8(part, None, q8, s8, act="none")
+        want, bound = ref.rms_norm(part, None, 1e-6, "none")
+        ref.assert_fp8(q8, s8, want, bound, f"part {i}")
+        api.cc_gemm_fp8(q8, s8, wq, sw, None, part, out[..., i * c:(i + 1) * c])
+        check_gemm(out[..., i * c:(i + 1) * c].reshape(t * hw, c), q8.view(t * hw, c), s8.view(t * hw, 1), wq, sw,
+                   None, part.reshape(t * hw, c), f"part {i}")
+    api.cc_check_device()
 
 
 def test_calls_on_two_streams_at_once():
