@@ -395,16 +395,14 @@ def _act(act: str) -> int:
 
 
 def _arg(t, dtype, name: str, dev: int) -> int | None:
-    """_ptr for a tensor on the current device `dev`, whose stream the call uses (one quick test: a call's host time
-    counts where its tensors are small)."""
+    """_ptr for a tensor on the current device `dev`, whose stream the call uses. A call's host time counts where its
+    tensors are small, so the tests that all pass come first (a tensor off the GPU has device -1)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
         return t.data_ptr()
-    ptr = _ptr(t, dtype, name)
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
-    return ptr
+    _ptr(t, dtype, name)  # says what is wrong with it, unless it is
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -415,11 +413,11 @@ def _last_rows(t, dtype, name: str, dev: int):
     """(pointer, rows, C, ld) of a [..., C] tensor whose rows are C channels next to each other at one stride `ld`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
+    if t.get_device() != dev or t.dtype is not dtype:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
     rows, c, ld = _row_layout(t, name)
     return t.data_ptr(), rows, c, ld
@@ -427,11 +425,12 @@ def _last_rows(t, dtype, name: str, dev: int):
 
 def _row_layout(t, name: str):
     """(rows, C, ld)"""
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name}: expected [..., C]")
-    c = t.shape[-1]
+    c = shape[-1]
     if t.is_contiguous():
-        return (t.numel() // c if c else 0), c, c
+        return (shape[0] if len(shape) == 2 else t.numel() // c if c else 0), c, c
     if t.stride(-1) != 1 and c > 1:
         raise ValueError(f"{name}: channels must be contiguous")
     rows, ld = 1, None
