@@ -541,7 +541,7 @@ def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
     dev, bf16, f8, f32 = torch.cuda.current_device(), torch.bfloat16, torch.float8_e4m3fn, torch.float32
     po, m, n, ld_out = _last_rows(out, bf16, "out", dev)
     k = a.shape[-1]
-    if a.shape[:-1] != out.shape[:-1] or wq.shape != (n, k):
+    if a.dim() != out.dim() or a.numel() != m * k or wq.shape != (n, k):
         raise ValueError("gemm_fp8: a must be [...,K] and wq [N,K] of out [...,N]")
     _scales_of(sa, a.dim(), m, k, "gemm_fp8: sa")
     if sw.shape != ((n + 127) // 128, (k + 127) // 128):
