@@ -5,15 +5,15 @@
 // where the groups allow it, so that a position's piece is 128 bytes). A slab
 // is independent of the others, and one of two ways takes it:
 //
-//  - gn_cluster_kernel: a cluster of up to 16 CTAs keeps the slab in its
+//  - gn_cluster_kernel: a cluster of up to 8 CTAs keeps the slab in its
 //    shared memory, exchanges the groups' moments through it and writes the
 //    result. x is read once; no workspace.
 //  - gn_moments_kernel, gn_merge_kernel, gn_apply_kernel: x is read twice.
 //
 // (One kernel that keeps slabs of up to 15 MB on all SMs and meets in global
 // memory, and one that reads a slab a second time out of L2, took 1.1 ms for
-// 16 frames of 219,648 x 256 where these three take 0.81 ms: 1.02 of the time
-// that copying 3 x 1.8 GB takes. Their CTAs spent their time meeting.)
+// 16 frames of 219,648 x 256 where these three take 0.79 ms, the time that
+// copying 3 x 1.8 GB takes. Their CTAs spent their time meeting.)
 //
 // A thread sums its values around a pivot, its first value, so that nothing
 // cancels where the mean is large against the deviation. The CTA then adds up
@@ -35,6 +35,7 @@ namespace cc {
 namespace {
 
 constexpr int kGnMaxChannels = 4096;
+constexpr int kMaxRanks = 8;  // CTAs in a cluster
 
 // Mean and sum of squared deviations of `n` values; two of them merge exactly
 // (in real arithmetic) into that of their union, without the cancellation
@@ -391,25 +392,23 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_cluster_kernel(const __grid_co
   __syncwarp();
   cluster_sync_all();
   // The ranks' moments in their order, around the first one's mean (which
-  // takes at most four bits if that rank is the odd one out of sixteen).
+  // takes at most three bits if that rank is the odd one out of eight).
   float2* col_stat = reinterpret_cast<float2*>(cols);
   const float count = static_cast<float>(a.p) * a.cpg;
   for (int g = threadIdx.x; g < groups; g += T) {
-    float pivot = 0.f, sum = 0.f, m2 = 0.f;
-    for (int k0 = 0; k0 < ranks; k0 += 8) {
-      float2 of[8];  // eight trips to the other CTAs at once
+    float sum = 0.f, m2 = 0.f;
+    float2 of[kMaxRanks];  // all trips to the other CTAs at once
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < ranks) of[k] = ld_cluster_f2(mapa_shared(smem_u32(&mom[g]), k0 + k));
-      if (k0 == 0) pivot = of[0].x;
+    for (int k = 0; k < kMaxRanks; ++k)
+      if (k < ranks) of[k] = ld_cluster_f2(mapa_shared(smem_u32(&mom[g]), k));
+    const float pivot = of[0].x;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k0 + k < ranks) {
-          const float c = static_cast<float>(max(0, min(a.rows_per_cta, a.p - (k0 + k) * a.rows_per_cta))) * a.cpg;
-          const float d = of[k].x - pivot;
-          sum = fmaf(c, d, sum);
-          m2 += fmaf(c * d, d, of[k].y);
-        }
+    for (int k = 0; k < kMaxRanks; ++k) {
+      if (k < ranks) {
+        const float c = static_cast<float>(max(0, min(a.rows_per_cta, a.p - k * a.rows_per_cta))) * a.cpg;
+        const float d = of[k].x - pivot;
+        sum = fmaf(c, d, sum);
+        m2 += fmaf(c * d, d, of[k].y);
       }
     }
     const float shift = sum / count;
@@ -581,21 +580,29 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
     g.rounds = (g.rows + lanes - 1) / lanes;
     g.smem = g.keep_at + static_cast<size_t>(g.rows) * slots * 16;
   };
-  for (int ranks = 1; ranks <= 16; ranks *= 2) {
-    cut(ranks, 256);
-    if (g.smem <= kMaxSmem) break;
-  }
-  if (g.smem <= kMaxSmem) {
-    g.cluster = true;
-    // two CTAs to an SM where eight of them hold the slab, and more CTAs while
-    // SMs are idle and a thread still has several vectors
-    while (g.ranks < 8 && (g.smem > kMaxSmem / 2 - 1024 || (g.units * g.ranks < 152 && g.rounds > 2)))
-      cut(g.ranks * 2, 256);
+  constexpr size_t kHalf = kMaxSmem / 2 - 1024;  // what leaves room for a second CTA on the SM
+  cut(1, 256);
+  // two CTAs to an SM where eight of them hold the slab, and more CTAs while
+  // SMs are idle and a thread still has several vectors
+  while (g.ranks < kMaxRanks && (g.smem > kHalf || (g.units * g.ranks < 152 && g.rounds > 2))) cut(g.ranks * 2, 256);
+  // Where the SMs hold one CTA of a cluster each, fifteen clusters of eight run
+  // at a time (the sixteenth waits for the first) and nothing fills their waits,
+  // and up to four clusters leave most SMs idle: two readings by all SMs are
+  // faster once there is enough to read.
+  // Clusters against two readings in us (silu):
+  //   16 x 12800 x 512, 32 groups   136 / 108   (16 x 7000, two CTAs to an SM: 60 / 64)
+  //   16 x 11520 x 64, 2 groups    28.0 / 20.7  (15 instances:              16.1 / 18.5)
+  //   1 x 5632 x 64, 2 groups, 22 rounds   8.5 / 7.2   (3840, 15 rounds:      7.2 / 7.2)
+  //   4 x 3240 x 208, 1 group, 45 rounds  12.4 / 10.4  (8 instances:         12.5 / 12.4)
+  // (Clusters of 16 CTAs lie between: 3 x 3234 x 168 e4m3 18.5 with 8, 12.9 with
+  // 16, 12.5 with two readings; 4 x 17253 x 112 22.7 with 16, 13.4.)
+  g.cluster = g.smem <= kMaxSmem && !(g.smem > kHalf && g.units > 15) && !(g.units <= 4 && g.rounds > 20);
+  if (g.cluster) {
     // 512 threads where each still has eight vectors and only one partial sum
     // to hand over: 4 x 3432 x 1024 (32 groups) takes 12.8 us against 13.5 with
     // 256; with eight partial sums, 3 x 3555 x 480 takes 12.5 against 11.5
-    const size_t room = g.smem > kMaxSmem / 2 - 1024 ? kMaxSmem : kMaxSmem / 2 - 1024;
     if (parts == 1 && g.rounds >= 16) {
+      const size_t room = g.smem > kHalf ? kMaxSmem : kHalf;
       cut(g.ranks, 512);
       if (g.smem > room) cut(g.ranks, 256);
     }
@@ -624,7 +631,6 @@ template <bool ONE, bool SILU, bool FP8, int T>
 cc_status launch_cluster(const char* what, GnArgs& a, const GnPlan& g, cudaStream_t s) {
   auto kern = gn_cluster_kernel<ONE, SILU, FP8, T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (e == cudaSuccess && g.ranks > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: kernel attributes: %s", what, cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(g.ranks, g.slabs, static_cast<unsigned>(g.units / g.slabs));

@@ -119,6 +119,18 @@ def test_group_norm_of_large_frames(n, p, c, groups, fp8):
     check_group_norm(x, rnd((c,), 28), rnd((c,), 29), groups, "silu", fp8, f"{(n, p, c, groups)}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,p,c,groups", [
+    (1, 3840, 64, 2), (1, 5700, 64, 2), (4, 5800, 64, 2), (5, 5800, 64, 2),  # few slabs: clusters or all SMs
+    (2, 1600, 208, 1), (2, 705, 424, 8), (1, 353, 792, 1), (1, 50, 4096, 1), (3, 21, 4096, 2),
+    (15, 9000, 64, 2), (16, 9000, 64, 2), (16, 6500, 64, 2),                 # many: clusters of one or two CTAs to an SM
+    (1, 17253, 112, 2), (2, 29001, 64, 4), (2, 30001, 64, 4),                # about as much as eight SMs hold
+])
+def test_group_norm_on_both_sides_of_the_choice_of_kernel(n, p, c, groups, fp8):
+    x = rnd((n, p, c), 90 + p, 1.0, 0.5)
+    check_group_norm(x, 1 + rnd((c,), 91, 0.3), rnd((c,), 92, 0.3), groups, "silu", fp8, f"{(n, p, c, groups)}")
+
+
 def test_group_norm_of_large_frames_replays_from_a_graph():
     for n, p, c, groups in ((3, 60000, 128, 16), (1, 200000, 256, 1)):
         x, y = rnd((n, p, c), 30), torch.empty((n, p, c), dtype=BF16, device=DEV)
