@@ -24,6 +24,7 @@ struct RowArgs {
   long long rows;
   long long ld_x;  // in vectors of eight channels
   int vecs;        // C / 8
+  int piece;       // vectors that a warp takes of a row at a time
   int blocks;      // ceil(C / 128)
   float inv_c;
   float eps;
@@ -61,30 +62,44 @@ __device__ __forceinline__ f32x2 sum_squares(const uint4& raw, f32x2 sum) {
   return sum;
 }
 
+// CTAs of a row kernel to an SM: three with 80 registers a thread, or four with
+// 64 and a few of them spilled. In us with three / with four: norm of
+// 439296 x 512 to bf16 149 / 145, to e4m3 (100000 rows) 35 / 38; with four
+// vectors to a lane (100000 x 1024) the norm takes 67 / 74, quantising 55 / 50,
+// and with one (100000 x 256) 14.5 / 17.0.
+template <int V, bool NORM, bool FP8>
+constexpr int row_ctas() {
+  return (V == 4 ? NORM : FP8) ? 3 : 4;
+}
+
 // Rows of up to 8 * TPR * V channels, TPR lanes each with V vectors of a row in
 // registers, so a row is read once and its sum costs shuffles only. A warp
 // loads R rows (about four 16-byte loads a lane) before it uses the first, and
 // walks the rows in steps of the grid; gamma stays in registers. Neighbouring
-// rows go to different CTAs, so few rows spread over the SMs.
+// rows go to different CTAs, so few rows spread over the SMs. Without a norm
+// longer rows come in pieces of whole blocks, as blockIdx.y says.
 //
 // Bound by memory where there are many rows: RMS norm + SiLU of 439296 x 512 in
 // 145 us (6.2 TB/s, 0.92 of a copy; a block per row took 1.6 ms), quantising
-// 13728 x 1024 in 5.9 us (7.2 TB/s, part of it out of L2). Few rows cost a
-// launch and a trip to memory: 17 x 2048 2.7 us, 5 x 1000 1.6 us, less than the
-// call on the host. 64 registers a thread (two more CTAs to an SM) are worth a
-// few spilled ones: 166 us became 145 with the paired arithmetic.
+// 13728 x 1024 in 5.9 us (7.2 TB/s, part of it out of L2) and 60000 x 2048 in 60
+// (6.2 TB/s). Few rows cost a launch and a trip to memory: 300 x 1024 2.0 us,
+// 5 x 1000 quantised 1.6 us, less than the call on the host. With SiLU to e4m3
+// the exponentials and reciprocals, 16 of them a clock and SM, take as long as
+// the bytes.
 template <int TPR, int V, bool NORM, bool SILU, bool FP8>
-__global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int R = V >= 4 ? 1 : 4 / V;
+__global__ void __launch_bounds__(kRowThreads, row_ctas<V, NORM, FP8>()) row_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int R = 4 / V;
   const int lane = threadIdx.x % TPR;
   const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / TPR);
   const long long first = static_cast<long long>(threadIdx.x / TPR) * gridDim.x + blockIdx.x;
+  const int v0 = NORM ? lane : blockIdx.y * a.piece + lane;
+  const int end = NORM ? a.vecs : min(a.vecs, static_cast<int>(blockIdx.y + 1) * a.piece);
   pdl_launch_dependents();
   pdl_wait();
   uint4 gamma[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int v = lane + i * TPR;
+    const int v = v0 + i * TPR;
     gamma[i] = NORM && a.gamma && v < a.vecs ? a.gamma[v]
                                              : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
   }
@@ -97,8 +112,8 @@ __global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const 
       const long long r = first + off + j * step;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int v = lane + i * TPR;
-        raw[j][i] = r < a.rows && v < a.vecs ? __ldcs(a.x + r * a.ld_x + v) : make_uint4(0, 0, 0, 0);
+        const int v = v0 + i * TPR;
+        raw[j][i] = r < a.rows && v < end ? __ldcs(a.x + r * a.ld_x + v) : make_uint4(0, 0, 0, 0);
       }
     }
     float rs[R];
@@ -123,16 +138,18 @@ __global__ void __launch_bounds__(kRowThreads, V == 8 ? 2 : 4) row_kernel(const 
       const long long r = first + off + j * step;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int v = lane + i * TPR;
-        finish_vector<NORM, SILU, FP8>(a, raw[j][i], gamma[i], NORM ? rs[j] : 1.f, r, v, r < a.rows && v < a.vecs);
+        const int v = v0 + i * TPR;
+        if (V > 2 && v - lane >= end) break;  // the same for the whole warp
+        finish_vector<NORM, SILU, FP8>(a, raw[j][i], gamma[i], NORM ? rs[j] : 1.f, r, v, r < a.rows && v < end);
       }
     }
   }
 }
 
-// Longer rows: one per CTA, up to four vectors a thread. (Longer than a warp
-// can keep in registers; a CTA sums them with one barrier a row.)
-template <bool NORM, bool SILU, bool FP8>
+// Norms of longer rows: one row per CTA, up to four vectors a thread, with one
+// barrier a row for its sum. 60000 x 2048 to e4m3 72 us, to bf16 76; a warp with
+// eight vectors a lane took 101 and 86, two vectors a thread take 97 and 96.
+template <bool SILU, bool FP8>
 __global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __grid_constant__ RowArgs a) {
   __shared__ float red[2][16];
   const int tid = threadIdx.x;
@@ -141,55 +158,56 @@ __global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __
   pdl_wait();
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     uint4 raw[4];
-    float rs = 0.f;
+    f32x2 sum = pair(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int v = tid + i * blockDim.x;
       raw[i] = v < a.vecs ? __ldcs(a.x + r * a.ld_x + v) : make_uint4(0, 0, 0, 0);
     }
-    if (NORM) {
-      f32x2 sum = pair(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum = sum_squares(raw[i], sum);
-      rs = lo(sum) + hi(sum);
+    for (int i = 0; i < 4; ++i) sum = sum_squares(raw[i], sum);
+    float rs = lo(sum) + hi(sum);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
-      if ((tid & 31) == 0) red[turn][tid >> 5] = rs;
-      __syncthreads();  // one per row: the two halves of `red` take turns
-      rs = 0.f;
-      for (int i = 0; i < blockDim.x / 32; ++i) rs += red[turn][i];
-      rs = 1.f / sqrtf(fmaf(rs, a.inv_c, a.eps));
-    }
+    for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
+    if ((tid & 31) == 0) red[turn][tid >> 5] = rs;
+    __syncthreads();  // one per row: the two halves of `red` take turns
+    rs = 0.f;
+    for (int i = 0; i < blockDim.x / 32; ++i) rs += red[turn][i];
+    rs = 1.f / sqrtf(fmaf(rs, a.inv_c, a.eps));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (i * static_cast<int>(blockDim.x) >= a.vecs) break;
       const int v = tid + i * blockDim.x;
-      const uint4 gamma = NORM && a.gamma && v < a.vecs
-                              ? a.gamma[v]
-                              : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-      finish_vector<NORM, SILU, FP8>(a, raw[i], gamma, rs, r, v, v < a.vecs);
+      const uint4 gamma =
+          a.gamma && v < a.vecs ? a.gamma[v] : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+      finish_vector<true, SILU, FP8>(a, raw[i], gamma, rs, r, v, v < a.vecs);
     }
   }
 }
 
 template <bool NORM, bool SILU, bool FP8>
-cc_status launch_rows(const char* what, const RowArgs& a, int sms, cudaStream_t stream) {
+cc_status launch_rows(const char* what, RowArgs& a, int sms, cudaStream_t stream) {
   const int lanes = a.vecs <= 16 ? 16 : 32;
   const int v = (a.vecs + lanes - 1) / lanes;
-  if (v > 8) {
-    const int threads = (a.vecs + 127) / 128 * 32;
-    const int grid = static_cast<int>(std::min<long long>(a.rows, static_cast<long long>(sms) * (2048 / threads)));
-    const cudaError_t e = launch_pdl(long_row_kernel<NORM, SILU, FP8>, dim3(grid), dim3(threads), 0, stream, a);
-    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
-    return launch_status(what);
+  void (*kern)(RowArgs);
+  int threads = kRowThreads, ctas, pieces = 1;
+  if (NORM && v > 4) {
+    kern = long_row_kernel<SILU, FP8>;
+    threads = (a.vecs + 127) / 128 * 32;
+    ctas = 2048 / threads;
+  } else {
+    kern = lanes == 16 ? row_kernel<16, 1, NORM, SILU, FP8>
+           : v == 1    ? row_kernel<32, 1, NORM, SILU, FP8>
+           : v == 2    ? row_kernel<32, 2, NORM, SILU, FP8>
+                       : row_kernel<32, 4, NORM, SILU, FP8>;
+    ctas = v > 2 ? row_ctas<4, NORM, FP8>() : row_ctas<1, NORM, FP8>();
+    pieces = (v + 3) / 4;
+    a.piece = (v + pieces - 1) / pieces * lanes;
   }
-  auto kern = lanes == 16 ? row_kernel<16, 1, NORM, SILU, FP8>
-              : v == 1    ? row_kernel<32, 1, NORM, SILU, FP8>
-              : v == 2    ? row_kernel<32, 2, NORM, SILU, FP8>
-              : v <= 4    ? row_kernel<32, 4, NORM, SILU, FP8>
-                          : row_kernel<32, 8, NORM, SILU, FP8>;
   // as many CTAs as fit, walking the rows
-  const int grid = static_cast<int>(std::min<long long>(a.rows, static_cast<long long>(sms) * (v > 4 ? 2 : 4)));
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kRowThreads), 0, stream, a);
+  const long long fit = (static_cast<long long>(sms) * ctas + pieces - 1) / pieces;
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(a.rows, fit)), pieces);
+  const cudaError_t e = launch_pdl(kern, grid, dim3(threads), 0, stream, a);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
 }

@@ -321,6 +321,21 @@ def test_quantize_matches_its_definition_bit_by_bit(rows, c, pad):
     assert torch.equal(y.t.view(torch.uint8), want.contiguous().view(torch.uint8))
 
 
+# four vectors to a lane, rows cut into pieces, a row to a CTA, and more rows than are taken at once
+MORE_ROW_SHAPES = [(4001, 616), (7, 520), (3001, 1160), (2600, 1536), (5, 1288), (1, 2056), (6001, 1032), (700, 5128)]
+
+
+@pytest.mark.parametrize("rows,c", MORE_ROW_SHAPES)
+def test_quantize_of_wide_rows(rows, c):
+    test_quantize_matches_its_definition_bit_by_bit(rows, c, 8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows,c", MORE_ROW_SHAPES)
+def test_rms_norm_of_wide_rows(rows, c, fp8):
+    test_rms_norm_matches_64_bits(rows, c, "silu", fp8, 8)
+
+
 def test_quantize_of_zeros_tiny_values_nan_and_infinity():
     x = torch.zeros((5, 256), dtype=BF16, device=DEV)
     x[1, :128] = 1e-38
