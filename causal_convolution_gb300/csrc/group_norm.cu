@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <numeric>
 
 #include "cc.h"
@@ -613,13 +614,24 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
   g.slab_groups = groups;
   g.units = n;
   g.threads = c > 2048 ? 512 : 256;
-  // runs of up to 32 vectors a thread, shorter ones while they would not fill
-  // the SMs (four CTAs of 256 threads to one): 16 x 219648 x 256 takes 790 us
-  // with 32, 794 with 64; 3 x 30000 x 1024 e4m3 104 and 113. (Launching a frame
-  // at a time, to find it in L2 the second time, took 1.0-1.1 ms.)
+  // Runs of 32 vectors a thread: 16 x 219648 x 256 takes 790 us with 32, 794
+  // with 64. (Launching a frame at a time, to find it in L2 the second time, took
+  // 1.0-1.1 ms.) What is not worth 1.5 rounds of the CTAs that run at a time is
+  // cut so that the last round is full, at about four vectors' time for a CTA's
+  // start and end: 2 x 21996 x 648 e4m3 57.2 -> 47.7 us, 7 x 14000 x 320 46.8 ->
+  // 38.2; from there on it gains nothing (3 x 50000 x 840 148 -> 151).
   const int lanes = g.threads / (c / 8);
-  const long long vecs = static_cast<long long>(n) * ((p - 1) / lanes + 1);
-  g.rows = lanes * static_cast<int>(std::min(32LL, std::max(8LL, vecs / 608)));
+  const int per = (p - 1) / lanes + 1;
+  const int at_once = 608 * 256 / g.threads;  // four CTAs of 256 threads to an SM
+  int run = 32;
+  if (static_cast<long long>(n) * per < 48LL * at_once) {
+    int best = INT_MAX;
+    for (int r = 8; r <= 40; ++r) {
+      const int cost = ((n * ((per - 1) / r + 1) - 1) / at_once + 1) * (r + 4);
+      if (cost < best) best = cost, run = r;
+    }
+  }
+  g.rows = lanes * run;
   g.runs = (p - 1) / g.rows + 1;
   g.cols_at = align16(red_bytes(c / 8));
   g.smem = g.cols_at + static_cast<size_t>(c / 8) * parts * 4;
