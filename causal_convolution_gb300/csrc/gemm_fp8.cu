@@ -8,7 +8,7 @@
 // and adds them, times sa[row][block] * sw[column block][block], to fp32
 // accumulators in its registers.
 //
-// Two kernels: CTA pairs with 256 x 256 tiles for many rows, and, for few, the
+// Two kernels: CTA pairs with tiles of 256 rows for many rows, and, for few, the
 // weights as the tensor core's 128-row side with K split over a cluster.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,13 +45,13 @@ constexpr int kKBytes = 128;  // bytes of K per stage: one scale block, one swiz
 
 // ------------------------------------------------------- CTA pairs, many rows --
 
-// Persistent pairs on 256 x 256 tiles (128 rows of a per CTA, the weights'
-// rows in halves). A tile's sums are two halves of 128 columns, each a scale
-// block of the weights, and each half has two accumulators in tensor memory
-// (4 x 128 columns, all of it), so that the MMAs of one run while the other is
-// read. An epilogue thread keeps 128 columns of its row in registers, which
-// takes half of the register file; eight warps with 128 columns each measured
-// faster than sixteen with 64.
+// Persistent pairs on tiles of 256 rows (128 of a per CTA) x 256 columns, or x
+// 128 where that fills the last round of tiles better. An accumulator holds 128
+// columns, one scale block of the weights; the one or two of a tile have four or
+// two buffers each in tensor memory (512 columns, all of it), so that the MMAs
+// of one run while another is read. An epilogue thread keeps half of the tile's
+// columns of its row in registers: with 256 columns half of the register file,
+// and eight warps with 128 columns each measured faster than sixteen with 64.
 //
 // What bounds it: the epilogue. A block of K takes the tensor core 512 cycles,
 // and a warp about 620 to read and add its 128 columns (two trips to tensor
@@ -59,22 +59,35 @@ constexpr int kKBytes = 128;  // bytes of K per stage: one scale block, one swiz
 // what the loop around them costs); a tile's end takes 2000 more, of which the
 // accumulators in reserve hide two blocks. Measured: 16384 x 4096 x 4096 in 178
 // us (3.1 PFLOP/s; 139 us with the epilogue left out), 13728 x 1024 x 1024 with
-// bias and residual 19 us, 439296 x 256 x 512 79 us (5.7 TB/s).
+// bias and residual 19 us, 439296 x 256 x 512 79 us (5.7 TB/s). A block of K of
+// the narrow tile takes 480 cycles of 384 that its 24 KB a CTA take to arrive.
+// (As two accumulators of 64 columns it took 580: an MMA with 64 columns takes as
+// long as one with 128.)
 constexpr int kPairRows = 128;     // of A, per CTA
-constexpr int kPairCols = 256;     // of the tile; each CTA loads half of them
-constexpr int kHalfCols = 128;     // of an accumulator; each CTA loads 64 of its weight rows
-constexpr int kPairABytes = kPairRows * kKBytes;
-constexpr int kPairBBytes = kPairCols / 2 * kKBytes;
-constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
-constexpr int kPairStages = 5;
-constexpr int kEpiWarps = 8;       // one per half of the columns and quarter of the rows
-constexpr int kEpiCols = kHalfCols;
-constexpr int kStageOutBytes = 32 * kEpiCols * 2;  // a warp's 32 rows, two pieces of 64 columns
-constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + kEpiWarps * kStageOutBytes + 256;
+constexpr int kAccCols = 128;      // of an accumulator; each CTA loads 64 of its weight rows
+constexpr int kEpiWarps = 8;       // one per half of the tile's columns and quarter of the rows
 constexpr int kPairThreads = 128 + 32 * kEpiWarps;  // a warpgroup to load and issue, two for the epilogue
 // registers a thread: 128 * 72 + 256 * 216 = 384 * 168, what the launch has
 constexpr int kIssueRegs = 72, kEpiRegs = 216;
-static_assert(kPairSmem <= 232448, "shared memory budget");
+
+// ACCS: accumulators side by side in a tile, one or two.
+template <int ACCS>
+struct PairShape {
+  static constexpr int kCols = ACCS * kAccCols;
+  static constexpr int kEpiCols = kCols / 2;     // of a warp
+  static constexpr int kBufs = 512 / kCols;      // of an accumulator: all of tensor memory
+  static constexpr int kABytes = kPairRows * kKBytes;
+  static constexpr int kBBytes = kAccCols / 2 * kKBytes;  // of an accumulator's weights
+  static constexpr int kStageBytes = kABytes + ACCS * kBBytes;
+  static constexpr int kStages = ACCS == 2 ? 5 : 8;
+  static constexpr int kPieceBytes = 32 * 64 * 2;  // a warp's 32 rows leave in pieces of 64 columns
+  static constexpr int kPieces = kEpiCols / 64;
+  static constexpr int kOutBytes = kPieces * kPieceBytes;
+  static constexpr int kBarBytes = 320;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kOutBytes + kBarBytes;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert((2 * kStages + 2 * ACCS * kBufs + kEpiWarps + 1) * 8 + 4 <= kBarBytes, "barriers");
+};
 
 // 64 sums of this thread's tensor memory lane, at %33 and on, into t0 .. t63;
 // then each pair of them, times %34, added to the accumulators %0 .. %31.
@@ -165,21 +178,22 @@ __device__ __forceinline__ float4 load_scales(const float* p, int kb, int kblock
   return v;
 }
 
+template <int ACCS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmRes, const __grid_constant__ CUtensorMap tmOut,
                     const __grid_constant__ Fp8GemmArgs args) {
+  using S = PairShape<ACCS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_out = smem + kPairStages * kPairStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + kEpiWarps * kStageOutBytes);
-  uint64_t* empty = full + kPairStages;
-  uint64_t* tfull = empty + kPairStages;  // [half][buffer]
-  uint64_t* tempty = tfull + 4;
-  uint64_t* rfull = tempty + 4;  // [kEpiWarps] residual pieces
+  uint8_t* s_out = smem + S::kStages * S::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + kEpiWarps * S::kOutBytes);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* tfull = empty + S::kStages;  // [accumulator][buffer]
+  uint64_t* tempty = tfull + ACCS * S::kBufs;
+  uint64_t* rfull = tempty + ACCS * S::kBufs;  // [kEpiWarps] residual pieces
   uint64_t* done = rfull + kEpiWarps;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  static_assert((2 * kPairStages + 8 + kEpiWarps + 1) * 8 + 4 <= 256, "barriers");
 
   // from a shuffle, so that the roles' branches are known to be uniform: without
   // it the whole kernel took a fifth longer
@@ -191,13 +205,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < S::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < ACCS * S::kBufs; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), kEpiWarps);  // the half's four warps of both CTAs
+      mbar_init(smem_u32(&tempty[i]), 2 * kEpiWarps / ACCS);  // the accumulator's warps in both CTAs
     }
     mbar_init(smem_u32(done), 1);
     for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(&rfull[i]), 1);
@@ -208,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (args.res) tma_prefetch_map(&tmRes);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), 2 * kPairCols);
+    tmem_alloc_pair(smem_u32(tmem_slot), ACCS * S::kBufs * kAccCols);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -228,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
         const int m0 = (2 * (tile / args.n_tiles) + static_cast<int>(rank)) * kPairRows;
-        const int n0 = tile % args.n_tiles * kPairCols + static_cast<int>(rank) * (kHalfCols / 2);
+        const int n0 = tile % args.n_tiles * S::kCols + static_cast<int>(rank) * (kAccCols / 2);
         for (int kb = 0; kb < args.kblocks; ++kb) {
           if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, args.err, tlim)) {
             ok = false;
@@ -236,12 +250,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           const uint32_t fb_local = smem_u32(&full[stage]);
           const uint32_t fb = mapa_shared(fb_local, 0);
-          if (leader) mbar_arrive_expect_tx(fb_local, 2 * kPairStageBytes);
-          const uint32_t dst = smem_u32(smem + stage * kPairStageBytes);
+          if (leader) mbar_arrive_expect_tx(fb_local, 2 * S::kStageBytes);
+          const uint32_t dst = smem_u32(smem + stage * S::kStageBytes);
           tma_load_2d_pair(dst, &tmA, fb, kb * kKBytes, m0);
-          tma_load_2d_pair(dst + kPairABytes, &tmB, fb, kb * kKBytes, n0);
-          tma_load_2d_pair(dst + kPairABytes + kPairBBytes / 2, &tmB, fb, kb * kKBytes, n0 + kHalfCols);
-          if (++stage == kPairStages) {
+#pragma unroll
+          for (int h = 0; h < ACCS; ++h)
+            tma_load_2d_pair(dst + S::kABytes + h * S::kBBytes, &tmB, fb, kb * kKBytes, n0 + h * kAccCols);
+          if (++stage == S::kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -250,31 +265,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok && leader) {
         // copies of both CTAs complete on the even CTA's barriers; let the
         // armed ones land (200 ms each at most) before the pair winds down
-        for (int s = 0; s < kPairStages; ++s)
+        for (int s = 0; s < S::kStages; ++s)
           (void)mbar_wait(smem_u32(&full[s]), (s < stage) ? phase : (phase ^ 1u), args.err, 200000000ull);
       }
     }
   } else if (warp == 1) {
     // ----------------------------------------- MMA issuer (even CTA only) --
     if (leader) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kPairRows, kHalfCols);
+      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kPairRows, kAccCols);
       int stage = 0;
       uint32_t phase = 0;
       int buf = 0;
       uint32_t buf_phase = 0;
       bool ok = true;
       const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t b_desc0 = sdesc_sw128(smem_u32(smem + kPairABytes), 16, 1024);
+      const uint64_t b_desc0 = sdesc_sw128(smem_u32(smem + S::kABytes), 16, 1024);
       for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
         for (int kb = 0; ok && kb < args.kblocks; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, args.err, tlim))) {
             ok = false;
             break;
           }
-          const uint64_t off = static_cast<uint64_t>(stage) * (kPairStageBytes >> 4);
+          const uint64_t off = static_cast<uint64_t>(stage) * (S::kStageBytes >> 4);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int acc = 2 * h + buf;
+          for (int h = 0; h < ACCS; ++h) {
+            const int acc = h * S::kBufs + buf;
             if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc]), buf_phase ^ 1u, args.err, tlim)))
               ok = false;
             if (ok) {
@@ -282,20 +297,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // 32 channels, 32 bytes on inside the swizzle row
-                  mma_f8_pair(tmem_base + acc * kHalfCols, a_desc0 + off + 2 * k,
-                              b_desc0 + off + h * (kPairBBytes / 2 >> 4) + 2 * k, idesc, k != 0 ? 1u : 0u);
+                  mma_f8_pair(tmem_base + acc * kAccCols, a_desc0 + off + 2 * k,
+                              b_desc0 + off + h * (S::kBBytes >> 4) + 2 * k, idesc, k != 0 ? 1u : 0u);
                 mma_commit_pair_both(smem_u32(&tfull[acc]));
-                if (h == 1) mma_commit_pair_both(smem_u32(&empty[stage]));
+                if (h == ACCS - 1) mma_commit_pair_both(smem_u32(&empty[stage]));
               }
               __syncwarp();
             }
           }
-          if (++stage == kPairStages) {
+          if (++stage == S::kStages) {
             stage = 0;
             phase ^= 1u;
           }
-          buf ^= 1;
-          buf_phase ^= buf == 0 ? 1u : 0u;
+          if (++buf == S::kBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
         }
       }
       // no MMA may still be running when tensor memory is released
@@ -308,13 +325,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quarter = warp & 3;  // tensor memory lanes this warp may read
     const int half = (warp - 4) >> 2;
-    uint8_t* stage_out = s_out + (warp - 4) * kStageOutBytes;
+    uint8_t* stage_out = s_out + (warp - 4) * S::kOutBytes;
     const uint32_t rbar = smem_u32(&rfull[warp - 4]);
     uint32_t rphase = 0;
-    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 2 * kHalfCols;
-    const uint32_t tfull0 = smem_u32(&tfull[2 * half]);
-    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[2 * half]), 0);
-    uint32_t it = 0;  // blocks of K so far: buffer it & 1, its phase (it >> 1) & 1
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 
+                           (ACCS == 2 ? half * S::kBufs * kAccCols : half * S::kEpiCols);
+    const int first_buf = ACCS == 2 ? half * S::kBufs : 0;
+    const uint32_t tfull0 = smem_u32(&tfull[first_buf]);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[first_buf]), 0);
+    uint32_t it = 0;  // blocks of K so far: buffer it % kBufs, its phase it / kBufs & 1
     bool ready = false;
     bool ok = true;
     // The scales come in fours and a group ahead, and are multiplied when their
@@ -324,10 +343,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     float4 ahead_a, ahead_w;
     auto scales_of = [&](int tile, int mt, int nt) {
       const int m = (2 * mt + static_cast<int>(rank)) * kPairRows + quarter * 32 + lane;
-      const int nb = 2 * nt + half;
-      row_on = tile < args.tiles && m < args.m && nb * kHalfCols < args.n;
+      const int n = nt * S::kCols + half * S::kEpiCols;
+      row_on = tile < args.tiles && m < args.m && n < args.n;
       row_scales = args.sa + static_cast<long long>(row_on ? m : 0) * args.kblocks;
-      col_scales = args.sw + static_cast<long long>(row_on ? nb : 0) * args.kblocks;
+      col_scales = args.sw + static_cast<long long>(row_on ? n / kScaleBlock : 0) * args.kblocks;
     };
     auto load_ahead = [&](int kb) {
       ahead_a = load_scales(row_scales, kb, args.kblocks, row_on);
@@ -339,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     load_ahead(0);
     for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
       const int m0 = (2 * mt + static_cast<int>(rank)) * kPairRows + quarter * 32;
-      const int n0 = nt * kPairCols + half * kEpiCols;
+      const int n0 = nt * S::kCols + half * S::kEpiCols;
       const bool any = m0 < args.m && n0 < args.n;  // uniform
       mt += mt_step;
       nt += nt_step;
@@ -347,9 +366,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         nt -= args.n_tiles;
         ++mt;
       }
-      f32x2 acc[kEpiCols / 2];
+      f32x2 acc[S::kEpiCols / 2];
 #pragma unroll
-      for (int j = 0; j < kEpiCols / 8; ++j) {
+      for (int j = 0; j < S::kEpiCols / 8; ++j) {
         const bool on = args.bias && n0 + 8 * j < args.n;
         const Vec8 t = unpack8(on ? __ldg(args.bias + (n0 >> 3) + j) : make_uint4(0, 0, 0, 0));
 #pragma unroll
@@ -367,9 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             load_ahead(0);
           }
         }
-        const uint32_t buf = it & 1;
+        const uint32_t buf = it % S::kBufs;
         if (!__all_sync(0xffffffffu, ready) &&
-            !__all_sync(0xffffffffu, mbar_wait(tfull0 + buf * 8, (it >> 1) & 1, args.err, tlim))) {
+            !__all_sync(0xffffffffu, mbar_wait(tfull0 + buf * 8, it / S::kBufs & 1, args.err, tlim))) {
           ok = false;
           break;
         }
@@ -377,18 +396,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const f32x2 ss = pair(now.x, now.x);
         now = make_float4(now.y, now.z, now.w, 0.f);
-        const uint32_t from = tbase + buf * kHalfCols;
-        add_sums64(from, acc, ss);
-        ready = add_sums64_release(from + 64, acc + 32, ss, tempty0 + buf * 8, lane == 0, tfull0 + (it & 1) * 8,
-                                   (it >> 1) & 1);
+        const uint32_t from = tbase + buf * kAccCols;
+        if (ACCS == 2) add_sums64(from, acc, ss);
+        constexpr int kLast = S::kEpiCols - 64;
+        ready = add_sums64_release(from + kLast, acc + kLast / 2, ss, tempty0 + buf * 8, lane == 0,
+                                   tfull0 + it % S::kBufs * 8, it / S::kBufs & 1);
         if (kb == 0 && args.res && any) {
           // the residual's piece, into staging rows that the previous tile's
           // stores have read by now (at the tile's start they had not)
           if (lane == 0) {
             bulk_wait_read_all();
-            mbar_arrive_expect_tx(rbar, kStageOutBytes);
-            tma_load_2d(smem_u32(stage_out), &tmRes, rbar, n0, m0);
-            tma_load_2d(smem_u32(stage_out + kStageOutBytes / 2), &tmRes, rbar, n0 + 64, m0);
+            mbar_arrive_expect_tx(rbar, S::kOutBytes);
+#pragma unroll
+            for (int g = 0; g < S::kPieces; ++g)
+              tma_load_2d(smem_u32(stage_out + g * S::kPieceBytes), &tmRes, rbar, n0 + 64 * g, m0);
           }
           __syncwarp();
         }
@@ -405,8 +426,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok) break;
       // 64 columns at a time, all loads in front of the first store
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint8_t* row = stage_out + g * (kStageOutBytes / 2) + lane * 128;
+      for (int g = 0; g < S::kPieces; ++g) {
+        uint8_t* row = stage_out + g * S::kPieceBytes + lane * 128;
         if (args.res) {
           uint4 extra[8];
 #pragma unroll
@@ -429,8 +450,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_2d(&tmOut, smem_u32(stage_out), n0, m0);
-        if (n0 + 64 < args.n) tma_store_2d(&tmOut, smem_u32(stage_out + kStageOutBytes / 2), n0 + 64, m0);
+#pragma unroll
+        for (int g = 0; g < S::kPieces; ++g)
+          if (n0 + 64 * g < args.n) tma_store_2d(&tmOut, smem_u32(stage_out + g * S::kPieceBytes), n0 + 64 * g, m0);
         bulk_commit();
       }
       __syncwarp();
@@ -444,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();  // the peer no longer reads this CTA's shared memory or signals its barriers
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, 2 * kPairCols);
+    tmem_dealloc_pair(tmem_base, ACCS * S::kBufs * kAccCols);
   }
 }
 
@@ -454,12 +476,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // its N side, so a call with one row moves the weights and wastes nothing but
 // tensor core time. K is split over the CTAs of a cluster, whose partial sums
 // meet in shared memory, in rank order: the weights stream through all SMs
-// although there are few output tiles. One row x 4096 x 4096: 5.6 us (3 TB/s,
-// of which half is the launch and the exchange); 64 rows: 8.3 us.
+// although there are few output tiles. One row x 4096 x 4096: 5.5 us (3 TB/s,
+// of which half is the launch and the exchange); 64 rows: 7.3 us.
 constexpr int kFewThreads = 192;
 constexpr int kFewMax = 64;       // rows
 constexpr int kFewScales = 4096;  // staged scales of a: MT x blocks of K per CTA
 constexpr int kFewStages = 6;
+constexpr int kFewRanks = 8;      // CTAs in a cluster
+
+// Shared memory of a CTA with kb_split blocks of K: stages, over which the
+// partial sums go when all are used up, and the scales.
+int few_smem(int mt, int kb_split) {
+  return 1024 + std::max(std::min(kFewStages, kb_split) * (128 + mt) * kKBytes, mt * 128 * 4) + mt * kb_split * 4 + 256;
+}
+constexpr int kMaxSmemOfTwo = 112 * 1024;  // of each of two CTAs on an SM
 
 template <int MT>
 struct FewShape {
@@ -468,13 +498,10 @@ struct FewShape {
   static constexpr int kStageBytes = kWBytes + kABytes;
   static constexpr uint32_t kTmemCols = 2 * MT;
   static constexpr int kPartBytes = MT * 128 * 4;  // partial sums, over the stages when all are used up
-  static int smem(int stages, int scales) {
-    return 1024 + std::max(stages * kStageBytes, kPartBytes) + scales * 4 + 256;
-  }
 };
 
 template <int MT>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 2)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ Fp8GemmArgs args, const int stages) {
   using S = FewShape<MT>;
@@ -603,19 +630,19 @@ __global__ void __launch_bounds__(kFewThreads)
         break;
       }
       tc_fence_after();
+      uint32_t r[MT / 16][16];  // all loads in front of the first wait
 #pragma unroll
-      for (int c = 0; c < MT; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tbase + buf * MT + c, r);
-        tmem_wait16(r);
-        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(ssa + kb * MT + c);
+      for (int i = 0; i < MT / 16; ++i) tmem_ld16(tbase + buf * MT + 16 * i, r[i]);
+#pragma unroll
+      for (int i = 0; i < MT / 16; ++i) {
+        tmem_wait16(r[i]);
+        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(ssa + kb * MT + 16 * i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const ulonglong2 s = sc[j];
-          acc[c / 2 + 2 * j] = fma2(pair(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), s.x,
-                                    acc[c / 2 + 2 * j]);
-          acc[c / 2 + 2 * j + 1] = fma2(pair(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), s.y,
-                                        acc[c / 2 + 2 * j + 1]);
+          f32x2* to = acc + 8 * i + 2 * j;
+          to[0] = fma2(pair(__uint_as_float(r[i][4 * j]), __uint_as_float(r[i][4 * j + 1])), s.x, to[0]);
+          to[1] = fma2(pair(__uint_as_float(r[i][4 * j + 2]), __uint_as_float(r[i][4 * j + 3])), s.y, to[1]);
         }
       }
       tc_fence_before();
@@ -627,6 +654,11 @@ __global__ void __launch_bounds__(kFewThreads)
   // the partial sums (the MMA warp waited for `done`)
   tc_fence_before();
   __syncthreads();
+  if (warp == 1) {
+    // before this CTA waits for others: what holds tensor memory then waits for nobody
+    tc_fence_after();
+    tmem_dealloc(tmem_base, S::kTmemCols);
+  }
   if (warp >= 2) {
     const int n = (warp & 3) * 32 + lane;
 #pragma unroll
@@ -645,12 +677,17 @@ __global__ void __launch_bounds__(kFewThreads)
     const int n = nt * 128 + c;
     if (m < args.m && n < args.n) {
       const uint32_t at = smem_u32(part + m * 128 + c);
+      float2 of[kFewRanks];  // all trips to the other CTAs at once
+#pragma unroll
+      for (uint32_t k = 0; k < kFewRanks; ++k)
+        if (k < ranks) of[k] = ld_cluster_f2(mapa_shared(at, k));
       float2 v = make_float2(0.f, 0.f);
-      for (uint32_t k = 0; k < ranks; ++k) {
-        float2 t;
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(t.x), "=f"(t.y) : "r"(mapa_shared(at, k)));
-        v.x += t.x;
-        v.y += t.y;
+#pragma unroll
+      for (uint32_t k = 0; k < kFewRanks; ++k) {
+        if (k < ranks) {
+          v.x += of[k].x;
+          v.y += of[k].y;
+        }
       }
       if (args.bias) {
         const float2 t = __bfloat1622float2(__ldg(reinterpret_cast<const __nv_bfloat162*>(args.bias) + (n >> 1)));
@@ -667,10 +704,6 @@ __global__ void __launch_bounds__(kFewThreads)
   }
   __syncwarp();
   cluster_sync_all();  // the peers have read this CTA's partial sums
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, S::kTmemCols);
-  }
 }
 
 // -------------------------------------------------------------------- launch --
@@ -684,10 +717,10 @@ cc_status launch_few(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const
   if ((st = encode_tiled_2d_u8(&ta, a, k, args.m, k, kKBytes, MT)) != CC_OK) return st;
   if ((st = encode_tiled_2d_u8(&tw, wq, k, args.n, k, kKBytes, 128)) != CC_OK) return st;
   const int stages = std::min(kFewStages, args.kb_split);
-  const int smem = S::smem(stages, MT * args.kb_split);
+  const int smem = few_smem(MT, args.kb_split);
   auto kern = fp8_few_kernel<MT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       S::smem(kFewStages, kFewScales));
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(MT, kFewScales / MT));
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(((args.n - 1) / 128 + 1) * ranks);
@@ -707,23 +740,25 @@ cc_status launch_few(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const
   return launch_status(what);
 }
 
+template <int ACCS>
 cc_status launch_pair(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const cc_fp8* wq, int k, int sms,
                       cudaStream_t stream) {
+  using S = PairShape<ACCS>;
   CUtensorMap ta, tb, to, tr;
   cc_status st;
   if ((st = encode_tiled_2d_u8(&ta, a, k, args.m, k, kKBytes, kPairRows)) != CC_OK) return st;
-  if ((st = encode_tiled_2d_u8(&tb, wq, k, args.n, k, kKBytes, kHalfCols / 2)) != CC_OK) return st;
+  if ((st = encode_tiled_2d_u8(&tb, wq, k, args.n, k, kKBytes, kAccCols / 2)) != CC_OK) return st;
   if ((st = encode_tiled_2d(&to, args.out, args.n, args.m, args.ld_out * 2, 64, 32)) != CC_OK) return st;
   tr = to;
   if (args.res && (st = encode_tiled_2d(&tr, args.res, args.n, args.m, args.ld_res * 2, 64, 32)) != CC_OK) return st;
   const long long m_tiles = (args.m - 1) / (2 * kPairRows) + 1;
-  args.n_tiles = (args.n - 1) / kPairCols + 1;
+  args.n_tiles = (args.n - 1) / S::kCols + 1;
   if (m_tiles * args.n_tiles > 0x7fffffffLL - 1024) return fail(CC_ERR_UNSUPPORTED, "%s: too many output tiles", what);
   args.tiles = static_cast<int>(m_tiles * args.n_tiles);
-  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<ACCS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
-  e = launch_pdl(fp8_pair_kernel, dim3(2 * std::min(args.tiles, sms / 2)), dim3(kPairThreads), kPairSmem, stream, ta,
-                 tb, tr, to, args);
+  e = launch_pdl(fp8_pair_kernel<ACCS>, dim3(2 * std::min(args.tiles, sms / 2)), dim3(kPairThreads), S::kSmem, stream,
+                 ta, tb, tr, to, args);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
 }
@@ -767,19 +802,41 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   args.timeout_ns = kWaitLimitNs;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  // Few rows: one N-side tile of the tensor core. At 64 rows x 4096 x 4096 it
-  // takes 8.3 us against the pairs' 14; with 128 rows it would take 24.
+  // Few rows: one N-side tile of the tensor core, K over the CTAs of a cluster
+  // while all of them run at once (one to an SM, or two where they are small;
+  // clusters of eight do not fill all SMs). Beyond that a second round costs more
+  // than the split saves: 64 x 4096 x 16384 takes 18 us on four CTAs each, 29 on
+  // eight; 1 x 4096 x 16384 with two to an SM 14.7 on four, 13.7 on eight. 64 x
+  // 4096 x 4096 takes 7.3 us, on pairs 11; 128 rows take longer than on pairs.
   if (m <= kFewMax) {
     const int mt = m <= 16 ? 16 : m <= 32 ? 32 : 64;
-    const int n_tiles = (n - 1) / 128 + 1;
+    const long long n_tiles = (n - 1) / 128 + 1;
     int ranks = 1;
-    while (ranks < 8 && 2 * ranks <= args.kblocks && static_cast<long long>(n_tiles) * ranks < di.sm_count) ranks *= 2;
-    args.kb_split = (args.kblocks - 1) / ranks + 1;
-    if (static_cast<long long>(mt) * args.kb_split <= kFewScales) {
+    auto split = [&](int r) { return (args.kblocks - 1) / r + 1; };
+    auto fits = [&](int r) { return static_cast<long long>(mt) * split(r) <= kFewScales; };
+    while (ranks < kFewRanks && 2 * ranks <= args.kblocks) {
+      const int next = 2 * ranks;
+      const bool two = mt < 64 && fits(next) && few_smem(mt, split(next)) <= kMaxSmemOfTwo;
+      if (fits(ranks) && n_tiles * next > (two ? 2 : 1) * di.sm_count - 4 * next) break;
+      ranks = next;
+    }
+    args.kb_split = split(ranks);
+    if (fits(ranks)) {
       if (mt == 16) return launch_few<16>(what, args, a, wq, k, ranks, s);
       if (mt == 32) return launch_few<32>(what, args, a, wq, k, ranks, s);
       return launch_few<64>(what, args, a, wq, k, ranks, s);
     }
   }
-  return launch_pair(what, args, a, wq, k, di.sm_count, s);
+  // Tiles of 256 columns or of 128: rounds of tiles times what a tile takes, in
+  // hundredths of a microsecond a block of K and at its end. In us, wide / narrow:
+  // 128 x 4096 x 4096 14.8 / 10.9, 100000 x 128 x 512 20.8 / 17.6 (one round
+  // either way, half the columns), 1546 x 3184 x 1264 13.7 / 12.8 (two and three
+  // rounds); 1024 x 4096 x 4096 16.4 / 19.9, 13728 x 1024 x 1024 16.9 / 19.2.
+  const long long pairs = di.sm_count / 2, m_tiles = (m - 1) / (2 * kPairRows) + 1;
+  auto cost = [&](long long cols, long long block, long long end) {
+    return ((m_tiles * ((n - 1) / cols + 1) - 1) / pairs + 1) * (args.kblocks * block + end);
+  };
+  if (cost(PairShape<1>::kCols, 25, 50) < cost(PairShape<2>::kCols, 36, 100))
+    return launch_pair<1>(what, args, a, wq, k, di.sm_count, s);
+  return launch_pair<2>(what, args, a, wq, k, di.sm_count, s);
 }

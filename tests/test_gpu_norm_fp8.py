@@ -424,6 +424,17 @@ def test_gemm_walks_many_tiles_and_blocks(m, n, k):
         assert torch.equal(gemm(a, sa, wq, sw, bias, res), first)  # the sums' order is fixed
 
 
+@pytest.mark.parametrize("m,n,k", [
+    (2300, 1800, 656), (2200, 1800, 1040), (40000, 504, 400),  # tiles of 256 columns
+    (4097, 1096, 144), (2310, 2040, 1040), (66, 136, 4096), (300, 200, 272),  # of 128
+    (700, 1000, 2064), (20000, 72, 144), (65, 8, 16),
+    (64, 12296, 272), (33, 8200, 1040), (50, 4104, 2064), (64, 1032, 4112), (17, 4096, 4112), (3, 4104, 1040),  # splits of K
+])
+def test_gemm_on_both_sides_of_the_choice_of_tiles(m, n, k):
+    test_gemm_matches_64_bits(m, n, k, "both")
+    test_gemm_matches_64_bits(m, n, k, "none")
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_gemm_with_strided_rows(m):
     # out and res as column slices of wider rows (packed q, k, v)
