@@ -583,16 +583,17 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
   while (g.ranks < kMaxRanks && (g.smem > kHalf || (g.units * g.ranks < 152 && g.rounds > 2))) cut(g.ranks * 2, 256);
   // Where the SMs hold one CTA of a cluster each, fifteen clusters of eight run
   // at a time (the sixteenth waits for the first) and nothing fills their waits,
-  // and up to four clusters leave most SMs idle: two readings by all SMs are
-  // faster once there is enough to read.
+  // and few clusters leave SMs idle: two readings by all SMs are faster once there
+  // is enough to read.
   // Clusters against two readings in us (silu):
   //   16 x 12800 x 512, 32 groups   136 / 108   (16 x 7000, two CTAs to an SM: 60 / 64)
   //   16 x 11520 x 64, 2 groups    28.0 / 20.7  (15 instances:              16.1 / 18.5)
   //   1 x 5632 x 64, 2 groups, 22 rounds   8.5 / 7.2   (3840, 15 rounds:      7.2 / 7.2)
-  //   4 x 3240 x 208, 1 group, 45 rounds  12.4 / 10.4  (8 instances:         12.5 / 12.4)
+  //   4 x 3240 x 208, 1 group, 45 rounds  12.4 / 9.4   (2160, 30 rounds:     10.1 / 8.7)
+  //   8 x 3240 x 208                      12.5 / 11.3  (2160:               10.3 / 11.6)
   // (Clusters of 16 CTAs lie between: 3 x 3234 x 168 e4m3 18.5 with 8, 12.9 with
   // 16, 12.5 with two readings; 4 x 17253 x 112 22.7 with 16, 13.4.)
-  g.cluster = g.smem <= kMaxSmem && !(g.smem > kHalf && g.units > 15) && !(g.units <= 4 && g.rounds > 20);
+  g.cluster = g.smem <= kMaxSmem && !(g.smem > kHalf && g.units > 15) && g.rounds <= 5 * std::max(4LL, g.units);
   if (g.cluster) {
     // 512 threads where each still has eight vectors and only one partial sum
     // to hand over: 4 x 3432 x 1024 (32 groups) takes 12.8 us against 13.5 with
@@ -614,14 +615,15 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8) {
   // 1.0-1.1 ms.) What is not worth 1.5 rounds of the CTAs that run at a time is
   // cut so that the last round is full, at about four vectors' time for a CTA's
   // start and end: 2 x 21996 x 648 e4m3 57.2 -> 47.7 us, 7 x 14000 x 320 46.8 ->
-  // 38.2; from there on it gains nothing (3 x 50000 x 840 148 -> 151).
+  // 38.2; from there on it gains nothing (3 x 50000 x 840 148 -> 151). Runs of at
+  // least four: 1 x 6192 x 624 e4m3 15.2 us with eight, 13.2 with four, 13.1 with two.
   const int lanes = g.threads / (c / 8);
   const int per = (p - 1) / lanes + 1;
   const int at_once = 608 * 256 / g.threads;  // four CTAs of 256 threads to an SM
   int run = 32;
   if (static_cast<long long>(n) * per < 48LL * at_once) {
     int best = INT_MAX;
-    for (int r = 8; r <= 40; ++r) {
+    for (int r = 4; r <= 40; ++r) {
       const int cost = ((n * ((per - 1) / r + 1) - 1) / at_once + 1) * (r + 4);
       if (cost < best) best = cost, run = r;
     }
