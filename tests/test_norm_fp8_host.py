@@ -58,7 +58,7 @@ def test_group_norm_workspace(lib, p):
     assert lib.cc_group_norm_workspace_bytes(2, 0, 64, 8) == 0
     assert lib.cc_group_norm_workspace_bytes(-1, 5, 64, 8) == 0
     # clusters of CTAs keep the slabs, and need none ...
-    for shape in ((2, 96, 64, 32), (4, 3432, 1024, 32), (5, 3400, 64, 2), (1, 2400, 64, 2)):
+    for shape in ((2, 96, 64, 32), (4, 3432, 1024, 32), (5, 2000, 64, 2), (1, 2000, 64, 2)):
         assert lib.cc_group_norm_workspace_bytes(*shape) == 0, shape
     # ... and two readings take slabs that are too large, or few and long
     for shape in ((2, 30001, 64, 4), (16, 9000, 64, 2), (1, 5700, 64, 2), (1, 353, 792, 1)):
