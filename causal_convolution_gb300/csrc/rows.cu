@@ -62,6 +62,16 @@ __device__ __forceinline__ f32x2 sum_squares(const uint4& raw, f32x2 sum) {
   return sum;
 }
 
+// 1 / sqrt(mean of squares + eps). The reciprocal root in one instruction (two
+// steps of 2^-24 off) saves e4m3 outputs 3-9 % (300000 x 128 35.8 -> 33.9 us,
+// 94467 x 160 23.3 -> 21.4); with it the bf16 kernel gets its registers dealt
+// worse (439296 x 512 145 -> 178), so that one divides.
+template <bool FP8>
+__device__ __forceinline__ float norm_factor(float sum, const RowArgs& a) {
+  const float v = fmaf(sum, a.inv_c, a.eps);
+  return FP8 ? rsqrtf(v) : 1.f / sqrtf(v);
+}
+
 // CTAs of a row kernel to an SM: three with 80 registers a thread, or four with
 // 64 and a few of them spilled. In us with three / with four: norm of
 // 439296 x 512 to bf16 149 / 145, to e4m3 (100000 rows) 35 / 38; with four
@@ -131,7 +141,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas<V, NORM, FP8>()) row_ker
         for (int j = 0; j < R; ++j) rs[j] += __shfl_xor_sync(0xffffffffu, rs[j], o);
       }
 #pragma unroll
-      for (int j = 0; j < R; ++j) rs[j] = 1.f / sqrtf(fmaf(rs[j], a.inv_c, a.eps));
+      for (int j = 0; j < R; ++j) rs[j] = norm_factor<FP8>(rs[j], a);
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(kMaxRowChannels / 32) long_row_kernel(const __
     __syncthreads();  // one per row: the two halves of `red` take turns
     rs = 0.f;
     for (int i = 0; i < blockDim.x / 32; ++i) rs += red[turn][i];
-    rs = 1.f / sqrtf(fmaf(rs, a.inv_c, a.eps));
+    rs = norm_factor<FP8>(rs, a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i * static_cast<int>(blockDim.x) >= a.vecs) break;
