@@ -62,8 +62,8 @@ __device__ __forceinline__ f32x2 sum_squares(const uint4& raw, f32x2 sum) {
   return sum;
 }
 
-// 1 / sqrt(mean of squares + eps). The reciprocal root in one instruction (two
-// steps of 2^-24 off) saves e4m3 outputs 3-9 % (300000 x 128 35.8 -> 33.9 us,
+// 1 / sqrt(mean of squares + eps). The reciprocal root (off by at most two units in
+// the last place) saves e4m3 outputs 3-9 % (300000 x 128 35.8 -> 33.9 us,
 // 94467 x 160 23.3 -> 21.4); with it the bf16 kernel gets its registers dealt
 // worse (439296 x 512 145 -> 178), so that one divides.
 template <bool FP8>

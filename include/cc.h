@@ -354,9 +354,10 @@ typedef enum cc_act { CC_ACT_NONE = 0, CC_ACT_SILU = 1 } cc_act;
  * values; one with an infinity gets an infinite scale, zeros for its finite
  * values and NaN for the infinite ones. */
 
-/* Bytes of workspace a group norm of these sizes needs (0 for empty or
- * invalid sizes). The contents need no preparation and nothing in them is
- * kept between calls; calls whose GPU work overlaps need one each. */
+/* Bytes of workspace a group norm of these sizes needs, for either output (0
+ * where the SMs keep all of x, and for empty or invalid sizes). The contents need
+ * no preparation and nothing in them is kept between calls; calls whose GPU work
+ * overlaps need one each. */
 size_t cc_group_norm_workspace_bytes(int n, int p, int c, int groups);
 
 /* Group norm of N instances (frames, for a causal decoder) of P positions,
