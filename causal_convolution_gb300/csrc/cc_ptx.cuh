@@ -374,6 +374,14 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 // Arrive on an mbarrier of a CTA in this cluster (default CTA-scope release:
 // the arrive only has to publish this thread's tcgen05 reads, which the
@@ -488,9 +496,9 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
 }
 
 // Arrive on the barrier at this shared offset in both CTAs of the pair once
-// the issuing thread's tcgen05 ops are done.
-__device__ __forceinline__ void mma_commit_pair_both(uint32_t bar) {
-  const uint16_t mask = 0x3;
+// the issuing thread's tcgen05 ops are done. `mask`: the pair's ranks in the
+// cluster.
+__device__ __forceinline__ void mma_commit_pair_both(uint32_t bar, uint16_t mask = 0x3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"(mask)

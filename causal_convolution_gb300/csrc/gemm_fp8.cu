@@ -31,7 +31,7 @@ struct Fp8GemmArgs {
   cc_bf16* out;
   int m, n, kblocks;
   int n_tiles, tiles;   // pair kernel
-  int kb_split;         // few-rows kernel: blocks of K per CTA
+  int kb_split;         // blocks of K per CTA (few rows) or pair (split tiles)
   long long ld_res, ld_out;
   unsigned int* err;
   unsigned long long timeout_ns;
@@ -63,6 +63,10 @@ constexpr int kKBytes = 128;  // bytes of K per stage: one scale block, one swiz
 // the narrow tile takes 480 cycles of 384 that its 24 KB a CTA take to arrive.
 // (As two accumulators of 64 columns it took 580: an MMA with 64 columns takes as
 // long as one with 128.)
+//
+// SPLITS: where there are few tiles, a cluster of two or four pairs takes a narrow
+// one, each pair a run of blocks of K. The pairs' sums meet in shared memory and
+// are added in the pairs' order, so results do not change from run to run.
 constexpr int kPairRows = 128;     // of A, per CTA
 constexpr int kAccCols = 128;      // of an accumulator; each CTA loads 64 of its weight rows
 constexpr int kEpiWarps = 8;       // one per half of the tile's columns and quarter of the rows
@@ -178,12 +182,13 @@ __device__ __forceinline__ float4 load_scales(const float* p, int kb, int kblock
   return v;
 }
 
-template <int ACCS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+template <int ACCS, int SPLITS>
+__global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmRes, const __grid_constant__ CUtensorMap tmOut,
                     const __grid_constant__ Fp8GemmArgs args) {
   using S = PairShape<ACCS>;
+  constexpr bool SPLIT = SPLITS > 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_out = smem + S::kStages * S::kStageBytes;
@@ -194,15 +199,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint64_t* rfull = tempty + ACCS * S::kBufs;  // [kEpiWarps] residual pieces
   uint64_t* done = rfull + kEpiWarps;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  // split: 128 rows of partial sums, padded so that a warp's stores do not collide
+  constexpr int kPartRow = S::kCols + 4;
+  static_assert(!SPLIT || (ACCS == 1 && kPairRows * kPartRow * 4 <= S::kStages * S::kStageBytes), "partial sums");
+  float* part = reinterpret_cast<float*>(smem);
 
   // from a shuffle, so that the roles' branches are known to be uniform: without
   // it the whole kernel took a fifth longer
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t cluster_rank = cluster_ctarank();
+  const uint32_t rank = SPLIT ? cluster_rank & 1 : cluster_rank;  // in the pair
+  const uint32_t even = cluster_rank - rank;                       // the pair's first CTA
+  const uint16_t both = static_cast<uint16_t>(0x3 << even);
   const bool leader = rank == 0;
-  const int pair_id = blockIdx.x >> 1;
-  const int pairs = gridDim.x >> 1;
+  // split: a cluster for each tile, kbs blocks of K from kb0 for this pair. (Whole
+  // tiles read args.kblocks where they use it: kept in a register it cost 1 %.)
+  const int pair_id = SPLIT ? blockIdx.x / (2 * SPLITS) : blockIdx.x >> 1;
+  const int pairs = SPLIT ? args.tiles : gridDim.x >> 1;
+  const int kb0 = SPLIT ? static_cast<int>(cluster_rank >> 1) * args.kb_split : 0;
+  const int kbs = SPLIT ? max(0, min(args.kb_split, args.kblocks - kb0)) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -243,19 +259,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
         const int m0 = (2 * (tile / args.n_tiles) + static_cast<int>(rank)) * kPairRows;
         const int n0 = tile % args.n_tiles * S::kCols + static_cast<int>(rank) * (kAccCols / 2);
-        for (int kb = 0; kb < args.kblocks; ++kb) {
+        for (int kb = 0; kb < (SPLIT ? kbs : args.kblocks); ++kb) {
           if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, args.err, tlim)) {
             ok = false;
             break;
           }
           const uint32_t fb_local = smem_u32(&full[stage]);
-          const uint32_t fb = mapa_shared(fb_local, 0);
+          const uint32_t fb = mapa_shared(fb_local, even);
           if (leader) mbar_arrive_expect_tx(fb_local, 2 * S::kStageBytes);
           const uint32_t dst = smem_u32(smem + stage * S::kStageBytes);
-          tma_load_2d_pair(dst, &tmA, fb, kb * kKBytes, m0);
+          tma_load_2d_pair(dst, &tmA, fb, (kb0 + kb) * kKBytes, m0);
 #pragma unroll
           for (int h = 0; h < ACCS; ++h)
-            tma_load_2d_pair(dst + S::kABytes + h * S::kBBytes, &tmB, fb, kb * kKBytes, n0 + h * kAccCols);
+            tma_load_2d_pair(dst + S::kABytes + h * S::kBBytes, &tmB, fb, (kb0 + kb) * kKBytes, n0 + h * kAccCols);
           if (++stage == S::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -281,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t b_desc0 = sdesc_sw128(smem_u32(smem + S::kABytes), 16, 1024);
       for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
-        for (int kb = 0; ok && kb < args.kblocks; ++kb) {
+        for (int kb = 0; ok && kb < (SPLIT ? kbs : args.kblocks); ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, args.err, tlim))) {
             ok = false;
             break;
@@ -299,8 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int k = 0; k < 4; ++k)  // 32 channels, 32 bytes on inside the swizzle row
                   mma_f8_pair(tmem_base + acc * kAccCols, a_desc0 + off + 2 * k,
                               b_desc0 + off + h * (S::kBBytes >> 4) + 2 * k, idesc, k != 0 ? 1u : 0u);
-                mma_commit_pair_both(smem_u32(&tfull[acc]));
-                if (h == ACCS - 1) mma_commit_pair_both(smem_u32(&empty[stage]));
+                mma_commit_pair_both(smem_u32(&tfull[acc]), both);
+                if (h == ACCS - 1) mma_commit_pair_both(smem_u32(&empty[stage]), both);
               }
               __syncwarp();
             }
@@ -316,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       // no MMA may still be running when tensor memory is released
-      if (elect_one()) mma_commit_pair_both(smem_u32(done));
+      if (elect_one()) mma_commit_pair_both(smem_u32(done), both);
       __syncwarp();
       (void)mbar_wait(smem_u32(done), 0, args.err, tlim);
     }
@@ -332,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                            (ACCS == 2 ? half * S::kBufs * kAccCols : half * S::kEpiCols);
     const int first_buf = ACCS == 2 ? half * S::kBufs : 0;
     const uint32_t tfull0 = smem_u32(&tfull[first_buf]);
-    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[first_buf]), 0);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[first_buf]), even);
     uint32_t it = 0;  // blocks of K so far: buffer it % kBufs, its phase it / kBufs & 1
     bool ready = false;
     bool ok = true;
@@ -355,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int mt = pair_id / args.n_tiles, nt = pair_id % args.n_tiles;
     const int mt_step = pairs / args.n_tiles, nt_step = pairs % args.n_tiles;
     scales_of(pair_id, mt, nt);
-    load_ahead(0);
+    load_ahead(kb0);
     for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
       const int m0 = (2 * mt + static_cast<int>(rank)) * kPairRows + quarter * 32;
       const int n0 = nt * S::kCols + half * S::kEpiCols;
@@ -369,18 +385,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       f32x2 acc[S::kEpiCols / 2];
 #pragma unroll
       for (int j = 0; j < S::kEpiCols / 8; ++j) {
-        const bool on = args.bias && n0 + 8 * j < args.n;
+        const bool on = args.bias && kb0 == 0 && n0 + 8 * j < args.n;
         const Vec8 t = unpack8(on ? __ldg(args.bias + (n0 >> 3) + j) : make_uint4(0, 0, 0, 0));
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[4 * j + e] = t.p[e];
       }
       float4 now = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int kb = 0; kb < args.kblocks; ++kb) {
+      for (int kb = 0; kb < (SPLIT ? kbs : args.kblocks); ++kb) {
         if ((kb & 3) == 0) {
           now = make_float4(ahead_a.x * ahead_w.x, ahead_a.y * ahead_w.y, ahead_a.z * ahead_w.z, ahead_a.w * ahead_w.w);
-          if (kb + 4 < args.kblocks) {
-            load_ahead(kb + 4);
+          if (kb + 4 < (SPLIT ? kbs : args.kblocks)) {
+            load_ahead(kb0 + kb + 4);
           } else {
             scales_of(tile + pairs, mt, nt);
             load_ahead(0);
@@ -401,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         constexpr int kLast = S::kEpiCols - 64;
         ready = add_sums64_release(from + kLast, acc + kLast / 2, ss, tempty0 + buf * 8, lane == 0,
                                    tfull0 + it % S::kBufs * 8, it / S::kBufs & 1);
-        if (kb == 0 && args.res && any) {
+        if (!SPLIT && kb == 0 && args.res && any) {
           // the residual's piece, into staging rows that the previous tile's
           // stores have read by now (at the tile's start they had not)
           if (lane == 0) {
@@ -415,6 +431,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       __syncwarp();
+      if (SPLIT) {
+        // every MMA has read the stages: this pair's sums go over them
+        float* to = part + (quarter * 32 + lane) * kPartRow + half * S::kEpiCols;
+#pragma unroll
+        for (int j = 0; j < S::kEpiCols / 4; ++j)
+          *reinterpret_cast<ulonglong2*>(to + 4 * j) = make_ulonglong2(acc[2 * j], acc[2 * j + 1]);
+        break;
+      }
       if (!any) continue;
       if (args.res) {
         if (!__all_sync(0xffffffffu, mbar_wait(rbar, rphase, args.err, tlim))) ok = false;
@@ -459,11 +483,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
+    if (SPLIT) {
+      cluster_sync_all();
+      // each pair finishes its share of the tile's rows, a warp to a row, in the pairs' order
+      constexpr int share = kPairRows / SPLITS;
+      const int r0 = static_cast<int>(cluster_rank >> 1) * share;
+      const int m0 = (2 * (pair_id / args.n_tiles) + static_cast<int>(rank)) * kPairRows;
+      const int n = pair_id % args.n_tiles * S::kCols + lane * 4;
+#pragma unroll 4
+      for (int r = r0 + warp - 4; r < r0 + share; r += kEpiWarps) {
+        const int m = m0 + r;
+        if (m >= args.m || n >= args.n) continue;
+        const uint32_t at = smem_u32(part + r * kPartRow + lane * 4);
+        float4 of[SPLITS];
+#pragma unroll
+        for (uint32_t i = 0; i < SPLITS; ++i) of[i] = ld_cluster_f4(mapa_shared(at, 2 * i + rank));
+        float4 v = of[0];
+#pragma unroll
+        for (int i = 1; i < SPLITS; ++i) {
+          v.x += of[i].x;
+          v.y += of[i].y;
+          v.z += of[i].z;
+          v.w += of[i].w;
+        }
+        if (args.res) {
+          const uint2 t = *reinterpret_cast<const uint2*>(args.res + m * args.ld_res + n);
+          v.x += __uint_as_float(t.x << 16);
+          v.y += __uint_as_float(t.x & 0xffff0000u);
+          v.z += __uint_as_float(t.y << 16);
+          v.w += __uint_as_float(t.y & 0xffff0000u);
+        }
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(args.out + m * args.ld_out + n) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
+      __syncwarp();
+    }
+  }
+  if (SPLIT && warp < 4) {  // (in the branches: here the epilogue's registers are not all warps')
+    __syncwarp();
+    cluster_sync_all();
   }
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the peer no longer reads this CTA's shared memory or signals its barriers
+  cluster_sync_all();  // the peers no longer read this CTA's shared memory or signals its barriers
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, ACCS * S::kBufs * kAccCols);
@@ -708,6 +772,30 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 // -------------------------------------------------------------------- launch --
 
+// A launch in clusters of `cluster` CTAs that may begin before the previous one ends.
+template <typename... Args>
+cc_status launch_clusters(const char* what, void (*kern)(Args...), int grid, int cluster, int threads, int smem,
+                          int max_smem, cudaStream_t stream, const Args&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+  return launch_status(what);
+}
+
 template <int MT>
 cc_status launch_few(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const cc_fp8* wq, int k, int ranks,
                      cudaStream_t stream) {
@@ -718,29 +806,11 @@ cc_status launch_few(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const
   if ((st = encode_tiled_2d_u8(&tw, wq, k, args.n, k, kKBytes, 128)) != CC_OK) return st;
   const int stages = std::min(kFewStages, args.kb_split);
   const int smem = few_smem(MT, args.kb_split);
-  auto kern = fp8_few_kernel<MT>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(MT, kFewScales / MT));
-  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(((args.n - 1) / 128 + 1) * ranks);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, ta, tw, args, stages);
-  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
-  return launch_status(what);
+  return launch_clusters(what, fp8_few_kernel<MT>, ((args.n - 1) / 128 + 1) * ranks, ranks, kFewThreads, smem,
+                         few_smem(MT, kFewScales / MT), stream, ta, tw, args, stages);
 }
 
-template <int ACCS>
+template <int ACCS, int SPLITS>
 cc_status launch_pair(const char* what, Fp8GemmArgs& args, const cc_fp8* a, const cc_fp8* wq, int k, int sms,
                       cudaStream_t stream) {
   using S = PairShape<ACCS>;
@@ -755,12 +825,9 @@ cc_status launch_pair(const char* what, Fp8GemmArgs& args, const cc_fp8* a, cons
   args.n_tiles = (args.n - 1) / S::kCols + 1;
   if (m_tiles * args.n_tiles > 0x7fffffffLL - 1024) return fail(CC_ERR_UNSUPPORTED, "%s: too many output tiles", what);
   args.tiles = static_cast<int>(m_tiles * args.n_tiles);
-  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<ACCS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
-  e = launch_pdl(fp8_pair_kernel<ACCS>, dim3(2 * std::min(args.tiles, sms / 2)), dim3(kPairThreads), S::kSmem, stream,
-                 ta, tb, tr, to, args);
-  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
-  return launch_status(what);
+  return launch_clusters(what, fp8_pair_kernel<ACCS, SPLITS>,
+                         2 * (SPLITS > 1 ? args.tiles * SPLITS : std::min(args.tiles, sms / 2)), 2 * SPLITS,
+                         kPairThreads, S::kSmem, S::kSmem, stream, ta, tb, tr, to, args);
 }
 
 }  // namespace
@@ -807,7 +874,7 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   // clusters of eight do not fill all SMs). Beyond that a second round costs more
   // than the split saves: 64 x 4096 x 16384 takes 18 us on four CTAs each, 29 on
   // eight; 1 x 4096 x 16384 with two to an SM 14.7 on four, 13.7 on eight. 64 x
-  // 4096 x 4096 takes 7.3 us, on pairs 11; 128 rows take longer than on pairs.
+  // 4096 x 4096 takes 7.3 us, on pairs 9.7; 128 rows take longer than on pairs.
   if (m <= kFewMax) {
     const int mt = m <= 16 ? 16 : m <= 32 ? 32 : 64;
     const long long n_tiles = (n - 1) / 128 + 1;
@@ -833,10 +900,26 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   // either way, half the columns), 1546 x 3184 x 1264 13.7 / 12.8 (two and three
   // rounds); 1024 x 4096 x 4096 16.4 / 19.9, 13728 x 1024 x 1024 16.9 / 19.2.
   const long long pairs = di.sm_count / 2, m_tiles = (m - 1) / (2 * kPairRows) + 1;
-  auto cost = [&](long long cols, long long block, long long end) {
-    return ((m_tiles * ((n - 1) / cols + 1) - 1) / pairs + 1) * (args.kblocks * block + end);
+  auto tiles = [&](int cols) { return m_tiles * ((n - 1) / cols + 1); };
+  auto cost = [&](int cols, long long block, long long end) {
+    return ((tiles(cols) - 1) / pairs + 1) * (args.kblocks * block + end);
   };
-  if (cost(PairShape<1>::kCols, 25, 50) < cost(PairShape<2>::kCols, 36, 100))
-    return launch_pair<1>(what, args, a, wq, k, di.sm_count, s);
-  return launch_pair<2>(what, args, a, wq, k, di.sm_count, s);
+  const long long wide = cost(PairShape<2>::kCols, 36, 100), narrow = cost(PairShape<1>::kCols, 25, 50);
+  // Few narrow tiles: two or four pairs to each, while all clusters run at once
+  // (of eight CTAs fifteen); putting the sums together takes 2 us. 256 x 512 x
+  // 16384 takes 32.8 us whole, 19.4 on two and 12.4 on four pairs; 128 x 4096 x
+  // 4096 11.1 and 9.7; 128 x 1024 x 1024, eight blocks, 5.3 and 6.0.
+  long long best = std::min(wide, narrow);
+  int splits = 1;
+  for (int next = 2; next <= 4; next *= 2) {
+    const int blocks = ((args.kblocks - 1) / next + 4) / 4 * 4;  // the scales come in fours
+    if (tiles(PairShape<1>::kCols) * 2 * next > di.sm_count - 8 * next || blocks * 25 + 250 >= best) continue;
+    best = blocks * 25 + 250;
+    splits = next;
+    args.kb_split = blocks;
+  }
+  if (splits == 4) return launch_pair<1, 4>(what, args, a, wq, k, di.sm_count, s);
+  if (splits == 2) return launch_pair<1, 2>(what, args, a, wq, k, di.sm_count, s);
+  if (narrow < wide) return launch_pair<1, 1>(what, args, a, wq, k, di.sm_count, s);
+  return launch_pair<2, 1>(what, args, a, wq, k, di.sm_count, s);
 }

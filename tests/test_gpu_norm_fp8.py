@@ -435,6 +435,28 @@ def test_gemm_on_both_sides_of_the_choice_of_tiles(m, n, k):
     test_gemm_matches_64_bits(m, n, k, "none")
 
 
+# few tiles and long K, whose blocks are divided among pairs of CTAs: evenly, with a short or an empty last share
+SPLIT_SHAPES = [(66, 136, 4096), (100, 1000, 5136), (400, 1656, 4112), (129, 8, 9232), (65, 264, 3088),
+                (200, 128, 2704), (1039, 120, 1584), (128, 4096, 4096), (513, 72, 16384)]
+
+
+@pytest.mark.parametrize("m,n,k", SPLIT_SHAPES)
+def test_gemm_with_divided_sums(m, n, k):
+    for extras in ("none", "bias", "both"):
+        test_gemm_matches_64_bits(m, n, k, extras)
+    a, sa = rnd_f8((m, k), 170 + m), rnd_scales((m, ref.blocks(k)), 171)
+    wq, sw = rnd_f8((n, k), 172 + n), rnd_scales((ref.blocks(n), ref.blocks(k)), 173)
+    res = rnd((m, n + 40), 174, 20.0)[:, 8:8 + n]
+    first = gemm(a, sa, wq, sw, None, res, ld_pad=24).clone()
+    check_gemm(first, a, sa, wq, sw, None, res, f"strided {m}x{n}x{k}")
+    io = res.contiguous()
+    for _ in range(3):  # in place, and the same every time
+        io.copy_(res)
+        api.cc_gemm_fp8(a, sa, wq, sw, None, io, io)
+        assert torch.equal(io, first)
+    api.cc_check_device()
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_gemm_with_strided_rows(m):
     # out and res as column slices of wider rows (packed q, k, v)
