@@ -874,7 +874,7 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   // clusters of eight do not fill all SMs). Beyond that a second round costs more
   // than the split saves: 64 x 4096 x 16384 takes 18 us on four CTAs each, 29 on
   // eight; 1 x 4096 x 16384 with two to an SM 14.7 on four, 13.7 on eight. 64 x
-  // 4096 x 4096 takes 7.3 us, on pairs 9.7; 128 rows take longer than on pairs.
+  // 4096 x 4096 takes 7.3 us, on pairs 9.4; 128 rows take longer than on pairs.
   if (m <= kFewMax) {
     const int mt = m <= 16 ? 16 : m <= 32 ? 32 : 64;
     const long long n_tiles = (n - 1) / 128 + 1;
