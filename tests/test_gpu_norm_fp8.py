@@ -648,3 +648,45 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     api.cc_check_device()
     assert all(torch.equal(t, w) for t, w in zip(y + o, want))
+
+
+def test_every_kind_of_product_on_two_streams_and_from_graphs():
+    # few rows, divided sums, narrow and wide tiles, between norms: no kernel of one stream may hold up the other's
+    shapes = [(3, 1024, 4096), (60, 2048, 1040), (100, 256, 4112), (300, 1024, 1040), (2300, 1800, 656), (20000, 136, 144)]
+    sets = []
+    for i, (m, n, k) in enumerate(shapes):
+        wq, sw = rnd_f8((n, k), 300 + i), rnd_scales((ref.blocks(n), ref.blocks(k)), 310 + i)
+        sets.append((rnd((m, k), 320 + i), wq, sw, rnd((n,), 330 + i)))
+
+    def run(out, stream=None):
+        for (x, wq, sw, bias), (y, s, o) in zip(sets, out):
+            api.cc_rms_norm_act_fp8(x, None, y, s, act="silu", stream=stream)
+            api.cc_gemm_fp8(y, s, wq, sw, bias, None, o, stream=stream)
+
+    def outputs():
+        return [(torch.zeros((m, k), dtype=torch.uint8, device=DEV).view(F8), torch.zeros((m, ref.blocks(k)), device=DEV),
+                 torch.zeros((m, n), dtype=BF16, device=DEV)) for m, n, k in shapes]
+
+    want, outs = outputs(), [outputs() for _ in range(4)]
+    run(want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(8):
+        for i in range(2):
+            run(outs[i], streams[i])
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(outs[2 + i])
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    api.cc_check_device()
+    for out in outs:
+        for got, w in zip(out, want):
+            assert torch.equal(got[2], w[2]) and torch.equal(got[1], w[1])
