@@ -466,7 +466,15 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_moments_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums.add(raw[j]);
   }
-  for (; i < n; ++i) sums.add(__ldg(x + static_cast<long long>(i) * step));
+  for (; i < n; i += 4) {
+    uint4 raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      raw[j] = i + j < n ? __ldg(x + static_cast<long long>(i + j) * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) sums.add(raw[j]);
+  }
   block_moments<ONE>(a, at, at.vecs * 8 / a.cpg, sums, n, rows, reinterpret_cast<float*>(smem),
                      reinterpret_cast<float*>(smem + a.cols_at),
                      a.part + (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * a.slab_groups);
@@ -506,6 +514,13 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_apply_kernel(const __grid_cons
   const uint4* x = a.x + row0 * a.vecs + at.v;
   pdl_launch_dependents();
   pdl_wait();
+  uint4 raw[4];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      raw[j] = i + j < n ? __ldcs(x + static_cast<long long>(i + j) * step) : make_uint4(0, 0, 0, 0);
+  };
+  load(0);  // in front of the statistics, which wait for memory twice
   Affine<ONE, SILU, FP8, T> affine;
   affine.load_params(a, at, 0);
   const float2* stat = a.stat + static_cast<long long>(blockIdx.y) * a.slab_groups;
@@ -514,10 +529,7 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_apply_kernel(const __grid_cons
   float* scales = FP8 ? a.scales + row0 * a.blocks : nullptr;
   const int end = FP8 ? (rows + at.lanes - 1) / at.lanes : n;
   for (int i = 0; i < end; i += 4) {
-    uint4 raw[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      raw[j] = i + j < n ? __ldcs(x + static_cast<long long>(i + j) * step) : make_uint4(0, 0, 0, 0);
+    if (i > 0) load(i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (i + j < end)
