@@ -131,6 +131,17 @@ def test_group_norm_on_both_sides_of_the_choice_of_kernel(n, p, c, groups, fp8):
     check_group_norm(x, 1 + rnd((c,), 91, 0.3), rnd((c,), 92, 0.3), groups, "silu", fp8, f"{(n, p, c, groups)}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,p,c,groups", [  # clusters of four to eight CTAs, some with a short or an empty last share
+    (12, 1001, 128, 4), (16, 1500, 128, 32), (20, 1001, 64, 2), (24, 997, 120, 8), (28, 700, 64, 2), (34, 501, 120, 8),
+    (40, 1300, 64, 4), (16, 13, 4096, 1), (17, 16, 4096, 1), (29, 9, 4096, 1), (3, 911, 1000, 25), (2, 1717, 1024, 32),
+    (80, 1501, 64, 2), (150, 601, 64, 8),
+])
+def test_group_norm_by_many_clusters(n, p, c, groups, fp8):
+    x = rnd((n, p, c), 190 + n, 1.0, -0.5)
+    check_group_norm(x, 1 + rnd((c,), 191, 0.3), rnd((c,), 192, 0.3), groups, "silu", fp8, f"{(n, p, c, groups)}")
+
+
 def test_group_norm_of_large_frames_replays_from_a_graph():
     for n, p, c, groups in ((3, 60000, 128, 16), (1, 200000, 256, 1)):
         x, y = rnd((n, p, c), 30), torch.empty((n, p, c), dtype=BF16, device=DEV)
