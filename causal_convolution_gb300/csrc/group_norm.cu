@@ -681,7 +681,7 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8, const GnCaps* caps) {
   return g;
 }
 
-// Asked of the driver once per device.
+// Asked of the CUDA runtime once per device.
 cc_status gn_caps(const char* what, int device, const GnCaps** out) {
   constexpr int kMaxDevices = 64;
   static std::mutex mu;
