@@ -619,20 +619,22 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8, const GnCaps* caps) {
   // 16, 12.5 with two readings; 4 x 17253 x 112 22.7 with 16, 13.4.)
   g.cluster = g.smem <= kMaxSmem && !(g.smem > kHalf && g.units > 15) && g.rounds <= 5 * std::max(4LL, g.units);
   if (g.cluster) {
-    // Several clusters of four or more: as many CTAs as let all clusters run at
-    // once, with the fewest rounds of vectors on an SM; a second CTA on it hides
+    // Many clusters, or several of four CTAs or more: as many CTAs as let all
+    // clusters run at once, with the fewest rounds of vectors on an SM; a second CTA on it hides
     // some of the first one's waits, so that its rounds count for a part. CTAs
     // are put two to an SM while others are idle unless their shared memory
     // forbids it, so it is asked for: 24 x 1500 x 128 to e4m3 9.7 -> 8.1 us,
-    // 20 x 3432 x 64 11.0 -> 8.0 (six CTAs), 12 x 3432 x 64 7.5 -> 7.0.
+    // 20 x 3432 x 64 11.0 -> 8.0 (six CTAs), 12 x 3432 x 64 7.5 -> 7.0,
+    // 75 x 1500 x 120 27.1 -> 19.0, 120 x 400 x 64 7.5 -> 6.3 (one CTA each).
     size_t least = 0;
-    if (caps && g.ranks >= 4) {
-      int best = INT_MAX, ranks = g.ranks, per_sm = 0;
-      for (int r = kMaxRanks; r >= 4; --r) {
+    int per_sm = 0;  // 0: as it comes
+    if (caps && (g.ranks >= 4 || g.units > 36)) {
+      int best = INT_MAX, ranks = g.ranks;
+      for (int r = kMaxRanks; r >= (g.units > 36 ? 1 : 4); --r) {
         cut(r, 256);
         for (int k = 1; k <= 3; ++k) {
           const int cost = g.rounds * (k == 1 ? 10 : k * (fp8 ? 8 : 9));
-          if (k * (g.smem + 1024) <= kMaxSmem + 1024 && g.units <= caps->at_once[r][k] && cost < best)
+          if (k * g.threads <= 1024 && k * (g.smem + 1024) <= kMaxSmem + 1024 && g.units <= caps->at_once[r][k] && cost < best)
             best = cost, ranks = r, per_sm = k;
         }
       }
@@ -642,7 +644,7 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8, const GnCaps* caps) {
     // 512 threads where each still has eight vectors and only one partial sum
     // to hand over: 4 x 3432 x 1024 (32 groups) takes 12.8 us against 13.5 with
     // 256; with eight partial sums, 3 x 3555 x 480 takes 12.5 against 11.5
-    if (parts == 1 && g.rounds >= 16) {
+    if (parts == 1 && g.rounds >= 16 && per_sm <= 2) {
       const size_t room = g.smem > kHalf ? kMaxSmem : kHalf;
       cut(g.ranks, 512);
       if (g.smem > room) cut(g.ranks, 256);
@@ -693,7 +695,7 @@ cc_status gn_caps(const char* what, int device, const GnCaps** out) {
     auto kern = gn_cluster_kernel<true, false, false, 256>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     GnCaps caps = {};
-    for (int r = 4; r <= kMaxRanks; ++r) {
+    for (int r = 1; r <= kMaxRanks; ++r) {
       for (int k = 1; k <= 3; ++k) {
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;

@@ -135,7 +135,7 @@ def test_group_norm_on_both_sides_of_the_choice_of_kernel(n, p, c, groups, fp8):
 @pytest.mark.parametrize("n,p,c,groups", [  # clusters of four to eight CTAs, some with a short or an empty last share
     (12, 1001, 128, 4), (16, 1500, 128, 32), (20, 1001, 64, 2), (24, 997, 120, 8), (28, 700, 64, 2), (34, 501, 120, 8),
     (40, 1300, 64, 4), (16, 13, 4096, 1), (17, 16, 4096, 1), (29, 9, 4096, 1), (3, 911, 1000, 25), (2, 1717, 1024, 32),
-    (80, 1501, 64, 2), (150, 601, 64, 8),
+    (80, 1501, 64, 2), (150, 601, 64, 8), (60, 1499, 128, 4), (75, 1497, 120, 8), (120, 401, 64, 8), (300, 400, 64, 2),
 ])
 def test_group_norm_by_many_clusters(n, p, c, groups, fp8):
     x = rnd((n, p, c), 190 + n, 1.0, -0.5)
