@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "cc.h"
+#include "cc_fp8_shares.h"
 #include "cc_host.h"
 #include "cc_ptx.cuh"
 #include "cc_rows.cuh"
@@ -167,7 +168,8 @@ __device__ __forceinline__ bool add_sums64_release(uint32_t taddr, f32x2* acc, f
 #undef CC_ADD_SUMS
 #undef CC_ACCUMULATORS
 
-// Four blocks' scales of a row of a, or of a block row of the weights.
+// Four blocks' scales of a row of a, or of a block row of the weights, from
+// block kb < kblocks on.
 __device__ __forceinline__ float4 load_scales(const float* p, int kb, int kblocks, bool on) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (on) {
@@ -219,7 +221,7 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
   const int pair_id = SPLIT ? blockIdx.x / (2 * SPLITS) : blockIdx.x >> 1;
   const int pairs = SPLIT ? args.tiles : gridDim.x >> 1;
   const int kb0 = SPLIT ? static_cast<int>(cluster_rank >> 1) * args.kb_split : 0;
-  const int kbs = SPLIT ? max(0, min(args.kb_split, args.kblocks - kb0)) : 0;
+  const int kbs = SPLIT ? blocks_in_share(args.kblocks, args.kb_split, kb0) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -372,7 +374,10 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
     int mt = pair_id / args.n_tiles, nt = pair_id % args.n_tiles;
     const int mt_step = pairs / args.n_tiles, nt_step = pairs % args.n_tiles;
     scales_of(pair_id, mt, nt);
-    load_ahead(kb0);
+    // A pair whose share of K is empty asks for the rows' first scales and uses
+    // none: at kb0 the rows have ended. (Asking for nothing there took 0.2 us more,
+    // 128 x 4096 x 4096 9.16 -> 9.39.)
+    load_ahead(SPLIT ? first_request(kbs, kb0) : 0);
     for (int tile = pair_id; ok && tile < args.tiles; tile += pairs) {
       const int m0 = (2 * mt + static_cast<int>(rank)) * kPairRows + quarter * 32;
       const int n0 = nt * S::kCols + half * S::kEpiCols;
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const int lane = threadIdx.x & 31;
   const int nt = blockIdx.x / ranks;
   const int kb0 = rank * args.kb_split;
-  const int kbs = max(0, min(args.kb_split, args.kblocks - kb0));
+  const int kbs = blocks_in_share(args.kblocks, args.kb_split, kb0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -920,7 +925,7 @@ extern "C" cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8*
   long long best = std::min(wide, narrow);
   int splits = 1;
   for (int next = 2; next <= 4; next *= 2) {
-    const int blocks = ((args.kblocks - 1) / next + 4) / 4 * 4;  // the scales come in fours
+    const int blocks = share_blocks(args.kblocks, next);
     if (tiles(PairShape<1>::kCols) * 2 * next > di.sm_count - 8 * next || blocks * 25 + 250 >= best) continue;
     best = blocks * 25 + 250;
     splits = next;
