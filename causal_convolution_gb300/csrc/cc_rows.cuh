@@ -1,5 +1,11 @@
 // Device helpers of the norm, quantisation and 8-bit product kernels: vectors
 // of eight channels, the activation, and e4m3 with a scale per 128 channels.
+//
+// These kernels start while the one in front of them, and through it the one
+// before that, may still be writing what they read after their wait. So they
+// read with ordinary loads: ld.global.nc is for data that nobody writes while
+// the kernel lives, and a line that an earlier kernel's loads left in an SM's
+// cache may be what it finds. It was no faster either.
 #pragma once
 
 #include <cuda_bf16.h>

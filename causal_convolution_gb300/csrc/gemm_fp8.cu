@@ -174,12 +174,12 @@ __device__ __forceinline__ float4 load_scales(const float* p, int kb, int kblock
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (on) {
     if ((kblocks & 3) == 0) {  // rows of scales start on 16-byte boundaries
-      v = __ldg(reinterpret_cast<const float4*>(p + kb));
+      v = *reinterpret_cast<const float4*>(p + kb);
     } else {
-      v.x = __ldg(p + kb);
-      if (kb + 1 < kblocks) v.y = __ldg(p + kb + 1);
-      if (kb + 2 < kblocks) v.z = __ldg(p + kb + 2);
-      if (kb + 3 < kblocks) v.w = __ldg(p + kb + 3);
+      v.x = p[kb];
+      if (kb + 1 < kblocks) v.y = p[kb + 1];
+      if (kb + 2 < kblocks) v.z = p[kb + 2];
+      if (kb + 3 < kblocks) v.w = p[kb + 3];
     }
   }
   return v;
@@ -392,7 +392,7 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
 #pragma unroll
       for (int j = 0; j < S::kEpiCols / 8; ++j) {
         const bool on = args.bias && kb0 == 0 && n0 + 8 * j < args.n;
-        const Vec8 t = unpack8(on ? __ldg(args.bias + (n0 >> 3) + j) : make_uint4(0, 0, 0, 0));
+        const Vec8 t = unpack8(on ? args.bias[(n0 >> 3) + j] : make_uint4(0, 0, 0, 0));
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[4 * j + e] = t.p[e];
       }
@@ -688,8 +688,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     // ssa[kb][row]: the rows' scales times the weights'
     for (int i = tid; i < MT * kbs; i += 128) {
       const int kb = i / MT, r = i % MT;
-      ssa[i] = r < args.m ? __ldg(args.sa + static_cast<long long>(r) * args.kblocks + kb0 + kb) *
-                                     __ldg(args.sw + static_cast<long long>(nt) * args.kblocks + kb0 + kb)
+      ssa[i] = r < args.m ? args.sa[static_cast<long long>(r) * args.kblocks + kb0 + kb] *
+                                     args.sw[static_cast<long long>(nt) * args.kblocks + kb0 + kb]
                                : 0.f;
     }
     __syncwarp();
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
       }
       if (args.bias) {
-        const float2 t = __bfloat1622float2(__ldg(reinterpret_cast<const __nv_bfloat162*>(args.bias) + (n >> 1)));
+        const float2 t = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(args.bias)[n >> 1]);
         v.x += t.x;
         v.y += t.y;
       }

@@ -285,8 +285,8 @@ struct Affine {
     // a thread without a vector computes zeros
     k = splat8(at.on ? 1.f : 0.f);
     b = splat8(0.f);
-    if (at.on && a.gamma) k = unpack8(__ldg(a.gamma + slab * a.slab_vecs + at.v));
-    if (at.on && a.beta) b = unpack8(__ldg(a.beta + slab * a.slab_vecs + at.v));
+    if (at.on && a.gamma) k = unpack8(a.gamma[slab * a.slab_vecs + at.v]);
+    if (at.on && a.beta) b = unpack8(a.beta[slab * a.slab_vecs + at.v]);
   }
   // stat(e): mean and factor of the thread's channel e
   template <typename Stat>
@@ -457,12 +457,12 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_moments_kernel(const __grid_co
   pdl_launch_dependents();
   pdl_wait();
   Sums<ONE> sums;
-  sums.start(n > 0 ? __ldg(x) : make_uint4(0, 0, 0, 0));
+  sums.start(n > 0 ? *x : make_uint4(0, 0, 0, 0));
   int i = 0;
   for (; i + 8 <= n; i += 8) {
     uint4 raw[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) raw[j] = __ldg(x + static_cast<long long>(i + j) * step);
+    for (int j = 0; j < 8; ++j) raw[j] = x[static_cast<long long>(i + j) * step];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums.add(raw[j]);
   }
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(T, 1024 / T) gn_moments_kernel(const __grid_co
     uint4 raw[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      raw[j] = i + j < n ? __ldg(x + static_cast<long long>(i + j) * step) : make_uint4(0, 0, 0, 0);
+      raw[j] = i + j < n ? x[static_cast<long long>(i + j) * step] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (i + j < n) sums.add(raw[j]);
