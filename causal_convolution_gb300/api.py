@@ -445,11 +445,13 @@ def _row_layout(t, name: str):
     return rows, c, c if ld is None else ld
 
 
-def _scales_of(scales, dims: int, rows: int, c: int, name: str) -> None:
-    """`scales` has a value for each row and 128 channels of a [..., C] tensor of `dims` dimensions."""
-    blocks = (c + 127) // 128
-    if scales.dim() != dims or scales.shape[-1] != blocks or scales.numel() != rows * blocks:
-        raise ValueError(f"{name} must be [..., {blocks}] for {rows} rows of {c} channels, got {tuple(scales.shape)}")
+def _scales_of(scales, t, rows: int, c: int, name: str) -> None:
+    """`scales` has a value for each row and 128 channels of t [..., C], whose leading sizes it shares. (Up to two
+    dimensions their number tells; more are compared.)"""
+    blocks, dims = (c + 127) // 128, t.dim()
+    if (scales.dim() != dims or scales.shape[-1] != blocks or scales.numel() != rows * blocks
+            or (dims > 2 and scales.shape[:-1] != t.shape[:-1])):
+        raise ValueError(f"{name} must be [..., {blocks}] for {tuple(t.shape)}, got {tuple(scales.shape)}")
 
 
 def cc_group_norm_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
@@ -481,7 +483,7 @@ def cc_group_norm_act_fp8(x, gamma, beta, y, scales, groups: int, ws, eps: float
                           stream=None) -> None:
     """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [N, ..., ceil(C/128)]."""
     n, p, c = _group_norm_sizes(x, gamma, beta, y)
-    _scales_of(scales, x.dim(), n * p, c, "group_norm_act_fp8: scales")
+    _scales_of(scales, x, n * p, c, "group_norm_act_fp8: scales")
     dev, bf16 = torch.cuda.current_device(), torch.bfloat16
     _check(_lib.load().cc_group_norm_act_fp8(
         _arg(x, bf16, "x", dev), _arg(gamma, bf16, "gamma", dev), _arg(beta, bf16, "beta", dev),
@@ -505,7 +507,7 @@ def cc_rms_norm_act_fp8(x, gamma, y, scales, eps: float = 1e-6, act: str = "silu
     px, rows, c, ld = _last_rows(x, bf16, "x", dev)
     if x.shape != y.shape or (gamma is not None and gamma.numel() != c):
         raise ValueError("rms_norm_act_fp8: x and y must share [...,C] and gamma hold C elements")
-    _scales_of(scales, x.dim(), rows, c, "rms_norm_act_fp8: scales")
+    _scales_of(scales, x, rows, c, "rms_norm_act_fp8: scales")
     _check(_lib.load().cc_rms_norm_act_fp8(
         px, _arg(gamma, bf16, "gamma", dev), _arg(y, torch.float8_e4m3fn, "y", dev),
         _arg(scales, torch.float32, "scales", dev), rows, c, ld, eps, _act(act), _raw_stream(stream, dev)))
@@ -519,7 +521,7 @@ def cc_fp8_quantize(x, y, scales, stream=None) -> None:
     px, rows, c, ld = _last_rows(x, torch.bfloat16, "x", dev)
     if x.shape != y.shape:
         raise ValueError("fp8_quantize: x and y must share [...,C]")
-    _scales_of(scales, x.dim(), rows, c, "fp8_quantize: scales")
+    _scales_of(scales, x, rows, c, "fp8_quantize: scales")
     _check(_lib.load().cc_fp8_quantize(px, _arg(y, torch.float8_e4m3fn, "y", dev),
                                        _arg(scales, torch.float32, "scales", dev), rows, c, ld,
                                        _raw_stream(stream, dev)))
@@ -540,10 +542,13 @@ def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
     may be rows at a stride (a slice of packed qkv)."""
     dev, bf16, f8, f32 = torch.cuda.current_device(), torch.bfloat16, torch.float8_e4m3fn, torch.float32
     po, m, n, ld_out = _last_rows(out, bf16, "out", dev)
-    k = a.shape[-1]
-    if a.dim() != out.dim() or a.numel() != m * k or wq.shape != (n, k):
-        raise ValueError("gemm_fp8: a must be [...,K] and wq [N,K] of out [...,N]")
-    _scales_of(sa, a.dim(), m, k, "gemm_fp8: sa")
+    dims = a.dim()
+    k = a.shape[-1] if dims else 0
+    if (dims != out.dim() or a.numel() != m * k or wq.shape != (n, k)
+            or (dims > 2 and a.shape[:-1] != out.shape[:-1])):
+        raise ValueError(f"gemm_fp8: a must be [...,K] and wq [N,K] of out [...,N], got {tuple(a.shape)}, "
+                         f"{tuple(wq.shape)} and {tuple(out.shape)}")
+    _scales_of(sa, a, m, k, "gemm_fp8: sa")
     if sw.shape != ((n + 127) // 128, (k + 127) // 128):
         raise ValueError("gemm_fp8: sw must be [ceil(N/128),ceil(K/128)]")
     if bias is not None and bias.numel() != n:
