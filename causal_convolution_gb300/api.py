@@ -420,7 +420,16 @@ def _last_rows(t, dtype, name: str, dev: int):
             raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
     rows, c, ld = _row_layout(t, name)
+    if rows > INT_MAX or c > INT_MAX:
+        _too_large(name, rows, c)
     return t.data_ptr(), rows, c, ld
+
+
+INT_MAX = 0x7FFFFFFF  # sizes are passed as C ints, of which ctypes keeps the low 32 bits without a word
+
+
+def _too_large(name: str, *sizes):
+    raise ValueError(f"{name}: sizes {sizes} must be at most {INT_MAX}")
 
 
 def _row_layout(t, name: str):
@@ -455,23 +464,28 @@ def _scales_of(scales, t, rows: int, c: int, name: str) -> None:
 
 
 def cc_group_norm_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
+    if n > INT_MAX or p > INT_MAX or c > INT_MAX or groups > INT_MAX:
+        return 0  # as for other sizes that the norm refuses
     return _lib.load().cc_group_norm_workspace_bytes(n, p, c, groups)
 
 
-def _group_norm_sizes(x, gamma, beta, y):
+def _group_norm_sizes(x, gamma, beta, y, groups: int):
     shape = x.shape
     if len(shape) < 2 or shape != y.shape:
         raise ValueError(f"group_norm_act: x and y must share [N,...,C], got {tuple(shape)} and {tuple(y.shape)}")
     n, c = shape[0], shape[-1]
     if (gamma is not None and gamma.numel() != c) or (beta is not None and beta.numel() != c):
         raise ValueError("group_norm_act: gamma and beta must hold C elements")
-    return n, shape[1] if len(shape) == 3 else math.prod(shape[1:-1]), c
+    p = shape[1] if len(shape) == 3 else math.prod(shape[1:-1])
+    if n > INT_MAX or p > INT_MAX or c > INT_MAX or abs(groups) > INT_MAX:
+        _too_large("group_norm_act", n, p, c, groups)
+    return n, p, c
 
 
 def cc_group_norm_act(x, gamma, beta, y, groups: int, ws, eps: float = 1e-6, act: str = "silu", stream=None) -> None:
     """Group norm of x [N, ..., C] over everything but N (view [N, D, H, W, C] as [N*D, H, W, C] for a norm per
     frame) and an activation ("silu" or "none"). gamma, beta: [C] or None."""
-    n, p, c = _group_norm_sizes(x, gamma, beta, y)
+    n, p, c = _group_norm_sizes(x, gamma, beta, y, groups)
     dev, bf16 = torch.cuda.current_device(), torch.bfloat16
     _check(_lib.load().cc_group_norm_act(
         _arg(x, bf16, "x", dev), _arg(gamma, bf16, "gamma", dev), _arg(beta, bf16, "beta", dev),
@@ -482,7 +496,7 @@ def cc_group_norm_act(x, gamma, beta, y, groups: int, ws, eps: float = 1e-6, act
 def cc_group_norm_act_fp8(x, gamma, beta, y, scales, groups: int, ws, eps: float = 1e-6, act: str = "silu",
                           stream=None) -> None:
     """The same, written as e4m3 (y, torch.float8_e4m3fn) with scales [N, ..., ceil(C/128)]."""
-    n, p, c = _group_norm_sizes(x, gamma, beta, y)
+    n, p, c = _group_norm_sizes(x, gamma, beta, y, groups)
     _scales_of(scales, x, n * p, c, "group_norm_act_fp8: scales")
     dev, bf16 = torch.cuda.current_device(), torch.bfloat16
     _check(_lib.load().cc_group_norm_act_fp8(
@@ -531,6 +545,8 @@ def cc_gemm_fp8_prepare(w, wq, sw, stream=None) -> None:
     """Weights w [N, K] (a 1x1x1 convolution's [Cout, Cin]) to e4m3 wq with scales sw [ceil(N/128), ceil(K/128)]."""
     if w.dim() != 2 or w.shape != wq.shape or tuple(sw.shape) != tuple((s + 127) // 128 for s in w.shape):
         raise ValueError("gemm_fp8_prepare: wq must be [N,K] and sw [ceil(N/128),ceil(K/128)] of w [N,K]")
+    if w.shape[0] > INT_MAX or w.shape[1] > INT_MAX:
+        _too_large("gemm_fp8_prepare", *w.shape)
     dev = torch.cuda.current_device()
     _check(_lib.load().cc_gemm_fp8_prepare(
         _arg(w, torch.bfloat16, "w", dev), _arg(wq, torch.float8_e4m3fn, "wq", dev),
@@ -548,6 +564,8 @@ def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
             or (dims > 2 and a.shape[:-1] != out.shape[:-1])):
         raise ValueError(f"gemm_fp8: a must be [...,K] and wq [N,K] of out [...,N], got {tuple(a.shape)}, "
                          f"{tuple(wq.shape)} and {tuple(out.shape)}")
+    if k > INT_MAX:
+        _too_large("gemm_fp8", m, n, k)
     _scales_of(sa, a, m, k, "gemm_fp8: sa")
     if sw.shape != ((n + 127) // 128, (k + 127) // 128):
         raise ValueError("gemm_fp8: sw must be [ceil(N/128),ceil(K/128)]")

@@ -1,5 +1,6 @@
 """Shapes that the binding of the norms and the 8-bit product refuses, on the
-host: tensors that hold the right number of elements under other sizes."""
+host: tensors that hold the right number of elements under other sizes, and sizes
+that a C int does not hold."""
 
 import pytest
 import torch
@@ -98,3 +99,58 @@ def test_scales_of_the_right_sizes_pass(calls):
         api.cc_rms_norm_act_fp8(x, None, y, s)
         api.cc_group_norm_act_fp8(x, None, None, y, s, 8, None)
     assert len(calls.seen) == 12
+
+
+INT = api.INT_MAX
+BIG = (1 << 32) + 5  # as a C int: 5
+
+
+def wide(rows, c, dtype=BF16):
+    """A [rows, c] view of one row or one element: sizes only."""
+    return t(1, 1, dtype=dtype).expand(rows, c) if c > INT else t(1, c, dtype=dtype).expand(rows, c)
+
+
+@pytest.mark.parametrize("rows", [INT + 1, BIG])
+def test_rows_beyond_an_int_are_refused(calls, rows):
+    x, y8, s = wide(rows, 8), wide(rows, 8, F8), wide(rows, 1, F32)
+    many = f"at most {INT}"
+    with pytest.raises(ValueError, match=many):
+        api.cc_rms_norm_act(x, None, x)
+    with pytest.raises(ValueError, match=many):
+        api.cc_rms_norm_act_fp8(x, None, y8, s)
+    with pytest.raises(ValueError, match=many):
+        api.cc_fp8_quantize(x, y8, s)
+    with pytest.raises(ValueError, match=many):
+        api.cc_gemm_fp8(wide(rows, 16, F8), s, t(8, 16, dtype=F8), t(1, 1, dtype=F32), None, None, x)
+    with pytest.raises(ValueError, match=many):  # as instances and as positions
+        api.cc_group_norm_act(x.unsqueeze(1), None, None, x.unsqueeze(1), 1, None)
+    with pytest.raises(ValueError, match=many):
+        api.cc_group_norm_act_fp8(x.unsqueeze(0), None, None, y8.unsqueeze(0), s.unsqueeze(0), 1, None)
+    assert not calls.seen
+    assert api.cc_group_norm_workspace_bytes(rows, 1, 8, 1) == api.cc_group_norm_workspace_bytes(1, rows, 8, 1) == 0
+    assert api.cc_group_norm_workspace_bytes(1, 30000, 8, (1 << 32) + 1) == 0
+    assert not calls.seen
+
+
+def test_positions_are_counted_before_they_are_refused(calls):
+    x = t(1, 1, 1, 8).expand(1, 1 << 16, 1 << 16, 8)  # 2^32 positions
+    with pytest.raises(ValueError, match=f"at most {INT}"):
+        api.cc_group_norm_act(x, None, None, x, 1, None)
+    assert not calls.seen
+
+
+def test_other_sizes_beyond_an_int_are_refused(calls):
+    many = f"at most {INT}"
+    x = t(2, 3, 8)
+    for groups in ((1 << 32) + 8, -(1 << 32) + 8):
+        with pytest.raises(ValueError, match=many):
+            api.cc_group_norm_act(x, None, None, x, groups, None)
+    for n, k in ((BIG + 11, 16), (16, BIG + 11)):
+        w = wide(n, k)
+        sw = t(1, 1, dtype=F32).expand((n + 127) // 128, (k + 127) // 128)
+        with pytest.raises(ValueError, match=many):
+            api.cc_gemm_fp8_prepare(w, w, sw)
+    with pytest.raises(ValueError, match=many):
+        api.cc_gemm_fp8(wide(1, k, F8), t(1, 1, dtype=F32).expand(1, (k + 127) // 128), wide(n, k, F8), sw, None, None,
+                        t(1, n))
+    assert not calls.seen
