@@ -347,12 +347,15 @@ typedef enum cc_act { CC_ACT_NONE = 0, CC_ACT_SILU = 1 } cc_act;
 
 /* e4m3 outputs (the *_fp8 functions here and cc_fp8_quantize): for each row of
  * C channels and block b of 128 of them (the last one may be shorter),
- *   scales[row][b] = max(max |v| / 448, 2^-126),  y = e4m3(v / scales[row][b])
- * from the unrounded fp32 v, rounded to nearest even; y [rows, C], scales
- * [rows, ceil(C / 128)]. cc_fp8_quantize's scales are correctly rounded
- * quotients; behind a norm they may be one step of 2^-23 off. A block that holds a NaN gets a NaN scale and NaN
- * values; one with an infinity gets an infinite scale, zeros for its finite
- * values and NaN for the infinite ones. */
+ *   scales[row][b] = s = max(max |v| / 448, 2^-126),  y = e4m3(v * r),  r = 1 / s,
+ * from the unrounded fp32 v; y [rows, C], scales [rows, ceil(C / 128)]. The
+ * quotients s and r and the product v * r are rounded to fp32 to nearest, the
+ * product then to e4m3, to nearest even. (v * r is within 2^-22 of v / s, so
+ * one value in some 2000, next to the middle of two e4m3 values, goes to the
+ * other one of the two than the quotient would.) Behind a norm s and r may each
+ * be one step of 2^-23 off as well. A block that holds a NaN gets a NaN scale
+ * and NaN values; one with an infinity gets an infinite scale, zeros for its
+ * finite values and NaN for the infinite ones. */
 
 /* Bytes of workspace a group norm of these sizes needs, for either output (0
  * where the SMs keep all of x, and for empty or invalid sizes). The contents need
@@ -392,7 +395,8 @@ cc_status cc_fp8_quantize(const cc_bf16* x, cc_fp8* y, float* scales, int rows, 
 
 /* Weights w [N, K] to e4m3 with one scale per 128 x 128 block (blocks at the
  * right and lower edges may be smaller): wq [N, K], sw [ceil(N / 128)][ceil(K / 128)],
- * each scale max(max |w| / 448, 2^-126). Needs K % 16 == 0, N <= 8388480 and
+ * each scale s = max(max |w| / 448, 2^-126) and each value e4m3(w * (1 / s)),
+ * rounded as by cc_fp8_quantize. Needs K % 16 == 0, N <= 8388480 and
  * K <= 2^24. */
 cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, int k, void* stream);
 
