@@ -83,7 +83,6 @@ struct GnArgs {
   int p;
   int vecs;        // C / 8
   int blocks;      // ceil(C / 128)
-  int slabs;       // per instance
   int slab_vecs;   // of every slab but, perhaps, the last
   int cpg;         // C / groups
   int gw_shift;    // log2 of gw = gcd(C / groups, 8): channels of a vector that always share a group
@@ -678,6 +677,7 @@ GnPlan gn_plan(int n, int p, int c, int groups, bool fp8, const GnCaps* caps) {
   g.rows = lanes * run;
   g.runs = (p - 1) / g.rows + 1;
   g.cols_at = align16(red_bytes(c / 8));
+  // partial sums and columns, at most 16 KB of each: no more than a launch has unasked
   g.smem = g.cols_at + static_cast<size_t>(c / 8) * parts * 4;
   g.ws_bytes = static_cast<size_t>(n) * (g.runs + 1) * groups * sizeof(float2);
   return g;
@@ -744,11 +744,6 @@ cc_status launch_cluster(const char* what, GnArgs& a, const GnPlan& g, cudaStrea
 template <bool ONE, bool SILU, bool FP8, int T>
 cc_status launch_twice(const char* what, GnArgs& a, const GnPlan& g, int n, cudaStream_t s) {
   auto moments = gn_moments_kernel<ONE, T>;
-  if (g.smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(moments, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(g.smem));
-    if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: kernel attributes: %s", what, cudaGetErrorString(e));
-  }
   cudaError_t e = launch_pdl(moments, dim3(g.runs, n), dim3(T), g.smem, s, a);
   if (e == cudaSuccess) e = launch_pdl(gn_merge_kernel, dim3(a.slab_groups, n), dim3(kMergeThreads), 0, s, a);
   if (e == cudaSuccess) e = launch_pdl(gn_apply_kernel<ONE, SILU, FP8, T>, dim3(g.runs, n), dim3(T), 0, s, a);
@@ -798,7 +793,6 @@ cc_status run_group_norm(const char* what, const cc_bf16* x, const cc_bf16* gamm
   a.p = p;
   a.vecs = c / 8;
   a.blocks = (c + kScaleBlock - 1) / kScaleBlock;
-  a.slabs = g.slabs;
   a.slab_vecs = g.slab_c / 8;
   a.cpg = c / groups;
   const int gw = std::gcd(a.cpg, 8);
