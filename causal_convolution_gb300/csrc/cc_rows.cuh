@@ -93,10 +93,10 @@ __device__ __forceinline__ uint2 pack8_e4m3(const Vec8& v) {
   return make_uint2(w[0], w[1]);
 }
 
-// v * sigmoid(v) = v / (1 + 2^(-v log2 e)). Below -88 the divisor is infinite
-// and the quotient 0. The exponential and the reciprocal are the hardware's
-// approximations, each good to about 2^-22, which the rounding to bf16 or e4m3
-// behind them hides.
+// v * sigmoid(v) = v / (1 + 2^(-v log2 e)). The exponential and the reciprocal are
+// the hardware's approximations, each good to about 2^-22 (and the exponent's
+// rounding to |v| 2^-24), which the rounding to bf16 or e4m3 behind them hides. The reciprocal of a divisor above 2^126 is 0:
+// below -87.3 the result is 0, off by less than 2^-119.
 template <bool SILU>
 __device__ __forceinline__ void activate8(Vec8& v) {
   if (SILU) {

@@ -342,7 +342,8 @@ cc_status cc_head_out_noalloc(const cc_bf16* x, const cc_bf16* wp, const cc_bf16
 
 /* ----------------------------------- norms with an activation [NORM] */
 
-/* What follows the affine part of a norm: nothing, or v * sigmoid(v). */
+/* What follows the affine part of a norm: nothing, or v * sigmoid(v) (0 below
+ * v = -87.3, where it is smaller than 2^-119). */
 typedef enum cc_act { CC_ACT_NONE = 0, CC_ACT_SILU = 1 } cc_act;
 
 /* e4m3 outputs (the *_fp8 functions here and cc_fp8_quantize): for each row of
