@@ -59,9 +59,11 @@ constexpr int kKBytes = 128;  // bytes of K per stage: one scale block, one swiz
 // and a warp about 620 to read and add its 128 columns (two trips to tensor
 // memory, 64 paired multiply-adds that the two warps of a scheduler share, and
 // what the loop around them costs); a tile's end takes 2000 more, of which the
-// accumulators in reserve hide two blocks. Measured: 16384 x 4096 x 4096 in 178
-// us (3.1 PFLOP/s; 139 us with the epilogue left out), 13728 x 1024 x 1024 with
-// bias and residual 19 us, 439296 x 256 x 512 79 us (5.7 TB/s). A block of K of
+// accumulators in reserve hide two blocks. Measured: 16384 x 4096 x 4096 in 180
+// us in the first milliseconds (3.0 PFLOP/s; 139 us with the epilogue left out)
+// and in 205 once the power limit holds the clock at 1.7 GHz, 13728 x 1024 x 1024
+// with bias and residual 19.5 us (16.8 where part of it comes out of L2; without the
+// residual 16.8 and 15.4), 439296 x 256 x 512 79 us (5.7 TB/s). A block of K of
 // the narrow tile takes 480 cycles of 384 that its 24 KB a CTA take to arrive.
 // (As two accumulators of 64 columns it took 580: an MMA with 64 columns takes as
 // long as one with 128.)

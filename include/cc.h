@@ -371,7 +371,9 @@ size_t cc_group_norm_workspace_bytes(int n, int p, int c, int groups);
  * held in fp32 and merged without cancellation; one rounding to bf16. x and
  * y: [N, P, C], not overlapping; gamma, beta: [C] or NULL (ones, zeros).
  * Needs C % 8 == 0, C <= 4096, groups dividing C, N <= 65535, eps > 0. Results
- * do not change from run to run. */
+ * do not change from run to run. The order of the sums is chosen by N and P, so
+ * the same frame in a call of one and in a call of four may differ in the last
+ * bits. */
 cc_status cc_group_norm_act(const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, cc_bf16* y, int n, int p,
                             int c, int groups, float eps, int act, void* ws, size_t ws_bytes, void* stream);
 cc_status cc_group_norm_act_fp8(const cc_bf16* x, const cc_bf16* gamma, const cc_bf16* beta, cc_fp8* y, float* scales,
@@ -403,8 +405,12 @@ cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, in
 
 /* out[m,n] = bf16( sum_b sa[m,b] sw[n/128,b] sum_{k in block b} a[m,k] wq[n,k]
  *                  + bias[n] + res[m,n] ),
- * b over the blocks of 128 of K; products and sums in fp32, one rounding. a:
- * [M, K] e4m3, sa: [M, ceil(K / 128)] (any fp32 values), wq, sw as written by
+ * b over the blocks of 128 of K; products and sums in fp32, one rounding; sa sw
+ * is a product of its own, rounded to fp32 before a block's sum is multiplied by
+ * it. Results do not change from run to run, but the order of the sums is chosen
+ * by M, so the same row among others may differ in its last bits. a:
+ * [M, K] e4m3, sa: [M, ceil(K / 128)] (any fp32 values whose products with sw are
+ * finite, and not below 2^-126 where their last bits count), wq, sw as written by
  * cc_gemm_fp8_prepare; bias: [N] or NULL; res: bf16 rows of stride ld_res
  * elements or NULL (ld_res is then ignored); out: bf16 rows of stride ld_out
  * elements, columns N .. ld_out-1 untouched; out may be res when their strides
