@@ -62,6 +62,12 @@ SIGNATURES = {
     "cc_fp8_quantize": (_I, [_P, _P, _P, _I, _I, _L, _P]),
     "cc_gemm_fp8_prepare": (_I, [_P, _P, _P, _I, _I, _P]),
     "cc_gemm_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _L, _L, _P]),
+    "cc_qk_norm_rope": (_I, [_P] * 8 + [_I] * 6 + [_L] * 4 + [_F, _I, _P]),
+    "cc_qk_norm_rope_append": (_I, [_P] * 13 + [_I] * 10 + [_L] * 10 + [_F, _I, _P]),
+    "cc_attn_paged_workspace_bytes": (_Z, [_I] * 5),
+    "cc_attn_paged": (_I, [_P] * 7 + [_I] * 8 + [_L] * 8 + [_F, _I, _P, _Z, _P]),
+    "cc_attn_cross_workspace_bytes": (_Z, [_I] * 6),
+    "cc_attn_cross": (_I, [_P] * 5 + [_I] * 6 + [_L] * 4 + [_F, _P, _Z, _P]),
     "cc_copy_to_host": (_I, [_P, _P, _Z, _I, _P]),
     "cc_debug_im2col_tile": (_I, [_P, _P] + [_I] * 19 + [_P]),
     "cc_debug_wait_timeout": (_I, [_L, _P]),

@@ -30,6 +30,8 @@ __all__ = [
     "cc_group_norm_workspace_bytes", "cc_group_norm_act", "cc_group_norm_act_fp8",
     "cc_rms_norm_act", "cc_rms_norm_act_fp8",
     "cc_fp8_quantize", "cc_gemm_fp8_prepare", "cc_gemm_fp8",
+    "cc_qk_norm_rope", "cc_qk_norm_rope_append",
+    "cc_attn_paged_workspace_bytes", "cc_attn_paged", "cc_attn_cross_workspace_bytes", "cc_attn_cross",
     "cc_debug_im2col_tile", "cc_debug_wait_timeout", "cc_debug_conv_bad_tile_order",
     "HEAD_COUT", "HEAD_G_CH",
 ]
@@ -579,6 +581,194 @@ def cc_gemm_fp8(a, sa, wq, sw, bias, res, out, stream=None) -> None:
     _check(_lib.load().cc_gemm_fp8(_arg(a, f8, "a", dev), _arg(sa, f32, "sa", dev), _arg(wq, f8, "wq", dev),
                                    _arg(sw, f32, "sw", dev), _arg(bias, bf16, "bias", dev), pr, po, m, n, k, ld_res,
                                    ld_out, _raw_stream(stream, dev)))
+
+
+# ---------------------------- heads: norm, rotation, a paged cache, attention --
+
+ROT_STYLES = {"pairs": 0, "halves": 1}  # CC_ROT_*
+
+
+def _on(t, dtype, name: str, dev: int) -> None:
+    """`t` is a tensor of this type on the current device."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+
+
+def _head_rows(t, name: str, dev: int):
+    """(pointer, leading shape, rows, heads, D, ld) of a bf16 tensor [..., heads, D] whose rows hold their heads side
+    by side and lie at one stride `ld`."""
+    _on(t, torch.bfloat16, name, dev)
+    shape = t.shape
+    if len(shape) < 3:
+        raise ValueError(f"{name}: expected [..., heads, D]")
+    heads, d = shape[-2:]
+    strides = t.stride()
+    if (strides[-1] != 1 and d > 1) or (strides[-2] != d and heads > 1):
+        raise ValueError(f"{name}: a row's heads and channels must be contiguous")
+    rows, ld = 1, None
+    for size, stride in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+        if size != 1:
+            if ld is None:
+                ld = stride
+            elif stride != ld * rows and rows:
+                raise ValueError(f"{name}: rows must lie at one stride")
+            rows *= size
+    if rows > INT_MAX or heads > INT_MAX or d > INT_MAX:
+        _too_large(name, rows, heads, d)
+    return t.data_ptr(), shape[:-2], rows, heads, d, heads * d if ld is None else ld
+
+
+def _rotation(rot, pos, rows: int, d: int, name: str, dev: int):
+    """(pointer of rot, positions, rd, pointer of pos)"""
+    prot, positions, rd = None, 0, 0
+    if rot is not None:
+        if rot.dim() != 3 or rot.shape[2] != 2:
+            raise ValueError(f"{name}: rot must be [positions, rd/2, 2], got {tuple(rot.shape)}")
+        prot, positions, rd = _arg(rot, torch.float32, "rot", dev), rot.shape[0], 2 * rot.shape[1]
+        if positions > INT_MAX or rd > INT_MAX:
+            _too_large(name, positions, rd)
+    if pos is not None and pos.numel() != rows:
+        raise ValueError(f"{name}: pos must hold a position for each of {rows} rows")
+    return prot, positions, rd, _arg(pos, torch.int32, "pos", dev)
+
+
+def _style(style: str) -> int:
+    if style not in ROT_STYLES:
+        raise ValueError(f"style: expected one of {sorted(ROT_STYLES)}, got {style!r}")
+    return ROT_STYLES[style]
+
+
+def _gamma(gamma, d: int, name: str, dev: int):
+    if gamma is not None and gamma.numel() != d:
+        raise ValueError(f"{name} must hold D elements")
+    return _arg(gamma, torch.bfloat16, name, dev)
+
+
+def cc_qk_norm_rope(q, k, gamma_q, gamma_k, rot, pos, q_out, k_out, eps: float = 1e-6, style: str = "pairs",
+                    stream=None) -> None:
+    """RMS norm over the channels of every head of q [..., heads, D] and k [..., kv_heads, D] (rows may be strided;
+    either may be None with its output) and the rotation of the first rd channels by pos[row] (None: the row's number)
+    as rot [positions, rd/2, 2], fp32 (cos, sin), says (None: no rotation). style: "pairs" or "halves"."""
+    dev = torch.cuda.current_device()
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
+        raise ValueError("qk_norm_rope: q and k come with their outputs, and one of them must be there")
+    pq = pk = pqo = pko = None
+    heads = kv_heads = ld_q = ld_k = ld_qo = ld_ko = 0
+    if k is not None:
+        pk, lead, rows, kv_heads, d, ld_k = _head_rows(k, "k", dev)
+        pko, _, _, _, _, ld_ko = _head_rows(k_out, "k_out", dev)
+        if k_out.shape != k.shape:
+            raise ValueError("qk_norm_rope: k_out must have k's shape")
+    if q is not None:
+        pq, lead_q, rows, heads, d, ld_q = _head_rows(q, "q", dev)
+        pqo, _, _, _, _, ld_qo = _head_rows(q_out, "q_out", dev)
+        if q_out.shape != q.shape or (k is not None and (lead_q != lead or k.shape[-1] != d)):
+            raise ValueError("qk_norm_rope: q, k and q_out must share rows and D")
+    prot, positions, rd, ppos = _rotation(rot, pos, rows, d, "qk_norm_rope", dev)
+    _check(_lib.load().cc_qk_norm_rope(
+        pq, pk, _gamma(gamma_q, d, "gamma_q", dev), _gamma(gamma_k, d, "gamma_k", dev), prot, ppos, pqo, pko, rows,
+        heads, kv_heads, d, rd, positions, ld_q, ld_k, ld_qo, ld_ko, eps, _style(style), _raw_stream(stream, dev)))
+
+
+def _paged(k_cache, v_cache, q_offsets, kv_lens, page_table, name: str, dev: int):
+    """Pointers, sizes and strides of a cache [pages, page_size, kv_heads, D] and of a step's plan."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    _on(k_cache, bf16, "k_cache", dev)
+    _on(v_cache, bf16, "v_cache", dev)
+    shape, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"{name}: k_cache and v_cache must share [pages, page_size, kv_heads, D]")
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError(f"{name}: a cached head's channels must be contiguous")
+    if page_table.dim() != 2 or kv_lens.numel() != page_table.shape[0] or q_offsets.numel() != kv_lens.numel() + 1:
+        raise ValueError(f"{name}: q_offsets must be [seqs + 1], kv_lens [seqs] and page_table [seqs, max_pages]")
+    seqs, max_pages = page_table.shape
+    if max(*shape, seqs, max_pages) > INT_MAX:
+        _too_large(name, *shape, seqs, max_pages)
+    return (k_cache.data_ptr(), v_cache.data_ptr(),
+            (_arg(q_offsets, i32, "q_offsets", dev), _arg(kv_lens, i32, "kv_lens", dev),
+             _arg(page_table, i32, "page_table", dev)),
+            (seqs, max_pages, shape[0], shape[1]), shape[2], shape[3], ks[:3] + vs[:3])
+
+
+def cc_qk_norm_rope_append(q, k, v, gamma_q, gamma_k, rot, pos, q_out, k_cache, v_cache, q_offsets, kv_lens,
+                           page_table, eps: float = 1e-6, style: str = "pairs", stream=None) -> None:
+    """cc_qk_norm_rope of the rows of a step's plan, with the keys and the values v [rows, kv_heads, D] written to
+    their tokens' slots in k_cache and v_cache [pages, page_size, kv_heads, D] (any strides). Sequence b owns rows
+    q_offsets[b] .. q_offsets[b + 1] - 1, the newest of its kv_lens[b] tokens; page_table [seqs, max_pages]. All three
+    are int32 on the GPU. pos None: a row's position is its token's in its sequence."""
+    dev = torch.cuda.current_device()
+    pq, lead, rows, heads, d, ld_q = _head_rows(q, "q", dev)
+    pqo, _, _, _, _, ld_qo = _head_rows(q_out, "q_out", dev)
+    pk, lead_k, _, kv_heads, _, ld_k = _head_rows(k, "k", dev)
+    pv, _, _, _, _, ld_v = _head_rows(v, "v", dev)
+    pkc, pvc, plan, sizes, cache_heads, cache_d, strides = _paged(k_cache, v_cache, q_offsets, kv_lens, page_table,
+                                                                  "qk_norm_rope_append", dev)
+    if (q_out.shape != q.shape or lead_k != lead or k.shape != v.shape or k.shape[-1] != d or cache_d != d
+            or cache_heads != kv_heads):
+        raise ValueError("qk_norm_rope_append: q, k, v and the cache must share rows, heads and D")
+    prot, positions, rd, ppos = _rotation(rot, pos, rows, d, "qk_norm_rope_append", dev)
+    _check(_lib.load().cc_qk_norm_rope_append(
+        pq, pk, pv, _gamma(gamma_q, d, "gamma_q", dev), _gamma(gamma_k, d, "gamma_k", dev), prot, ppos, pqo, pkc, pvc,
+        *plan, rows, *sizes, heads, kv_heads, d, rd, positions, ld_q, ld_k, ld_v, ld_qo, *strides, eps, _style(style),
+        _raw_stream(stream, dev)))
+
+
+def cc_attn_paged_workspace_bytes(rows: int, seqs: int, heads: int, kv_heads: int, d: int) -> int:
+    if max(rows, seqs, heads, kv_heads, d) > INT_MAX:
+        return 0  # as for other sizes that the call refuses
+    return _lib.load().cc_attn_paged_workspace_bytes(rows, seqs, heads, kv_heads, d)
+
+
+def cc_attn_paged(q, k_cache, v_cache, o, q_offsets, kv_lens, page_table, ws, scale: float | None = None,
+                  causal_block: int = 1, stream=None) -> None:
+    """Attention of a plan's rows q [rows, heads, D] over the cache (as for cc_qk_norm_rope_append). A token sees those
+    up to the end of its own block of `causal_block` new tokens (1: up to itself; 0: all of its sequence)."""
+    dev = torch.cuda.current_device()
+    pq, _, rows, heads, d, ld_q = _head_rows(q, "q", dev)
+    po, _, _, _, _, ld_o = _head_rows(o, "o", dev)
+    pk, pv, plan, sizes, kv_heads, cache_d, strides = _paged(k_cache, v_cache, q_offsets, kv_lens, page_table,
+                                                             "attn_paged", dev)
+    if o.shape != q.shape or cache_d != d:
+        raise ValueError("attn_paged: q, o and the cache must share rows and D")
+    if abs(causal_block) > INT_MAX:
+        _too_large("attn_paged", causal_block)
+    _check(_lib.load().cc_attn_paged(
+        pq, pk, pv, po, *plan, rows, *sizes, heads, kv_heads, d, ld_q, ld_o, *strides,
+        d ** -0.5 if scale is None else scale, causal_block, _arg(ws, torch.uint8, "ws", dev),
+        0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
+
+
+def cc_attn_cross_workspace_bytes(n: int, lq: int, lk: int, heads: int, kv_heads: int, d: int) -> int:
+    if max(n, lq, lk, heads, kv_heads, d) > INT_MAX:
+        return 0
+    return _lib.load().cc_attn_cross_workspace_bytes(n, lq, lk, heads, kv_heads, d)
+
+
+def cc_attn_cross(q, k, v, o, kv_lens, ws, scale: float | None = None, stream=None) -> None:
+    """Attention of q [N, Lq, heads, D] to an encoder's k, v [N, Lk, kv_heads, D] (rows may be strided), of which
+    kv_lens [N] (int32 on the GPU; None: all) count."""
+    dev = torch.cuda.current_device()
+    pq, lead, _, heads, d, ld_q = _head_rows(q, "q", dev)
+    pk, lead_k, _, kv_heads, _, ld_k = _head_rows(k, "k", dev)
+    pv, _, _, _, _, ld_v = _head_rows(v, "v", dev)
+    po, _, _, _, _, ld_o = _head_rows(o, "o", dev)
+    if len(lead) != 2 or len(lead_k) != 2 or lead[0] != lead_k[0] or o.shape != q.shape or v.shape != k.shape \
+            or k.shape[-1] != d:
+        raise ValueError("attn_cross: q and o must be [N,Lq,heads,D], k and v [N,Lk,kv_heads,D]")
+    if kv_lens is not None and kv_lens.numel() != lead[0]:
+        raise ValueError("attn_cross: kv_lens must hold N values")
+    _check(_lib.load().cc_attn_cross(
+        pq, pk, pv, po, _arg(kv_lens, torch.int32, "kv_lens", dev), *lead, lead_k[1], heads, kv_heads, d, ld_q, ld_k,
+        ld_v, ld_o, d ** -0.5 if scale is None else scale, _arg(ws, torch.uint8, "ws", dev),
+        0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
 
 
 # -------------------------------------------------------- result read-back --

@@ -53,6 +53,10 @@
  *  [NORM], [FP8] no page: the norms in front of the convolutions and the
  *         attention, and the 1x1x1 products around the attention and in the
  *         shortcuts, in 8 bits.
+ *  [HEADS] no page: the operators of a transformer that makes the decoder's
+ *         latents chunk by chunk, between the 8-bit products: head norms with
+ *         rotation, a paged cache of keys and values and the attention over it,
+ *         attention to an encoder's states.
  *  [HOST] no page: a transfer helper for the chunk-by-chunk decode loop.
  */
 #ifndef CC_H_
@@ -420,6 +424,95 @@ cc_status cc_gemm_fp8_prepare(const cc_bf16* w, cc_fp8* wq, float* sw, int n, in
 cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8* wq, const float* sw, const cc_bf16* bias,
                       const cc_bf16* res, cc_bf16* out, int m, int n, int k, int64_t ld_res, int64_t ld_out,
                       void* stream);
+
+/* ------------------- heads: norm, rotation and a paged cache [HEADS] */
+
+/* Rows of heads: row r's head h has its D channels at r * ld + h * D.
+ *
+ * The plan of a step over a paged cache, three device arrays that do not change
+ * while a call runs: sequence b of `seqs` owns the rows q_offsets[b] ..
+ * q_offsets[b + 1] - 1 (q_offsets has seqs + 1 values that do not fall), which
+ * are its newest tokens; kv_lens[b] counts its tokens with them; token p lies in
+ * page page_table[b * max_pages + p / page_size], slot p % page_size. Entries of
+ * the table behind a sequence's last page are not read. Rows in front of the
+ * first and behind the last sequence are left as they are. A plan that points
+ * outside of the cache or the table (kv_lens below the number of new tokens or
+ * above max_pages * page_size, a page below 0 or from `pages` on), or a position
+ * outside of the rotation's table, makes cc_check_device() report CC_ERR_DEVICE;
+ * no access leaves the caller's memory then, and what the rows concerned come to
+ * is not defined.
+ *
+ * The cache: page g, slot s, head h at g * page + s * token + h * head elements
+ * (strides of k and of v, multiples of 8 and at least D), `pages` pages of
+ * page_size slots. Needs page_size % 16 == 0. */
+
+/* How channels pair up for a rotation of rd of them: neighbours (2i, 2i + 1), or
+ * halves (i, i + rd / 2). */
+typedef enum cc_rot { CC_ROT_PAIRS = 0, CC_ROT_HALVES = 1 } cc_rot;
+
+/* RMS norm of each head and the rotation of its first rd channels by the row's
+ * position, in fp32, rounded once:
+ *   y = x / sqrt(mean_c x[c]^2 + eps) * gamma[c],  over the head's D channels;
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos) for each pair i,
+ * (cos, sin) = rot[pos[r]][i]; channels from rd on are not rotated. gamma_q,
+ * gamma_k: [D] or NULL (ones); rot: [positions][rd / 2] pairs of floats (NULL
+ * where rd is 0); pos: [rows] or NULL (row r has position r). q_out may be q and
+ * k_out may be k when their strides are the same; otherwise they do not overlap.
+ * heads or kv_heads may be 0 (those pointers are then not read). Needs
+ * D % 16 == 0, D <= 256, rd % 16 == 0, rd <= D, row strides % 8 == 0, eps > 0. */
+cc_status cc_qk_norm_rope(const cc_bf16* q, const cc_bf16* k, const cc_bf16* gamma_q, const cc_bf16* gamma_k,
+                          const float* rot, const int32_t* pos, cc_bf16* q_out, cc_bf16* k_out, int rows, int heads,
+                          int kv_heads, int d, int rd, int positions, int64_t ld_q, int64_t ld_k, int64_t ld_qo,
+                          int64_t ld_ko, float eps, int style, void* stream);
+
+/* The same for the rows of a plan, with the keys and the values v (as they are)
+ * written to their tokens' slots in the cache. pos NULL: a row's position is its
+ * token's. Two rows of a call must not have the same slot. q, k and v must not
+ * overlap the cache. */
+cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, const cc_bf16* v, const cc_bf16* gamma_q,
+                                 const cc_bf16* gamma_k, const float* rot, const int32_t* pos, cc_bf16* q_out,
+                                 cc_bf16* k_cache, cc_bf16* v_cache, const int32_t* q_offsets, const int32_t* kv_lens,
+                                 const int32_t* page_table, int rows, int seqs, int max_pages, int pages,
+                                 int page_size, int heads, int kv_heads, int d, int rd, int positions, int64_t ld_q,
+                                 int64_t ld_k, int64_t ld_v, int64_t ld_qo, int64_t k_page, int64_t k_token,
+                                 int64_t k_head, int64_t v_page, int64_t v_token, int64_t v_head, float eps, int style,
+                                 void* stream);
+
+/* Attention of a plan's rows over the cache:
+ *   o[r,h,:] = sum_{j < limit(r)} p_j v[j, h / group, :],
+ *   p = softmax_{j < limit(r)}(scale * q[r,h,:] . k[j, h / group, :]),
+ * group = heads / kv_heads. The i-th of n new tokens of a sequence of L tokens
+ * sees the first limit = L - n + min(n, (i / causal_block + 1) * causal_block)
+ * tokens: with causal_block 1 those up to itself, with F those up to the end of
+ * its own block of F tokens (a frame); causal_block 0: all L. (With
+ * causal_block 0 L may be less than n.) Rows that see no token become zeros.
+ * Scores, softmax and sums in fp32, the weights rounded to bf16 for the product
+ * with v, one rounding at the end. Keys and values behind a sequence's end may
+ * hold anything, NaN included; those that some of its tokens see and others do
+ * not should be finite. Results do not change from run to run, but the split of
+ * the sums depends on the whole plan. ws: at least
+ * cc_attn_paged_workspace_bytes() (0 for sizes that the call refuses; calls
+ * whose GPU work overlaps need one each; its contents need no preparation).
+ * o must not overlap q or the cache. Needs D % 16 == 0, D <= 128, heads %
+ * kv_heads == 0, group <= 128, ld_q, ld_o % 8 == 0, scale finite and > 0. */
+size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d);
+cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16* v_cache, cc_bf16* o,
+                        const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table, int rows,
+                        int seqs, int max_pages, int pages, int page_size, int heads, int kv_heads, int d,
+                        int64_t ld_q, int64_t ld_o, int64_t k_page, int64_t k_token, int64_t k_head, int64_t v_page,
+                        int64_t v_token, int64_t v_head, float scale, int causal_block, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Attention of lq query rows to lk keys in each of n instances (an encoder's
+ * states), without causality: q, o: [n, lq] rows of heads, k, v: [n, lk] rows of
+ * kv_heads (row strides ld_*, instances lq and lk rows apart). kv_lens: [n], how
+ * many of an instance's keys count (0 .. lk, anything else is reported by
+ * cc_check_device() and taken as the nearer of the two), or NULL (all lk). The
+ * others may hold anything. Otherwise as cc_attn_paged; lk may be 0. */
+size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d);
+cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_bf16* v, cc_bf16* o, const int32_t* kv_lens,
+                        int n, int lq, int lk, int heads, int kv_heads, int d, int64_t ld_q, int64_t ld_k,
+                        int64_t ld_v, int64_t ld_o, float scale, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------- result read-back [HOST] */
 
