@@ -3,9 +3,28 @@
 //
 //   o_i = sum_{j < limit(i)} softmax_j(scale q_i . k_j) v_j
 //
-// Simple form: a warp per query row and head walks the keys 32 at a time with a
-// running maximum and sum; a lane takes a key's product, then four channels of
-// the weighted sum.
+// Work. An item is up to 256 query rows of one sequence and one key head -- two
+// halves of 128 rows, a row being a (token, query head of the group) pair, so
+// that grouped heads share the keys they read -- and all the 128-key tiles that
+// any of its rows sees. The items' tiles, laid end to end (sequence, rows, head),
+// are cut into equal runs, one for each CTA of a persistent grid: single tokens
+// over long caches, ragged batches and causal chunks all spread evenly over the
+// SMs. An item cut by a run's end leaves partial sums in the workspace, which a
+// second kernel joins; where whole items spread well enough nothing is cut.
+// The lengths are read on the device, so every CTA finds its run by itself.
+//
+// Kernel. Warp 8 finds the run and streams q, k and v tiles with TMA (a box per
+// page piece); warp 9 issues the MMAs: S = q k^T (128 x 128, K = D) into tensor
+// memory, then O += P v with P read from tensor memory, where it takes the place
+// of S. Warps 0-3 and 4-7 are two softmax streams: they turn a tile of S into
+// P = bf16(exp2(kx S - c)), one row to a thread. Items of two halves give each
+// stream a half and both the same keys; items of one half give the streams every
+// other tile, and their sums are joined at the end. While a stream works on its
+// S, the tensor cores run the other's products.
+//
+// c, the row's scale, moves in steps of 16 (powers of two: 2^16) and only up, so
+// all but a few tiles leave it where it is; when it moves, the stream itself
+// multiplies its O and sum by the exact power of two.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,115 +40,822 @@
 namespace cc {
 namespace {
 
-constexpr int kHeadsThreads = 128;
+constexpr int kAhThreads = 320;   // 8 softmax warps, TMA, MMA
+constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
+constexpr int kAhKeys = 128;      // keys per tile
+constexpr int kAhHalf = 128;      // rows per half
+constexpr int kAhBlockBytes = 128 * 128;  // 128 rows x 64 channels
+constexpr int kAhItems = 4;       // item descriptors in flight
+constexpr float kAhGrain = 16.f;  // step of a row's scale c, in powers of two
+// Tiles that cutting items costs a call, in time of its critical path: the
+// partial sums' way through L2 and the joining kernel.
+constexpr int kAhSplitCost = 4;
 
-struct HeadsArgs {
-  const __nv_bfloat16 *q, *k, *v;
-  __nv_bfloat16* o;
+struct AhArgs {
   KvPlan plan;      // q_offsets nullptr: sequence b owns rows b * lq .. (b + 1) * lq - 1; page_table nullptr: page b
   int lq;
-  long long rows;
-  int heads, group, d;
-  long long ld_q, ld_o, k_page, k_token, k_head, v_page, v_token, v_head;
+  int rows, heads, kv_heads, group, d;
+  int tq;           // tokens of a half: 128 / group
+  int box;          // slots per TMA box: pieces of this size never cross a page
+  __nv_bfloat16* o;
+  long long ld_o;
   float kx;         // scale * log2(e)
-  int block;
+  unsigned block;   // causal block, 0: none
+  int may_split;
+  int slot_rows;    // rows a partial slot holds
+  float* part;      // [2 * ctas][slot_rows][d]
+  float2* part_cl;  // [2 * ctas][slot_rows] (c, l)
+  int4* meta;       // [2 * ctas]: 0 unused, 1 goes on, 2 ends its item; first row, tokens, head
   unsigned int* err;
+  unsigned long long timeout_ns;
 };
 
-__global__ void __launch_bounds__(kHeadsThreads) attn_heads_simple_kernel(const __grid_constant__ HeadsArgs a) {
-  __shared__ float sq[kHeadsThreads / 32][128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && a.plan.q_offsets) {
-    for (int b = threadIdx.x; b < a.plan.seqs; b += kHeadsThreads) {
-      if (a.plan.q_offsets[b + 1] < a.plan.q_offsets[b] || a.plan.q_offsets[b + 1] > a.rows)
-        atomicOr(a.err, DEVERR_BOUNDS);
-    }
-  }
-  const long long unit = static_cast<long long>(blockIdx.x) * (kHeadsThreads / 32) + warp;
-  if (unit >= a.rows * a.heads) return;
-  const int r = static_cast<int>(unit / a.heads), h = static_cast<int>(unit % a.heads), hk = h / a.group;
-  int seq, begin, end;
+// A piece of an item, as the roles of a CTA pass it on.
+struct __align__(16) AhItem {
+  int q_row;        // row of the item's first token
+  int tokens;       // of the item
+  int head;         // key head
+  int t_begin, t_end, t_all;  // this piece's key tiles, of all
+  int len;          // keys of the sequence
+  int first;        // the item's first token among the new ones
+  int fresh;        // new tokens of the sequence
+  int slot;         // partial slot, -1: the whole item
+  int seq;
+  int last;         // no item: the CTA is done
+};
+
+struct Seq {
+  int begin, n, len, m;  // first row, new tokens, keys, items along the rows
+};
+
+__device__ __forceinline__ Seq load_seq(const AhArgs& a, int b) {
+  Seq s = {0, 0, 0, 0};
+  if (b >= a.plan.seqs) return s;
   if (a.plan.q_offsets) {
-    int lo = 0, hi = a.plan.seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.plan.q_offsets[mid] <= r) lo = mid; else hi = mid;
+    s.begin = a.plan.q_offsets[b];
+    const int end = a.plan.q_offsets[b + 1];
+    s.len = a.plan.kv_lens[b];
+    const long long n = static_cast<long long>(end) - s.begin;
+    if (n != 0 && (n < 0 || s.begin < 0 || end > a.rows || s.len < 0 || (a.block && s.len < n) ||
+                   s.len > static_cast<long long>(a.plan.max_pages) * a.plan.page_size)) {
+      atomicOr(a.err, DEVERR_BOUNDS);
+      return {0, 0, 0, 0};
     }
-    seq = lo;
-    begin = a.plan.q_offsets[seq];
-    end = a.plan.q_offsets[seq + 1];
-    if (r < begin || r >= end) return;
+    s.n = static_cast<int>(n);
   } else {
-    seq = r / a.lq;
-    begin = seq * a.lq;
-    end = begin + a.lq;
+    s.begin = b * a.lq;
+    s.n = a.lq;
+    s.len = a.plan.page_size;
+    if (a.plan.kv_lens) {
+      const int len = a.plan.kv_lens[b];
+      if (len < 0 || len > s.len) atomicOr(a.err, DEVERR_BOUNDS);
+      s.len = max(0, min(len, s.len));
+    }
   }
-  const long long most = static_cast<long long>(a.plan.max_pages) * a.plan.page_size;
-  long long len = a.plan.kv_lens ? a.plan.kv_lens[seq] : a.plan.page_size;
-  const int n = end - begin;
-  if (len < 0 || len > most || (a.block > 0 && len < n)) {
-    if (lane == 0) atomicOr(a.err, DEVERR_BOUNDS);
-    len = len < 0 ? 0 : len > most ? most : len;
-  }
-  const int i = r - begin;
-  long long limit = len;
-  if (a.block > 0) limit = len - n + min(static_cast<long long>(n), (static_cast<long long>(i) / a.block + 1) * a.block);
-  for (int c = lane; c < a.d; c += 32) sq[warp][c] = __bfloat162float(a.q[r * a.ld_q + h * a.d + c]);
-  __syncwarp();
-  float m = __int_as_float(0xff800000u), l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (long long j0 = 0; j0 < limit; j0 += 32) {
-    const long long j = j0 + lane;
-    float s = __int_as_float(0xff800000u);
-    long long vrow = -1;
-    if (j < limit) {
-      int page = seq, slot = static_cast<int>(j);
-      if (a.plan.page_table) {
-        const int pg = static_cast<int>(j / a.plan.page_size);
-        slot = static_cast<int>(j - static_cast<long long>(pg) * a.plan.page_size);
-        page = a.plan.page_table[static_cast<long long>(seq) * a.plan.max_pages + pg];
-      }
-      if (page < 0 || page >= a.plan.pages) {
-        atomicOr(a.err, DEVERR_BOUNDS);
-      } else {
-        const uint4* kp = reinterpret_cast<const uint4*>(a.k + page * a.k_page + slot * a.k_token + hk * a.k_head);
-        vrow = page * a.v_page + slot * a.v_token + hk * a.v_head;
-        float dot = 0.f;
-        for (int c = 0; c < a.d / 8; ++c) {
-          const Vec8 f = unpack8(kp[c]);
+  s.m = (s.n + 2 * a.tq - 1) / (2 * a.tq);
+  return s;
+}
+
+// How many of a sequence's keys its i-th new token sees.
+__device__ __forceinline__ int key_limit(unsigned block, int n, int len, int i) {
+  if (block == 0) return len;
+  const unsigned end = (static_cast<unsigned>(i) / block + 1) * block;
+  return len - n + static_cast<int>(min(static_cast<unsigned>(n), end));
+}
+
+// Key tiles of the m-th item of a sequence.
+__device__ __forceinline__ int item_tiles(const AhArgs& a, int n, int len, int m) {
+  const int lim = key_limit(a.block, n, len, min(n, (m + 1) * 2 * a.tq) - 1);
+  return static_cast<int>((static_cast<unsigned>(lim) + kAhKeys - 1) / kAhKeys);
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(f[e], sq[warp][c * 8 + e], dot);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Units of work (tiles, at least one to an item) of lane's sequence over all
+// heads. Whole warps call it: the items of a causal sequence are summed by all
+// lanes.
+__device__ __forceinline__ long long seq_units(const AhArgs& a, const Seq& s, int lane) {
+  long long w = 0;
+  if (s.m > 0 && (a.block == 0 || s.m == 1))
+    w = static_cast<long long>(s.m) * max(1, item_tiles(a, s.n, s.len, s.m - 1));
+  unsigned todo = __ballot_sync(0xffffffffu, s.m > 1 && a.block != 0);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
+    const int m = __shfl_sync(0xffffffffu, s.m, src);
+    long long sum = 0;
+    for (int i = lane; i < m; i += 32) sum += max(1, item_tiles(a, n, len, i));
+    sum = warp_sum(sum);
+    if (lane == src) w = sum;
+  }
+  return w * a.kv_heads;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// A CTA's run of units [at, end) and where it stands: sequence, item, head and
+// tile. All lanes of a warp hold the same values.
+struct Run {
+  long long at, end;
+  bool split;
+  int b;
+  Seq s;
+  int m, h, t, t_all;
+};
+
+// Finds the CTA's run; false if it is empty.
+__device__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
+  long long units = 0, items = 0;
+  int most = 0;
+  Seq s = {};
+  long long w = 0;
+  for (int b0 = 0; b0 < a.plan.seqs; b0 += 32) {
+    s = load_seq(a, b0 + lane);
+    w = seq_units(a, s, lane);
+    units += w;
+    items += static_cast<long long>(s.m) * a.kv_heads;
+    if (s.m > 0) most = max(most, item_tiles(a, s.n, s.len, s.m - 1));
+  }
+  units = warp_sum(units);
+  items = warp_sum(items);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (units == 0) return false;
+  const long long per = max(2ll, (units + ctas - 1) / ctas);
+  const long long whole = max(static_cast<long long>(most), ((items + ctas - 1) / ctas * units + items - 1) / items);
+  r.split = a.may_split && whole > per + kAhSplitCost;
+  r.at = cta * per;
+  r.end = min(units, r.at + per);
+  if (r.at >= units) return false;
+  // the sequence, item, head and tile of unit r.at
+  long long before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    if (a.plan.seqs > 32) {  // else the lanes still hold the only ones
+      s = load_seq(a, b0 + lane);
+      w = seq_units(a, s, lane);
+    }
+    const long long upto = before + warp_scan(w, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, r.at < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.b = b0 + src;
+      r.s = {__shfl_sync(0xffffffffu, s.begin, src), __shfl_sync(0xffffffffu, s.n, src),
+             __shfl_sync(0xffffffffu, s.len, src), __shfl_sync(0xffffffffu, s.m, src)};
+      before = __shfl_sync(0xffffffffu, upto - w, src);
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  long long rest = r.at - before;
+  for (int m0 = 0;; m0 += 32) {
+    const int m = m0 + lane;
+    const int tiles = m < r.s.m ? max(1, item_tiles(a, r.s.n, r.s.len, m)) : 0;
+    const long long upto = warp_scan(static_cast<long long>(tiles) * a.kv_heads, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, rest < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.m = m0 + src;
+      const int t_all = __shfl_sync(0xffffffffu, tiles, src);
+      rest -= __shfl_sync(0xffffffffu, upto, src) - static_cast<long long>(t_all) * a.kv_heads;
+      r.t_all = t_all;
+      r.h = static_cast<int>(rest / t_all);
+      r.t = static_cast<int>(rest - static_cast<long long>(r.h) * t_all);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return true;
+}
+
+// On to the next item (its units start at r.at).
+__device__ __forceinline__ void next_item(const AhArgs& a, Run& r) {
+  r.t = 0;
+  if (++r.h < a.kv_heads) return;
+  r.h = 0;
+  if (++r.m >= r.s.m) {
+    r.m = 0;
+    do {
+      r.s = load_seq(a, ++r.b);
+    } while (r.s.m == 0 && r.b < a.plan.seqs);
+    if (r.s.m == 0) return;
+  }
+  r.t_all = max(1, item_tiles(a, r.s.n, r.s.len, r.m));
+}
+
+// 2^(c - top) for scales c <= top: a power of two, 0 where it would be subnormal
+// (or c is -inf), 1 where both are the same infinity.
+__device__ __forceinline__ float pow2_diff(float c, float top) {
+  if (c == top) return 1.f;
+  const float e = c - top;
+  return e > -127.f ? __int_as_float((127 + static_cast<int>(e)) << 23) : 0.f;
+}
+
+constexpr float kNegInf = -INFINITY;
+// c of a row all of whose visible scores are -inf: its sum is 0 and its result NaN
+constexpr float kNoScore = -3.0e38f;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+
+// NB: 64-channel blocks of a head; STAGES: k or v tiles in flight.
+template <int NB, int STAGES>
+struct AhSmem {
+  static constexpr int kTile = NB * kAhBlockBytes;
+  static constexpr int kQ = 2 * kTile;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 4;
+};
+
+template <int NB, int STAGES>
+__global__ void __launch_bounds__(kAhThreads, 1)
+    attn_heads_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AhArgs a) {
+  using Sm = AhSmem<NB, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = sQ + Sm::kQ;
+  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // stream 1's (c, l) of single halves
+  AhItem* items = reinterpret_cast<AhItem*>(sCL + kAhHalf);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_empty = kv_full + STAGES;
+  uint64_t* item_full = kv_empty + STAGES;
+  uint64_t* item_empty = item_full + kAhItems;
+  uint64_t* q_full = item_empty + kAhItems;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_ready = q_empty + 1;  // [2] S of a stream complete
+  uint64_t* p_ready = s_ready + 2;  // [2] P of a stream written, and O on its scale
+  uint64_t* pv_done = p_ready + 2;  // [2] the last product of a stream complete
+  uint64_t* o_free = pv_done + 2;   // [2] O of a stream read out
+  uint64_t* cl_ready = o_free + 2;
+  uint64_t* done = cl_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&kv_full[i]), 1);
+      mbar_init(smem_u32(&kv_empty[i]), 1);
+    }
+    for (int i = 0; i < kAhItems; ++i) {
+      mbar_init(smem_u32(&item_full[i]), 1);
+      mbar_init(smem_u32(&item_empty[i]), 9);
+    }
+    mbar_init(smem_u32(q_full), 1);
+    mbar_init(smem_u32(q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_ready[i]), 1);
+      mbar_init(smem_u32(&p_ready[i]), 4);
+      mbar_init(smem_u32(&pv_done[i]), 1);
+      mbar_init(smem_u32(&o_free[i]), 4);
+    }
+    mbar_init(smem_u32(cl_ready), 4);
+    mbar_init(smem_u32(done), 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint64_t tlim = a.timeout_ns;
+
+  if (warp == 8) {
+    // -------------------------------------------- run, items and TMA loads --
+    Run r;
+    bool ok = true, any = find_run(a, blockIdx.x, gridDim.x, lane, r);
+    if (a.may_split && lane < 2) a.meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+    __syncwarp();
+    int stage = 0, slot = 0;
+    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
+    // one tile of keys (or values): a box per piece of a page, a lane to a box
+    auto load_tile = [&](const CUtensorMap* map, int b, int h, int len, int t) {
+      const int boxes = (min(kAhKeys, len - t * kAhKeys) + a.box - 1) / a.box;
+      int page = b, at = t * kAhKeys + lane * a.box;
+      if (lane < boxes && a.plan.page_table) {
+        const int n = at / a.plan.page_size;
+        at -= n * a.plan.page_size;
+        page = a.plan.page_table[static_cast<long long>(b) * a.plan.max_pages + n];
+        if (page < 0 || page >= a.plan.pages) {
+          atomicOr(a.err, DEVERR_BOUNDS);
+          page = a.plan.pages;  // out of the map's range: the box reads as zeros
         }
-        s = dot * a.kx;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_empty[stage]), kv_ph ^ 1u, a.err, tlim))) return false;
+      const uint32_t full = smem_u32(&kv_full[stage]);
+      if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * a.box * 128 * NB));
+      __syncwarp();
+      if (lane < boxes) {
+        const uint32_t dst = smem_u32(sKV + stage * Sm::kTile) + static_cast<uint32_t>(lane * a.box) * 128u;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) tma_load_4d(dst + i * kAhBlockBytes, map, full, i * 64, h, at, page);
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        kv_ph ^= 1u;
+      }
+      return true;
+    };
+    if (any && !r.split && r.t > 0) {  // whole items: from the first one that starts in the run
+      r.at += r.t_all - r.t;
+      next_item(a, r);
+    }
+    while (ok) {
+      const bool more = any && r.at < r.end && r.b < a.plan.seqs;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_empty[slot]), it_ph ^ 1u, a.err, tlim))) {
+        ok = false;
+        break;
+      }
+      AhItem it = {};
+      it.last = !more;
+      if (more) {
+        it.first = r.m * 2 * a.tq;
+        it.tokens = min(2 * a.tq, r.s.n - it.first);
+        it.q_row = r.s.begin + it.first;
+        it.head = r.h;
+        it.len = r.s.len;
+        it.fresh = r.s.n;
+        it.seq = r.b;
+        it.t_all = item_tiles(a, r.s.n, r.s.len, r.m);
+        it.t_begin = r.t;
+        it.t_end = r.split ? static_cast<int>(min(static_cast<long long>(it.t_all), r.t + (r.end - r.at))) : it.t_all;
+        it.slot = -1;
+        if (it.t_begin > 0 || it.t_end < it.t_all) {
+          const int which = it.t_begin > 0 ? 0 : 1;
+          it.slot = 2 * blockIdx.x + which;
+          if (lane == 0) {
+            a.meta[it.slot] = make_int4(it.t_end < it.t_all ? 1 : 2, it.q_row, it.tokens, it.head);
+          }
+        }
+      }
+      if (lane == 0) {
+        items[slot] = it;
+        mbar_arrive(smem_u32(&item_full[slot]));  // releases the descriptor
+      }
+      __syncwarp();
+      if (++slot == kAhItems) {
+        slot = 0;
+        it_ph ^= 1u;
+      }
+      if (!more) break;
+      const int n = it.t_end - it.t_begin;
+      if (n > 0) {
+        const bool two = it.tokens > a.tq;
+        const int ahead = two ? 1 : 2;
+        for (int t = 0; ok && t < min(ahead, n); ++t) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t);
+        if (!ok) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_empty), q_ph ^ 1u, a.err, tlim))) {
+          ok = false;
+          break;
+        }
+        q_ph ^= 1u;
+        if (lane == 0) {
+          const uint32_t full = smem_u32(q_full);
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>((two ? 2 : 1) * NB * a.tq * a.group * 128));
+          for (int s = 0; s < (two ? 2 : 1); ++s)
+            for (int i = 0; i < NB; ++i)
+              tma_load_4d(smem_u32(sQ + s * Sm::kTile + i * kAhBlockBytes), &tmQ, full, i * 64, it.head * a.group,
+                          it.q_row + s * a.tq, 0);
+        }
+        __syncwarp();
+        for (int t = 0; ok && t < n; ++t) {
+          ok = load_tile(&tmV, it.seq, it.head, it.len, it.t_begin + t);
+          if (ok && t + ahead < n) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t + ahead);
+        }
+      }
+      r.at += max(1, n);
+      next_item(a, r);
+    }
+    if (!ok) {  // copies in flight land before the CTA goes
+      for (int i = 0; i < STAGES; ++i)
+        (void)mbar_wait(smem_u32(&kv_full[i]), (i < stage) ? kv_ph : (kv_ph ^ 1u), a.err, 200000000ull);
+      (void)mbar_wait(smem_u32(q_full), q_ph ^ 1u, a.err, 200000000ull);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMA --
+    const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
+    const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
+    const int steps = a.d / 16;
+    const uint64_t q0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t k0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
+    const uint64_t v0 = sdesc_sw128(smem_u32(sKV), kAhBlockBytes, 1024);
+    int stage = 0, slot = 0;
+    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
+    uint32_t p_ph = 0, of_ph = 0;  // a bit per stream
+    bool used[2] = {false, false};  // the stream's O was written by an item before
+    bool ok = true;
+    auto next_tile = [&](int& at) {  // waits for the next k or v tile
+      at = stage;
+      const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[stage]), kv_ph, a.err, tlim));
+      if (++stage == STAGES) {
+        stage = 0;
+        kv_ph ^= 1u;
+      }
+      tc_fence_after();
+      return got;
+    };
+    auto scores = [&](int s, int half, int at, bool release, bool q_last) {
+      const uint64_t ad = q0 + static_cast<uint64_t>(half) * (Sm::kTile >> 4);
+      const uint64_t bd = k0 + static_cast<uint64_t>(at) * (Sm::kTile >> 4);
+      if (elect_one()) {
+        for (int k = 0; k < steps; ++k) {
+          const uint64_t off = (k >> 2) * (kAhBlockBytes >> 4) + (k & 3) * 2;
+          mma_bf16(tmem + s * 128, ad + off, bd + off, idesc_s, k ? 1u : 0u);
+        }
+        mma_commit(smem_u32(&s_ready[s]));
+        if (release) mma_commit(smem_u32(&kv_empty[at]));
+        if (q_last) mma_commit(smem_u32(q_empty));
+      }
+      __syncwarp();
+    };
+    while (ok) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
+      const AhItem it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
+      if (++slot == kAhItems) {
+        slot = 0;
+        it_ph ^= 1u;
+      }
+      if (it.last) break;
+      const int n = it.t_end - it.t_begin;
+      if (n <= 0) continue;
+      const bool two = it.tokens > a.tq;
+      const int jobs = two ? 2 * n : n;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_full), q_ph, a.err, tlim))) break;
+      q_ph ^= 1u;
+      tc_fence_after();
+      int ks = 0, vs = 0;
+      // the first scores of both streams
+      for (int j = 0; ok && j < min(2, jobs); ++j) {
+        if (!two || j == 0) ok = next_tile(ks);
+        if (ok) scores(j, two ? j : 0, ks, !two || j == 1, j == jobs - 1 );
+      }
+      for (int j = 0; ok && j < jobs; ++j) {
+        const int s = j & 1;
+        if (!two || s == 0) {
+          ok = next_tile(vs);
+          if (!ok) break;
+          const int t = it.t_begin + (two ? j >> 1 : j);
+          const int valid = it.len - t * kAhKeys;
+          if (valid < kAhKeys) {
+            // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
+            uint8_t* base = sKV + vs * Sm::kTile;
+            for (int i = lane; i < (kAhKeys - valid) * 8; i += 32) {
+#pragma unroll
+              for (int blk = 0; blk < NB; ++blk)
+                *reinterpret_cast<uint4*>(base + blk * kAhBlockBytes + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        // the last item's sums of the streams that this one writes have been read
+        if (j == 0 || (two && j == 1)) {
+          for (int o = s; o < (two ? s + 1 : 2); ++o) {
+            if (!used[o]) continue;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[o]), (of_ph >> o) & 1u, a.err, tlim));
+            of_ph ^= 1u << o;
+          }
+        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[s]), (p_ph >> s) & 1u, a.err, tlim));
+        if (!ok) break;
+        p_ph ^= 1u << s;
+        tc_fence_after();
+        const uint64_t bd = v0 + static_cast<uint64_t>(vs) * (Sm::kTile >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kAhKeys / 16; ++k)
+            mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + k * 8, bd + k * 128, idesc_o, (j < 2 && k == 0) ? 0u : 1u);
+          mma_commit(smem_u32(&pv_done[s]));
+          if (!two || s == 1) mma_commit(smem_u32(&kv_empty[vs]));
+        }
+        __syncwarp();
+        if (j + 2 < jobs) {
+          if (!two || s == 0) ok = next_tile(ks);
+          if (ok) scores(s, two ? s : 0, ks, !two || s == 1, j + 2 == jobs - 1);
+        }
+      }
+      // who reads this item's sums arrives on o_free of both streams, or each stream on its own
+      used[0] = used[1] = true;
+    }
+    if (elect_one()) mma_commit(smem_u32(done));
+    __syncwarp();
+    (void)mbar_wait(smem_u32(done), 0, a.err, tlim);
+  } else {
+    // -------------------------------------------------------------- softmax --
+    const int s = warp >> 2;  // stream
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t sCol = tmem + lanes + s * 128;
+    const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+    int slot = 0;
+    uint32_t it_ph = 0, s_ph = 0, cl_ph = 0;
+    uint32_t pv_ph[2] = {0, 0};  // products of each stream so far
+    bool ok = true;
+    while (ok) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
+      const AhItem it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
+      if (++slot == kAhItems) {
+        slot = 0;
+        it_ph ^= 1u;
+      }
+      if (it.last) break;
+      const int n = it.t_end - it.t_begin;
+      const bool two = it.tokens > a.tq;
+      const int tok = (two ? s * a.tq : 0) + row_tok;  // of the item
+      const bool row_ok = row < a.tq * a.group && tok < it.tokens;
+      const int limit = row_ok ? key_limit(a.block, it.fresh, it.len, it.first + tok) : 0x7fffffff;
+      const bool active = __any_sync(0xffffffffu, row_ok);
+      const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
+      float c = kNegInf, l = 0.f;
+      for (int i = 0; ok && i < mine; ++i) {
+        const int t = it.t_begin + (two ? i : 2 * i + s);
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[s]), s_ph, a.err, tlim))) {
+          ok = false;
+          break;
+        }
+        s_ph ^= 1u;
+        if (active) {
+          tc_fence_after();
+          uint32_t sv[128];
+          tmem_ld128_wait(sCol, sv);
+          const int lim = limit - t * kAhKeys;
+          if (__any_sync(0xffffffffu, lim < kAhKeys)) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
+          }
+          float m0 = kNegInf, m1 = kNegInf;
+#pragma unroll
+          for (int e = 0; e < 128; e += 4) {
+            m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
+            m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
+          }
+          const float up = ceilf(fmaxf(m0, m1) * a.kx * (1.f / kAhGrain)) * kAhGrain;
+          const bool moves = row_ok && up > c;
+          if (__any_sync(0xffffffffu, moves)) {
+            const float top = moves ? up : c;
+            const float f = pow2_diff(c, top);
+            if (i > 0) {  // O is on the old scale; the stream's last product has to be complete
+              if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph[s] - 1) & 1u, a.err, tlim))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              for (int col = 0; col < a.d; col += 16) {
+                uint32_t o[16];
+                tmem_ld16(tmem + lanes + 256 + s * 128 + col, o);
+                tmem_wait16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(tmem + lanes + 256 + s * 128 + col, o);
+              }
+              tmem_st_wait();
+            }
+            l *= f;
+            c = top;
+          }
+          const float base = c == kNegInf ? 0.f : c;
+          const f32x2 kx2 = pair(a.kx, a.kx), nb2 = pair(-base, -base);
+          f32x2 sum0 = pair(0.f, 0.f), sum1 = pair(0.f, 0.f);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int at = half * 64 + 2 * e;
+              const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
+              const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+              if (e & 1)
+                sum1 = add2(sum1, pair(p0, p1));
+              else
+                sum0 = add2(sum0, pair(p0, p1));
+              pk[e] = pack_bf16(p0, p1);
+            }
+            tmem_st32(sCol + half * 32, pk);
+          }
+          sum0 = add2(sum0, sum1);
+          l += lo(sum0) + hi(sum0);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        ++pv_ph[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_ready[s]));
+      }
+      if (!ok) break;
+      const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
+      if (n > 0 && !two && s == 1) {
+        // hand (c, l) over; stream 0 reads both sums
+        if (mine > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[1]), (pv_ph[1] - 1) & 1u, a.err, tlim));
+          if (!ok) break;
+          sCL[row] = make_float2(c, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(cl_ready));
+        }
+        continue;
+      }
+      if (!two && s == 1) continue;
+      float c1 = kNegInf, l1 = 0.f;
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph[s] - 1) & 1u, a.err, tlim));
+        if (ok && other > 0) {
+          // stream 1 arrives after its own last product, so that O of both is complete
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(cl_ready), cl_ph, a.err, tlim));
+          cl_ph ^= 1u;
+          const float2 cl = sCL[row];
+          c1 = cl.x;
+          l1 = cl.y;
+        }
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float top = fmaxf(c, c1);
+      const float f0 = pow2_diff(c, top), f1 = pow2_diff(c1, top);
+      const float sum = l * f0 + l1 * f1;
+      if (active || n == 0) {
+        if (it.slot < 0) {
+          const bool sees = n > 0 && limit > 0;
+          const float inv = 1.f / sum;
+          __nv_bfloat16* dst = a.o + static_cast<long long>(it.q_row + tok) * a.ld_o +
+                               static_cast<long long>(it.head * a.group + row_head) * a.d;
+          for (int col = 0; col < a.d; col += 16) {
+            uint32_t o[16] = {}, o1[16] = {};
+            if (n > 0) {
+              tmem_ld16(tmem + lanes + 256 + s * 128 + col, o);
+              if (other > 0) tmem_ld16(tmem + lanes + 384 + col, o1);
+              tmem_wait16(o);
+              tmem_wait16(o1);
+            }
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float x0 = __uint_as_float(o[2 * e]) * f0, x1 = __uint_as_float(o[2 * e + 1]) * f0;
+              if (other > 0) {
+                x0 = fmaf(__uint_as_float(o1[2 * e]), f1, x0);
+                x1 = fmaf(__uint_as_float(o1[2 * e + 1]), f1, x1);
+              }
+              pk[e] = sees ? pack_bf16(x0 * inv, x1 * inv) : 0u;
+            }
+            if (row_ok) {
+              *reinterpret_cast<uint4*>(dst + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            }
+          }
+        } else {
+          const int r = (two ? s * kAhHalf : 0) + row;
+          float* dst = a.part + (static_cast<long long>(it.slot) * a.slot_rows + r) * a.d;
+          for (int col = 0; col < a.d; col += 16) {
+            uint32_t o[16], o1[16] = {};
+            tmem_ld16(tmem + lanes + 256 + s * 128 + col, o);
+            if (other > 0) tmem_ld16(tmem + lanes + 384 + col, o1);
+            tmem_wait16(o);
+            tmem_wait16(o1);
+            if (row_ok) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  x[i] = __uint_as_float(o[e + i]) * f0;
+                  if (other > 0) x[i] = fmaf(__uint_as_float(o1[e + i]), f1, x[i]);
+                }
+                *reinterpret_cast<float4*>(dst + col + e) = make_float4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          }
+          if (row_ok) {
+            const bool sees = limit > it.t_begin * kAhKeys;
+            a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + r] =
+                make_float2(sees && top == kNegInf ? kNoScore : top, sum);
+          }
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&o_free[s]));
+          if (!two) mbar_arrive(smem_u32(&o_free[1]));
+        }
       }
     }
-    float top = s;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial sums of cut items: o = sum_p 2^(c_p - c) O_p / sum_p
+// 2^(c_p - c) l_p over the pieces p of a row, c = max_p c_p. blockIdx.x: the CTA
+// whose run an item was cut out of first; its pieces go on in the slots 0 of the
+// CTAs behind it. Rows with many pieces are shared by the CTA's warps.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __grid_constant__ AhArgs a, int ctas) {
+  __shared__ float sO[8][128];
+  __shared__ float sL[8];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int first = blockIdx.x;
+  const int4 head = a.meta[2 * first + 1];
+  if (head.x == 0) return;
+  // pieces: slot 1 of `first`, then slot 0 of the CTAs behind it up to the one that ends the item
+  int pieces = 1;
+  for (int j0 = first + 1;; j0 += 32) {
+    const int j = j0 + (threadIdx.x & 31);
+    const bool ends = j >= ctas || a.meta[2 * j].x != 1;
+    const unsigned hit = __ballot_sync(0xffffffffu, ends);
+    if (hit) {
+      pieces += __ffs(hit);
+      break;
+    }
+    pieces += 32;
+  }
+  pieces = min(pieces, ctas - first);
+  const int q_row = head.y, tokens = head.z, h = head.w;
+  const bool two = tokens > a.tq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool shared_rows = pieces > 8;
+  const int rows = tokens * a.group;
+  const int step = shared_rows ? gridDim.y : gridDim.y * 8;
+  for (int i0 = shared_rows ? blockIdx.y : blockIdx.y * 8; i0 < rows; i0 += step) {
+    const int i = shared_rows ? i0 : i0 + warp;
+    if (!shared_rows && i >= rows) break;
+    const int tok = i / a.group, g = i - tok * a.group;
+    const int r = two && tok >= a.tq ? kAhHalf + (tok - a.tq) * a.group + g : i;
+    auto slot_of = [&](int p) { return static_cast<long long>(p == 0 ? 2 * first + 1 : 2 * (first + p)) * a.slot_rows + r; };
+    float top = kNegInf;
+    for (int p = lane; p < pieces; p += 32) top = fmaxf(top, a.part_cl[slot_of(p)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float mn = fmaxf(m, top), base = mn == __int_as_float(0xff800000u) ? 0.f : mn;
-    const float f = exp2f(m - base), p = vrow >= 0 ? exp2f(s - base) : 0.f;
-    m = mn;
-    float sum = p;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * f + sum;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] *= f;
-    for (int t = 0; t < 32; ++t) {
-      const float w = __shfl_sync(0xffffffffu, p, t);
-      const long long at = __shfl_sync(0xffffffffu, vrow, t);
-      if (at < 0 || lane * 4 >= a.d) continue;
-      const uint2 raw = *reinterpret_cast<const uint2*>(a.v + at + lane * 4);
-      acc[0] = fmaf(w, __uint_as_float(raw.x << 16), acc[0]);
-      acc[1] = fmaf(w, __uint_as_float(raw.x & 0xffff0000u), acc[1]);
-      acc[2] = fmaf(w, __uint_as_float(raw.y << 16), acc[2]);
-      acc[3] = fmaf(w, __uint_as_float(raw.y & 0xffff0000u), acc[3]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    const bool on = lane * 4 < a.d;
+#pragma unroll 4
+    for (int p = shared_rows ? warp : 0; p < pieces; p += shared_rows ? 8 : 1) {
+      const long long at = slot_of(p);
+      const float2 cl = a.part_cl[at];
+      const float4 v = on ? *reinterpret_cast<const float4*>(a.part + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float f = pow2_diff(cl.x, top);
+      l = fmaf(cl.y, f, l);
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
     }
-  }
-  if (lane * 4 < a.d) {
-    const float inv = limit > 0 ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      a.o[r * a.ld_o + h * a.d + lane * 4 + e] = __float2bfloat16_rn(limit > 0 ? acc[e] * inv : 0.f);
+    if (shared_rows) {
+      *reinterpret_cast<float4*>(&sO[warp][lane * 4]) = acc;
+      if (lane == 0) sL[warp] = l;
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < 8; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(&sO[w][lane * 4]);
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+          l += sL[w];
+        }
+      }
+      __syncthreads();
+    }
+    if (on && (!shared_rows || warp == 0)) {
+      const float inv = 1.f / l;
+      const bool sees = top != kNegInf;
+      *reinterpret_cast<uint2*>(a.o + static_cast<long long>(q_row + tok) * a.ld_o +
+                                static_cast<long long>(h * a.group + g) * a.d + lane * 4) =
+          sees ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv)) : make_uint2(0u, 0u);
+    }
   }
 }
 
@@ -147,19 +873,89 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
     return fail(CC_ERR_UNSUPPORTED, "%s: at most 65536 heads, 128 to a key head", what);
   if (ld_q < (int64_t)heads * d || ld_o < (int64_t)heads * d || ld_q % 8 || ld_o % 8)
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
+  if (ld_q >= (1ll << 38) || ld_o >= (1ll << 38))
+    return fail(CC_ERR_UNSUPPORTED, "%s: row strides must be below 2^38 elements", what);
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(CC_ERR_INVALID, "%s: scale must be finite and > 0", what);
   return CC_OK;
 }
 
-cc_status launch_attn(const char* what, HeadsArgs& a, void* stream) {
+// Rows that a partial slot holds: those of a half where no item can have more.
+int slot_rows(int64_t tokens, int group) {
+  const int tq = kAhHalf / group;
+  return tokens <= tq ? static_cast<int>(tokens) * group : 2 * kAhHalf;
+}
+
+size_t part_bytes(int rows, int d) { return (size_t)2 * kAhMaxCtas * rows * d * 4; }
+
+size_t workspace_bytes(int64_t tokens, int group, int d) {
+  const int rows = slot_rows(tokens, group);
+  return part_bytes(rows, d) + (size_t)2 * kAhMaxCtas * (rows * 8 + 16);
+}
+
+struct CacheSide {
+  const cc_bf16* p;
+  int64_t page, token, head;
+};
+
+cc_status encode_side(CUtensorMap* map, const CacheSide& c, const AhArgs& a) {
+  const uint64_t dims[4] = {(uint64_t)a.d, (uint64_t)a.kv_heads, (uint64_t)a.plan.page_size, (uint64_t)a.plan.pages};
+  const uint64_t strides[3] = {2ull * c.head, 2ull * c.token, 2ull * c.page};
+  return encode_tiled_4d(map, c.p, dims, strides, 64, 1, a.box);
+}
+
+template <int NB, int STAGES>
+cc_status launch_attn(const char* what, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, AhArgs& a,
+                      int grid, cudaStream_t stream) {
+  auto kern = attn_heads_kernel<NB, STAGES>;
+  constexpr int kSmem = AhSmem<NB, STAGES>::kBytes;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
+  e = launch_pdl(kern, dim3(grid), dim3(kAhThreads), kSmem, stream, tq, tk, tv, a);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+  return launch_status(what);
+}
+
+// keys: no sequence has more.
+cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, const CacheSide& k, const CacheSide& v,
+                   int64_t keys, int64_t max_tokens, void* ws, size_t ws_bytes, void* stream) {
+  a.group = a.heads / a.kv_heads;
+  a.tq = kAhHalf / a.group;
+  a.may_split = (keys + kAhKeys - 1) / kAhKeys > kAhSplitCost;
+  a.slot_rows = slot_rows(max_tokens, a.group);
+  if (a.may_split) {
+    const size_t need = workspace_bytes(max_tokens, a.group, a.d);
+    if (!ws) return fail(CC_ERR_INVALID, "%s: null workspace", what);
+    if (!aligned16(ws)) return fail(CC_ERR_INVALID, "%s: pointers must be 16-byte aligned", what);
+    if (ws_bytes < need) return fail(CC_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", what, ws_bytes, need);
+    a.part = static_cast<float*>(ws);
+    a.part_cl = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_bytes(a.slot_rows, a.d));
+    a.meta = reinterpret_cast<int4*>(a.part_cl + (size_t)2 * kAhMaxCtas * a.slot_rows);
+  }
   DeviceInfo di;
-  const cc_status st = device_info(&di);
+  cc_status st = device_info(&di);
   if (st != CC_OK) return st;
   a.err = di.err_word;
-  const long long units = a.rows * a.heads, ctas = (units + 3) / 4;
-  if (ctas > 0x7fffffffLL) return fail(CC_ERR_UNSUPPORTED, "%s: too many rows", what);
-  attn_heads_simple_kernel<<<static_cast<unsigned>(ctas), kHeadsThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.timeout_ns = kWaitLimitNs;
+  CUtensorMap tq = {}, tk = {}, tv = {};
+  const uint64_t qdims[4] = {(uint64_t)a.d, (uint64_t)a.heads, (uint64_t)a.rows, 1};
+  const uint64_t qstrides[3] = {2ull * a.d, 2ull * ld_q, 2ull * ld_q};
+  if ((st = encode_tiled_4d(&tq, q, qdims, qstrides, 64, a.group, a.tq)) != CC_OK) return st;
+  if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
+  const int grid = std::min(kAhMaxCtas, di.sm_count);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  st = a.d > 64 ? launch_attn<2, 5>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 12>(what, tq, tk, tv, a, grid, cs);
+  if (st != CC_OK || !a.may_split) return st;
+  // the joining kernel's CTAs: a row to each where few items are cut into many pieces, else eight
+  const int join_y = a.slot_rows <= 32 ? a.slot_rows : a.slot_rows / 8;
+  const cudaError_t e = launch_pdl(attn_heads_join_kernel, dim3(grid, join_y), dim3(kJoinThreads), 0, cs, a, grid);
+  if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
+}
+
+bool sizes_ok(int64_t heads, int64_t kv_heads, int64_t d) {
+  return heads > 0 && kv_heads > 0 && heads % kv_heads == 0 && heads / kv_heads <= kAhHalf && d > 0 && d % 16 == 0 &&
+         d <= 128;
 }
 
 }  // namespace
@@ -167,9 +963,15 @@ cc_status launch_attn(const char* what, HeadsArgs& a, void* stream) {
 
 using namespace cc;
 
-extern "C" size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d) { return 0; }
+extern "C" size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d) {
+  if (rows <= 0 || seqs <= 0 || !sizes_ok(heads, kv_heads, d)) return 0;
+  return workspace_bytes(rows, heads / kv_heads, d);
+}
 
-extern "C" size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d) { return 0; }
+extern "C" size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d) {
+  if (n <= 0 || lq <= 0 || lk <= kAhSplitCost * kAhKeys || !sizes_ok(heads, kv_heads, d)) return 0;
+  return workspace_bytes(lq, heads / kv_heads, d);
+}
 
 extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16* v_cache, cc_bf16* o,
                                    const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table,
@@ -185,24 +987,21 @@ extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, con
   if ((st = check_cache_strides(what, k_page, k_token, k_head, d)) != CC_OK ||
       (st = check_cache_strides(what, v_page, v_token, v_head, d)) != CC_OK)
     return st;
+  if (rows > 1 << 30) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
   if (causal_block < 0) return fail(CC_ERR_INVALID, "%s: the causal block must not be negative", what);
-  HeadsArgs a = {};
-  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  a.k = reinterpret_cast<const __nv_bfloat16*>(k_cache);
-  a.v = reinterpret_cast<const __nv_bfloat16*>(v_cache);
-  a.o = reinterpret_cast<__nv_bfloat16*>(o);
+  AhArgs a = {};
   a.plan = {q_offsets, kv_lens, page_table, seqs, max_pages, pages, page_size};
   a.rows = rows;
   a.heads = heads;
-  a.group = heads / kv_heads;
+  a.kv_heads = kv_heads;
   a.d = d;
-  a.ld_q = ld_q;
+  a.box = std::min(kAhKeys, page_size & -page_size);
+  a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
-  a.k_page = k_page, a.k_token = k_token, a.k_head = k_head;
-  a.v_page = v_page, a.v_token = v_token, a.v_head = v_head;
   a.kx = scale * 1.4426950408889634f;
-  a.block = causal_block;
-  return launch_attn(what, a, stream);
+  a.block = std::min(causal_block, 1 << 30);
+  return run_attn(what, a, q, ld_q, {k_cache, k_page, k_token, k_head}, {v_cache, v_page, v_token, v_head},
+                  (int64_t)max_pages * page_size, rows, ws, ws_bytes, stream);
 }
 
 extern "C" cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_bf16* v, cc_bf16* o,
@@ -217,22 +1016,19 @@ extern "C" cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_
   if (!aligned16(kv_lens)) return fail(CC_ERR_INVALID, "%s: pointers must be 16-byte aligned", what);
   if (ld_k < (int64_t)kv_heads * d || ld_v < (int64_t)kv_heads * d || ld_k % 8 || ld_v % 8)
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
-  if ((int64_t)n * lq > 0x7fffffffLL) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^31 - 1 query rows", what);
-  HeadsArgs a = {};
-  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  a.k = reinterpret_cast<const __nv_bfloat16*>(k);
-  a.v = reinterpret_cast<const __nv_bfloat16*>(v);
-  a.o = reinterpret_cast<__nv_bfloat16*>(o);
+  if ((int64_t)n * lq > 1 << 30) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
+  if ((double)ld_k * lk >= 0x1p38 || (double)ld_v * lk >= 0x1p38)
+    return fail(CC_ERR_UNSUPPORTED, "%s: an instance's keys must lie within 2^38 elements", what);
+  AhArgs a = {};
   a.plan = {nullptr, kv_lens, nullptr, n, 1, n, lk};
   a.lq = lq;
-  a.rows = static_cast<long long>(n) * lq;
+  a.rows = n * lq;
   a.heads = heads;
-  a.group = heads / kv_heads;
+  a.kv_heads = kv_heads;
   a.d = d;
-  a.ld_q = ld_q;
+  a.box = kAhKeys;
+  a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
-  a.k_page = ld_k * lk, a.k_token = ld_k, a.k_head = d;
-  a.v_page = ld_v * lk, a.v_token = ld_v, a.v_head = d;
   a.kx = scale * 1.4426950408889634f;
-  return launch_attn(what, a, stream);
+  return run_attn(what, a, q, ld_q, {k, ld_k * lk, ld_k, d}, {v, ld_v * lk, ld_v, d}, lk, lq, ws, ws_bytes, stream);
 }

@@ -105,11 +105,11 @@ ATTN = [({n: None}, 1, NULLS) for n in ("q", "o")] + [
 
 def test_attention_refusals(lib, p):
     refusals(lib, p, "cc_attn_paged", PAGED, ATTN + PLAN + [
-        (dict(rows=-1), 1, "negative"), (dict(causal_block=-1), 1, "causal block"), (dict(v_cache=None), 1, NULLS)])
+        (dict(rows=-1), 1, "negative"), (dict(rows=(1 << 30) + 1), 2, "2^30"), (dict(causal_block=-1), 1, "causal block"), (dict(v_cache=None), 1, NULLS)])
     refusals(lib, p, "cc_attn_cross", CROSS, ATTN + [
         (dict(k=None), 1, NULLS), (dict(v=None), 1, NULLS), (dict(n=-1), 1, "negative"), (dict(lq=-1), 1, "negative"),
         (dict(lk=-1), 1, "negative"), (dict(kv_lens=8), 1, "aligned"), (dict(ld_k=120), 1, "strides"),
-        (dict(ld_v=132), 1, "strides"), (dict(n=1 << 16, lq=1 << 16), 2, "2^31")])
+        (dict(ld_v=132), 1, "strides"), (dict(n=1 << 16, lq=1 << 16), 2, "2^30")])
     assert call(lib, "cc_attn_paged", PAGED, None, rows=0)[0] == 0
     assert call(lib, "cc_attn_paged", PAGED, None, seqs=0)[0] == 0
     assert call(lib, "cc_attn_cross", CROSS, None, n=0)[0] == 0
