@@ -40,7 +40,9 @@
 namespace cc {
 namespace {
 
-constexpr int kAhThreads = 320;   // 8 softmax warps, TMA, MMA
+constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
+constexpr int kAhMmaWarp = 17;
+constexpr int kAhThreads = 576;
 constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
 constexpr int kAhKeys = 128;      // keys per tile
 constexpr int kAhHalf = 128;      // rows per half
@@ -281,7 +283,7 @@ template <int NB, int STAGES>
 struct AhSmem {
   static constexpr int kTile = NB * kAhBlockBytes;
   static constexpr int kQ = 2 * kTile;
-  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 4;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 8 + 4 * kAhHalf * 4;
 };
 
 template <int NB, int STAGES>
@@ -293,8 +295,9 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + Sm::kQ;
-  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // stream 1's (c, l) of single halves
-  AhItem* items = reinterpret_cast<AhItem*>(sCL + kAhHalf);
+  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // [2][128] stream 1's (c, l) of single halves
+  float* sX = reinterpret_cast<float*>(sCL + 2 * kAhHalf);            // [4][128] what warps of the same rows exchange
+  AhItem* items = reinterpret_cast<AhItem*>(sX + 4 * kAhHalf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + STAGES;
@@ -319,21 +322,21 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 9);
+      mbar_init(smem_u32(&item_empty[i]), 17);
     }
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_ready[i]), 1);
-      mbar_init(smem_u32(&p_ready[i]), 4);
+      mbar_init(smem_u32(&p_ready[i]), 8);
       mbar_init(smem_u32(&pv_done[i]), 1);
-      mbar_init(smem_u32(&o_free[i]), 4);
+      mbar_init(smem_u32(&o_free[i]), 8);
     }
-    mbar_init(smem_u32(cl_ready), 4);
+    mbar_init(smem_u32(cl_ready), 8);
     mbar_init(smem_u32(done), 1);
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kAhMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   pdl_wait();
   const uint64_t tlim = a.timeout_ns;
 
-  if (warp == 8) {
+  if (warp == kAhTmaWarp) {
     // -------------------------------------------- run, items and TMA loads --
     Run r;
     bool ok = true, any = find_run(a, blockIdx.x, gridDim.x, lane, r);
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         (void)mbar_wait(smem_u32(&kv_full[i]), (i < stage) ? kv_ph : (kv_ph ^ 1u), a.err, 200000000ull);
       (void)mbar_wait(smem_u32(q_full), q_ph ^ 1u, a.err, 200000000ull);
     }
-  } else if (warp == 9) {
+  } else if (warp == kAhMmaWarp) {
     // ------------------------------------------------------------------ MMA --
     const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
     const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
@@ -552,6 +555,11 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 #pragma unroll
           for (int k = 0; k < kAhKeys / 16; ++k)
             mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + k * 8, bd + k * 128, idesc_o, (j < 2 && k == 0) ? 0u : 1u);
+          if (!two) {  // and what the weights' rounding left
+#pragma unroll
+            for (int k = 0; k < kAhKeys / 16; ++k)
+              mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + 64 + k * 8, bd + k * 128, idesc_o, 1u);
+          }
           mma_commit(smem_u32(&pv_done[s]));
           if (!two || s == 1) mma_commit(smem_u32(&kv_empty[vs]));
         }
@@ -569,14 +577,17 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     (void)mbar_wait(smem_u32(done), 0, a.err, tlim);
   } else {
     // -------------------------------------------------------------- softmax --
-    const int s = warp >> 2;  // stream
+    const int s = warp >> 3;         // stream
+    const int hf = (warp >> 2) & 1;  // half of a tile's keys
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t sCol = tmem + lanes + s * 128;
+    const uint32_t s_col = tmem + lanes + s * 128, o_col = tmem + lanes + 256 + s * 128;
+    const uint32_t mates = 1 + s * 4 + (warp & 3);  // barrier of the two warps that share these rows
+    float* my_x = sX + (2 * s + hf) * kAhHalf + row;
+    const float* mate_x = sX + (2 * s + 1 - hf) * kAhHalf + row;
     const int row_tok = row / a.group, row_head = row - row_tok * a.group;
     int slot = 0;
-    uint32_t it_ph = 0, s_ph = 0, cl_ph = 0;
-    uint32_t pv_ph[2] = {0, 0};  // products of each stream so far
+    uint32_t it_ph = 0, s_ph = 0, cl_ph = 0, pv_ph = 0;  // pv_ph: products of the stream so far
     bool ok = true;
     while (ok) {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
@@ -605,158 +616,169 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         s_ph ^= 1u;
         if (active) {
           tc_fence_after();
-          uint32_t sv[128];
-          tmem_ld128_wait(sCol, sv);
-          const int lim = limit - t * kAhKeys;
-          if (__any_sync(0xffffffffu, lim < kAhKeys)) {
+          const int lim = limit - t * kAhKeys - hf * 64;
+          bool sure = i == 0 || !two;
+          for (;;) {
+            uint32_t sv[64];
+            tmem_ld64_wait(s_col + hf * 64, sv);
+            if (__any_sync(0xffffffffu, lim < 64)) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
-          }
-          float m0 = kNegInf, m1 = kNegInf;
-#pragma unroll
-          for (int e = 0; e < 128; e += 4) {
-            m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
-            m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
-          }
-          const float up = ceilf(fmaxf(m0, m1) * a.kx * (1.f / kAhGrain)) * kAhGrain;
-          const bool moves = row_ok && up > c;
-          if (__any_sync(0xffffffffu, moves)) {
-            const float top = moves ? up : c;
-            const float f = pow2_diff(c, top);
-            if (i > 0) {  // O is on the old scale; the stream's last product has to be complete
-              if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph[s] - 1) & 1u, a.err, tlim))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              for (int col = 0; col < a.d; col += 16) {
-                uint32_t o[16];
-                tmem_ld16(tmem + lanes + 256 + s * 128 + col, o);
-                tmem_wait16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(tmem + lanes + 256 + s * 128 + col, o);
-              }
-              tmem_st_wait();
+              for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
             }
-            l *= f;
-            c = top;
-          }
-          const float base = c == kNegInf ? 0.f : c;
-          const f32x2 kx2 = pair(a.kx, a.kx), nb2 = pair(-base, -base);
-          f32x2 sum0 = pair(0.f, 0.f), sum1 = pair(0.f, 0.f);
+            float m0 = kNegInf, m1 = kNegInf;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int at = half * 64 + 2 * e;
-              const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
-              const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-              if (e & 1)
-                sum1 = add2(sum1, pair(p0, p1));
-              else
-                sum0 = add2(sum0, pair(p0, p1));
-              pk[e] = pack_bf16(p0, p1);
+            for (int e = 0; e < 64; e += 4) {
+              m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
+              m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
             }
-            tmem_st32(sCol + half * 32, pk);
+            const float up = ceilf(fmaxf(m0, m1) * a.kx * (1.f / kAhGrain)) * kAhGrain;
+            if (sure) {
+              *my_x = up;
+              named_barrier_sync(mates, 64);
+              const float both = fmaxf(up, *mate_x);
+              const bool moves = row_ok && both > c;
+              if (__any_sync(0xffffffffu, moves)) {
+                const float top = moves ? both : c;
+                const float f = pow2_diff(c, top);
+                if (i > 0) {  // O is on the old scale; the stream's last product has to be complete
+                  if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph - 1) & 1u, a.err, tlim))) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                  for (int col = hf * 16; col < a.d; col += 32) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + col, o);
+                    tmem_wait16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st16(o_col + col, o);
+                  }
+                }
+                l *= f;
+                c = top;
+              }
+            }
+            const float base = c == kNegInf ? 0.f : c;
+            const f32x2 kx2 = pair(a.kx, a.kx), nb2 = pair(-base, -base);
+            f32x2 sum = pair(0.f, 0.f);
+            if (two) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+                const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+                sum = add2(sum, pair(p0, p1));
+                pk[e] = pack_bf16(p0, p1);
+              }
+              // Scales hardly ever move, so the weights are taken on the old one before that is known. The barrier
+              // also keeps a warp's weights from its mate's scores, whose place they take.
+              if (!sure && named_barrier_or(mates, 64, row_ok && up > c)) {
+                sure = true;
+                continue;
+              }
+              tmem_st32(s_col + hf * 32, pk);
+            } else {
+              // few rows: the products wait for memory, and a second one takes what the first rounding leaves
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                uint32_t p_hi[16], p_lo[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int at = part * 32 + 2 * e;
+                  const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
+                  const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+                  sum = add2(sum, pair(p0, p1));
+                  p_hi[e] = pack_bf16(p0, p1);
+                  p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
+                }
+                tmem_st16(s_col + hf * 32 + part * 16, p_hi);
+                tmem_st16(s_col + 64 + hf * 32 + part * 16, p_lo);
+              }
+            }
+            l += lo(sum) + hi(sum);
+            break;
           }
-          sum0 = add2(sum0, sum1);
-          l += lo(sum0) + hi(sum0);
+          if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
         }
-        ++pv_ph[s];
+        ++pv_ph;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_ready[s]));
       }
       if (!ok) break;
       const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
-      if (n > 0 && !two && s == 1) {
-        // hand (c, l) over; stream 0 reads both sums
+      if (!two && s == 1) {
+        // hand (c, l) over to stream 0, which reads both sums
         if (mine > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[1]), (pv_ph[1] - 1) & 1u, a.err, tlim));
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[1]), (pv_ph - 1) & 1u, a.err, tlim));
           if (!ok) break;
-          sCL[row] = make_float2(c, l);
+          sCL[hf * kAhHalf + row] = make_float2(c, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(cl_ready));
         }
         continue;
       }
-      if (!two && s == 1) continue;
       float c1 = kNegInf, l1 = 0.f;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph[s] - 1) & 1u, a.err, tlim));
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph - 1) & 1u, a.err, tlim));
         if (ok && other > 0) {
           // stream 1 arrives after its own last product, so that O of both is complete
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(cl_ready), cl_ph, a.err, tlim));
           cl_ph ^= 1u;
-          const float2 cl = sCL[row];
-          c1 = cl.x;
-          l1 = cl.y;
+          c1 = sCL[row].x;
+          l1 = sCL[row].y + sCL[kAhHalf + row].y;
         }
         if (!ok) break;
         tc_fence_after();
+        // the row's whole sum; the second barrier keeps the next item's maxima from what is read here
+        *my_x = l;
+        named_barrier_sync(mates, 64);
+        l += *mate_x;
+        named_barrier_sync(mates, 64);
       }
       const float top = fmaxf(c, c1);
       const float f0 = pow2_diff(c, top), f1 = pow2_diff(c1, top);
       const float sum = l * f0 + l1 * f1;
-      if (active || n == 0) {
-        if (it.slot < 0) {
-          const bool sees = n > 0 && limit > 0;
-          const float inv = 1.f / sum;
-          __nv_bfloat16* dst = a.o + static_cast<long long>(it.q_row + tok) * a.ld_o +
-                               static_cast<long long>(it.head * a.group + row_head) * a.d;
-          for (int col = 0; col < a.d; col += 16) {
-            uint32_t o[16] = {}, o1[16] = {};
-            if (n > 0) {
-              tmem_ld16(tmem + lanes + 256 + s * 128 + col, o);
-              if (other > 0) tmem_ld16(tmem + lanes + 384 + col, o1);
-              tmem_wait16(o);
-              tmem_wait16(o1);
-            }
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float x0 = __uint_as_float(o[2 * e]) * f0, x1 = __uint_as_float(o[2 * e + 1]) * f0;
-              if (other > 0) {
-                x0 = fmaf(__uint_as_float(o1[2 * e]), f1, x0);
-                x1 = fmaf(__uint_as_float(o1[2 * e + 1]), f1, x1);
-              }
-              pk[e] = sees ? pack_bf16(x0 * inv, x1 * inv) : 0u;
-            }
-            if (row_ok) {
-              *reinterpret_cast<uint4*>(dst + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-              *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-            }
-          }
-        } else {
-          const int r = (two ? s * kAhHalf : 0) + row;
-          float* dst = a.part + (static_cast<long long>(it.slot) * a.slot_rows + r) * a.d;
-          for (int col = 0; col < a.d; col += 16) {
-            uint32_t o[16], o1[16] = {};
-            tmem_ld16(tmem + lanes + 256 + s * 128 + col, o);
-            if (other > 0) tmem_ld16(tmem + lanes + 384 + col, o1);
+      if (active) {
+        const bool sees = n > 0 && limit > 0;
+        const float inv = 1.f / sum;
+        const int r = (two ? s * kAhHalf : 0) + row;
+        __nv_bfloat16* dst = a.o + static_cast<long long>(it.q_row + tok) * a.ld_o +
+                             static_cast<long long>(it.head * a.group + row_head) * a.d;
+        float* part = a.part + (static_cast<long long>(it.slot) * a.slot_rows + r) * a.d;
+        for (int col = hf * 16; col < a.d; col += 32) {
+          uint32_t o[16] = {}, o1[16] = {};
+          if (n > 0) {
+            tmem_ld16(o_col + col, o);
+            if (other > 0) tmem_ld16(o_col + 128 + col, o1);
             tmem_wait16(o);
             tmem_wait16(o1);
-            if (row_ok) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                float x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  x[i] = __uint_as_float(o[e + i]) * f0;
-                  if (other > 0) x[i] = fmaf(__uint_as_float(o1[e + i]), f1, x[i]);
-                }
-                *reinterpret_cast<float4*>(dst + col + e) = make_float4(x[0], x[1], x[2], x[3]);
-              }
-            }
           }
-          if (row_ok) {
-            const bool sees = limit > it.t_begin * kAhKeys;
-            a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + r] =
-                make_float2(sees && top == kNegInf ? kNoScore : top, sum);
+          float x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[e] = __uint_as_float(o[e]) * f0;
+            if (other > 0) x[e] = fmaf(__uint_as_float(o1[e]), f1, x[e]);
           }
+          if (row_ok && it.slot < 0) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pk[e] = sees ? pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv) : 0u;
+            *reinterpret_cast<uint4*>(dst + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          } else if (row_ok) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(part + col + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+          __syncwarp();
+        }
+        if (row_ok && it.slot >= 0 && hf == 0) {
+          const bool any = limit > it.t_begin * kAhKeys;
+          a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + r] =
+              make_float2(any && top == kNegInf ? kNoScore : top, sum);
         }
       }
       if (n > 0) {
@@ -772,7 +794,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kAhMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -944,7 +966,7 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
   const int grid = std::min(kAhMaxCtas, di.sm_count);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  st = a.d > 64 ? launch_attn<2, 5>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 12>(what, tq, tk, tv, a, grid, cs);
+  st = a.d > 64 ? launch_attn<2, 4>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 8>(what, tq, tk, tv, a, grid, cs);
   if (st != CC_OK || !a.may_split) return st;
   // the joining kernel's CTAs: a row to each where few items are cut into many pieces, else eight
   const int join_y = a.slot_rows <= 32 ? a.slot_rows : a.slot_rows / 8;
