@@ -41,8 +41,8 @@ namespace cc {
 namespace {
 
 constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
-constexpr int kAhMmaWarp = 17;
-constexpr int kAhThreads = 576;
+constexpr int kAhMmaWarp = 17;    // and 18, one for each stream
+constexpr int kAhThreads = 608;
 constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
 constexpr int kAhKeys = 128;      // keys per tile
 constexpr int kAhHalf = 128;      // rows per half
@@ -318,14 +318,14 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&kv_full[i]), 1);
-      mbar_init(smem_u32(&kv_empty[i]), 1);
+      mbar_init(smem_u32(&kv_empty[i]), 2);
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 17);
+      mbar_init(smem_u32(&item_empty[i]), 18);
     }
     mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_empty), 1);
+    mbar_init(smem_u32(q_empty), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_ready[i]), 1);
       mbar_init(smem_u32(&p_ready[i]), 8);
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       mbar_init(smem_u32(&o_free[i]), 8);
     }
     mbar_init(smem_u32(cl_ready), 8);
-    mbar_init(smem_u32(done), 1);
+    mbar_init(smem_u32(done), 2);
     fence_mbar_init();
   }
   if (warp == kAhMmaWarp) {
@@ -459,40 +459,51 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         (void)mbar_wait(smem_u32(&kv_full[i]), (i < stage) ? kv_ph : (kv_ph ^ 1u), a.err, 200000000ull);
       (void)mbar_wait(smem_u32(q_full), q_ph ^ 1u, a.err, 200000000ull);
     }
-  } else if (warp == kAhMmaWarp) {
-    // ------------------------------------------------------------------ MMA --
+  } else if (warp >= kAhMmaWarp) {
+    // ---------------------------------- MMA, a warp per stream: while one waits
+    // for its weights or is held up by a full queue, the other's products go on
+    const int s = warp - kAhMmaWarp;
     const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
     const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
     const int steps = a.d / 16;
     const uint64_t q0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t k0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
     const uint64_t v0 = sdesc_sw128(smem_u32(sKV), kAhBlockBytes, 1024);
+    const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
     int stage = 0, slot = 0;
-    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
-    uint32_t p_ph = 0, of_ph = 0;  // a bit per stream
-    bool used[2] = {false, false};  // the stream's O was written by an item before
+    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0, p_ph = 0, of_ph = 0;
+    bool used = false;  // the stream's O was written by an item before
     bool ok = true;
-    auto next_tile = [&](int& at) {  // waits for the next k or v tile
-      at = stage;
+    // waits for the next k or v tile; its stage, -1 where the wait ran out
+    auto next_tile = [&]() {
+      const int at = stage;
       const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[stage]), kv_ph, a.err, tlim));
       if (++stage == STAGES) {
         stage = 0;
         kv_ph ^= 1u;
       }
       tc_fence_after();
-      return got;
+      return got ? at : -1;
     };
-    auto scores = [&](int s, int half, int at, bool release, bool q_last) {
+    // the other stream's tile
+    auto skip_tile = [&]() {
+      const int at = next_tile();
+      if (lane == 0 && at >= 0) mbar_arrive(smem_u32(&kv_empty[at]));
+      __syncwarp();
+      return at >= 0;
+    };
+    auto scores = [&](int half, int at, bool last) {
       const uint64_t ad = q0 + static_cast<uint64_t>(half) * (Sm::kTile >> 4);
       const uint64_t bd = k0 + static_cast<uint64_t>(at) * (Sm::kTile >> 4);
       if (elect_one()) {
-        for (int k = 0; k < steps; ++k) {
+#pragma unroll
+        for (int k = 0; k < NB * 4; ++k) {
           const uint64_t off = (k >> 2) * (kAhBlockBytes >> 4) + (k & 3) * 2;
-          mma_bf16(tmem + s * 128, ad + off, bd + off, idesc_s, k ? 1u : 0u);
+          if (k < steps) mma_bf16(s_tmem, ad + off, bd + off, idesc_s, k ? 1u : 0u);
         }
         mma_commit(smem_u32(&s_ready[s]));
-        if (release) mma_commit(smem_u32(&kv_empty[at]));
-        if (q_last) mma_commit(smem_u32(q_empty));
+        mma_commit(smem_u32(&kv_empty[at]));
+        if (last) mma_commit(smem_u32(q_empty));
       }
       __syncwarp();
     };
@@ -509,68 +520,76 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int n = it.t_end - it.t_begin;
       if (n <= 0) continue;
       const bool two = it.tokens > a.tq;
-      const int jobs = two ? 2 * n : n;
+      const int half = two ? s : 0;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_full), q_ph, a.err, tlim))) break;
       q_ph ^= 1u;
       tc_fence_after();
-      int ks = 0, vs = 0;
-      // the first scores of both streams
-      for (int j = 0; ok && j < min(2, jobs); ++j) {
-        if (!two || j == 0) ok = next_tile(ks);
-        if (ok) scores(j, two ? j : 0, ks, !two || j == 1, j == jobs - 1 );
+      // the tiles come as k of the first one (single halves: two), then v of each with k of the one (two) ahead
+      const int ahead = two ? 1 : 2;
+      const int last = two ? n - 1 : ((n - 1 - s) & ~1) + s;  // the stream's last tile
+      if (!two && s >= n) {  // no tile is this stream's
+        if (lane == 0) mbar_arrive(smem_u32(q_empty));
+        __syncwarp();
       }
-      for (int j = 0; ok && j < jobs; ++j) {
-        const int s = j & 1;
-        if (!two || s == 0) {
-          ok = next_tile(vs);
-          if (!ok) break;
-          const int t = it.t_begin + (two ? j >> 1 : j);
-          const int valid = it.len - t * kAhKeys;
-          if (valid < kAhKeys) {
-            // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
-            uint8_t* base = sKV + vs * Sm::kTile;
-            for (int i = lane; i < (kAhKeys - valid) * 8; i += 32) {
-#pragma unroll
-              for (int blk = 0; blk < NB; ++blk)
-                *reinterpret_cast<uint4*>(base + blk * kAhBlockBytes + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+      for (int i = 0; ok && i < min(ahead, n); ++i) {
+        if (two || i == s) {
+          const int at = next_tile();
+          ok = at >= 0;
+          if (ok) scores(half, at, i == last);
+        } else {
+          ok = skip_tile();
         }
-        // the last item's sums of the streams that this one writes have been read
-        if (j == 0 || (two && j == 1)) {
-          for (int o = s; o < (two ? s + 1 : 2); ++o) {
-            if (!used[o]) continue;
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[o]), (of_ph >> o) & 1u, a.err, tlim));
-            of_ph ^= 1u << o;
-          }
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const bool mine = two || (i & 1) == s;
+        if (!mine) {
+          ok = skip_tile() && (i + ahead >= n || skip_tile());
+          continue;
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[s]), (p_ph >> s) & 1u, a.err, tlim));
+        const int vs = next_tile();
+        ok = vs >= 0;
         if (!ok) break;
-        p_ph ^= 1u << s;
+        const int valid = it.len - (it.t_begin + i) * kAhKeys;
+        if (valid < kAhKeys) {
+          // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
+          uint8_t* base = sKV + vs * Sm::kTile;
+          for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk)
+              *reinterpret_cast<uint4*>(base + blk * kAhBlockBytes + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const bool first = i == (two ? 0 : s);
+        if (first && used) {  // the sums of the item before have been read
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[s]), of_ph, a.err, tlim));
+          of_ph ^= 1u;
+        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[s]), p_ph, a.err, tlim));
+        if (!ok) break;
+        p_ph ^= 1u;
+        used = true;
         tc_fence_after();
         const uint64_t bd = v0 + static_cast<uint64_t>(vs) * (Sm::kTile >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kAhKeys / 16; ++k)
-            mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + k * 8, bd + k * 128, idesc_o, (j < 2 && k == 0) ? 0u : 1u);
+            mma_bf16_ta(o_tmem, s_tmem + k * 8, bd + k * 128, idesc_o, (first && k == 0) ? 0u : 1u);
           if (!two) {  // and what the weights' rounding left
 #pragma unroll
-            for (int k = 0; k < kAhKeys / 16; ++k)
-              mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + 64 + k * 8, bd + k * 128, idesc_o, 1u);
+            for (int k = 0; k < kAhKeys / 16; ++k) mma_bf16_ta(o_tmem, s_tmem + 64 + k * 8, bd + k * 128, idesc_o, 1u);
           }
           mma_commit(smem_u32(&pv_done[s]));
-          if (!two || s == 1) mma_commit(smem_u32(&kv_empty[vs]));
+          mma_commit(smem_u32(&kv_empty[vs]));
         }
         __syncwarp();
-        if (j + 2 < jobs) {
-          if (!two || s == 0) ok = next_tile(ks);
-          if (ok) scores(s, two ? s : 0, ks, !two || s == 1, j + 2 == jobs - 1);
+        if (i + ahead < n) {
+          const int at = next_tile();
+          ok = at >= 0;
+          if (ok) scores(half, at, i + ahead == last);
         }
       }
-      // who reads this item's sums arrives on o_free of both streams, or each stream on its own
-      used[0] = used[1] = true;
     }
     if (elect_one()) mma_commit(smem_u32(done));
     __syncwarp();
@@ -786,7 +805,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&o_free[s]));
-          if (!two) mbar_arrive(smem_u32(&o_free[1]));
+          if (other > 0) mbar_arrive(smem_u32(&o_free[1]));
         }
       }
     }
