@@ -40,18 +40,19 @@
 namespace cc {
 namespace {
 
-constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
-constexpr int kAhMmaWarp = 17;    // and 18, one for each stream
-constexpr int kAhThreads = 608;
+constexpr int kAhTmaWarp = 8;     // behind 8 softmax warps
+constexpr int kAhMmaWarp = 9;     // and 10, one for each stream
+constexpr int kAhThreads = 352;
 constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
-constexpr int kAhKeys = 128;      // keys per tile
+constexpr int kAhKeys = 64;       // keys per tile
 constexpr int kAhHalf = 128;      // rows per half
-constexpr int kAhBlockBytes = 128 * 128;  // 128 rows x 64 channels
+constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 channels
+constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 64 keys (or values) x 64 channels
 constexpr int kAhItems = 4;       // item descriptors in flight
 constexpr float kAhGrain = 16.f;  // step of a row's scale c, in powers of two
 // Tiles that cutting items costs a call, in time of its critical path: the
 // partial sums' way through L2 and the joining kernel.
-constexpr int kAhSplitCost = 4;
+constexpr int kAhSplitCost = 8;
 
 struct AhArgs {
   KvPlan plan;      // q_offsets nullptr: sequence b owns rows b * lq .. (b + 1) * lq - 1; page_table nullptr: page b
@@ -194,7 +195,7 @@ __device__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
   items = warp_sum(items);
   most = __reduce_max_sync(0xffffffffu, most);
   if (units == 0) return false;
-  const long long per = max(2ll, (units + ctas - 1) / ctas);
+  const long long per = max(4ll, (units + ctas - 1) / ctas);
   const long long whole = max(static_cast<long long>(most), ((items + ctas - 1) / ctas * units + items - 1) / items);
   r.split = a.may_split && whole > per + kAhSplitCost;
   r.at = cta * per;
@@ -281,9 +282,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // NB: 64-channel blocks of a head; STAGES: k or v tiles in flight.
 template <int NB, int STAGES>
 struct AhSmem {
-  static constexpr int kTile = NB * kAhBlockBytes;
-  static constexpr int kQ = 2 * kTile;
-  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 8 + 4 * kAhHalf * 4;
+  static constexpr int kTile = NB * kAhKvBlock;
+  static constexpr int kQHalf = NB * kAhQBlock;
+  static constexpr int kQ = 2 * kQHalf;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + kAhHalf * 8;
 };
 
 template <int NB, int STAGES>
@@ -295,9 +297,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + Sm::kQ;
-  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // [2][128] stream 1's (c, l) of single halves
-  float* sX = reinterpret_cast<float*>(sCL + 2 * kAhHalf);            // [4][128] what warps of the same rows exchange
-  AhItem* items = reinterpret_cast<AhItem*>(sX + 4 * kAhHalf);
+  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // stream 1's (c, l) of single halves
+  AhItem* items = reinterpret_cast<AhItem*>(sCL + kAhHalf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + STAGES;
@@ -305,10 +306,10 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint64_t* item_empty = item_full + kAhItems;
   uint64_t* q_full = item_empty + kAhItems;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* s_ready = q_empty + 1;  // [2] S of a stream complete
-  uint64_t* p_ready = s_ready + 2;  // [2] P of a stream written, and O on its scale
-  uint64_t* pv_done = p_ready + 2;  // [2] the last product of a stream complete
-  uint64_t* o_free = pv_done + 2;   // [2] O of a stream read out
+  uint64_t* s_ready = q_empty + 1;  // [2][2] S of a stream complete, two buffers each
+  uint64_t* p_ready = s_ready + 4;  // [2][2] P in its place, and O on its scale
+  uint64_t* pv_done = p_ready + 4;  // [2][2] its product complete
+  uint64_t* o_free = pv_done + 4;   // [2] O of a stream read out
   uint64_t* cl_ready = o_free + 2;
   uint64_t* done = cl_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -322,17 +323,17 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 18);
+      mbar_init(smem_u32(&item_empty[i]), 10);
     }
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 2);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s_ready[i]), 1);
-      mbar_init(smem_u32(&p_ready[i]), 8);
+      mbar_init(smem_u32(&p_ready[i]), 4);
       mbar_init(smem_u32(&pv_done[i]), 1);
-      mbar_init(smem_u32(&o_free[i]), 8);
     }
-    mbar_init(smem_u32(cl_ready), 8);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&o_free[i]), 4);
+    mbar_init(smem_u32(cl_ready), 4);
     mbar_init(smem_u32(done), 2);
     fence_mbar_init();
   }
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       if (lane < boxes) {
         const uint32_t dst = smem_u32(sKV + stage * Sm::kTile) + static_cast<uint32_t>(lane * a.box) * 128u;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) tma_load_4d(dst + i * kAhBlockBytes, map, full, i * 64, h, at, page);
+        for (int i = 0; i < NB; ++i) tma_load_4d(dst + i * kAhKvBlock, map, full, i * 64, h, at, page);
       }
       if (++stage == STAGES) {
         stage = 0;
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int n = it.t_end - it.t_begin;
       if (n > 0) {
         const bool two = it.tokens > a.tq;
-        const int ahead = two ? 1 : 2;
+        const int ahead = two ? 2 : 4;  // two tiles of scores ahead in each stream
         for (int t = 0; ok && t < min(ahead, n); ++t) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t);
         if (!ok) break;
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_empty), q_ph ^ 1u, a.err, tlim))) {
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           mbar_arrive_expect_tx(full, static_cast<uint32_t>((two ? 2 : 1) * NB * a.tq * a.group * 128));
           for (int s = 0; s < (two ? 2 : 1); ++s)
             for (int i = 0; i < NB; ++i)
-              tma_load_4d(smem_u32(sQ + s * Sm::kTile + i * kAhBlockBytes), &tmQ, full, i * 64, it.head * a.group,
+              tma_load_4d(smem_u32(sQ + s * Sm::kQHalf + i * kAhQBlock), &tmQ, full, i * 64, it.head * a.group,
                           it.q_row + s * a.tq, 0);
         }
         __syncwarp();
@@ -468,10 +469,11 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     const int steps = a.d / 16;
     const uint64_t q0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t k0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
-    const uint64_t v0 = sdesc_sw128(smem_u32(sKV), kAhBlockBytes, 1024);
+    const uint64_t v0 = sdesc_sw128(smem_u32(sKV), kAhKvBlock, 1024);
     const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
     int stage = 0, slot = 0;
-    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0, p_ph = 0, of_ph = 0;
+    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0, of_ph = 0;
+    uint32_t done_s = 0, done_p = 0;  // tiles of scores and products issued
     bool used = false;  // the stream's O was written by an item before
     bool ok = true;
     // waits for the next k or v tile; its stage, -1 where the wait ran out
@@ -493,19 +495,21 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       return at >= 0;
     };
     auto scores = [&](int half, int at, bool last) {
-      const uint64_t ad = q0 + static_cast<uint64_t>(half) * (Sm::kTile >> 4);
+      const uint64_t ad = q0 + static_cast<uint64_t>(half) * (Sm::kQHalf >> 4);
       const uint64_t bd = k0 + static_cast<uint64_t>(at) * (Sm::kTile >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < NB * 4; ++k) {
-          const uint64_t off = (k >> 2) * (kAhBlockBytes >> 4) + (k & 3) * 2;
-          if (k < steps) mma_bf16(s_tmem, ad + off, bd + off, idesc_s, k ? 1u : 0u);
+          if (k < steps)
+            mma_bf16(s_tmem + (done_s & 1) * 64, ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2,
+                     bd + (k >> 2) * (kAhKvBlock >> 4) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
         }
-        mma_commit(smem_u32(&s_ready[s]));
+        mma_commit(smem_u32(&s_ready[2 * s + (done_s & 1)]));
         mma_commit(smem_u32(&kv_empty[at]));
         if (last) mma_commit(smem_u32(q_empty));
       }
       __syncwarp();
+      ++done_s;
     };
     while (ok) {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
@@ -524,15 +528,15 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_full), q_ph, a.err, tlim))) break;
       q_ph ^= 1u;
       tc_fence_after();
-      // the tiles come as k of the first one (single halves: two), then v of each with k of the one (two) ahead
-      const int ahead = two ? 1 : 2;
+      // the tiles come as k of the first two of each stream, then v of each with k of the one that far ahead
+      const int ahead = two ? 2 : 4;
       const int last = two ? n - 1 : ((n - 1 - s) & ~1) + s;  // the stream's last tile
       if (!two && s >= n) {  // no tile is this stream's
         if (lane == 0) mbar_arrive(smem_u32(q_empty));
         __syncwarp();
       }
       for (int i = 0; ok && i < min(ahead, n); ++i) {
-        if (two || i == s) {
+        if (two || (i & 1) == s) {
           const int at = next_tile();
           ok = at >= 0;
           if (ok) scores(half, at, i == last);
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk)
-              *reinterpret_cast<uint4*>(base + blk * kAhBlockBytes + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(base + blk * kAhKvBlock + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -566,24 +570,25 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[s]), of_ph, a.err, tlim));
           of_ph ^= 1u;
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[s]), p_ph, a.err, tlim));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[2 * s + (done_p & 1)]), (done_p >> 1) & 1u, a.err, tlim));
         if (!ok) break;
-        p_ph ^= 1u;
+        const uint32_t p_tmem = s_tmem + (done_p & 1) * 64;
         used = true;
         tc_fence_after();
         const uint64_t bd = v0 + static_cast<uint64_t>(vs) * (Sm::kTile >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kAhKeys / 16; ++k)
-            mma_bf16_ta(o_tmem, s_tmem + k * 8, bd + k * 128, idesc_o, (first && k == 0) ? 0u : 1u);
+            mma_bf16_ta(o_tmem, p_tmem + k * 8, bd + k * 128, idesc_o, (first && k == 0) ? 0u : 1u);
           if (!two) {  // and what the weights' rounding left
 #pragma unroll
-            for (int k = 0; k < kAhKeys / 16; ++k) mma_bf16_ta(o_tmem, s_tmem + 64 + k * 8, bd + k * 128, idesc_o, 1u);
+            for (int k = 0; k < kAhKeys / 16; ++k) mma_bf16_ta(o_tmem, p_tmem + 32 + k * 8, bd + k * 128, idesc_o, 1u);
           }
-          mma_commit(smem_u32(&pv_done[s]));
+          mma_commit(smem_u32(&pv_done[2 * s + (done_p & 1)]));
           mma_commit(smem_u32(&kv_empty[vs]));
         }
         __syncwarp();
+        ++done_p;
         if (i + ahead < n) {
           const int at = next_tile();
           ok = at >= 0;
@@ -596,17 +601,14 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     (void)mbar_wait(smem_u32(done), 0, a.err, tlim);
   } else {
     // -------------------------------------------------------------- softmax --
-    const int s = warp >> 3;         // stream
-    const int hf = (warp >> 2) & 1;  // half of a tile's keys
+    const int s = warp >> 2;  // stream
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + s * 128, o_col = tmem + lanes + 256 + s * 128;
-    const uint32_t mates = 1 + s * 4 + (warp & 3);  // barrier of the two warps that share these rows
-    float* my_x = sX + (2 * s + hf) * kAhHalf + row;
-    const float* mate_x = sX + (2 * s + 1 - hf) * kAhHalf + row;
     const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+    const f32x2 kx2 = pair(a.kx, a.kx);
     int slot = 0;
-    uint32_t it_ph = 0, s_ph = 0, cl_ph = 0, pv_ph = 0;  // pv_ph: products of the stream so far
+    uint32_t it_ph = 0, cl_ph = 0, tiles = 0;  // tiles: of the stream so far
     bool ok = true;
     while (ok) {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
@@ -626,114 +628,98 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const bool active = __any_sync(0xffffffffu, row_ok);
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
       float c = kNegInf, l = 0.f;
-      for (int i = 0; ok && i < mine; ++i) {
+      for (int i = 0; ok && i < mine; ++i, ++tiles) {
         const int t = it.t_begin + (two ? i : 2 * i + s);
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[s]), s_ph, a.err, tlim))) {
+        const uint32_t buf = tiles & 1;
+        const uint32_t cols = s_col + buf * 64;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[2 * s + buf]), (tiles >> 1) & 1u, a.err, tlim))) {
           ok = false;
           break;
         }
-        s_ph ^= 1u;
         if (active) {
           tc_fence_after();
-          const int lim = limit - t * kAhKeys - hf * 64;
-          bool sure = i == 0 || !two;
-          for (;;) {
-            uint32_t sv[64];
-            tmem_ld64_wait(s_col + hf * 64, sv);
-            if (__any_sync(0xffffffffu, lim < 64)) {
+          uint32_t sv[64];
+          tmem_ld64_wait(cols, sv);
+          const int lim = limit - t * kAhKeys;
+          if (__any_sync(0xffffffffu, lim < kAhKeys)) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
-            }
-            float m0 = kNegInf, m1 = kNegInf;
+            for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
+          }
+          float m0 = kNegInf, m1 = kNegInf;
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-              m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
-              m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
-            }
-            const float up = ceilf(fmaxf(m0, m1) * a.kx * (1.f / kAhGrain)) * kAhGrain;
-            if (sure) {
-              *my_x = up;
-              named_barrier_sync(mates, 64);
-              const float both = fmaxf(up, *mate_x);
-              const bool moves = row_ok && both > c;
-              if (__any_sync(0xffffffffu, moves)) {
-                const float top = moves ? both : c;
-                const float f = pow2_diff(c, top);
-                if (i > 0) {  // O is on the old scale; the stream's last product has to be complete
-                  if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph - 1) & 1u, a.err, tlim))) {
-                    ok = false;
-                    break;
-                  }
-                  tc_fence_after();
-                  for (int col = hf * 16; col < a.d; col += 32) {
-                    uint32_t o[16];
-                    tmem_ld16(o_col + col, o);
-                    tmem_wait16(o);
+          for (int e = 0; e < 64; e += 4) {
+            m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
+            m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
+          }
+          const float up = ceilf(fmaxf(m0, m1) * a.kx * (1.f / kAhGrain)) * kAhGrain;
+          const bool moves = row_ok && up > c;
+          if (__any_sync(0xffffffffu, moves)) {
+            const float top = moves ? up : c;
+            const float f = pow2_diff(c, top);
+            if (i > 0) {  // O is on the old scale; the stream's last product has to be complete
+              if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + ((tiles - 1) & 1)]), ((tiles - 1) >> 1) & 1u, a.err, tlim))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              for (int col = 0; col < a.d; col += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_col + col, o);
+                tmem_wait16(o);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st16(o_col + col, o);
-                  }
-                }
-                l *= f;
-                c = top;
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_col + col, o);
               }
             }
-            const float base = c == kNegInf ? 0.f : c;
-            const f32x2 kx2 = pair(a.kx, a.kx), nb2 = pair(-base, -base);
-            f32x2 sum = pair(0.f, 0.f);
-            if (two) {
-              uint32_t pk[32];
+            l *= f;
+            c = top;
+          }
+          const float base = c == kNegInf ? 0.f : c;
+          const f32x2 nb2 = pair(-base, -base);
+          f32x2 sum = pair(0.f, 0.f);
+          if (two) {
+            uint32_t pk[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+            for (int e = 0; e < 32; ++e) {
+              const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+              const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+              sum = add2(sum, pair(p0, p1));
+              pk[e] = pack_bf16(p0, p1);
+            }
+            tmem_st32(cols, pk);
+          } else {
+            // few rows: the products wait for memory, and a second one takes what the first rounding leaves
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              uint32_t p_hi[16], p_lo[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int at = part * 32 + 2 * e;
+                const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
                 const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
                 sum = add2(sum, pair(p0, p1));
-                pk[e] = pack_bf16(p0, p1);
+                p_hi[e] = pack_bf16(p0, p1);
+                p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
               }
-              // Scales hardly ever move, so the weights are taken on the old one before that is known. The barrier
-              // also keeps a warp's weights from its mate's scores, whose place they take.
-              if (!sure && named_barrier_or(mates, 64, row_ok && up > c)) {
-                sure = true;
-                continue;
-              }
-              tmem_st32(s_col + hf * 32, pk);
-            } else {
-              // few rows: the products wait for memory, and a second one takes what the first rounding leaves
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                uint32_t p_hi[16], p_lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int at = part * 32 + 2 * e;
-                  const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
-                  const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-                  sum = add2(sum, pair(p0, p1));
-                  p_hi[e] = pack_bf16(p0, p1);
-                  p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
-                }
-                tmem_st16(s_col + hf * 32 + part * 16, p_hi);
-                tmem_st16(s_col + 64 + hf * 32 + part * 16, p_lo);
-              }
+              tmem_st16(cols + part * 16, p_hi);
+              tmem_st16(cols + 32 + part * 16, p_lo);
             }
-            l += lo(sum) + hi(sum);
-            break;
           }
-          if (!ok) break;
+          l += lo(sum) + hi(sum);
           tmem_st_wait();
           tc_fence_before();
         }
-        ++pv_ph;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_ready[s]));
+        if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * s + buf]));
       }
       if (!ok) break;
       const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
       if (!two && s == 1) {
         // hand (c, l) over to stream 0, which reads both sums
         if (mine > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[1]), (pv_ph - 1) & 1u, a.err, tlim));
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 + ((tiles - 1) & 1)]), ((tiles - 1) >> 1) & 1u, a.err, tlim));
           if (!ok) break;
-          sCL[hf * kAhHalf + row] = make_float2(c, l);
+          sCL[row] = make_float2(c, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(cl_ready));
         }
@@ -741,21 +727,16 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       float c1 = kNegInf, l1 = 0.f;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[s]), (pv_ph - 1) & 1u, a.err, tlim));
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + ((tiles - 1) & 1)]), ((tiles - 1) >> 1) & 1u, a.err, tlim));
         if (ok && other > 0) {
           // stream 1 arrives after its own last product, so that O of both is complete
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(cl_ready), cl_ph, a.err, tlim));
           cl_ph ^= 1u;
           c1 = sCL[row].x;
-          l1 = sCL[row].y + sCL[kAhHalf + row].y;
+          l1 = sCL[row].y;
         }
         if (!ok) break;
         tc_fence_after();
-        // the row's whole sum; the second barrier keeps the next item's maxima from what is read here
-        *my_x = l;
-        named_barrier_sync(mates, 64);
-        l += *mate_x;
-        named_barrier_sync(mates, 64);
       }
       const float top = fmaxf(c, c1);
       const float f0 = pow2_diff(c, top), f1 = pow2_diff(c1, top);
@@ -767,7 +748,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         __nv_bfloat16* dst = a.o + static_cast<long long>(it.q_row + tok) * a.ld_o +
                              static_cast<long long>(it.head * a.group + row_head) * a.d;
         float* part = a.part + (static_cast<long long>(it.slot) * a.slot_rows + r) * a.d;
-        for (int col = hf * 16; col < a.d; col += 32) {
+        for (int col = 0; col < a.d; col += 16) {
           uint32_t o[16] = {}, o1[16] = {};
           if (n > 0) {
             tmem_ld16(o_col + col, o);
@@ -794,7 +775,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           }
           __syncwarp();
         }
-        if (row_ok && it.slot >= 0 && hf == 0) {
+        if (row_ok && it.slot >= 0) {
           const bool any = limit > it.t_begin * kAhKeys;
           a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + r] =
               make_float2(any && top == kNegInf ? kNoScore : top, sum);
@@ -985,7 +966,7 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
   const int grid = std::min(kAhMaxCtas, di.sm_count);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  st = a.d > 64 ? launch_attn<2, 4>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 8>(what, tq, tk, tv, a, grid, cs);
+  st = a.d > 64 ? launch_attn<2, 10>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 16>(what, tq, tk, tv, a, grid, cs);
   if (st != CC_OK || !a.may_split) return st;
   // the joining kernel's CTAs: a row to each where few items are cut into many pieces, else eight
   const int join_y = a.slot_rows <= 32 ? a.slot_rows : a.slot_rows / 8;
