@@ -41,18 +41,19 @@ namespace cc {
 namespace {
 
 constexpr int kAhTmaWarp = 8;     // behind 8 softmax warps
-constexpr int kAhMmaWarp = 9;     // and 10, one for each stream
-constexpr int kAhThreads = 352;
+constexpr int kAhMmaWarp = 9;
+constexpr int kAhThreads = 320;
 constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
-constexpr int kAhKeys = 64;       // keys per tile
+constexpr int kAhKeys = 128;      // keys per tile, in two halves for the softmax
 constexpr int kAhHalf = 128;      // rows per half
 constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 channels
-constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 64 keys (or values) x 64 channels
+constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
 constexpr int kAhItems = 4;       // item descriptors in flight
-constexpr float kAhGrain = 16.f;  // step of a row's scale c, in powers of two
+constexpr int kAhOut = 32 * 128;  // bytes through which a softmax warp's 32 rows of output go
+constexpr float kAhRoom = 1048576.f;  // 2^20: how far a row's weights may pass its scale
 // Tiles that cutting items costs a call, in time of its critical path: the
 // partial sums' way through L2 and the joining kernel.
-constexpr int kAhSplitCost = 8;
+constexpr int kAhSplitCost = 4;
 
 struct AhArgs {
   KvPlan plan;      // q_offsets nullptr: sequence b owns rows b * lq .. (b + 1) * lq - 1; page_table nullptr: page b
@@ -71,6 +72,7 @@ struct AhArgs {
   int4* meta;       // [2 * ctas]: 0 unused, 1 goes on, 2 ends its item; first row, tokens, head
   unsigned int* err;
   unsigned long long timeout_ns;
+  unsigned long long inv_ctas;  // ceil(2^64 / CTAs): exact quotients of anything below 2^56
 };
 
 // A piece of an item, as the roles of a CTA pass it on.
@@ -195,9 +197,11 @@ __device__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
   items = warp_sum(items);
   most = __reduce_max_sync(0xffffffffu, most);
   if (units == 0) return false;
-  const long long per = max(4ll, (units + ctas - 1) / ctas);
-  const long long whole = max(static_cast<long long>(most), ((items + ctas - 1) / ctas * units + items - 1) / items);
-  r.split = a.may_split && whole > per + kAhSplitCost;
+  const long long per = max(2ll, static_cast<long long>(__umul64hi(units + ctas - 1, a.inv_ctas)));
+  // what the longest run would be with whole items (all of them of the average's size), against cut ones
+  const float whole = fmaxf(static_cast<float>(most), ceilf(__fdividef(static_cast<float>(items), static_cast<float>(ctas))) *
+                                                          __fdividef(static_cast<float>(units), static_cast<float>(items)));
+  r.split = a.may_split && whole > static_cast<float>(per + kAhSplitCost);
   r.at = cta * per;
   r.end = min(units, r.at + per);
   if (r.at >= units) return false;
@@ -232,8 +236,12 @@ __device__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
       const int t_all = __shfl_sync(0xffffffffu, tiles, src);
       rest -= __shfl_sync(0xffffffffu, upto, src) - static_cast<long long>(t_all) * a.kv_heads;
       r.t_all = t_all;
-      r.h = static_cast<int>(rest / t_all);
-      r.t = static_cast<int>(rest - static_cast<long long>(r.h) * t_all);
+      // rest / t_all is below 2^16, so a quotient of floats is at most one off
+      r.h = static_cast<int>(__fdividef(static_cast<float>(rest), static_cast<float>(t_all)));
+      long long left = rest - static_cast<long long>(r.h) * t_all;
+      if (left < 0) --r.h, left += t_all;
+      if (left >= t_all) ++r.h, left -= t_all;
+      r.t = static_cast<int>(left);
       break;
     }
     rest -= __shfl_sync(0xffffffffu, upto, 31);
@@ -285,7 +293,7 @@ struct AhSmem {
   static constexpr int kTile = NB * kAhKvBlock;
   static constexpr int kQHalf = NB * kAhQBlock;
   static constexpr int kQ = 2 * kQHalf;
-  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + kAhHalf * 8;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 8 * kAhOut + 1024 + kAhHalf * 8;
 };
 
 template <int NB, int STAGES>
@@ -297,7 +305,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + Sm::kQ;
-  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // stream 1's (c, l) of single halves
+  uint8_t* sO = sKV + STAGES * Sm::kTile;
+  float2* sCL = reinterpret_cast<float2*>(sO + 8 * kAhOut);  // stream 1's (c, l) of single halves
   AhItem* items = reinterpret_cast<AhItem*>(sCL + kAhHalf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
   uint64_t* kv_full = bars;
@@ -306,8 +315,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint64_t* item_empty = item_full + kAhItems;
   uint64_t* q_full = item_empty + kAhItems;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* s_ready = q_empty + 1;  // [2][2] S of a stream complete, two buffers each
-  uint64_t* p_ready = s_ready + 4;  // [2][2] P in its place, and O on its scale
+  uint64_t* s_ready = q_empty + 1;  // [2] S of a stream complete
+  uint64_t* p_ready = s_ready + 2;  // [2][2] half of its P in its place, and O on its scale
   uint64_t* pv_done = p_ready + 4;  // [2][2] its product complete
   uint64_t* o_free = pv_done + 4;   // [2] O of a stream read out
   uint64_t* cl_ready = o_free + 2;
@@ -319,22 +328,24 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&kv_full[i]), 1);
-      mbar_init(smem_u32(&kv_empty[i]), 2);
+      mbar_init(smem_u32(&kv_empty[i]), 1);
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 10);
+      mbar_init(smem_u32(&item_empty[i]), 9);
     }
     mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_empty), 2);
+    mbar_init(smem_u32(q_empty), 1);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&s_ready[i]), 1);
       mbar_init(smem_u32(&p_ready[i]), 4);
       mbar_init(smem_u32(&pv_done[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&o_free[i]), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_ready[i]), 1);
+      mbar_init(smem_u32(&o_free[i]), 4);
+    }
     mbar_init(smem_u32(cl_ready), 4);
-    mbar_init(smem_u32(done), 2);
+    mbar_init(smem_u32(done), 1);
     fence_mbar_init();
   }
   if (warp == kAhMmaWarp) {
@@ -430,7 +441,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int n = it.t_end - it.t_begin;
       if (n > 0) {
         const bool two = it.tokens > a.tq;
-        const int ahead = two ? 2 : 4;  // two tiles of scores ahead in each stream
+        const int ahead = two ? 1 : 2;  // a tile of scores ahead in each stream
         for (int t = 0; ok && t < min(ahead, n); ++t) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t);
         if (!ok) break;
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_empty), q_ph ^ 1u, a.err, tlim))) {
@@ -460,21 +471,22 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         (void)mbar_wait(smem_u32(&kv_full[i]), (i < stage) ? kv_ph : (kv_ph ^ 1u), a.err, 200000000ull);
       (void)mbar_wait(smem_u32(q_full), q_ph ^ 1u, a.err, 200000000ull);
     }
-  } else if (warp >= kAhMmaWarp) {
-    // ---------------------------------- MMA, a warp per stream: while one waits
-    // for its weights or is held up by a full queue, the other's products go on
-    const int s = warp - kAhMmaWarp;
+  } else if (warp == kAhMmaWarp) {
+    // ------------------------------------------------------------------ MMA --
+    // The streams take turns: a stream's product and its next scores are issued
+    // together, so that it is back at its softmax while the other's run. (A warp
+    // per stream mixes the two in the queue; both then finish late, together, and
+    // the tensor cores wait for both softmaxes: 4100 clocks a tile of two halves
+    // instead of 2500.)
     const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
     const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
     const int steps = a.d / 16;
     const uint64_t q0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t k0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
     const uint64_t v0 = sdesc_sw128(smem_u32(sKV), kAhKvBlock, 1024);
-    const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
     int stage = 0, slot = 0;
-    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0, of_ph = 0;
-    uint32_t done_s = 0, done_p = 0;  // tiles of scores and products issued
-    bool used = false;  // the stream's O was written by an item before
+    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
+    uint32_t p_ph = 0, of_ph = 0, used = 0;  // a bit per stream; used: its O was written by an item before
     bool ok = true;
     // waits for the next k or v tile; its stage, -1 where the wait ran out
     auto next_tile = [&]() {
@@ -487,29 +499,21 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       tc_fence_after();
       return got ? at : -1;
     };
-    // the other stream's tile
-    auto skip_tile = [&]() {
-      const int at = next_tile();
-      if (lane == 0 && at >= 0) mbar_arrive(smem_u32(&kv_empty[at]));
-      __syncwarp();
-      return at >= 0;
-    };
-    auto scores = [&](int half, int at, bool last) {
+    auto scores = [&](int s, int half, int at, bool release, bool last) {
       const uint64_t ad = q0 + static_cast<uint64_t>(half) * (Sm::kQHalf >> 4);
       const uint64_t bd = k0 + static_cast<uint64_t>(at) * (Sm::kTile >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < NB * 4; ++k) {
           if (k < steps)
-            mma_bf16(s_tmem + (done_s & 1) * 64, ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2,
+            mma_bf16(tmem + s * 128, ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2,
                      bd + (k >> 2) * (kAhKvBlock >> 4) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
         }
-        mma_commit(smem_u32(&s_ready[2 * s + (done_s & 1)]));
-        mma_commit(smem_u32(&kv_empty[at]));
+        mma_commit(smem_u32(&s_ready[s]));
+        if (release) mma_commit(smem_u32(&kv_empty[at]));
         if (last) mma_commit(smem_u32(q_empty));
       }
       __syncwarp();
-      ++done_s;
     };
     while (ok) {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
@@ -524,75 +528,66 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int n = it.t_end - it.t_begin;
       if (n <= 0) continue;
       const bool two = it.tokens > a.tq;
-      const int half = two ? s : 0;
+      const int jobs = two ? 2 * n : n;  // of two halves a tile is a job for each stream in turn, of one every other tile
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_full), q_ph, a.err, tlim))) break;
       q_ph ^= 1u;
       tc_fence_after();
-      // the tiles come as k of the first two of each stream, then v of each with k of the one that far ahead
-      const int ahead = two ? 2 : 4;
-      const int last = two ? n - 1 : ((n - 1 - s) & ~1) + s;  // the stream's last tile
-      if (!two && s >= n) {  // no tile is this stream's
-        if (lane == 0) mbar_arrive(smem_u32(q_empty));
-        __syncwarp();
+      int ks = 0, vs = 0;
+      for (int j = 0; ok && j < min(2, jobs); ++j) {
+        if (!two || j == 0) ks = next_tile();
+        ok = ks >= 0;
+        if (ok) scores(j, two ? j : 0, ks, !two || j == 1, j == jobs - 1);
       }
-      for (int i = 0; ok && i < min(ahead, n); ++i) {
-        if (two || (i & 1) == s) {
-          const int at = next_tile();
-          ok = at >= 0;
-          if (ok) scores(half, at, i == last);
-        } else {
-          ok = skip_tile();
-        }
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        const bool mine = two || (i & 1) == s;
-        if (!mine) {
-          ok = skip_tile() && (i + ahead >= n || skip_tile());
-          continue;
-        }
-        const int vs = next_tile();
-        ok = vs >= 0;
-        if (!ok) break;
-        const int valid = it.len - (it.t_begin + i) * kAhKeys;
-        if (valid < kAhKeys) {
-          // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
-          uint8_t* base = sKV + vs * Sm::kTile;
-          for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
+      for (int j = 0; ok && j < jobs; ++j) {
+        const int s = j & 1;
+        if (!two || s == 0) {
+          vs = next_tile();
+          ok = vs >= 0;
+          if (!ok) break;
+          const int valid = it.len - (it.t_begin + (two ? j >> 1 : j)) * kAhKeys;
+          if (valid < kAhKeys) {
+            // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
+            uint8_t* base = sKV + vs * Sm::kTile;
+            for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
 #pragma unroll
-            for (int blk = 0; blk < NB; ++blk)
-              *reinterpret_cast<uint4*>(base + blk * kAhKvBlock + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+              for (int blk = 0; blk < NB; ++blk)
+                *reinterpret_cast<uint4*>(base + blk * kAhKvBlock + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          fence_proxy_async_smem();
+        }
+        if (j < 2 && (used >> s & 1u)) {  // the sums of the item before have been read
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[s]), of_ph >> s & 1u, a.err, tlim));
+          of_ph ^= 1u << s;
+          if (!ok) break;
+        }
+        used |= 1u << s;
+        const uint64_t bd = v0 + static_cast<uint64_t>(vs) * (Sm::kTile >> 4);
+        for (int h = 0; ok && h < 2; ++h) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[2 * s + h]), p_ph >> s & 1u, a.err, tlim));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t p_tmem = tmem + s * 128 + h * 64, o_tmem = tmem + 256 + s * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ta(o_tmem, p_tmem + k * 8, bd + (4 * h + k) * 128, idesc_o, (j < 2 && h == 0 && k == 0) ? 0u : 1u);
+            if (!two) {  // and what the weights' rounding left
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_bf16_ta(o_tmem, p_tmem + 32 + k * 8, bd + (4 * h + k) * 128, idesc_o, 1u);
+            }
+            mma_commit(smem_u32(&pv_done[2 * s + h]));
+            if (h == 1 && (!two || s == 1)) mma_commit(smem_u32(&kv_empty[vs]));
+          }
           __syncwarp();
         }
-        const bool first = i == (two ? 0 : s);
-        if (first && used) {  // the sums of the item before have been read
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[s]), of_ph, a.err, tlim));
-          of_ph ^= 1u;
-        }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[2 * s + (done_p & 1)]), (done_p >> 1) & 1u, a.err, tlim));
         if (!ok) break;
-        const uint32_t p_tmem = s_tmem + (done_p & 1) * 64;
-        used = true;
-        tc_fence_after();
-        const uint64_t bd = v0 + static_cast<uint64_t>(vs) * (Sm::kTile >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kAhKeys / 16; ++k)
-            mma_bf16_ta(o_tmem, p_tmem + k * 8, bd + k * 128, idesc_o, (first && k == 0) ? 0u : 1u);
-          if (!two) {  // and what the weights' rounding left
-#pragma unroll
-            for (int k = 0; k < kAhKeys / 16; ++k) mma_bf16_ta(o_tmem, p_tmem + 32 + k * 8, bd + k * 128, idesc_o, 1u);
-          }
-          mma_commit(smem_u32(&pv_done[2 * s + (done_p & 1)]));
-          mma_commit(smem_u32(&kv_empty[vs]));
-        }
-        __syncwarp();
-        ++done_p;
-        if (i + ahead < n) {
-          const int at = next_tile();
-          ok = at >= 0;
-          if (ok) scores(half, at, i + ahead == last);
+        p_ph ^= 1u << s;
+        if (j + 2 < jobs) {
+          if (!two || s == 0) ks = next_tile();
+          ok = ks >= 0;
+          if (ok) scores(s, two ? s : 0, ks, !two || s == 1, j + 2 == jobs - 1);
         }
       }
     }
@@ -630,94 +625,119 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       float c = kNegInf, l = 0.f;
       for (int i = 0; ok && i < mine; ++i, ++tiles) {
         const int t = it.t_begin + (two ? i : 2 * i + s);
-        const uint32_t buf = tiles & 1;
-        const uint32_t cols = s_col + buf * 64;
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[2 * s + buf]), (tiles >> 1) & 1u, a.err, tlim))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[s]), tiles & 1u, a.err, tlim))) {
           ok = false;
           break;
         }
-        if (active) {
-          tc_fence_after();
-          uint32_t sv[64];
-          tmem_ld64_wait(cols, sv);
-          const int lim = limit - t * kAhKeys;
-          if (__any_sync(0xffffffffu, lim < kAhKeys)) {
+        tc_fence_after();
+        const bool masked = __any_sync(0xffffffffu, limit - t * kAhKeys < kAhKeys);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (active) {
+            const uint32_t cols = s_col + h * 64;
+            const int lim = limit - t * kAhKeys - h * 64;
+            uint32_t sv[64];
+            tmem_ld64_wait(cols, sv);
+            if (masked) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
-          }
-          float m0 = kNegInf, m1 = kNegInf;
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
-            m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
-          }
-          const float up = ceilf(fmaxf(m0, m1) * a.kx * (1.f / kAhGrain)) * kAhGrain;
-          const bool moves = row_ok && up > c;
-          if (__any_sync(0xffffffffu, moves)) {
-            const float top = moves ? up : c;
-            const float f = pow2_diff(c, top);
-            if (i > 0) {  // O is on the old scale; the stream's last product has to be complete
-              if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + ((tiles - 1) & 1)]), ((tiles - 1) >> 1) & 1u, a.err, tlim))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              for (int col = 0; col < a.d; col += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_col + col, o);
-                tmem_wait16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(o_col + col, o);
-              }
+              for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
             }
-            l *= f;
-            c = top;
-          }
-          const float base = c == kNegInf ? 0.f : c;
-          const f32x2 nb2 = pair(-base, -base);
-          f32x2 sum = pair(0.f, 0.f);
-          if (two) {
-            uint32_t pk[32];
+            // Puts the rows of `off` on the scale of their largest score here, and O and l with them (O once the
+            // stream's last product is complete).
+            auto rescale = [&](bool off, float room) {
+              float m[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
-              const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-              sum = add2(sum, pair(p0, p1));
-              pk[e] = pack_bf16(p0, p1);
-            }
-            tmem_st32(cols, pk);
-          } else {
-            // few rows: the products wait for memory, and a second one takes what the first rounding leaves
+              for (int e = 0; e < 64; e += 8) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t p_hi[16], p_lo[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int at = part * 32 + 2 * e;
-                const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
-                const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-                sum = add2(sum, pair(p0, p1));
-                p_hi[e] = pack_bf16(p0, p1);
-                p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
+                for (int j = 0; j < 4; ++j)
+                  m[j] = max3(__uint_as_float(sv[e + 2 * j]), __uint_as_float(sv[e + 2 * j + 1]), m[j]);
               }
-              tmem_st16(cols + part * 16, p_hi);
-              tmem_st16(cols + 32 + part * 16, p_lo);
+              const float up = ceilf(max3(m[0], m[1], fmaxf(m[2], m[3])) * a.kx);
+              const float top = off && up > c + room ? up : c;
+              if (!__any_sync(0xffffffffu, top != c)) return true;
+              const float f = pow2_diff(c, top);
+              if (i + h > 0) {
+                const uint32_t last = h ? tiles : tiles - 1;
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + 1 - h]), last & 1u, a.err, tlim)))
+                  return false;
+                tc_fence_after();
+                for (int col = 0; col < a.d; col += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(o_col + col, o);
+                  tmem_wait16(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(o_col + col, o);
+                }
+              }
+              l *= f;
+              c = top;
+              return true;
+            };
+            if (two) {
+              uint32_t pk[32];
+              f32x2 sum;
+              for (bool again = false;; again = true) {
+                const float base = c == kNegInf ? 0.f : c;
+                const f32x2 nb2 = pair(-base, -base);
+                f32x2 sum1 = pair(0.f, 0.f);
+                sum = pair(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+                  const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+                  if (e & 1)
+                    sum1 = add2(sum1, pair(p0, p1));
+                  else
+                    sum = add2(sum, pair(p0, p1));
+                  pk[e] = pack_bf16(p0, p1);
+                }
+                sum = add2(sum, sum1);
+                // on the old scale: fine while no weight is far above 1, which their sum tells without a maximum
+                const bool off = row_ok && (c == kNegInf || !(lo(sum) + hi(sum) < kAhRoom));
+                if (again || !__any_sync(0xffffffffu, off)) break;
+                ok = rescale(off, 0.f);
+                if (!ok) break;
+              }
+              tmem_st32(cols, pk);
+              l += lo(sum) + hi(sum);
+            } else {
+              // few rows: the products wait for memory, and a second one takes what the first rounding leaves
+              ok = rescale(row_ok, 16.f);
+              const float base = c == kNegInf ? 0.f : c;
+              const f32x2 nb2 = pair(-base, -base);
+              f32x2 sum = pair(0.f, 0.f);
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                uint32_t p_hi[16], p_lo[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int at = part * 32 + 2 * e;
+                  const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
+                  const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+                  sum = add2(sum, pair(p0, p1));
+                  p_hi[e] = pack_bf16(p0, p1);
+                  p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
+                }
+                tmem_st16(cols + part * 16, p_hi);
+                tmem_st16(cols + 32 + part * 16, p_lo);
+              }
+              l += lo(sum) + hi(sum);
             }
+            tmem_st_wait();
+            tc_fence_before();
+            if (!ok) break;
           }
-          l += lo(sum) + hi(sum);
-          tmem_st_wait();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * s + h]));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * s + buf]));
       }
       if (!ok) break;
       const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
       if (!two && s == 1) {
         // hand (c, l) over to stream 0, which reads both sums
         if (mine > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 + ((tiles - 1) & 1)]), ((tiles - 1) >> 1) & 1u, a.err, tlim));
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[3]), (tiles - 1) & 1u, a.err, tlim));
           if (!ok) break;
           sCL[row] = make_float2(c, l);
           __syncwarp();
@@ -727,7 +747,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       float c1 = kNegInf, l1 = 0.f;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + ((tiles - 1) & 1)]), ((tiles - 1) >> 1) & 1u, a.err, tlim));
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + 1]), (tiles - 1) & 1u, a.err, tlim));
         if (ok && other > 0) {
           // stream 1 arrives after its own last product, so that O of both is complete
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(cl_ready), cl_ph, a.err, tlim));
@@ -745,33 +765,53 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         const bool sees = n > 0 && limit > 0;
         const float inv = 1.f / sum;
         const int r = (two ? s * kAhHalf : 0) + row;
-        __nv_bfloat16* dst = a.o + static_cast<long long>(it.q_row + tok) * a.ld_o +
-                             static_cast<long long>(it.head * a.group + row_head) * a.d;
-        float* part = a.part + (static_cast<long long>(it.slot) * a.slot_rows + r) * a.d;
-        for (int col = 0; col < a.d; col += 16) {
-          uint32_t o[16] = {}, o1[16] = {};
-          if (n > 0) {
-            tmem_ld16(o_col + col, o);
-            if (other > 0) tmem_ld16(o_col + 128 + col, o1);
-            tmem_wait16(o);
-            tmem_wait16(o1);
+        // through shared memory, so that a warp's stores cover whole sectors of a few rows at a time
+        uint8_t* stage = sO + warp * kAhOut;
+        const bool whole = it.slot < 0;
+        const int64_t my_row = whole ? (it.q_row + tok) * a.ld_o + static_cast<int64_t>(it.head * a.group + row_head) * a.d
+                                     : (static_cast<int64_t>(it.slot) * a.slot_rows + r) * a.d;
+        const unsigned ok_rows = __ballot_sync(0xffffffffu, row_ok);
+        for (int col = 0; col < a.d; col += 32) {
+          uint32_t o[32];
+          float x[32];
+          if (n > 0) tmem_ld32_wait(o_col + col, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+          if (other > 0) {
+            tmem_ld32_wait(o_col + 128 + col, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
           }
-          float x[16];
+          if (whole) {  // 64 bytes a row: four lanes take a row's, eight rows at a time
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            x[e] = __uint_as_float(o[e]) * f0;
-            if (other > 0) x[e] = fmaf(__uint_as_float(o1[e]), f1, x[e]);
-          }
-          if (row_ok && it.slot < 0) {
-            uint32_t pk[8];
+            for (int j = 0; j < 4; ++j) {
+              uint32_t pk[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) pk[e] = sees ? pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv) : 0u;
-            *reinterpret_cast<uint4*>(dst + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          } else if (row_ok) {
+              for (int e = 0; e < 4; ++e)
+                pk[e] = sees ? pack_bf16(x[8 * j + 2 * e] * inv, x[8 * j + 2 * e + 1] * inv) : 0u;
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(part + col + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const int from = i * 8 + (lane >> 2), j = lane & 3;
+              const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 8;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + from * 64 + ((j ^ (from >> 1 & 3)) << 4));
+              if ((ok_rows >> from & 1) && col + j * 8 < a.d) *reinterpret_cast<uint4*>(a.o + at) = v;
+            }
+          } else {  // 128 bytes a row: eight lanes, four rows at a time
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int from = i * 4 + (lane >> 3), j = lane & 7;
+              const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 4;
+              const float4 v = *reinterpret_cast<const float4*>(stage + from * 128 + ((j ^ (from & 7)) << 4));
+              if ((ok_rows >> from & 1) && col + j * 4 < a.d) *reinterpret_cast<float4*>(a.part + at) = v;
+            }
           }
           __syncwarp();
         }
@@ -965,8 +1005,9 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   if ((st = encode_tiled_4d(&tq, q, qdims, qstrides, 64, a.group, a.tq)) != CC_OK) return st;
   if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
   const int grid = std::min(kAhMaxCtas, di.sm_count);
+  a.inv_ctas = ~0ull / grid + 1;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  st = a.d > 64 ? launch_attn<2, 10>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 16>(what, tq, tk, tv, a, grid, cs);
+  st = a.d > 64 ? launch_attn<2, 4>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 8>(what, tq, tk, tv, a, grid, cs);
   if (st != CC_OK || !a.may_split) return st;
   // the joining kernel's CTAs: a row to each where few items are cut into many pieces, else eight
   const int join_y = a.slot_rows <= 32 ? a.slot_rows : a.slot_rows / 8;
