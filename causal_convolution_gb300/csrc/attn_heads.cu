@@ -40,16 +40,16 @@
 namespace cc {
 namespace {
 
-constexpr int kAhTmaWarp = 8;     // behind 8 softmax warps
-constexpr int kAhMmaWarp = 9;
-constexpr int kAhThreads = 320;
+constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
+constexpr int kAhMmaWarp = 17;
+constexpr int kAhThreads = 576;
 constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
 constexpr int kAhKeys = 128;      // keys per tile, in two halves for the softmax
 constexpr int kAhHalf = 128;      // rows per half
 constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 channels
 constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
 constexpr int kAhItems = 4;       // item descriptors in flight
-constexpr int kAhOut = 32 * 128;  // bytes through which a softmax warp's 32 rows of output go
+constexpr int kAhOut = 1024;      // bytes through which a softmax warp's output goes
 constexpr float kAhRoom = 1048576.f;  // 2^20: how far a row's weights may pass its scale
 // Tiles that cutting items costs a call, in time of its critical path: the
 // partial sums' way through L2 and the joining kernel.
@@ -287,13 +287,38 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
+// mbar_wait for a whole warp, with a few tries before the first look at the
+// clock, whose latency would come on top of a wait that is nearly over.
+__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, const AhArgs& a) {
+  const uint32_t at = smem_u32(bar);
+  for (int i = 0; i < 16; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+  }
+  return __all_sync(0xffffffffu, mbar_wait(at, parity, a.err, a.timeout_ns));
+}
+
+// A value that all lanes hold, said in a way that the compiler keeps it in
+// uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// A matrix descriptor as sdesc_sw128 makes it, in halves: only the low one, the
+// address, changes from product to product.
+__device__ __forceinline__ uint32_t sdesc_low(const void* p, uint32_t lbo_bytes) {
+  return static_cast<uint32_t>(sdesc_sw128(smem_u32(p), lbo_bytes, 1024));
+}
+__device__ __forceinline__ uint64_t sdesc_of(uint32_t low) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "n"(static_cast<int>(64u | 1u << 14 | 2u << 29)));
+  return d;
+}
+
 // NB: 64-channel blocks of a head; STAGES: k or v tiles in flight.
 template <int NB, int STAGES>
 struct AhSmem {
   static constexpr int kTile = NB * kAhKvBlock;
   static constexpr int kQHalf = NB * kAhQBlock;
   static constexpr int kQ = 2 * kQHalf;
-  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 8 * kAhOut + 1024 + kAhHalf * 8;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 16 * kAhOut + 1024 + 2 * kAhHalf * 8 + 4 * kAhHalf * 4;
 };
 
 template <int NB, int STAGES>
@@ -306,8 +331,9 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + Sm::kQ;
   uint8_t* sO = sKV + STAGES * Sm::kTile;
-  float2* sCL = reinterpret_cast<float2*>(sO + 8 * kAhOut);  // stream 1's (c, l) of single halves
-  AhItem* items = reinterpret_cast<AhItem*>(sCL + kAhHalf);
+  float2* sCL = reinterpret_cast<float2*>(sO + 16 * kAhOut);  // [2][128] stream 1's (c, l) of single halves
+  float* sX = reinterpret_cast<float*>(sCL + 2 * kAhHalf);    // [4][128] what warps of the same rows exchange
+  AhItem* items = reinterpret_cast<AhItem*>(sX + 4 * kAhHalf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + STAGES;
@@ -316,9 +342,9 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint64_t* q_full = item_empty + kAhItems;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_ready = q_empty + 1;  // [2] S of a stream complete
-  uint64_t* p_ready = s_ready + 2;  // [2][2] half of its P in its place, and O on its scale
-  uint64_t* pv_done = p_ready + 4;  // [2][2] its product complete
-  uint64_t* o_free = pv_done + 4;   // [2] O of a stream read out
+  uint64_t* p_ready = s_ready + 2;  // [2] P in its place, and O on its scale
+  uint64_t* pv_done = p_ready + 2;  // [2] the item's last product of a stream complete
+  uint64_t* o_free = pv_done + 2;   // [2] O of a stream read out
   uint64_t* cl_ready = o_free + 2;
   uint64_t* done = cl_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -332,19 +358,17 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 9);
+      mbar_init(smem_u32(&item_empty[i]), 17);
     }
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 1);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&p_ready[i]), 4);
-      mbar_init(smem_u32(&pv_done[i]), 1);
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_ready[i]), 1);
-      mbar_init(smem_u32(&o_free[i]), 4);
+      mbar_init(smem_u32(&p_ready[i]), 8);
+      mbar_init(smem_u32(&pv_done[i]), 1);
+      mbar_init(smem_u32(&o_free[i]), 8);
     }
-    mbar_init(smem_u32(cl_ready), 4);
+    mbar_init(smem_u32(cl_ready), 8);
     mbar_init(smem_u32(done), 1);
     fence_mbar_init();
   }
@@ -476,14 +500,11 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     // The streams take turns: a stream's product and its next scores are issued
     // together, so that it is back at its softmax while the other's run. (A warp
     // per stream mixes the two in the queue; both then finish late, together, and
-    // the tensor cores wait for both softmaxes: 4100 clocks a tile of two halves
-    // instead of 2500.)
+    // the tensor cores wait for both softmaxes.)
     const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
     const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
     const int steps = a.d / 16;
-    const uint64_t q0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t k0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
-    const uint64_t v0 = sdesc_sw128(smem_u32(sKV), kAhKvBlock, 1024);
+    const uint32_t q0 = sdesc_low(sQ, 16), k0 = sdesc_low(sKV, 16), v0 = sdesc_low(sKV, kAhKvBlock);
     int stage = 0, slot = 0;
     uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
     uint32_t p_ph = 0, of_ph = 0, used = 0;  // a bit per stream; used: its O was written by an item before
@@ -491,23 +512,22 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     // waits for the next k or v tile; its stage, -1 where the wait ran out
     auto next_tile = [&]() {
       const int at = stage;
-      const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[stage]), kv_ph, a.err, tlim));
+      const bool got = warp_wait(&kv_full[stage], kv_ph, a);
       if (++stage == STAGES) {
         stage = 0;
         kv_ph ^= 1u;
       }
-      tc_fence_after();
       return got ? at : -1;
     };
     auto scores = [&](int s, int half, int at, bool release, bool last) {
-      const uint64_t ad = q0 + static_cast<uint64_t>(half) * (Sm::kQHalf >> 4);
-      const uint64_t bd = k0 + static_cast<uint64_t>(at) * (Sm::kTile >> 4);
+      const uint32_t ad = q0 + half * (Sm::kQHalf >> 4), bd = k0 + at * (Sm::kTile >> 4);
+      tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < NB * 4; ++k) {
           if (k < steps)
-            mma_bf16(tmem + s * 128, ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2,
-                     bd + (k >> 2) * (kAhKvBlock >> 4) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
+            mma_bf16(tmem + s * 128, sdesc_of(ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2),
+                     sdesc_of(bd + (k >> 2) * (kAhKvBlock >> 4) + (k & 3) * 2), idesc_s, k ? 1u : 0u);
         }
         mma_commit(smem_u32(&s_ready[s]));
         if (release) mma_commit(smem_u32(&kv_empty[at]));
@@ -515,23 +535,23 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       __syncwarp();
     };
-    while (ok) {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
-      const AhItem it = items[slot];
+    while (true) {
+      if (!warp_wait(&item_full[slot], it_ph, a)) break;
+      const AhItem* it = &items[slot];
+      const int last = uniform(it->last), t_begin = uniform(it->t_begin), len = uniform(it->len);
+      const int n = uniform(it->t_end) - t_begin;
+      const bool two = uniform(it->tokens) > a.tq;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
       if (++slot == kAhItems) {
         slot = 0;
         it_ph ^= 1u;
       }
-      if (it.last) break;
-      const int n = it.t_end - it.t_begin;
+      if (last) break;
       if (n <= 0) continue;
-      const bool two = it.tokens > a.tq;
       const int jobs = two ? 2 * n : n;  // of two halves a tile is a job for each stream in turn, of one every other tile
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_full), q_ph, a.err, tlim))) break;
+      if (!warp_wait(q_full, q_ph, a)) break;
       q_ph ^= 1u;
-      tc_fence_after();
       int ks = 0, vs = 0;
       for (int j = 0; ok && j < min(2, jobs); ++j) {
         if (!two || j == 0) ks = next_tile();
@@ -544,7 +564,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           vs = next_tile();
           ok = vs >= 0;
           if (!ok) break;
-          const int valid = it.len - (it.t_begin + (two ? j >> 1 : j)) * kAhKeys;
+          const int valid = len - (t_begin + (two ? j >> 1 : j)) * kAhKeys;
           if (valid < kAhKeys) {
             // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
             uint8_t* base = sKV + vs * Sm::kTile;
@@ -558,55 +578,58 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           }
         }
         if (j < 2 && (used >> s & 1u)) {  // the sums of the item before have been read
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_free[s]), of_ph >> s & 1u, a.err, tlim));
+          ok = warp_wait(&o_free[s], of_ph >> s & 1u, a);
           of_ph ^= 1u << s;
           if (!ok) break;
         }
         used |= 1u << s;
-        const uint64_t bd = v0 + static_cast<uint64_t>(vs) * (Sm::kTile >> 4);
-        for (int h = 0; ok && h < 2; ++h) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_ready[2 * s + h]), p_ph >> s & 1u, a.err, tlim));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t p_tmem = tmem + s * 128 + h * 64, o_tmem = tmem + 256 + s * 128;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_ta(o_tmem, p_tmem + k * 8, bd + (4 * h + k) * 128, idesc_o, (j < 2 && h == 0 && k == 0) ? 0u : 1u);
-            if (!two) {  // and what the weights' rounding left
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_bf16_ta(o_tmem, p_tmem + 32 + k * 8, bd + (4 * h + k) * 128, idesc_o, 1u);
-            }
-            mma_commit(smem_u32(&pv_done[2 * s + h]));
-            if (h == 1 && (!two || s == 1)) mma_commit(smem_u32(&kv_empty[vs]));
-          }
-          __syncwarp();
-        }
+        ok = warp_wait(&p_ready[s], p_ph >> s & 1u, a);
         if (!ok) break;
         p_ph ^= 1u << s;
+        const uint32_t bd = v0 + vs * (Sm::kTile >> 4), p_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
+        tc_fence_after();
+        if (elect_one()) {
+          // P of a tile's halves: columns 0-31 and 64-95, what their rounding left: 32-63 and 96-127
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ta(o_tmem, p_tmem + (k >> 2) * 64 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, (j >= 2 || k) ? 1u : 0u);
+          if (!two) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_ta(o_tmem, p_tmem + (k >> 2) * 64 + 32 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, 1u);
+          }
+          if (j + 2 >= jobs) mma_commit(smem_u32(&pv_done[s]));
+          if (!two || s == 1) mma_commit(smem_u32(&kv_empty[vs]));
+        }
+        __syncwarp();
         if (j + 2 < jobs) {
           if (!two || s == 0) ks = next_tile();
           ok = ks >= 0;
           if (ok) scores(s, two ? s : 0, ks, !two || s == 1, j + 2 == jobs - 1);
         }
       }
+      if (!ok) break;
     }
     if (elect_one()) mma_commit(smem_u32(done));
     __syncwarp();
     (void)mbar_wait(smem_u32(done), 0, a.err, tlim);
   } else {
     // -------------------------------------------------------------- softmax --
-    const int s = warp >> 2;  // stream
+    const int s = warp >> 3;         // stream
+    const int hf = (warp >> 2) & 1;  // half of a tile's keys
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lanes + s * 128, o_col = tmem + lanes + 256 + s * 128;
+    const uint32_t s_col = tmem + lanes + s * 128 + hf * 64, o_col = tmem + lanes + 256 + s * 128;
+    const uint32_t mates = 1 + s * 4 + (warp & 3);  // barrier of the two warps that share these rows
+    float* my_x = sX + (2 * s + hf) * kAhHalf + row;
+    const float* mate_x = sX + (2 * s + 1 - hf) * kAhHalf + row;
     const int row_tok = row / a.group, row_head = row - row_tok * a.group;
     const f32x2 kx2 = pair(a.kx, a.kx);
     int slot = 0;
-    uint32_t it_ph = 0, cl_ph = 0, tiles = 0;  // tiles: of the stream so far
+    uint32_t it_ph = 0, cl_ph = 0, s_ph = 0, pv_ph = 0;
     bool ok = true;
     while (ok) {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_full[slot]), it_ph, a.err, tlim))) break;
+      if (!warp_wait(&item_full[slot], it_ph, a)) break;
       const AhItem it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
@@ -623,123 +646,124 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const bool active = __any_sync(0xffffffffu, row_ok);
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
       float c = kNegInf, l = 0.f;
-      for (int i = 0; ok && i < mine; ++i, ++tiles) {
+      for (int i = 0; i < mine; ++i) {
         const int t = it.t_begin + (two ? i : 2 * i + s);
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[s]), tiles & 1u, a.err, tlim))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool masked = __any_sync(0xffffffffu, limit - t * kAhKeys < kAhKeys);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (active) {
-            const uint32_t cols = s_col + h * 64;
-            const int lim = limit - t * kAhKeys - h * 64;
-            uint32_t sv[64];
-            tmem_ld64_wait(cols, sv);
+        ok = warp_wait(&s_ready[s], s_ph, a);
+        if (!ok) break;
+        s_ph ^= 1u;
+        if (active) {
+          tc_fence_after();
+          const int lim = limit - t * kAhKeys - hf * 64;
+          const bool masked = __any_sync(0xffffffffu, lim < 64);
+          uint32_t sv[64];
+          auto load = [&]() {
+            tmem_ld64_wait(s_col, sv);
             if (masked) {
 #pragma unroll
               for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
             }
-            // Puts the rows of `off` on the scale of their largest score here, and O and l with them (O once the
-            // stream's last product is complete).
-            auto rescale = [&](bool off, float room) {
-              float m[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+          };
+          // Puts the rows of `off` on the scale of their largest score in this tile, and l and O with them (O's last
+          // product was complete before these scores were). Both warps of a row come here together, and the barrier
+          // keeps their weights from scores that the other one has not read.
+          auto rescale = [&](bool off, float room) {
+            float m[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-              for (int e = 0; e < 64; e += 8) {
+            for (int e = 0; e < 64; e += 8) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  m[j] = max3(__uint_as_float(sv[e + 2 * j]), __uint_as_float(sv[e + 2 * j + 1]), m[j]);
+              for (int j = 0; j < 4; ++j)
+                m[j] = max3(__uint_as_float(sv[e + 2 * j]), __uint_as_float(sv[e + 2 * j + 1]), m[j]);
+            }
+            float up = ceilf(max3(m[0], m[1], fmaxf(m[2], m[3])) * a.kx);
+            *my_x = up;
+            named_barrier_sync(mates, 64);
+            up = fmaxf(up, *mate_x);
+            const float top = off && up > c + room ? up : c;
+            if (!__any_sync(0xffffffffu, top != c)) return;
+            const float f = pow2_diff(c, top);
+            if (i > 0) {
+              for (int col = hf * 16; col < a.d; col += 32) {
+                uint32_t o[16];
+                tmem_ld16(o_col + col, o);
+                tmem_wait16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_col + col, o);
               }
-              const float up = ceilf(max3(m[0], m[1], fmaxf(m[2], m[3])) * a.kx);
-              const float top = off && up > c + room ? up : c;
-              if (!__any_sync(0xffffffffu, top != c)) return true;
-              const float f = pow2_diff(c, top);
-              if (i + h > 0) {
-                const uint32_t last = h ? tiles : tiles - 1;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + 1 - h]), last & 1u, a.err, tlim)))
-                  return false;
-                tc_fence_after();
-                for (int col = 0; col < a.d; col += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(o_col + col, o);
-                  tmem_wait16(o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st16(o_col + col, o);
-                }
-              }
-              l *= f;
-              c = top;
-              return true;
-            };
-            if (two) {
-              uint32_t pk[32];
-              f32x2 sum;
-              for (bool again = false;; again = true) {
-                const float base = c == kNegInf ? 0.f : c;
-                const f32x2 nb2 = pair(-base, -base);
-                f32x2 sum1 = pair(0.f, 0.f);
-                sum = pair(0.f, 0.f);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
-                  const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-                  if (e & 1)
-                    sum1 = add2(sum1, pair(p0, p1));
-                  else
-                    sum = add2(sum, pair(p0, p1));
-                  pk[e] = pack_bf16(p0, p1);
-                }
-                sum = add2(sum, sum1);
-                // on the old scale: fine while no weight is far above 1, which their sum tells without a maximum
-                const bool off = row_ok && (c == kNegInf || !(lo(sum) + hi(sum) < kAhRoom));
-                if (again || !__any_sync(0xffffffffu, off)) break;
-                ok = rescale(off, 0.f);
-                if (!ok) break;
-              }
-              tmem_st32(cols, pk);
-              l += lo(sum) + hi(sum);
-            } else {
-              // few rows: the products wait for memory, and a second one takes what the first rounding leaves
-              ok = rescale(row_ok, 16.f);
+            }
+            l *= f;
+            c = top;
+          };
+          load();
+          if (two) {
+            // Weights on the scale in hand, which is fine while none is far above 1; their sum tells that without a
+            // maximum. Rows without a scale, and those that outgrow theirs, get one, and the tile is done again.
+            for (bool again = i == 0;; again = true) {
+              if (again) rescale(row_ok, i == 0 ? 0.f : 8.f);
               const float base = c == kNegInf ? 0.f : c;
               const f32x2 nb2 = pair(-base, -base);
-              f32x2 sum = pair(0.f, 0.f);
+              f32x2 sum = pair(0.f, 0.f), sum1 = sum;
+              uint32_t pk[32];
 #pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                uint32_t p_hi[16], p_lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int at = part * 32 + 2 * e;
-                  const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
-                  const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+              for (int e = 0; e < 32; ++e) {
+                const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+                const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+                if (e & 1)
+                  sum1 = add2(sum1, pair(p0, p1));
+                else
                   sum = add2(sum, pair(p0, p1));
-                  p_hi[e] = pack_bf16(p0, p1);
-                  p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
-                }
-                tmem_st16(cols + part * 16, p_hi);
-                tmem_st16(cols + 32 + part * 16, p_lo);
+                pk[e] = pack_bf16(p0, p1);
               }
-              l += lo(sum) + hi(sum);
+              sum = add2(sum, sum1);
+              const float total = lo(sum) + hi(sum);
+              if (!again && named_barrier_or(mates, 64, row_ok && (c == kNegInf || !(total < kAhRoom)))) {
+                load();
+                continue;
+              }
+              tmem_st32(s_col, pk);
+              l += total;
+              break;
             }
-            tmem_st_wait();
-            tc_fence_before();
-            if (!ok) break;
+          } else {
+            // few rows: the products wait for memory, and a second one takes what the first rounding leaves
+            rescale(row_ok, i == 0 ? 0.f : 16.f);
+            const float base = c == kNegInf ? 0.f : c;
+            const f32x2 nb2 = pair(-base, -base);
+            f32x2 sum = pair(0.f, 0.f);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              uint32_t p_hi[16], p_lo[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int at = part * 32 + 2 * e;
+                const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
+                const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
+                sum = add2(sum, pair(p0, p1));
+                p_hi[e] = pack_bf16(p0, p1);
+                p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
+              }
+              tmem_st16(s_col + part * 16, p_hi);
+              tmem_st16(s_col + 32 + part * 16, p_lo);
+            }
+            l += lo(sum) + hi(sum);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * s + h]));
+          tmem_st_wait();
+          tc_fence_before();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_ready[s]));
       }
       if (!ok) break;
       const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
+      if (mine > 0) {
+        ok = warp_wait(&pv_done[s], pv_ph, a);
+        pv_ph ^= 1u;
+        if (!ok) break;
+      }
       if (!two && s == 1) {
         // hand (c, l) over to stream 0, which reads both sums
         if (mine > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[3]), (tiles - 1) & 1u, a.err, tlim));
-          if (!ok) break;
-          sCL[row] = make_float2(c, l);
+          sCL[hf * kAhHalf + row] = make_float2(c, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(cl_ready));
         }
@@ -747,16 +771,20 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       float c1 = kNegInf, l1 = 0.f;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * s + 1]), (tiles - 1) & 1u, a.err, tlim));
-        if (ok && other > 0) {
+        if (other > 0) {
           // stream 1 arrives after its own last product, so that O of both is complete
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(cl_ready), cl_ph, a.err, tlim));
+          ok = warp_wait(cl_ready, cl_ph, a);
           cl_ph ^= 1u;
+          if (!ok) break;
           c1 = sCL[row].x;
-          l1 = sCL[row].y;
+          l1 = sCL[row].y + sCL[kAhHalf + row].y;
         }
-        if (!ok) break;
         tc_fence_after();
+        // the row's whole sum; the second barrier keeps the next item's maxima from what is read here
+        *my_x = l;
+        named_barrier_sync(mates, 64);
+        l += *mate_x;
+        named_barrier_sync(mates, 64);
       }
       const float top = fmaxf(c, c1);
       const float f0 = pow2_diff(c, top), f1 = pow2_diff(c1, top);
@@ -765,13 +793,13 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         const bool sees = n > 0 && limit > 0;
         const float inv = 1.f / sum;
         const int r = (two ? s * kAhHalf : 0) + row;
-        // through shared memory, so that a warp's stores cover whole sectors of a few rows at a time
+        // through shared memory, so that a warp's stores cover more than a sector of a row
         uint8_t* stage = sO + warp * kAhOut;
         const bool whole = it.slot < 0;
         const int64_t my_row = whole ? (it.q_row + tok) * a.ld_o + static_cast<int64_t>(it.head * a.group + row_head) * a.d
                                      : (static_cast<int64_t>(it.slot) * a.slot_rows + r) * a.d;
         const unsigned ok_rows = __ballot_sync(0xffffffffu, row_ok);
-        for (int col = 0; col < a.d; col += 32) {
+        for (int col = hf * 32; col < a.d; col += 64) {  // the two warps of a row take turns
           uint32_t o[32];
           float x[32];
           if (n > 0) tmem_ld32_wait(o_col + col, o);
@@ -782,40 +810,50 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
           }
-          if (whole) {  // 64 bytes a row: four lanes take a row's, eight rows at a time
+          if (whole) {  // 64 bytes a row, 16 rows at a time
+            uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t pk[4];
+            for (int e = 0; e < 16; ++e) pk[e] = sees ? pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv) : 0u;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                pk[e] = sees ? pack_bf16(x[8 * j + 2 * e] * inv, x[8 * j + 2 * e + 1] * inv) : 0u;
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int pass = 0; pass < 2; ++pass) {
+              if (lane >> 4 == pass) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  *reinterpret_cast<uint4*>(stage + (lane & 15) * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
+                      make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r16 = i * 8 + (lane >> 2), j = lane & 3, from = pass * 16 + r16;
+                const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 8;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + r16 * 64 + ((j ^ (r16 >> 1 & 3)) << 4));
+                if ((ok_rows >> from & 1) && col + j * 8 < a.d) *reinterpret_cast<uint4*>(a.o + at) = v;
+              }
+              __syncwarp();
             }
-            __syncwarp();
+          } else {  // 128 bytes a row, eight rows at a time
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int from = i * 8 + (lane >> 2), j = lane & 3;
-              const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 8;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + from * 64 + ((j ^ (from >> 1 & 3)) << 4));
-              if ((ok_rows >> from & 1) && col + j * 8 < a.d) *reinterpret_cast<uint4*>(a.o + at) = v;
-            }
-          } else {  // 128 bytes a row: eight lanes, four rows at a time
+            for (int pass = 0; pass < 4; ++pass) {
+              if (lane >> 3 == pass) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                  make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-            __syncwarp();
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<float4*>(stage + (lane & 7) * 128 + ((j ^ (lane & 7)) << 4)) =
+                      make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+              }
+              __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int from = i * 4 + (lane >> 3), j = lane & 7;
-              const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 4;
-              const float4 v = *reinterpret_cast<const float4*>(stage + from * 128 + ((j ^ (from & 7)) << 4));
-              if ((ok_rows >> from & 1) && col + j * 4 < a.d) *reinterpret_cast<float4*>(a.part + at) = v;
+              for (int i = 0; i < 2; ++i) {
+                const int r8 = i * 4 + (lane >> 3), j = lane & 7, from = pass * 8 + r8;
+                const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 4;
+                const float4 v = *reinterpret_cast<const float4*>(stage + r8 * 128 + ((j ^ r8) << 4));
+                if ((ok_rows >> from & 1) && col + j * 4 < a.d) *reinterpret_cast<float4*>(a.part + at) = v;
+              }
+              __syncwarp();
             }
           }
-          __syncwarp();
         }
-        if (row_ok && it.slot >= 0) {
+        if (row_ok && it.slot >= 0 && hf == 0) {
           const bool any = limit > it.t_begin * kAhKeys;
           a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + r] =
               make_float2(any && top == kNegInf ? kNoScore : top, sum);
