@@ -41,8 +41,8 @@ namespace cc {
 namespace {
 
 constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
-constexpr int kAhMmaWarp = 17;
-constexpr int kAhThreads = 576;
+constexpr int kAhMmaWarp = 17;    // and 18, one for each stream
+constexpr int kAhThreads = 608;
 constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
 constexpr int kAhKeys = 128;      // keys per tile, in two halves for the softmax
 constexpr int kAhHalf = 128;      // rows per half
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint64_t* pv_done = p_ready + 2;  // [2] the item's last product of a stream complete
   uint64_t* o_free = pv_done + 2;   // [2] O of a stream read out
   uint64_t* cl_ready = o_free + 2;
-  uint64_t* done = cl_ready + 1;
+  uint64_t* turns = cl_ready + 1;   // [4] a job of the MMA warps issued
+  uint64_t* done = turns + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -354,22 +355,23 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&kv_full[i]), 1);
-      mbar_init(smem_u32(&kv_empty[i]), 1);
+      mbar_init(smem_u32(&kv_empty[i]), 2);
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 17);
+      mbar_init(smem_u32(&item_empty[i]), 18);
     }
     mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_empty), 1);
+    mbar_init(smem_u32(q_empty), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_ready[i]), 1);
       mbar_init(smem_u32(&p_ready[i]), 8);
       mbar_init(smem_u32(&pv_done[i]), 1);
       mbar_init(smem_u32(&o_free[i]), 8);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&turns[i]), 1);
     mbar_init(smem_u32(cl_ready), 8);
-    mbar_init(smem_u32(done), 1);
+    mbar_init(smem_u32(done), 2);
     fence_mbar_init();
   }
   if (warp == kAhMmaWarp) {
@@ -495,19 +497,24 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         (void)mbar_wait(smem_u32(&kv_full[i]), (i < stage) ? kv_ph : (kv_ph ^ 1u), a.err, 200000000ull);
       (void)mbar_wait(smem_u32(q_full), q_ph ^ 1u, a.err, 200000000ull);
     }
-  } else if (warp == kAhMmaWarp) {
-    // ------------------------------------------------------------------ MMA --
-    // The streams take turns: a stream's product and its next scores are issued
-    // together, so that it is back at its softmax while the other's run. (A warp
-    // per stream mixes the two in the queue; both then finish late, together, and
-    // the tensor cores wait for both softmaxes.)
+  } else if (warp >= kAhMmaWarp) {
+    // ------------------------------------------------ MMA, a warp per stream --
+    // A product and the stream's next scores are a job. Jobs are issued one after
+    // the other, streams in turn, so that a stream is back at its softmax while
+    // the other's job runs; the queue holds next to nothing, so a warp that has
+    // its turn has done its waiting before. In clocks for a tile of two halves
+    // (2048 of products): one warp for both streams 3500, two without turns, which
+    // mix the streams and finish both late, 4100.
+    const int s = uniform(warp - kAhMmaWarp);
     const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
     const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
     const int steps = a.d / 16;
     const uint32_t q0 = sdesc_low(sQ, 16), k0 = sdesc_low(sKV, 16), v0 = sdesc_low(sKV, kAhKvBlock);
+    const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
     int stage = 0, slot = 0;
-    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
-    uint32_t p_ph = 0, of_ph = 0, used = 0;  // a bit per stream; used: its O was written by an item before
+    uint32_t kv_ph = 0, it_ph = 0, q_ph = 0, p_ph = 0, of_ph = 0;
+    uint32_t job = 0;   // number of the item's first job, of both streams
+    bool used = false;  // the stream's O was written by an item before
     bool ok = true;
     // waits for the next k or v tile; its stage, -1 where the wait ran out
     auto next_tile = [&]() {
@@ -519,18 +526,31 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       return got ? at : -1;
     };
-    auto scores = [&](int s, int half, int at, bool release, bool last) {
+    // the other stream's tile
+    auto skip_tile = [&]() {
+      const int at = next_tile();
+      if (lane == 0 && at >= 0) mbar_arrive(smem_u32(&kv_empty[at]));
+      __syncwarp();
+      return at >= 0;
+    };
+    // job j waits until the one in front of it has been issued, and says when it has been
+    auto turn = [&](uint32_t j) { return j == 0 || warp_wait(&turns[(j - 1) & 3], (j - 1) >> 2 & 1u, a); };
+    auto issued = [&](uint32_t j) {
+      if (lane == 0) mbar_arrive(smem_u32(&turns[j & 3]));
+      __syncwarp();
+    };
+    auto scores = [&](int half, int at, bool last) {
       const uint32_t ad = q0 + half * (Sm::kQHalf >> 4), bd = k0 + at * (Sm::kTile >> 4);
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < NB * 4; ++k) {
           if (k < steps)
-            mma_bf16(tmem + s * 128, sdesc_of(ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2),
+            mma_bf16(s_tmem, sdesc_of(ad + (k >> 2) * (kAhQBlock >> 4) + (k & 3) * 2),
                      sdesc_of(bd + (k >> 2) * (kAhKvBlock >> 4) + (k & 3) * 2), idesc_s, k ? 1u : 0u);
         }
         mma_commit(smem_u32(&s_ready[s]));
-        if (release) mma_commit(smem_u32(&kv_empty[at]));
+        mma_commit(smem_u32(&kv_empty[at]));
         if (last) mma_commit(smem_u32(q_empty));
       }
       __syncwarp();
@@ -549,66 +569,85 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       if (last) break;
       if (n <= 0) continue;
-      const int jobs = two ? 2 * n : n;  // of two halves a tile is a job for each stream in turn, of one every other tile
+      const int half = two ? s : 0;
+      const int jobs = two ? 2 * n : n;  // of two halves a tile is a job for each stream, of one every other tile
+      const int firsts = min(2, jobs);   // in front of them, each stream's first scores
       if (!warp_wait(q_full, q_ph, a)) break;
       q_ph ^= 1u;
-      int ks = 0, vs = 0;
-      for (int j = 0; ok && j < min(2, jobs); ++j) {
-        if (!two || j == 0) ks = next_tile();
-        ok = ks >= 0;
-        if (ok) scores(j, two ? j : 0, ks, !two || j == 1, j == jobs - 1);
-      }
-      for (int j = 0; ok && j < jobs; ++j) {
-        const int s = j & 1;
-        if (!two || s == 0) {
-          vs = next_tile();
-          ok = vs >= 0;
-          if (!ok) break;
-          const int valid = len - (t_begin + (two ? j >> 1 : j)) * kAhKeys;
-          if (valid < kAhKeys) {
-            // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
-            uint8_t* base = sKV + vs * Sm::kTile;
-            for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
-#pragma unroll
-              for (int blk = 0; blk < NB; ++blk)
-                *reinterpret_cast<uint4*>(base + blk * kAhKvBlock + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+      if (s >= jobs && lane == 0) mbar_arrive(smem_u32(q_empty));
+      __syncwarp();
+      // the tiles come as k of each stream's first, then v of each with k of the one that far ahead
+      const int ahead = two ? 1 : 2;
+      for (int i = 0; ok && i < min(ahead, n); ++i) {
+        if (!two && i != s) {
+          ok = skip_tile();
+          continue;
         }
-        if (j < 2 && (used >> s & 1u)) {  // the sums of the item before have been read
-          ok = warp_wait(&o_free[s], of_ph >> s & 1u, a);
-          of_ph ^= 1u << s;
-          if (!ok) break;
-        }
-        used |= 1u << s;
-        ok = warp_wait(&p_ready[s], p_ph >> s & 1u, a);
+        const int ks = next_tile();
+        ok = ks >= 0 && turn(job + s);
         if (!ok) break;
-        p_ph ^= 1u << s;
-        const uint32_t bd = v0 + vs * (Sm::kTile >> 4), p_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
+        scores(half, ks, s + 2 >= jobs);
+        issued(job + s);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const bool more = i + ahead < n;
+        if (!two && (i & 1) != s) {
+          ok = skip_tile() && (!more || skip_tile());
+          continue;
+        }
+        const int j = two ? 2 * i + s : i;
+        const int vs = next_tile();
+        ok = vs >= 0;
+        if (!ok) break;
+        const int valid = len - (t_begin + i) * kAhKeys;
+        if (valid < kAhKeys) {
+          // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
+          uint8_t* base = sKV + vs * Sm::kTile;
+          for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk)
+              *reinterpret_cast<uint4*>(base + blk * kAhKvBlock + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        int ks = 0;
+        if (two && more) ks = next_tile();  // of one half memory sets the pace: no product waits for a tile it does not need
+        ok = ks >= 0;
+        if (ok && j < 2 && used) {  // the sums of the item before have been read
+          ok = warp_wait(&o_free[s], of_ph, a);
+          of_ph ^= 1u;
+        }
+        used = true;
+        ok = ok && warp_wait(&p_ready[s], p_ph, a) && turn(job + firsts + j);
+        if (!ok) break;
+        p_ph ^= 1u;
+        const uint32_t bd = v0 + vs * (Sm::kTile >> 4);
         tc_fence_after();
         if (elect_one()) {
           // P of a tile's halves: columns 0-31 and 64-95, what their rounding left: 32-63 and 96-127
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_bf16_ta(o_tmem, p_tmem + (k >> 2) * 64 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, (j >= 2 || k) ? 1u : 0u);
+            mma_bf16_ta(o_tmem, s_tmem + (k >> 2) * 64 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, (j >= 2 || k) ? 1u : 0u);
           if (!two) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_bf16_ta(o_tmem, p_tmem + (k >> 2) * 64 + 32 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, 1u);
+              mma_bf16_ta(o_tmem, s_tmem + (k >> 2) * 64 + 32 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, 1u);
           }
           if (j + 2 >= jobs) mma_commit(smem_u32(&pv_done[s]));
-          if (!two || s == 1) mma_commit(smem_u32(&kv_empty[vs]));
+          mma_commit(smem_u32(&kv_empty[vs]));
         }
         __syncwarp();
-        if (j + 2 < jobs) {
-          if (!two || s == 0) ks = next_tile();
+        if (more) {
+          if (!two) ks = next_tile();
           ok = ks >= 0;
-          if (ok) scores(s, two ? s : 0, ks, !two || s == 1, j + 2 == jobs - 1);
+          if (!ok) break;
+          scores(half, ks, j + 4 >= jobs);
         }
+        issued(job + firsts + j);
       }
       if (!ok) break;
+      job += firsts + jobs;
     }
     if (elect_one()) mma_commit(smem_u32(done));
     __syncwarp();
