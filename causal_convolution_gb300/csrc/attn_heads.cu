@@ -32,10 +32,8 @@
 #include <cmath>
 
 #include "cc.h"
+#include "cc_heads.cuh"
 #include "cc_host.h"
-#include "cc_paged.cuh"
-#include "cc_ptx.cuh"
-#include "cc_rows.cuh"
 
 namespace cc {
 namespace {
@@ -43,259 +41,14 @@ namespace {
 constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
 constexpr int kAhMmaWarp = 17;    // and 18, one for each stream
 constexpr int kAhThreads = 608;
-constexpr int kAhMaxCtas = 152;   // one per SM of a GB300
-constexpr int kAhKeys = 128;      // keys per tile, in two halves for the softmax
+constexpr int kAhTileShift = 7;
+constexpr int kAhKeys = 1 << kAhTileShift;  // keys per tile, in two halves for the softmax
 constexpr int kAhHalf = 128;      // rows per half
 constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 channels
 constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
-constexpr int kAhItems = 4;       // item descriptors in flight
 constexpr int kAhOut = 1024;      // bytes through which a softmax warp's output goes
 constexpr float kAhRoom = 1048576.f;  // 2^20: how far a row's weights may pass its scale
-// Tiles that cutting items costs a call, in time of its critical path: the
-// partial sums' way through L2 and the joining kernel.
-constexpr int kAhSplitCost = 4;
-
-struct AhArgs {
-  KvPlan plan;      // q_offsets nullptr: sequence b owns rows b * lq .. (b + 1) * lq - 1; page_table nullptr: page b
-  int lq;
-  int rows, heads, kv_heads, group, d;
-  int tq;           // tokens of a half: 128 / group
-  int box;          // slots per TMA box: pieces of this size never cross a page
-  __nv_bfloat16* o;
-  long long ld_o;
-  float kx;         // scale * log2(e)
-  unsigned block;   // causal block, 0: none
-  int may_split;
-  int slot_rows;    // rows a partial slot holds
-  float* part;      // [2 * ctas][slot_rows][d]
-  float2* part_cl;  // [2 * ctas][slot_rows] (c, l)
-  int4* meta;       // [2 * ctas]: 0 unused, 1 goes on, 2 ends its item; first row, tokens, head
-  unsigned int* err;
-  unsigned long long timeout_ns;
-  unsigned long long inv_ctas;  // ceil(2^64 / CTAs): exact quotients of anything below 2^56
-};
-
-// A piece of an item, as the roles of a CTA pass it on.
-struct __align__(16) AhItem {
-  int q_row;        // row of the item's first token
-  int tokens;       // of the item
-  int head;         // key head
-  int t_begin, t_end, t_all;  // this piece's key tiles, of all
-  int len;          // keys of the sequence
-  int first;        // the item's first token among the new ones
-  int fresh;        // new tokens of the sequence
-  int slot;         // partial slot, -1: the whole item
-  int seq;
-  int last;         // no item: the CTA is done
-};
-
-struct Seq {
-  int begin, n, len, m;  // first row, new tokens, keys, items along the rows
-};
-
-__device__ __forceinline__ Seq load_seq(const AhArgs& a, int b) {
-  Seq s = {0, 0, 0, 0};
-  if (b >= a.plan.seqs) return s;
-  if (a.plan.q_offsets) {
-    s.begin = a.plan.q_offsets[b];
-    const int end = a.plan.q_offsets[b + 1];
-    s.len = a.plan.kv_lens[b];
-    const long long n = static_cast<long long>(end) - s.begin;
-    if (n != 0 && (n < 0 || s.begin < 0 || end > a.rows || s.len < 0 || (a.block && s.len < n) ||
-                   s.len > static_cast<long long>(a.plan.max_pages) * a.plan.page_size)) {
-      atomicOr(a.err, DEVERR_BOUNDS);
-      return {0, 0, 0, 0};
-    }
-    s.n = static_cast<int>(n);
-  } else {
-    s.begin = b * a.lq;
-    s.n = a.lq;
-    s.len = a.plan.page_size;
-    if (a.plan.kv_lens) {
-      const int len = a.plan.kv_lens[b];
-      if (len < 0 || len > s.len) atomicOr(a.err, DEVERR_BOUNDS);
-      s.len = max(0, min(len, s.len));
-    }
-  }
-  s.m = (s.n + 2 * a.tq - 1) / (2 * a.tq);
-  return s;
-}
-
-// How many of a sequence's keys its i-th new token sees.
-__device__ __forceinline__ int key_limit(unsigned block, int n, int len, int i) {
-  if (block == 0) return len;
-  const unsigned end = (static_cast<unsigned>(i) / block + 1) * block;
-  return len - n + static_cast<int>(min(static_cast<unsigned>(n), end));
-}
-
-// Key tiles of the m-th item of a sequence.
-__device__ __forceinline__ int item_tiles(const AhArgs& a, int n, int len, int m) {
-  const int lim = key_limit(a.block, n, len, min(n, (m + 1) * 2 * a.tq) - 1);
-  return static_cast<int>((static_cast<unsigned>(lim) + kAhKeys - 1) / kAhKeys);
-}
-
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Units of work (tiles, at least one to an item) of lane's sequence over all
-// heads. Whole warps call it: the items of a causal sequence are summed by all
-// lanes.
-__device__ __forceinline__ long long seq_units(const AhArgs& a, const Seq& s, int lane) {
-  long long w = 0;
-  if (s.m > 0 && (a.block == 0 || s.m == 1))
-    w = static_cast<long long>(s.m) * max(1, item_tiles(a, s.n, s.len, s.m - 1));
-  unsigned todo = __ballot_sync(0xffffffffu, s.m > 1 && a.block != 0);
-  while (todo) {
-    const int src = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
-    const int m = __shfl_sync(0xffffffffu, s.m, src);
-    long long sum = 0;
-    for (int i = lane; i < m; i += 32) sum += max(1, item_tiles(a, n, len, i));
-    sum = warp_sum(sum);
-    if (lane == src) w = sum;
-  }
-  return w * a.kv_heads;
-}
-
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += up;
-  }
-  return v;
-}
-
-// A CTA's run of units [at, end) and where it stands: sequence, item, head and
-// tile. All lanes of a warp hold the same values.
-struct Run {
-  long long at, end;
-  bool split;
-  int b;
-  Seq s;
-  int m, h, t, t_all;
-};
-
-// Finds the CTA's run; false if it is empty.
-__device__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
-  long long units = 0, items = 0;
-  int most = 0;
-  Seq s = {};
-  long long w = 0;
-  for (int b0 = 0; b0 < a.plan.seqs; b0 += 32) {
-    s = load_seq(a, b0 + lane);
-    w = seq_units(a, s, lane);
-    units += w;
-    items += static_cast<long long>(s.m) * a.kv_heads;
-    if (s.m > 0) most = max(most, item_tiles(a, s.n, s.len, s.m - 1));
-  }
-  units = warp_sum(units);
-  items = warp_sum(items);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (units == 0) return false;
-  const long long per = max(2ll, static_cast<long long>(__umul64hi(units + ctas - 1, a.inv_ctas)));
-  // what the longest run would be with whole items (all of them of the average's size), against cut ones
-  const float whole = fmaxf(static_cast<float>(most), ceilf(__fdividef(static_cast<float>(items), static_cast<float>(ctas))) *
-                                                          __fdividef(static_cast<float>(units), static_cast<float>(items)));
-  r.split = a.may_split && whole > static_cast<float>(per + kAhSplitCost);
-  r.at = cta * per;
-  r.end = min(units, r.at + per);
-  if (r.at >= units) return false;
-  // the sequence, item, head and tile of unit r.at
-  long long before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    if (a.plan.seqs > 32) {  // else the lanes still hold the only ones
-      s = load_seq(a, b0 + lane);
-      w = seq_units(a, s, lane);
-    }
-    const long long upto = before + warp_scan(w, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, r.at < upto);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.b = b0 + src;
-      r.s = {__shfl_sync(0xffffffffu, s.begin, src), __shfl_sync(0xffffffffu, s.n, src),
-             __shfl_sync(0xffffffffu, s.len, src), __shfl_sync(0xffffffffu, s.m, src)};
-      before = __shfl_sync(0xffffffffu, upto - w, src);
-      break;
-    }
-    before = __shfl_sync(0xffffffffu, upto, 31);
-  }
-  long long rest = r.at - before;
-  for (int m0 = 0;; m0 += 32) {
-    const int m = m0 + lane;
-    const int tiles = m < r.s.m ? max(1, item_tiles(a, r.s.n, r.s.len, m)) : 0;
-    const long long upto = warp_scan(static_cast<long long>(tiles) * a.kv_heads, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, rest < upto);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.m = m0 + src;
-      const int t_all = __shfl_sync(0xffffffffu, tiles, src);
-      rest -= __shfl_sync(0xffffffffu, upto, src) - static_cast<long long>(t_all) * a.kv_heads;
-      r.t_all = t_all;
-      // rest / t_all is below 2^16, so a quotient of floats is at most one off
-      r.h = static_cast<int>(__fdividef(static_cast<float>(rest), static_cast<float>(t_all)));
-      long long left = rest - static_cast<long long>(r.h) * t_all;
-      if (left < 0) --r.h, left += t_all;
-      if (left >= t_all) ++r.h, left -= t_all;
-      r.t = static_cast<int>(left);
-      break;
-    }
-    rest -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return true;
-}
-
-// On to the next item (its units start at r.at).
-__device__ __forceinline__ void next_item(const AhArgs& a, Run& r) {
-  r.t = 0;
-  if (++r.h < a.kv_heads) return;
-  r.h = 0;
-  if (++r.m >= r.s.m) {
-    r.m = 0;
-    do {
-      r.s = load_seq(a, ++r.b);
-    } while (r.s.m == 0 && r.b < a.plan.seqs);
-    if (r.s.m == 0) return;
-  }
-  r.t_all = max(1, item_tiles(a, r.s.n, r.s.len, r.m));
-}
-
-// 2^(c - top) for scales c <= top: a power of two, 0 where it would be subnormal
-// (or c is -inf), 1 where both are the same infinity.
-__device__ __forceinline__ float pow2_diff(float c, float top) {
-  if (c == top) return 1.f;
-  const float e = c - top;
-  return e > -127.f ? __int_as_float((127 + static_cast<int>(e)) << 23) : 0.f;
-}
-
-constexpr float kNegInf = -INFINITY;
-// c of a row all of whose visible scores are -inf: its sum is 0 and its result NaN
-constexpr float kNoScore = -3.0e38f;
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float m;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-  return m;
-}
-
-// mbar_wait for a whole warp, with a few tries before the first look at the
-// clock, whose latency would come on top of a wait that is nearly over.
-__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, const AhArgs& a) {
-  const uint32_t at = smem_u32(bar);
-  for (int i = 0; i < 16; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
-  }
-  return __all_sync(0xffffffffu, mbar_wait(at, parity, a.err, a.timeout_ns));
-}
+constexpr int kAhSplitCost = 4;  // measured: the partial sums' way through L2 and the joining kernel
 
 // A value that all lanes hold, said in a way that the compiler keeps it in
 // uniform registers.
@@ -434,26 +187,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       }
       AhItem it = {};
       it.last = !more;
-      if (more) {
-        it.first = r.m * 2 * a.tq;
-        it.tokens = min(2 * a.tq, r.s.n - it.first);
-        it.q_row = r.s.begin + it.first;
-        it.head = r.h;
-        it.len = r.s.len;
-        it.fresh = r.s.n;
-        it.seq = r.b;
-        it.t_all = item_tiles(a, r.s.n, r.s.len, r.m);
-        it.t_begin = r.t;
-        it.t_end = r.split ? static_cast<int>(min(static_cast<long long>(it.t_all), r.t + (r.end - r.at))) : it.t_all;
-        it.slot = -1;
-        if (it.t_begin > 0 || it.t_end < it.t_all) {
-          const int which = it.t_begin > 0 ? 0 : 1;
-          it.slot = 2 * blockIdx.x + which;
-          if (lane == 0) {
-            a.meta[it.slot] = make_int4(it.t_end < it.t_all ? 1 : 2, it.q_row, it.tokens, it.head);
-          }
-        }
-      }
+      if (more) it = make_item(a, r, lane);
       if (lane == 0) {
         items[slot] = it;
         mbar_arrive(smem_u32(&item_full[slot]));  // releases the descriptor
@@ -667,8 +401,10 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     int slot = 0;
     uint32_t it_ph = 0, cl_ph = 0, s_ph = 0, pv_ph = 0;
     bool ok = true;
-    while (ok) {
-      if (!warp_wait(&item_full[slot], it_ph, a)) break;
+    while (true) {
+      // A warp whose wait ran out goes through the rest of its item without waiting, as its mate counts on it at the
+      // barriers, and both leave together here.
+      if (!named_barrier_and(mates, 64, ok && warp_wait(&item_full[slot], it_ph, a))) break;
       const AhItem it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
@@ -687,8 +423,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       float c = kNegInf, l = 0.f;
       for (int i = 0; i < mine; ++i) {
         const int t = it.t_begin + (two ? i : 2 * i + s);
-        ok = warp_wait(&s_ready[s], s_ph, a);
-        if (!ok) break;
+        ok = ok && warp_wait(&s_ready[s], s_ph, a);
         s_ph ^= 1u;
         if (active) {
           tc_fence_after();
@@ -792,12 +527,10 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_ready[s]));
       }
-      if (!ok) break;
       const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
       if (mine > 0) {
-        ok = warp_wait(&pv_done[s], pv_ph, a);
+        ok = ok && warp_wait(&pv_done[s], pv_ph, a);
         pv_ph ^= 1u;
-        if (!ok) break;
       }
       if (!two && s == 1) {
         // hand (c, l) over to stream 0, which reads both sums
@@ -812,9 +545,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       if (n > 0) {
         if (other > 0) {
           // stream 1 arrives after its own last product, so that O of both is complete
-          ok = warp_wait(cl_ready, cl_ph, a);
+          ok = ok && warp_wait(cl_ready, cl_ph, a);
           cl_ph ^= 1u;
-          if (!ok) break;
           c1 = sCL[row].x;
           l1 = sCL[row].y + sCL[kAhHalf + row].y;
         }
@@ -1018,17 +750,25 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
   return CC_OK;
 }
 
+constexpr int kFewRows = 16;       // query rows of an item of the few-rows kernel
+constexpr int kFewTileShift = 6;   // its tiles: 64 keys
+constexpr int kFewSplitCost = 6;
+
+// Few rows to a sequence on average: the kernel whose CTAs do little but read the
+// cache. (The other one takes 128 rows of a key head at once.)
+bool few_rows(int64_t rows, int64_t seqs, int group) { return group <= kFewRows && rows * group <= kFewRows * seqs; }
+
 // Rows that a partial slot holds: those of a half where no item can have more.
 int slot_rows(int64_t tokens, int group) {
   const int tq = kAhHalf / group;
   return tokens <= tq ? static_cast<int>(tokens) * group : 2 * kAhHalf;
 }
 
-size_t part_bytes(int rows, int d) { return (size_t)2 * kAhMaxCtas * rows * d * 4; }
+size_t part_bytes(int ctas, int rows, int d) { return (size_t)2 * ctas * rows * d * 4; }
 
-size_t workspace_bytes(int64_t tokens, int group, int d) {
-  const int rows = slot_rows(tokens, group);
-  return part_bytes(rows, d) + (size_t)2 * kAhMaxCtas * (rows * 8 + 16);
+size_t workspace_bytes(bool few, int64_t tokens, int group, int d) {
+  const int ctas = few ? kAhMaxCtas : kAhMaxCtas / 2, rows = few ? kFewRows : slot_rows(tokens, group);
+  return part_bytes(ctas, rows, d) + (size_t)2 * ctas * (rows * 8 + 16);
 }
 
 struct CacheSide {
@@ -1055,36 +795,50 @@ cc_status launch_attn(const char* what, const CUtensorMap& tq, const CUtensorMap
   return launch_status(what);
 }
 
-// keys: no sequence has more.
+// keys: no sequence has more; max_tokens: nor new tokens; seqs: sequences that the rows belong to.
 cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, const CacheSide& k, const CacheSide& v,
                    int64_t keys, int64_t max_tokens, void* ws, size_t ws_bytes, void* stream) {
   a.group = a.heads / a.kv_heads;
-  a.tq = kAhHalf / a.group;
-  a.may_split = (keys + kAhKeys - 1) / kAhKeys > kAhSplitCost;
-  a.slot_rows = slot_rows(max_tokens, a.group);
+  const bool few = few_rows(a.rows, a.plan.seqs, a.group);
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.ld_q = ld_q;
+  a.tq = (few ? kFewRows : kAhHalf) / a.group;
+  a.item_tokens = few ? a.tq : 2 * a.tq;
+  a.tile_shift = few ? kFewTileShift : kAhTileShift;
+  a.split_cost = few ? kFewSplitCost : kAhSplitCost;
+  const int tile = 1 << a.tile_shift;
+  a.box = std::min(tile, a.box);
+  a.may_split = (keys + tile - 1) / tile > a.split_cost;
+  a.slot_rows = few ? kFewRows : slot_rows(max_tokens, a.group);
+  DeviceInfo di;
+  cc_status st;
   if (a.may_split) {
-    const size_t need = workspace_bytes(max_tokens, a.group, a.d);
+    const size_t need = workspace_bytes(few, max_tokens, a.group, a.d);
     if (!ws) return fail(CC_ERR_INVALID, "%s: null workspace", what);
     if (!aligned16(ws)) return fail(CC_ERR_INVALID, "%s: pointers must be 16-byte aligned", what);
     if (ws_bytes < need) return fail(CC_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", what, ws_bytes, need);
+    const int ctas = few ? kAhMaxCtas : kAhMaxCtas / 2;
     a.part = static_cast<float*>(ws);
-    a.part_cl = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_bytes(a.slot_rows, a.d));
-    a.meta = reinterpret_cast<int4*>(a.part_cl + (size_t)2 * kAhMaxCtas * a.slot_rows);
+    a.part_cl = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_bytes(ctas, a.slot_rows, a.d));
+    a.meta = reinterpret_cast<int4*>(a.part_cl + (size_t)2 * ctas * a.slot_rows);
   }
-  DeviceInfo di;
-  cc_status st = device_info(&di);
-  if (st != CC_OK) return st;
+  if ((st = device_info(&di)) != CC_OK) return st;
   a.err = di.err_word;
   a.timeout_ns = kWaitLimitNs;
-  CUtensorMap tq = {}, tk = {}, tv = {};
-  const uint64_t qdims[4] = {(uint64_t)a.d, (uint64_t)a.heads, (uint64_t)a.rows, 1};
-  const uint64_t qstrides[3] = {2ull * a.d, 2ull * ld_q, 2ull * ld_q};
-  if ((st = encode_tiled_4d(&tq, q, qdims, qstrides, 64, a.group, a.tq)) != CC_OK) return st;
+  CUtensorMap tk = {}, tv = {};
   if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
-  const int grid = std::min(kAhMaxCtas, di.sm_count);
+  const int grid = std::min(kAhMaxCtas, 2 * di.sm_count) / (few ? 1 : 2);
   a.inv_ctas = ~0ull / grid + 1;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  st = a.d > 64 ? launch_attn<2, 4>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 8>(what, tq, tk, tv, a, grid, cs);
+  if (few) {
+    st = launch_few_rows(what, tk, tv, a, grid, cs);
+  } else {
+    CUtensorMap tq = {};
+    const uint64_t qdims[4] = {(uint64_t)a.d, (uint64_t)a.heads, (uint64_t)a.rows, 1};
+    const uint64_t qstrides[3] = {2ull * a.d, 2ull * ld_q, 2ull * ld_q};
+    if ((st = encode_tiled_4d(&tq, q, qdims, qstrides, 64, a.group, a.tq)) != CC_OK) return st;
+    st = a.d > 64 ? launch_attn<2, 4>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 8>(what, tq, tk, tv, a, grid, cs);
+  }
   if (st != CC_OK || !a.may_split) return st;
   // the joining kernel's CTAs: a row to each where few items are cut into many pieces, else eight
   const int join_y = a.slot_rows <= 32 ? a.slot_rows : a.slot_rows / 8;
@@ -1105,12 +859,16 @@ using namespace cc;
 
 extern "C" size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d) {
   if (rows <= 0 || seqs <= 0 || !sizes_ok(heads, kv_heads, d)) return 0;
-  return workspace_bytes(rows, heads / kv_heads, d);
+  const int group = heads / kv_heads;
+  return workspace_bytes(few_rows(rows, seqs, group), rows, group, d);
 }
 
 extern "C" size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d) {
-  if (n <= 0 || lq <= 0 || lk <= kAhSplitCost * kAhKeys || !sizes_ok(heads, kv_heads, d)) return 0;
-  return workspace_bytes(lq, heads / kv_heads, d);
+  if (n <= 0 || lq <= 0 || !sizes_ok(heads, kv_heads, d)) return 0;
+  const int group = heads / kv_heads;
+  const bool few = few_rows((int64_t)n * lq, n, group);
+  if (lk <= (few ? kFewSplitCost << kFewTileShift : kAhSplitCost << kAhTileShift)) return 0;  // nothing is cut
+  return workspace_bytes(few, lq, group, d);
 }
 
 extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16* v_cache, cc_bf16* o,
@@ -1135,7 +893,7 @@ extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, con
   a.heads = heads;
   a.kv_heads = kv_heads;
   a.d = d;
-  a.box = std::min(kAhKeys, page_size & -page_size);
+  a.box = page_size & -page_size;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
   a.kx = scale * 1.4426950408889634f;
@@ -1166,7 +924,7 @@ extern "C" cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_
   a.heads = heads;
   a.kv_heads = kv_heads;
   a.d = d;
-  a.box = kAhKeys;
+  a.box = 1 << 30;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
   a.kx = scale * 1.4426950408889634f;

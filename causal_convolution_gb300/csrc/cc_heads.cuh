@@ -1,0 +1,301 @@
+// What the attention kernels with heads share: the items of work and how the
+// CTAs of a persistent grid divide them, waits, and the arithmetic of partial
+// sums.
+//
+// An item is up to item_tokens new tokens of one sequence, with the query heads
+// of one key head, and all the key tiles that any of them sees. The items' tiles,
+// laid end to end (sequence, tokens, head), are cut into equal runs, one for each
+// CTA. An item cut by a run's end leaves partial sums in the workspace, which a
+// second kernel joins; where whole items spread well enough nothing is cut. The
+// lengths are read on the device, so every CTA finds its run by itself.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "cc_host.h"
+#include "cc_paged.cuh"
+#include "cc_ptx.cuh"
+#include "cc_rows.cuh"
+
+namespace cc {
+
+constexpr int kAhMaxCtas = 304;   // two per SM of a GB300
+constexpr int kAhItems = 4;       // item descriptors in flight
+
+struct AhArgs {
+  KvPlan plan;      // q_offsets nullptr: sequence b owns rows b * lq .. (b + 1) * lq - 1; page_table nullptr: page b
+  int lq;
+  int rows, heads, kv_heads, group, d;
+  int tq;           // tokens of a half: as many as fit its rows
+  int item_tokens;  // of an item: one half or two
+  int tile_shift;   // keys of a tile: 2^tile_shift
+  int split_cost;   // tiles that cutting items costs a call, on its critical path
+  int box;          // slots per TMA box: pieces of this size never cross a page
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  long long ld_q, ld_o;
+  float kx;         // scale * log2(e)
+  unsigned block;   // causal block, 0: none
+  int may_split;
+  int slot_rows;    // rows a partial slot holds
+  float* part;      // [2 * ctas][slot_rows][d]
+  float2* part_cl;  // [2 * ctas][slot_rows] (c, l)
+  int4* meta;       // [2 * ctas]: 0 unused, 1 goes on, 2 ends its item; first row, tokens, head
+  unsigned int* err;
+  unsigned long long timeout_ns;
+  unsigned long long inv_ctas;  // ceil(2^64 / CTAs): exact quotients of anything below 2^56
+};
+
+// A piece of an item, as the roles of a CTA pass it on.
+struct __align__(16) AhItem {
+  int q_row;        // row of the item's first token
+  int tokens;       // of the item
+  int head;         // key head
+  int t_begin, t_end, t_all;  // this piece's key tiles, of all
+  int len;          // keys of the sequence
+  int first;        // the item's first token among the new ones
+  int fresh;        // new tokens of the sequence
+  int slot;         // partial slot, -1: the whole item
+  int seq;
+  int last;         // no item: the CTA is done
+};
+
+struct Seq {
+  int begin, n, len, m;  // first row, new tokens, keys, items along the rows
+};
+
+__device__ __forceinline__ Seq load_seq(const AhArgs& a, int b) {
+  Seq s = {0, 0, 0, 0};
+  if (b >= a.plan.seqs) return s;
+  if (a.plan.q_offsets) {
+    s.begin = a.plan.q_offsets[b];
+    const int end = a.plan.q_offsets[b + 1];
+    s.len = a.plan.kv_lens[b];
+    const long long n = static_cast<long long>(end) - s.begin;
+    if (n != 0 && (n < 0 || s.begin < 0 || end > a.rows || s.len < 0 || (a.block && s.len < n) ||
+                   s.len > static_cast<long long>(a.plan.max_pages) * a.plan.page_size)) {
+      atomicOr(a.err, DEVERR_BOUNDS);
+      return {0, 0, 0, 0};
+    }
+    s.n = static_cast<int>(n);
+  } else {
+    s.begin = b * a.lq;
+    s.n = a.lq;
+    s.len = a.plan.page_size;
+    if (a.plan.kv_lens) {
+      const int len = a.plan.kv_lens[b];
+      if (len < 0 || len > s.len) atomicOr(a.err, DEVERR_BOUNDS);
+      s.len = max(0, min(len, s.len));
+    }
+  }
+  s.m = (s.n + a.item_tokens - 1) / a.item_tokens;
+  return s;
+}
+
+// How many of a sequence's keys its i-th new token sees.
+__device__ __forceinline__ int key_limit(unsigned block, int n, int len, int i) {
+  if (block == 0) return len;
+  const unsigned end = (static_cast<unsigned>(i) / block + 1) * block;
+  return len - n + static_cast<int>(min(static_cast<unsigned>(n), end));
+}
+
+// Key tiles of the m-th item of a sequence.
+__device__ __forceinline__ int item_tiles(const AhArgs& a, int n, int len, int m) {
+  const int lim = key_limit(a.block, n, len, min(n, (m + 1) * a.item_tokens) - 1);
+  return static_cast<int>((static_cast<unsigned>(lim) + (1u << a.tile_shift) - 1) >> a.tile_shift);
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Units of work (tiles, at least one to an item) of lane's sequence over all
+// heads. Whole warps call it: the items of a causal sequence are summed by all
+// lanes.
+__device__ __forceinline__ long long seq_units(const AhArgs& a, const Seq& s, int lane) {
+  long long w = 0;
+  if (s.m > 0 && (a.block == 0 || s.m == 1))
+    w = static_cast<long long>(s.m) * max(1, item_tiles(a, s.n, s.len, s.m - 1));
+  unsigned todo = __ballot_sync(0xffffffffu, s.m > 1 && a.block != 0);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
+    const int m = __shfl_sync(0xffffffffu, s.m, src);
+    long long sum = 0;
+    for (int i = lane; i < m; i += 32) sum += max(1, item_tiles(a, n, len, i));
+    sum = warp_sum(sum);
+    if (lane == src) w = sum;
+  }
+  return w * a.kv_heads;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// A CTA's run of units [at, end) and where it stands: sequence, item, head and
+// tile. All lanes of a warp hold the same values.
+struct Run {
+  long long at, end;
+  bool split;
+  int b;
+  Seq s;
+  int m, h, t, t_all;
+};
+
+// Finds the CTA's run; false if it is empty.
+__device__ __forceinline__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
+  long long units = 0, items = 0;
+  int most = 0;
+  Seq s = {};
+  long long w = 0;
+  for (int b0 = 0; b0 < a.plan.seqs; b0 += 32) {
+    s = load_seq(a, b0 + lane);
+    w = seq_units(a, s, lane);
+    units += w;
+    items += static_cast<long long>(s.m) * a.kv_heads;
+    if (s.m > 0) most = max(most, item_tiles(a, s.n, s.len, s.m - 1));
+  }
+  units = warp_sum(units);
+  items = warp_sum(items);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (units == 0) return false;
+  const long long per = max(2ll, static_cast<long long>(__umul64hi(units + ctas - 1, a.inv_ctas)));
+  // what the longest run would be with whole items (all of them of the average's size), against cut ones
+  const float whole = fmaxf(static_cast<float>(most), ceilf(__fdividef(static_cast<float>(items), static_cast<float>(ctas))) *
+                                                          __fdividef(static_cast<float>(units), static_cast<float>(items)));
+  r.split = a.may_split && whole > static_cast<float>(per + a.split_cost);
+  r.at = cta * per;
+  r.end = min(units, r.at + per);
+  if (r.at >= units) return false;
+  // the sequence, item, head and tile of unit r.at
+  long long before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    if (a.plan.seqs > 32) {  // else the lanes still hold the only ones
+      s = load_seq(a, b0 + lane);
+      w = seq_units(a, s, lane);
+    }
+    const long long upto = before + warp_scan(w, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, r.at < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.b = b0 + src;
+      r.s = {__shfl_sync(0xffffffffu, s.begin, src), __shfl_sync(0xffffffffu, s.n, src),
+             __shfl_sync(0xffffffffu, s.len, src), __shfl_sync(0xffffffffu, s.m, src)};
+      before = __shfl_sync(0xffffffffu, upto - w, src);
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  long long rest = r.at - before;
+  for (int m0 = 0;; m0 += 32) {
+    const int m = m0 + lane;
+    const int tiles = m < r.s.m ? max(1, item_tiles(a, r.s.n, r.s.len, m)) : 0;
+    const long long upto = warp_scan(static_cast<long long>(tiles) * a.kv_heads, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, rest < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.m = m0 + src;
+      const int t_all = __shfl_sync(0xffffffffu, tiles, src);
+      rest -= __shfl_sync(0xffffffffu, upto, src) - static_cast<long long>(t_all) * a.kv_heads;
+      r.t_all = t_all;
+      // rest / t_all is below 2^16, so a quotient of floats is at most one off
+      r.h = static_cast<int>(__fdividef(static_cast<float>(rest), static_cast<float>(t_all)));
+      long long left = rest - static_cast<long long>(r.h) * t_all;
+      if (left < 0) --r.h, left += t_all;
+      if (left >= t_all) ++r.h, left -= t_all;
+      r.t = static_cast<int>(left);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return true;
+}
+
+// On to the next item (its units start at r.at).
+__device__ __forceinline__ void next_item(const AhArgs& a, Run& r) {
+  r.t = 0;
+  if (++r.h < a.kv_heads) return;
+  r.h = 0;
+  if (++r.m >= r.s.m) {
+    r.m = 0;
+    do {
+      r.s = load_seq(a, ++r.b);
+    } while (r.s.m == 0 && r.b < a.plan.seqs);
+    if (r.s.m == 0) return;
+  }
+  r.t_all = max(1, item_tiles(a, r.s.n, r.s.len, r.m));
+}
+
+// 2^(c - top) for scales c <= top: a power of two, 0 where it would be subnormal
+// (or c is -inf), 1 where both are the same infinity.
+__device__ __forceinline__ float pow2_diff(float c, float top) {
+  if (c == top) return 1.f;
+  const float e = c - top;
+  return e > -127.f ? __int_as_float((127 + static_cast<int>(e)) << 23) : 0.f;
+}
+
+constexpr float kNegInf = -INFINITY;
+// c of a row all of whose visible scores are -inf: its sum is 0 and its result NaN
+constexpr float kNoScore = -3.0e38f;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+
+// mbar_wait for a whole warp, with a few tries before the first look at the
+// clock, whose latency would come on top of a wait that is nearly over.
+__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, const AhArgs& a) {
+  const uint32_t at = smem_u32(bar);
+  for (int i = 0; i < 16; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+  }
+  return __all_sync(0xffffffffu, mbar_wait(at, parity, a.err, a.timeout_ns));
+}
+
+// The piece of an item at the head of a run; says in the workspace's directory
+// where its partial sums go on or end.
+__device__ __forceinline__ AhItem make_item(const AhArgs& a, const Run& r, int lane) {
+  AhItem it = {};
+  it.first = r.m * a.item_tokens;
+  it.tokens = min(a.item_tokens, r.s.n - it.first);
+  it.q_row = r.s.begin + it.first;
+  it.head = r.h;
+  it.len = r.s.len;
+  it.fresh = r.s.n;
+  it.seq = r.b;
+  it.t_all = item_tiles(a, r.s.n, r.s.len, r.m);
+  it.t_begin = r.t;
+  it.t_end = r.split ? static_cast<int>(min(static_cast<long long>(it.t_all), r.t + (r.end - r.at))) : it.t_all;
+  it.slot = -1;
+  if (it.t_begin > 0 || it.t_end < it.t_all) {
+    it.slot = 2 * blockIdx.x + (it.t_begin > 0 ? 0 : 1);
+    if (lane == 0) a.meta[it.slot] = make_int4(it.t_end < it.t_all ? 1 : 2, it.q_row, it.tokens, it.head);
+  }
+  return it;
+}
+
+// Launches the kernel for few rows to a sequence (attn_few_rows.cu).
+cc_status launch_few_rows(const char* what, const CUtensorMap& tk, const CUtensorMap& tv, AhArgs& a, int grid,
+                          cudaStream_t stream);
+
+}  // namespace cc
