@@ -590,26 +590,36 @@ ROT_STYLES = {"pairs": 0, "halves": 1}  # CC_ROT_*
 
 def _on(t, dtype, name: str, dev: int) -> None:
     """`t` is a tensor of this type on the current device."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype:
-        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
 def _head_rows(t, name: str, dev: int):
-    """(pointer, leading shape, rows, heads, D, ld) of a bf16 tensor [..., heads, D] whose rows hold their heads side
-    by side and lie at one stride `ld`."""
-    _on(t, torch.bfloat16, name, dev)
-    shape = t.shape
+    """(pointer, shape, rows, ld) of a bf16 tensor [..., heads, D] whose rows hold their heads side by side and lie at
+    one stride `ld`. (What usually comes, rows at a stride, is told first.)"""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev:
+        shape, strides = t.shape, t.stride()
+        if len(shape) == 3:
+            rows, heads, d = shape
+            if rows > 1 and strides[2] == 1 and strides[1] == d and rows | heads | d <= INT_MAX:
+                return t.data_ptr(), shape, rows, strides[0]
+        elif len(shape) == 4:
+            n, rows, heads, d = shape
+            if rows > 1 and strides[3] == 1 and strides[2] == d and strides[0] == rows * strides[1] \
+                    and n * rows | heads | d <= INT_MAX:
+                return t.data_ptr(), shape, n * rows, strides[1]
+    else:
+        _on(t, torch.bfloat16, name, dev)
+        shape, strides = t.shape, t.stride()
     if len(shape) < 3:
         raise ValueError(f"{name}: expected [..., heads, D]")
     heads, d = shape[-2:]
-    strides = t.stride()
     if (strides[-1] != 1 and d > 1) or (strides[-2] != d and heads > 1):
         raise ValueError(f"{name}: a row's heads and channels must be contiguous")
     rows, ld = 1, None
@@ -622,19 +632,23 @@ def _head_rows(t, name: str, dev: int):
             rows *= size
     if rows > INT_MAX or heads > INT_MAX or d > INT_MAX:
         _too_large(name, rows, heads, d)
-    return t.data_ptr(), shape[:-2], rows, heads, d, heads * d if ld is None else ld
+    return t.data_ptr(), shape, rows, heads * d if ld is None else ld
 
 
-def _rotation(rot, pos, rows: int, d: int, name: str, dev: int):
+def _rotation(rot, pos, rows: int, name: str, dev: int):
     """(pointer of rot, positions, rd, pointer of pos)"""
     prot, positions, rd = None, 0, 0
     if rot is not None:
-        if rot.dim() != 3 or rot.shape[2] != 2:
-            raise ValueError(f"{name}: rot must be [positions, rd/2, 2], got {tuple(rot.shape)}")
-        prot, positions, rd = _arg(rot, torch.float32, "rot", dev), rot.shape[0], 2 * rot.shape[1]
+        prot = _arg(rot, torch.float32, "rot", dev)
+        shape = rot.shape
+        if len(shape) != 3 or shape[2] != 2:
+            raise ValueError(f"{name}: rot must be [positions, rd/2, 2], got {tuple(shape)}")
+        positions, rd = shape[0], 2 * shape[1]
         if positions > INT_MAX or rd > INT_MAX:
             _too_large(name, positions, rd)
-    if pos is not None and pos.numel() != rows:
+    if pos is None:
+        return prot, positions, rd, None
+    if pos.numel() != rows:
         raise ValueError(f"{name}: pos must hold a position for each of {rows} rows")
     return prot, positions, rd, _arg(pos, torch.int32, "pos", dev)
 
@@ -646,7 +660,9 @@ def _style(style: str) -> int:
 
 
 def _gamma(gamma, d: int, name: str, dev: int):
-    if gamma is not None and gamma.numel() != d:
+    if gamma is None:
+        return None
+    if gamma.numel() != d:
         raise ValueError(f"{name} must hold D elements")
     return _arg(gamma, torch.bfloat16, name, dev)
 
@@ -662,16 +678,18 @@ def cc_qk_norm_rope(q, k, gamma_q, gamma_k, rot, pos, q_out, k_out, eps: float =
     pq = pk = pqo = pko = None
     heads = kv_heads = ld_q = ld_k = ld_qo = ld_ko = 0
     if k is not None:
-        pk, lead, rows, kv_heads, d, ld_k = _head_rows(k, "k", dev)
-        pko, _, _, _, _, ld_ko = _head_rows(k_out, "k_out", dev)
-        if k_out.shape != k.shape:
+        pk, shape, rows, ld_k = _head_rows(k, "k", dev)
+        pko, out, _, ld_ko = _head_rows(k_out, "k_out", dev)
+        if out != shape:
             raise ValueError("qk_norm_rope: k_out must have k's shape")
+        kv_heads, d = shape[-2:]
     if q is not None:
-        pq, lead_q, rows, heads, d, ld_q = _head_rows(q, "q", dev)
-        pqo, _, _, _, _, ld_qo = _head_rows(q_out, "q_out", dev)
-        if q_out.shape != q.shape or (k is not None and (lead_q != lead or k.shape[-1] != d)):
+        pq, shape_q, rows, ld_q = _head_rows(q, "q", dev)
+        pqo, out, _, ld_qo = _head_rows(q_out, "q_out", dev)
+        heads, d = shape_q[-2:]
+        if out != shape_q or (k is not None and (shape_q[:-2] != shape[:-2] or shape[-1] != d)):
             raise ValueError("qk_norm_rope: q, k and q_out must share rows and D")
-    prot, positions, rd, ppos = _rotation(rot, pos, rows, d, "qk_norm_rope", dev)
+    prot, positions, rd, ppos = _rotation(rot, pos, rows, "qk_norm_rope", dev)
     _check(_lib.load().cc_qk_norm_rope(
         pq, pk, _gamma(gamma_q, d, "gamma_q", dev), _gamma(gamma_k, d, "gamma_k", dev), prot, ppos, pqo, pko, rows,
         heads, kv_heads, d, rd, positions, ld_q, ld_k, ld_qo, ld_ko, eps, _style(style), _raw_stream(stream, dev)))
@@ -680,22 +698,24 @@ def cc_qk_norm_rope(q, k, gamma_q, gamma_k, rot, pos, q_out, k_out, eps: float =
 def _paged(k_cache, v_cache, q_offsets, kv_lens, page_table, name: str, dev: int):
     """Pointers, sizes and strides of a cache [pages, page_size, kv_heads, D] and of a step's plan."""
     bf16, i32 = torch.bfloat16, torch.int32
-    _on(k_cache, bf16, "k_cache", dev)
-    _on(v_cache, bf16, "v_cache", dev)
+    for cache in (k_cache, v_cache):
+        if not isinstance(cache, torch.Tensor) or cache.dtype is not bf16 or cache.get_device() != dev:
+            _on(cache, bf16, "k_cache" if cache is k_cache else "v_cache", dev)
     shape, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"{name}: k_cache and v_cache must share [pages, page_size, kv_heads, D]")
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError(f"{name}: a cached head's channels must be contiguous")
-    if page_table.dim() != 2 or kv_lens.numel() != page_table.shape[0] or q_offsets.numel() != kv_lens.numel() + 1:
+    plan = (_arg(q_offsets, i32, "q_offsets", dev), _arg(kv_lens, i32, "kv_lens", dev),
+            _arg(page_table, i32, "page_table", dev))
+    table = page_table.shape
+    if len(table) != 2 or kv_lens.numel() != table[0] or q_offsets.numel() != table[0] + 1:
         raise ValueError(f"{name}: q_offsets must be [seqs + 1], kv_lens [seqs] and page_table [seqs, max_pages]")
-    seqs, max_pages = page_table.shape
-    if max(*shape, seqs, max_pages) > INT_MAX:
-        _too_large(name, *shape, seqs, max_pages)
-    return (k_cache.data_ptr(), v_cache.data_ptr(),
-            (_arg(q_offsets, i32, "q_offsets", dev), _arg(kv_lens, i32, "kv_lens", dev),
-             _arg(page_table, i32, "page_table", dev)),
-            (seqs, max_pages, shape[0], shape[1]), shape[2], shape[3], ks[:3] + vs[:3])
+    pages, page_size, kv_heads, d = shape
+    seqs, max_pages = table
+    if pages | page_size | kv_heads | d | seqs | max_pages > INT_MAX:
+        _too_large(name, *shape, *table)
+    return k_cache.data_ptr(), v_cache.data_ptr(), plan, (seqs, max_pages, pages, page_size), kv_heads, d, ks[:3] + vs[:3]
 
 
 def cc_qk_norm_rope_append(q, k, v, gamma_q, gamma_k, rot, pos, q_out, k_cache, v_cache, q_offsets, kv_lens,
@@ -705,20 +725,20 @@ def cc_qk_norm_rope_append(q, k, v, gamma_q, gamma_k, rot, pos, q_out, k_cache, 
     q_offsets[b] .. q_offsets[b + 1] - 1, the newest of its kv_lens[b] tokens; page_table [seqs, max_pages]. All three
     are int32 on the GPU. pos None: a row's position is its token's in its sequence."""
     dev = torch.cuda.current_device()
-    pq, lead, rows, heads, d, ld_q = _head_rows(q, "q", dev)
-    pqo, _, _, _, _, ld_qo = _head_rows(q_out, "q_out", dev)
-    pk, lead_k, _, kv_heads, _, ld_k = _head_rows(k, "k", dev)
-    pv, _, _, _, _, ld_v = _head_rows(v, "v", dev)
-    pkc, pvc, plan, sizes, cache_heads, cache_d, strides = _paged(k_cache, v_cache, q_offsets, kv_lens, page_table,
-                                                                  "qk_norm_rope_append", dev)
-    if (q_out.shape != q.shape or lead_k != lead or k.shape != v.shape or k.shape[-1] != d or cache_d != d
-            or cache_heads != kv_heads):
+    pq, shape, rows, ld_q = _head_rows(q, "q", dev)
+    pqo, out, _, ld_qo = _head_rows(q_out, "q_out", dev)
+    pk, shape_k, _, ld_k = _head_rows(k, "k", dev)
+    pv, shape_v, _, ld_v = _head_rows(v, "v", dev)
+    pkc, pvc, plan, sizes, kv_heads, d, strides = _paged(k_cache, v_cache, q_offsets, kv_lens, page_table,
+                                                         "qk_norm_rope_append", dev)
+    if (out != shape or shape_k[:-2] != shape[:-2] or shape_k != shape_v or shape[-1] != d or shape_k[-1] != d
+            or shape_k[-2] != kv_heads):
         raise ValueError("qk_norm_rope_append: q, k, v and the cache must share rows, heads and D")
-    prot, positions, rd, ppos = _rotation(rot, pos, rows, d, "qk_norm_rope_append", dev)
+    prot, positions, rd, ppos = _rotation(rot, pos, rows, "qk_norm_rope_append", dev)
     _check(_lib.load().cc_qk_norm_rope_append(
         pq, pk, pv, _gamma(gamma_q, d, "gamma_q", dev), _gamma(gamma_k, d, "gamma_k", dev), prot, ppos, pqo, pkc, pvc,
-        *plan, rows, *sizes, heads, kv_heads, d, rd, positions, ld_q, ld_k, ld_v, ld_qo, *strides, eps, _style(style),
-        _raw_stream(stream, dev)))
+        *plan, rows, *sizes, shape[-2], kv_heads, d, rd, positions, ld_q, ld_k, ld_v, ld_qo, *strides, eps,
+        _style(style), _raw_stream(stream, dev)))
 
 
 def cc_attn_paged_workspace_bytes(rows: int, seqs: int, heads: int, kv_heads: int, d: int) -> int:
@@ -732,16 +752,15 @@ def cc_attn_paged(q, k_cache, v_cache, o, q_offsets, kv_lens, page_table, ws, sc
     """Attention of a plan's rows q [rows, heads, D] over the cache (as for cc_qk_norm_rope_append). A token sees those
     up to the end of its own block of `causal_block` new tokens (1: up to itself; 0: all of its sequence)."""
     dev = torch.cuda.current_device()
-    pq, _, rows, heads, d, ld_q = _head_rows(q, "q", dev)
-    po, _, _, _, _, ld_o = _head_rows(o, "o", dev)
-    pk, pv, plan, sizes, kv_heads, cache_d, strides = _paged(k_cache, v_cache, q_offsets, kv_lens, page_table,
-                                                             "attn_paged", dev)
-    if o.shape != q.shape or cache_d != d:
+    pq, shape, rows, ld_q = _head_rows(q, "q", dev)
+    po, out, _, ld_o = _head_rows(o, "o", dev)
+    pk, pv, plan, sizes, kv_heads, d, strides = _paged(k_cache, v_cache, q_offsets, kv_lens, page_table, "attn_paged", dev)
+    if out != shape or shape[-1] != d:
         raise ValueError("attn_paged: q, o and the cache must share rows and D")
     if abs(causal_block) > INT_MAX:
         _too_large("attn_paged", causal_block)
     _check(_lib.load().cc_attn_paged(
-        pq, pk, pv, po, *plan, rows, *sizes, heads, kv_heads, d, ld_q, ld_o, *strides,
+        pq, pk, pv, po, *plan, rows, *sizes, shape[-2], kv_heads, d, ld_q, ld_o, *strides,
         d ** -0.5 if scale is None else scale, causal_block, _arg(ws, torch.uint8, "ws", dev),
         0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
 
@@ -756,18 +775,19 @@ def cc_attn_cross(q, k, v, o, kv_lens, ws, scale: float | None = None, stream=No
     """Attention of q [N, Lq, heads, D] to an encoder's k, v [N, Lk, kv_heads, D] (rows may be strided), of which
     kv_lens [N] (int32 on the GPU; None: all) count."""
     dev = torch.cuda.current_device()
-    pq, lead, _, heads, d, ld_q = _head_rows(q, "q", dev)
-    pk, lead_k, _, kv_heads, _, ld_k = _head_rows(k, "k", dev)
-    pv, _, _, _, _, ld_v = _head_rows(v, "v", dev)
-    po, _, _, _, _, ld_o = _head_rows(o, "o", dev)
-    if len(lead) != 2 or len(lead_k) != 2 or lead[0] != lead_k[0] or o.shape != q.shape or v.shape != k.shape \
-            or k.shape[-1] != d:
+    pq, shape, _, ld_q = _head_rows(q, "q", dev)
+    pk, shape_k, _, ld_k = _head_rows(k, "k", dev)
+    pv, shape_v, _, ld_v = _head_rows(v, "v", dev)
+    po, out, _, ld_o = _head_rows(o, "o", dev)
+    if len(shape) != 4 or len(shape_k) != 4 or shape[0] != shape_k[0] or out != shape or shape_v != shape_k \
+            or shape_k[3] != shape[3]:
         raise ValueError("attn_cross: q and o must be [N,Lq,heads,D], k and v [N,Lk,kv_heads,D]")
-    if kv_lens is not None and kv_lens.numel() != lead[0]:
+    n, lq, heads, d = shape
+    if kv_lens is not None and kv_lens.numel() != n:
         raise ValueError("attn_cross: kv_lens must hold N values")
     _check(_lib.load().cc_attn_cross(
-        pq, pk, pv, po, _arg(kv_lens, torch.int32, "kv_lens", dev), *lead, lead_k[1], heads, kv_heads, d, ld_q, ld_k,
-        ld_v, ld_o, d ** -0.5 if scale is None else scale, _arg(ws, torch.uint8, "ws", dev),
+        pq, pk, pv, po, _arg(kv_lens, torch.int32, "kv_lens", dev), n, lq, shape_k[1], heads, shape_k[2], d, ld_q,
+        ld_k, ld_v, ld_o, d ** -0.5 if scale is None else scale, _arg(ws, torch.uint8, "ws", dev),
         0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
 
 

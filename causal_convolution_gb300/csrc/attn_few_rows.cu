@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kFrThreads, 2)
     if (a.may_split && lane < 2) a.meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
     __syncwarp();
     if (any && !r.split && r.t > 0) {  // whole items: from the first one that starts in the run
-      r.at += r.t_all - r.t;
+      r.at += max(1, r.tiles) - r.t;
       next_item(a, r);
     }
     while (ok) {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kFrThreads, 2)
           ph ^= 1u;
         }
       }
-      r.at += max(1, it.t_end - it.t_begin);
+      r.at += static_cast<unsigned>(max(1, it.t_end - it.t_begin));
       next_item(a, r);
     }
     if (!ok) {  // copies in flight land before the CTA goes
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       long long at_q[2], at_o[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = (lane >> 2) + 8 * i, tok = r / a.group, h = it.head * a.group + r - tok * a.group;
-        limit[i] = r < rows ? key_limit(a.block, it.fresh, it.len, it.first + tok) : 0;
+        const int r = (lane >> 2) + 8 * i, tok = static_cast<int>(quotient(r, a.inv_group)), h = it.head * a.group + r - tok * a.group;
+        limit[i] = r < rows ? key_limit(a, it.fresh, it.len, it.first + tok) : 0;
         at_q[i] = (it.q_row + tok) * a.ld_q + static_cast<long long>(h) * a.d;
         at_o[i] = (it.q_row + tok) * a.ld_o + static_cast<long long>(h) * a.d;
       }
@@ -305,52 +305,49 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       const float f0 = pow2_diff(c[0], top[0]), f1 = pow2_diff(c[1], top[1]);
 #pragma unroll
       for (int j = 0; j < NB * 8; ++j) acc[j][0] *= f0, acc[j][1] *= f0, acc[j][2] *= f1, acc[j][3] *= f1;
-      // handed down from warp to warp; the last one has them all
-      for (int from = 3; from > 0; --from) {
-        if (w == from) {
+      // a quarter of the channels at a time; each warp adds up and writes one
+      constexpr int Q = NB * 2;
+      float4 res[Q];
 #pragma unroll
-          for (int j = 0; j < NB * 8; ++j) {
-            if (j < 2 * steps) sSum[j * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int j = 0; j < Q; ++j)
+          sSum[(w * Q + j) * 32 + lane] =
+              make_float4(acc[q * Q + j][0], acc[q * Q + j][1], acc[q * Q + j][2], acc[q * Q + j][3]);
+        named_barrier_sync(1, 128);
+        if (w == q) {
+#pragma unroll
+          for (int j = 0; j < Q; ++j) {
+            float4 v = sSum[j * 32 + lane];
+#pragma unroll
+            for (int from = 1; from < 4; ++from) {
+              const float4 x = sSum[(from * Q + j) * 32 + lane];
+              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+            res[j] = v;
           }
         }
         named_barrier_sync(1, 128);
-        if (w == from - 1) {
-#pragma unroll
-          for (int j = 0; j < NB * 8; ++j) {
-            if (j < 2 * steps) {
-              const float4 v = sSum[j * 32 + lane];
-              acc[j][0] += v.x, acc[j][1] += v.y, acc[j][2] += v.z, acc[j][3] += v.w;
-            }
-          }
-        }
       }
-      if (w == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!in[i]) continue;
-          const int r = (lane >> 2) + 8 * i;
-          if (it.slot < 0) {
-            const bool sees = n > 0 && limit[i] > 0;
-            const float inv = 1.f / sum[i];
+      for (int i = 0; i < 2; ++i) {
+        if (!in[i]) continue;
+        const bool sees = n > 0 && limit[i] > 0;
+        const float inv = 1.f / sum[i];
+        const long long at = static_cast<long long>(it.slot) * a.slot_rows + (lane >> 2) + 8 * i;
 #pragma unroll
-            for (int j = 0; j < NB * 8; ++j) {
-              if (j < 2 * steps)
-                *reinterpret_cast<uint32_t*>(a.o + at_o[i] + j * 8 + (lane & 3) * 2) =
-                    sees ? pack_bf16(acc[j][2 * i] * inv, acc[j][2 * i + 1] * inv) : 0u;
-            }
-          } else {
-            const long long at = static_cast<long long>(it.slot) * a.slot_rows + r;
-#pragma unroll
-            for (int j = 0; j < NB * 8; ++j) {
-              if (j < 2 * steps)
-                *reinterpret_cast<float2*>(a.part + at * a.d + j * 8 + (lane & 3) * 2) =
-                    make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
-            }
-            if ((lane & 3) == 0) {
-              const bool any = limit[i] > it.t_begin * kFrKeys;
-              a.part_cl[at] = make_float2(any && top[i] == kNegInf ? kNoScore : top[i], sum[i]);
-            }
-          }
+        for (int j = 0; j < Q; ++j) {
+          const int col = (w * Q + j) * 8 + (lane & 3) * 2;
+          const float x0 = i ? res[j].z : res[j].x, x1 = i ? res[j].w : res[j].y;
+          if (col >= a.d) break;
+          if (it.slot < 0)
+            *reinterpret_cast<uint32_t*>(a.o + at_o[i] + col) = sees ? pack_bf16(x0 * inv, x1 * inv) : 0u;
+          else
+            *reinterpret_cast<float2*>(a.part + at * a.d + col) = make_float2(x0, x1);
+        }
+        if (it.slot >= 0 && w == 0 && (lane & 3) == 0) {
+          const bool any = limit[i] > it.t_begin * kFrKeys;
+          a.part_cl[at] = make_float2(any && top[i] == kNegInf ? kNoScore : top[i], sum[i]);
         }
       }
     }
@@ -363,7 +360,8 @@ cc_status launch(const char* what, const CUtensorMap& tk, const CUtensorMap& tv,
   auto kern = attn_few_rows_kernel<NB, STAGES>;
   constexpr int kSmem = FrSmem<NB, STAGES>::kBytes;
   static_assert(kSmem <= 115712, "two CTAs to an SM");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, a.device, ready);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
   e = launch_pdl(kern, dim3(grid), dim3(kFrThreads), kSmem, stream, tk, tv, a);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       return true;
     };
     if (any && !r.split && r.t > 0) {  // whole items: from the first one that starts in the run
-      r.at += r.t_all - r.t;
+      r.at += max(1, r.tiles) - r.t;
       next_item(a, r);
     }
     while (ok) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           if (ok && t + ahead < n) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t + ahead);
         }
       }
-      r.at += max(1, n);
+      r.at += static_cast<unsigned>(max(1, n));
       next_item(a, r);
     }
     if (!ok) {  // copies in flight land before the CTA goes
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     const uint32_t mates = 1 + s * 4 + (warp & 3);  // barrier of the two warps that share these rows
     float* my_x = sX + (2 * s + hf) * kAhHalf + row;
     const float* mate_x = sX + (2 * s + 1 - hf) * kAhHalf + row;
-    const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+    const int row_tok = static_cast<int>(quotient(row, a.inv_group)), row_head = row - row_tok * a.group;
     const f32x2 kx2 = pair(a.kx, a.kx);
     int slot = 0;
     uint32_t it_ph = 0, cl_ph = 0, s_ph = 0, pv_ph = 0;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const bool two = it.tokens > a.tq;
       const int tok = (two ? s * a.tq : 0) + row_tok;  // of the item
       const bool row_ok = row < a.tq * a.group && tok < it.tokens;
-      const int limit = row_ok ? key_limit(a.block, it.fresh, it.len, it.first + tok) : 0x7fffffff;
+      const int limit = row_ok ? key_limit(a, it.fresh, it.len, it.first + tok) : 0x7fffffff;
       const bool active = __any_sync(0xffffffffu, row_ok);
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
       float c = kNegInf, l = 0.f;
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
   for (int i0 = shared_rows ? blockIdx.y : blockIdx.y * 8; i0 < rows; i0 += step) {
     const int i = shared_rows ? i0 : i0 + warp;
     if (!shared_rows && i >= rows) break;
-    const int tok = i / a.group, g = i - tok * a.group;
+    const int tok = static_cast<int>(quotient(i, a.inv_group)), g = i - tok * a.group;
     const int r = two && tok >= a.tq ? kAhHalf + (tok - a.tq) * a.group + g : i;
     auto slot_of = [&](int p) { return static_cast<long long>(p == 0 ? 2 * first + 1 : 2 * (first + p)) * a.slot_rows + r; };
     float top = kNegInf;
@@ -788,7 +788,8 @@ cc_status launch_attn(const char* what, const CUtensorMap& tq, const CUtensorMap
   auto kern = attn_heads_kernel<NB, STAGES>;
   constexpr int kSmem = AhSmem<NB, STAGES>::kBytes;
   static_assert(kSmem <= 232448, "shared memory budget");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, a.device, ready);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: shared-memory attribute: %s", what, cudaGetErrorString(e));
   e = launch_pdl(kern, dim3(grid), dim3(kAhThreads), kSmem, stream, tq, tk, tv, a);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
@@ -808,7 +809,10 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   a.split_cost = few ? kFewSplitCost : kAhSplitCost;
   const int tile = 1 << a.tile_shift;
   a.box = std::min(tile, a.box);
-  a.may_split = (keys + tile - 1) / tile > a.split_cost;
+  const int64_t tiles = std::max<int64_t>(1, (keys + tile - 1) / tile);
+  if (((a.rows / a.item_tokens + (int64_t)a.plan.seqs) * a.kv_heads) * (double)tiles >= 0x1p31)
+    return fail(CC_ERR_UNSUPPORTED, "%s: rows, heads and keys make 2^31 tiles or more", what);
+  a.may_split = tiles > a.split_cost;
   a.slot_rows = few ? kFewRows : slot_rows(max_tokens, a.group);
   DeviceInfo di;
   cc_status st;
@@ -824,11 +828,15 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   }
   if ((st = device_info(&di)) != CC_OK) return st;
   a.err = di.err_word;
+  a.device = di.device;
   a.timeout_ns = kWaitLimitNs;
   CUtensorMap tk = {}, tv = {};
   if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
   const int grid = std::min(kAhMaxCtas, 2 * di.sm_count) / (few ? 1 : 2);
-  a.inv_ctas = ~0ull / grid + 1;
+  a.inv_ctas = inverse(grid);
+  a.inv_tokens = inverse(a.item_tokens);
+  a.inv_block = a.block ? inverse(a.block) : 0;
+  a.inv_group = inverse(a.group);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (few) {
     st = launch_few_rows(what, tk, tv, a, grid, cs);

@@ -46,9 +46,17 @@ struct AhArgs {
   float2* part_cl;  // [2 * ctas][slot_rows] (c, l)
   int4* meta;       // [2 * ctas]: 0 unused, 1 goes on, 2 ends its item; first row, tokens, head
   unsigned int* err;
+  int device;
   unsigned long long timeout_ns;
-  unsigned long long inv_ctas;  // ceil(2^64 / CTAs): exact quotients of anything below 2^56
+  // ceil(2^64 / divisor) for quotient(): CTAs, tokens of an item, the causal block, heads of a group
+  unsigned long long inv_ctas, inv_tokens, inv_block, inv_group;
 };
+
+// x / divisor: exact, as x and the divisors are below 2^31. 0 stands for a divisor of 1.
+__host__ __device__ constexpr unsigned long long inverse(unsigned divisor) { return divisor == 1 ? 0 : ~0ull / divisor + 1; }
+__device__ __forceinline__ unsigned quotient(unsigned x, unsigned long long inv) {
+  return inv ? static_cast<unsigned>(__umul64hi(x, inv)) : x;
+}
 
 // A piece of an item, as the roles of a CTA pass it on.
 struct __align__(16) AhItem {
@@ -92,136 +100,140 @@ __device__ __forceinline__ Seq load_seq(const AhArgs& a, int b) {
       s.len = max(0, min(len, s.len));
     }
   }
-  s.m = (s.n + a.item_tokens - 1) / a.item_tokens;
+  s.m = static_cast<int>(quotient(s.n + a.item_tokens - 1, a.inv_tokens));
   return s;
 }
 
 // How many of a sequence's keys its i-th new token sees.
-__device__ __forceinline__ int key_limit(unsigned block, int n, int len, int i) {
-  if (block == 0) return len;
-  const unsigned end = (static_cast<unsigned>(i) / block + 1) * block;
+__device__ __forceinline__ int key_limit(const AhArgs& a, int n, int len, int i) {
+  if (a.block == 0) return len;
+  const unsigned end = (quotient(i, a.inv_block) + 1) * a.block;
   return len - n + static_cast<int>(min(static_cast<unsigned>(n), end));
 }
 
 // Key tiles of the m-th item of a sequence.
-__device__ __forceinline__ int item_tiles(const AhArgs& a, int n, int len, int m) {
-  const int lim = key_limit(a.block, n, len, min(n, (m + 1) * a.item_tokens) - 1);
+__device__ __forceinline__ int item_tiles(const AhArgs& a, const Seq& s, int m) {
+  const int lim = key_limit(a, s.n, s.len, min(s.n, (m + 1) * a.item_tokens) - 1);
   return static_cast<int>((static_cast<unsigned>(lim) + (1u << a.tile_shift) - 1) >> a.tile_shift);
 }
 
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Units of work (tiles, at least one to an item) of lane's sequence over all
-// heads. Whole warps call it: the items of a causal sequence are summed by all
-// lanes.
-__device__ __forceinline__ long long seq_units(const AhArgs& a, const Seq& s, int lane) {
-  long long w = 0;
-  if (s.m > 0 && (a.block == 0 || s.m == 1))
-    w = static_cast<long long>(s.m) * max(1, item_tiles(a, s.n, s.len, s.m - 1));
-  unsigned todo = __ballot_sync(0xffffffffu, s.m > 1 && a.block != 0);
-  while (todo) {
-    const int src = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
-    const int m = __shfl_sync(0xffffffffu, s.m, src);
-    long long sum = 0;
-    for (int i = lane; i < m; i += 32) sum += max(1, item_tiles(a, n, len, i));
-    sum = warp_sum(sum);
-    if (lane == src) w = sum;
-  }
-  return w * a.kv_heads;
-}
-
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
+// Inclusive sums over the lanes.
+__device__ __forceinline__ unsigned warp_scan(unsigned v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, v, o);
+    const unsigned up = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += up;
   }
   return v;
 }
 
+__device__ __forceinline__ Seq seq_of_lane(const Seq& s, int src) {
+  return {__shfl_sync(0xffffffffu, s.begin, src), __shfl_sync(0xffffffffu, s.n, src),
+          __shfl_sync(0xffffffffu, s.len, src), __shfl_sync(0xffffffffu, s.m, src)};
+}
+
+// Units of work of lane's sequence over all heads: its tiles, at least one to an
+// item. most: the tiles of its largest item, the last one. Whole warps call it: the
+// items of a causal sequence are summed by all lanes.
+__device__ __forceinline__ unsigned seq_units(const AhArgs& a, const Seq& s, int lane, int& most) {
+  most = s.m > 0 ? max(1, item_tiles(a, s, s.m - 1)) : 0;
+  unsigned w = static_cast<unsigned>(s.m) * most;
+  unsigned todo = __ballot_sync(0xffffffffu, s.m > 1 && a.block != 0);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const Seq one = seq_of_lane(s, src);
+    unsigned sum = 0;
+    for (int i = lane; i < one.m; i += 32) sum += max(1, item_tiles(a, one, i));
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == src) w = sum;
+  }
+  return w * a.kv_heads;
+}
+
 // A CTA's run of units [at, end) and where it stands: sequence, item, head and
 // tile. All lanes of a warp hold the same values.
 struct Run {
-  long long at, end;
+  unsigned at, end;
   bool split;
   int b;
   Seq s;
-  int m, h, t, t_all;
+  int m, h, t, tiles;  // tiles: of the item
 };
 
-// Finds the CTA's run; false if it is empty.
+// Finds the CTA's run; false if it is empty. (The host has made sure that units
+// stay below 2^31. This runs once, on cold instructions, before anything else can
+// start: what counts is that it is short.)
 __device__ __forceinline__ bool find_run(const AhArgs& a, int cta, int ctas, int lane, Run& r) {
-  long long units = 0, items = 0;
-  int most = 0;
+  unsigned w = 0, units = 0, items = 0;
+  int most = 0, top = 0;
   Seq s = {};
-  long long w = 0;
-  for (int b0 = 0; b0 < a.plan.seqs; b0 += 32) {
-    s = load_seq(a, b0 + lane);
-    w = seq_units(a, s, lane);
-    units += w;
-    items += static_cast<long long>(s.m) * a.kv_heads;
-    if (s.m > 0) most = max(most, item_tiles(a, s.n, s.len, s.m - 1));
-  }
-  units = warp_sum(units);
-  items = warp_sum(items);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (units == 0) return false;
-  const long long per = max(2ll, static_cast<long long>(__umul64hi(units + ctas - 1, a.inv_ctas)));
-  // what the longest run would be with whole items (all of them of the average's size), against cut ones
-  const float whole = fmaxf(static_cast<float>(most), ceilf(__fdividef(static_cast<float>(items), static_cast<float>(ctas))) *
-                                                          __fdividef(static_cast<float>(units), static_cast<float>(items)));
-  r.split = a.may_split && whole > static_cast<float>(per + a.split_cost);
-  r.at = cta * per;
-  r.end = min(units, r.at + per);
-  if (r.at >= units) return false;
-  // the sequence, item, head and tile of unit r.at
-  long long before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    if (a.plan.seqs > 32) {  // else the lanes still hold the only ones
-      s = load_seq(a, b0 + lane);
-      w = seq_units(a, s, lane);
+  r.b = -1;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {  // all sequences' units; then the sequence of the run's first one
+    unsigned before = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.plan.seqs; b0 += 32) {
+      if (pass == 0 || a.plan.seqs > 32) {  // else the lanes still hold the only ones
+        s = load_seq(a, b0 + lane);
+        w = seq_units(a, s, lane, most);
+      }
+      if (pass == 0) {
+        units += w;
+        items += static_cast<unsigned>(s.m) * a.kv_heads;
+        top = max(top, most);
+      } else {
+        const unsigned upto = before + warp_scan(w, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, r.at < upto);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          r.b = b0 + src;
+          r.s = seq_of_lane(s, src);
+          before = __shfl_sync(0xffffffffu, upto - w, src);
+          break;
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+      }
     }
-    const long long upto = before + warp_scan(w, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, r.at < upto);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.b = b0 + src;
-      r.s = {__shfl_sync(0xffffffffu, s.begin, src), __shfl_sync(0xffffffffu, s.n, src),
-             __shfl_sync(0xffffffffu, s.len, src), __shfl_sync(0xffffffffu, s.m, src)};
-      before = __shfl_sync(0xffffffffu, upto - w, src);
-      break;
+    if (pass == 0) {
+      units = __reduce_add_sync(0xffffffffu, units);
+      items = __reduce_add_sync(0xffffffffu, items);
+      top = __reduce_max_sync(0xffffffffu, top);
+      const unsigned per = max(2u, quotient(units + ctas - 1, a.inv_ctas));
+      // what the longest run would be with whole items (all of them of the average's size), against cut ones
+      const float whole = fmaxf(static_cast<float>(top), static_cast<float>(quotient(items + ctas - 1, a.inv_ctas)) *
+                                                             __fdividef(static_cast<float>(units), static_cast<float>(items)));
+      r.split = a.may_split && whole > static_cast<float>(per + a.split_cost);
+      r.at = cta * per;
+      r.end = min(units, r.at + per);
+      if (r.at >= units) return false;
+    } else {
+      w = r.at - before;  // into the sequence
     }
-    before = __shfl_sync(0xffffffffu, upto, 31);
   }
-  long long rest = r.at - before;
-  for (int m0 = 0;; m0 += 32) {
+  if (r.b < 0) return false;  // lengths that changed meanwhile
+  for (int m0 = 0; m0 < r.s.m; m0 += 32) {
     const int m = m0 + lane;
-    const int tiles = m < r.s.m ? max(1, item_tiles(a, r.s.n, r.s.len, m)) : 0;
-    const long long upto = warp_scan(static_cast<long long>(tiles) * a.kv_heads, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, rest < upto);
+    const int tiles = m < r.s.m ? item_tiles(a, r.s, m) : 0;
+    const unsigned size = m < r.s.m ? static_cast<unsigned>(max(1, tiles)) * a.kv_heads : 0;
+    const unsigned upto = warp_scan(size, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, w < upto);
     if (hit) {
       const int src = __ffs(hit) - 1;
       r.m = m0 + src;
-      const int t_all = __shfl_sync(0xffffffffu, tiles, src);
-      rest -= __shfl_sync(0xffffffffu, upto, src) - static_cast<long long>(t_all) * a.kv_heads;
-      r.t_all = t_all;
-      // rest / t_all is below 2^16, so a quotient of floats is at most one off
-      r.h = static_cast<int>(__fdividef(static_cast<float>(rest), static_cast<float>(t_all)));
-      long long left = rest - static_cast<long long>(r.h) * t_all;
-      if (left < 0) --r.h, left += t_all;
-      if (left >= t_all) ++r.h, left -= t_all;
-      r.t = static_cast<int>(left);
-      break;
+      r.tiles = __shfl_sync(0xffffffffu, tiles, src);
+      w -= __shfl_sync(0xffffffffu, upto - size, src);
+      // w / tiles is below 2^16, so a quotient of floats is at most one off
+      const int len = max(1, r.tiles);
+      r.h = static_cast<int>(__fdividef(static_cast<float>(w), static_cast<float>(len)));
+      r.t = static_cast<int>(w) - r.h * len;
+      if (r.t < 0) --r.h, r.t += len;
+      if (r.t >= len) ++r.h, r.t -= len;
+      return true;
     }
-    rest -= __shfl_sync(0xffffffffu, upto, 31);
+    w -= __shfl_sync(0xffffffffu, upto, 31);
   }
-  return true;
+  return false;
 }
 
 // On to the next item (its units start at r.at).
@@ -236,7 +248,7 @@ __device__ __forceinline__ void next_item(const AhArgs& a, Run& r) {
     } while (r.s.m == 0 && r.b < a.plan.seqs);
     if (r.s.m == 0) return;
   }
-  r.t_all = max(1, item_tiles(a, r.s.n, r.s.len, r.m));
+  r.tiles = item_tiles(a, r.s, r.m);
 }
 
 // 2^(c - top) for scales c <= top: a power of two, 0 where it would be subnormal
@@ -283,9 +295,9 @@ __device__ __forceinline__ AhItem make_item(const AhArgs& a, const Run& r, int l
   it.len = r.s.len;
   it.fresh = r.s.n;
   it.seq = r.b;
-  it.t_all = item_tiles(a, r.s.n, r.s.len, r.m);
+  it.t_all = r.tiles;
   it.t_begin = r.t;
-  it.t_end = r.split ? static_cast<int>(min(static_cast<long long>(it.t_all), r.t + (r.end - r.at))) : it.t_all;
+  it.t_end = r.split ? min(it.t_all, r.t + static_cast<int>(r.end - r.at)) : it.t_all;
   it.slot = -1;
   if (it.t_begin > 0 || it.t_end < it.t_all) {
     it.slot = 2 * blockIdx.x + (it.t_begin > 0 ? 0 : 1);

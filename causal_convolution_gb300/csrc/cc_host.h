@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstddef>
 #include <cstdint>
@@ -47,6 +48,15 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device,
+// number `device` (below 64); a bit of `ready` says where that has been done.
+inline cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& ready) {
+  if (ready.load(std::memory_order_relaxed) >> device & 1) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(1ull << device, std::memory_order_relaxed);
+  return e;
 }
 
 // Per-device facts, cached on first use.

@@ -23,25 +23,15 @@ struct KvPlan {
 
 enum PlaceResult { PLACE_OK, PLACE_NONE, PLACE_BAD };
 
-// The place of row r: position p in its sequence, page and slot. LANES lanes
-// call it together (`mask`, of which this is number `lane`) and search the
-// offsets LANES at a time. PLACE_NONE: the row is no sequence's; PLACE_BAD: the
-// plan gives it no place within the cache.
-template <int LANES>
-__device__ __forceinline__ PlaceResult find_place(const KvPlan& plan, int r, int lane, unsigned mask, long long& p,
-                                                  int& seq, int& page, int& slot) {
-  // the last b with q_offsets[b] <= r lies in [lo, lo + count)
-  int lo = 0, count = plan.seqs;
-  while (count > 1) {
-    const int step = (count + LANES - 1) / LANES;
-    const int first = lane * step;
-    const bool below = first < count && plan.q_offsets[lo + first] <= r;
-    const int hits = __popc(__ballot_sync(mask, below) & mask);
-    const int at = hits > 0 ? (hits - 1) * step : 0;
-    lo += at;
-    count = min(step, count - at);
+// The place of row r: position p in its sequence, page and slot. PLACE_NONE: the
+// row is no sequence's; PLACE_BAD: the plan gives it no place within the cache.
+__device__ __forceinline__ PlaceResult find_place(const KvPlan& plan, int r, long long& p, int& page, int& slot) {
+  // the last b with q_offsets[b] <= r, if the offsets do not fall
+  int lo = 0;
+  for (int hi = plan.seqs; hi - lo > 1;) {
+    const int mid = (lo + hi) >> 1;
+    (plan.q_offsets[mid] <= r ? lo : hi) = mid;
   }
-  seq = lo;
   const int begin = plan.q_offsets[lo], end = plan.q_offsets[lo + 1], len = plan.kv_lens[lo];
   if (r < begin || r >= end) return PLACE_NONE;
   p = static_cast<long long>(len) - end + r;

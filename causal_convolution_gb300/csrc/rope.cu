@@ -21,6 +21,7 @@ namespace cc {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 256;  // most rows of a CTA
 
 struct RopeArgs {
   const uint4 *q, *k, *v;  // v: append only
@@ -29,8 +30,10 @@ struct RopeArgs {
   const int* pos;
   uint4 *q_out, *k_out, *v_out;
   long long rows;
-  int heads, kv_heads, all_heads;  // all_heads: heads + kv_heads, append: + kv_heads values
-  int chunks;                      // ceil(all_heads / HC)
+  int heads, kv_heads;
+  int cta_rows;                    // rows of a CTA
+  unsigned chunks;                 // groups of heads that CTAs take: of queries, of keys, of values
+  int q_chunks, k_chunks;
   int vecs;                        // D / 8
   int rot_vecs;                    // rd / 8
   int positions;
@@ -42,127 +45,147 @@ struct RopeArgs {
   unsigned int* err;
 };
 
-// LPH lanes hold a head, eight channels each; they take HC heads of a row, so
-// that the rotation's factors are loaded once for them and HC loads of a lane
-// are in flight.
+// A CTA takes up to kRopeRows rows and, of each, HC neighbouring heads of one
+// kind (queries, keys or, copied as they are, values): its threads first look up
+// where the rows belong, one row each, so that the chain of loads behind a place
+// (sequence, length, page) is waited for once. Then LPH lanes hold a head, eight
+// channels each, and load the next row's heads before they work on this one's; a
+// row's rotation factors are loaded once for its HC heads.
+//
+// Bound by memory where there are many rows: MEASURED
 template <int LPH, int HC, bool HALVES, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
-  const int lane = threadIdx.x % LPH;
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ long long s_out[kRopeRows];
+  __shared__ int s_pos[kRopeRows];  // -1: the row is left out
+  constexpr int kSlots = kRopeThreads / LPH;
+  const int lane = threadIdx.x % LPH, group = threadIdx.x / LPH;
   const unsigned mask = LPH == 32 ? 0xffffffffu
                                   : ((1u << (LPH % 32)) - 1u) << (threadIdx.x % 32 / LPH * LPH);
   const bool on = lane < a.vecs;
+  const unsigned block = blockIdx.x / a.chunks;  // of rows
+  const int chunk = static_cast<int>(blockIdx.x - block * a.chunks);
+  const int kind = (chunk >= a.q_chunks) + (chunk >= a.q_chunks + a.k_chunks);
+  const int h0 = (chunk - (kind == 0 ? 0 : kind == 1 ? a.q_chunks : a.q_chunks + a.k_chunks)) * HC;
+  const int heads = min(HC, (kind == 0 ? a.heads : a.kv_heads) - h0);
+  const long long r0 = static_cast<long long>(block) * a.cta_rows;
+  const int rows = static_cast<int>(min(static_cast<long long>(a.cta_rows), a.rows - r0));
+  const long long ld = kind == 0 ? a.ld_q : kind == 1 ? a.ld_k : a.ld_v;
+  const uint4* x = (kind == 0 ? a.q : kind == 1 ? a.k : a.v) + r0 * ld + h0 * a.vecs + lane;
+  const long long out_head = kind == 0 ? a.vecs : kind == 1 ? a.ko_head : a.vo_head;
+  uint4* y = (kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out) + h0 * out_head + lane;
+  const uint4* gamma = kind == 0 ? a.gamma_q : a.gamma_k;
   pdl_launch_dependents();
   pdl_wait();
-  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  const uint4 gq = on && a.gamma_q ? a.gamma_q[lane] : ones;
-  const uint4 gk = on && a.gamma_k ? a.gamma_k[lane] : ones;
-  const long long units = a.rows * a.chunks;
-  constexpr int kSlots = kRopeThreads / LPH;
-  for (long long u = static_cast<long long>(blockIdx.x) * kSlots + threadIdx.x / LPH; u < units;
-       u += static_cast<long long>(gridDim.x) * kSlots) {
-    const long long r = u / a.chunks;
-    const int h0 = static_cast<int>(u - r * a.chunks) * HC;
-    uint4 raw[HC];
+  auto load = [&](int i, uint4 (&raw)[HC]) {
 #pragma unroll
-    for (int j = 0; j < HC; ++j) {
-      const int h = h0 + j;
-      raw[j] = make_uint4(0, 0, 0, 0);
-      if (!on || h >= a.all_heads) continue;
-      const uint4* src = h < a.heads                    ? a.q + r * a.ld_q + h * a.vecs
-                         : h < a.heads + a.kv_heads ? a.k + r * a.ld_k + (h - a.heads) * a.vecs
-                                                        : a.v + r * a.ld_v + (h - a.heads - a.kv_heads) * a.vecs;
-      raw[j] = __ldcs(src + lane);
-    }
-    // where the row belongs
-    long long p = r, ko = r * a.ko_row, vo = 0;
+    for (int j = 0; j < HC; ++j)
+      raw[j] = on && j < heads ? __ldcs(x + i * ld + j * a.vecs) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 next[HC];
+  if (group < rows) load(group, next);
+  const Vec8 g = kind < 2 && on && gamma ? unpack8(gamma[lane]) : splat8(1.f);
+  if (threadIdx.x < rows) {
+    const long long r = r0 + threadIdx.x;
+    long long p = r, out = r * (kind == 0 ? a.ld_qo : a.ko_row);
+    bool bad = false, none = false;
     if (APPEND) {
-      int seq, page, slot;
-      const PlaceResult res = find_place<LPH>(a.plan, static_cast<int>(r), lane, mask, p, seq, page, slot);
-      if (res != PLACE_OK) {
-        if (res == PLACE_BAD && lane == 0) atomicOr(a.err, DEVERR_BOUNDS);
-        continue;
-      }
-      ko = page * a.ko_page + slot * a.ko_row;
-      vo = page * a.vo_page + slot * a.vo_row;
+      int page = 0, slot = 0;
+      const PlaceResult res = find_place(a.plan, static_cast<int>(r), p, page, slot);
+      bad = res == PLACE_BAD;
+      none = res == PLACE_NONE;
+      if (kind > 0) out = kind == 1 ? page * a.ko_page + slot * a.ko_row : page * a.vo_page + slot * a.vo_row;
     }
     if (a.pos) p = a.pos[r];
-    if (a.rot_vecs > 0 && (p < 0 || p >= a.positions)) {
-      if (lane == 0) atomicOr(a.err, DEVERR_BOUNDS);
+    bad = bad || (!none && a.rot_vecs > 0 && (p < 0 || p >= a.positions));
+    if (bad) atomicOr(a.err, DEVERR_BOUNDS);
+    s_pos[threadIdx.x] = bad || none ? -1 : a.rot_vecs > 0 ? static_cast<int>(p) : 0;
+    s_out[threadIdx.x] = out;
+  }
+  __syncthreads();
+  const bool turn = kind < 2 && lane < a.rot_vecs;
+  const int half = a.rot_vecs / 2;
+  const int other = threadIdx.x % 32 - lane + (turn ? (lane < half ? lane + half : lane - half) : lane);
+  for (int i = group; i < rows; i += kSlots) {
+    uint4 raw[HC];
+#pragma unroll
+    for (int j = 0; j < HC; ++j) raw[j] = next[j];
+    if (i + kSlots < rows) load(i + kSlots, next);
+    const int p = s_pos[i];
+    if (p < 0) continue;
+    uint4* dst = y + s_out[i];
+    if (APPEND && kind == 2) {
+#pragma unroll
+      for (int j = 0; j < HC; ++j) {
+        if (on && j < heads) dst[j * out_head] = raw[j];
+      }
       continue;
     }
     // the factors of this lane's channels
-    const bool turn = lane < a.rot_vecs;
-    const int half = a.rot_vecs / 2;
     float c[HALVES ? 8 : 4], s[HALVES ? 8 : 4];
     if (turn) {
-      const float4* t = reinterpret_cast<const float4*>(a.rot + p * (a.rot_vecs * 4)) +
+      const float4* t = reinterpret_cast<const float4*>(a.rot + static_cast<long long>(p) * (a.rot_vecs * 4)) +
                         (HALVES ? (lane < half ? lane : lane - half) * 4 : lane * 2);
 #pragma unroll
-      for (int i = 0; i < (HALVES ? 4 : 2); ++i) {
-        const float4 f = t[i];
-        c[2 * i] = f.x, s[2 * i] = f.y, c[2 * i + 1] = f.z, s[2 * i + 1] = f.w;
+      for (int e = 0; e < (HALVES ? 4 : 2); ++e) {
+        const float4 f = t[e];
+        c[2 * e] = f.x, s[2 * e] = f.y, c[2 * e + 1] = f.z, s[2 * e + 1] = f.w;
+      }
+      if (HALVES && lane < half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = -s[e];
       }
     }
 #pragma unroll
     for (int j = 0; j < HC; ++j) {
-      const int h = h0 + j;
-      if (h >= a.all_heads) break;
-      if (APPEND && h >= a.heads + a.kv_heads) {
-        if (on) a.v_out[vo + (h - a.heads - a.kv_heads) * a.vo_head + lane] = raw[j];
-        continue;
-      }
+      if (j >= heads) break;
       Vec8 f = unpack8(raw[j]);
       f32x2 sq = pair(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sq = fma2(f.p[i], f.p[i], sq);
+      for (int e = 0; e < 4; ++e) sq = fma2(f.p[e], f.p[e], sq);
       float sum = lo(sq) + hi(sq);
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-      const float rs = 1.f / sqrtf(fmaf(sum, a.inv_d, a.eps));
-      const Vec8 g = unpack8(h < a.heads ? gq : gk);
+      const float rs = rsqrtf(fmaf(sum, a.inv_d, a.eps));  // off by at most two units in the last place
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f.p[i] = mul2(g.p[i], mul2(f.p[i], pair(rs, rs)));
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = f[i];
+      for (int e = 0; e < 4; ++e) f.p[e] = mul2(g.p[e], mul2(f.p[e], pair(rs, rs)));
       if (HALVES) {
-        const int base = threadIdx.x % 32 - lane;
-        const int other = base + (turn ? (lane < half ? lane + half : lane - half) : lane);
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = __shfl_sync(mask, y[i], other);
-          if (turn) y[i] = lane < half ? y[i] * c[i] - z * s[i] : z * s[i] + y[i] * c[i];
+        for (int e = 0; e < 8; ++e) {
+          const float z = __shfl_sync(mask, f[e], other);
+          v[e] = turn ? fmaf(z, s[e], f[e] * c[e]) : f[e];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.p[e] = pair(v[2 * e], v[2 * e + 1]);
       } else if (turn) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = y[2 * i], x1 = y[2 * i + 1];
-          y[2 * i] = x0 * c[i] - x1 * s[i];
-          y[2 * i + 1] = x0 * s[i] + x1 * c[i];
+        for (int e = 0; e < 4; ++e) {
+          const float x0 = lo(f.p[e]), x1 = hi(f.p[e]);
+          f.p[e] = pair(x0 * c[e] - x1 * s[e], x0 * s[e] + x1 * c[e]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f.p[i] = pair(y[2 * i], y[2 * i + 1]);
-      const uint4 res = pack8(f);
-      if (!on) continue;
-      if (h < a.heads)
-        a.q_out[r * a.ld_qo + h * a.vecs + lane] = res;
-      else
-        a.k_out[ko + (h - a.heads) * a.ko_head + lane] = res;
+      if (on) dst[j * out_head] = pack8(f);
     }
   }
 }
 
-template <int LPH, int HC, bool APPEND>
+template <int LPH, bool APPEND>
 cc_status launch_rope(const char* what, RopeArgs& a, int style, int sms, cudaStream_t stream) {
-  a.chunks = (a.all_heads + HC - 1) / HC;
-  const long long units = a.rows * a.chunks;
-  constexpr int kSlots = kRopeThreads / LPH;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>((units + kSlots - 1) / kSlots, sms * 8ll));
+  constexpr int kSlots = kRopeThreads / LPH, HC = 2;
+  a.q_chunks = (a.heads + HC - 1) / HC;
+  a.k_chunks = (a.kv_heads + HC - 1) / HC;
+  const long long chunks = a.q_chunks + static_cast<long long>(APPEND ? 2 : 1) * a.k_chunks;
+  a.chunks = static_cast<unsigned>(chunks);
+  // rows of a CTA: as many as leave about twelve CTAs to an SM, whole rounds of its lanes
+  const long long want = a.rows * chunks / (sms * 12ll) / kSlots * kSlots;
+  a.cta_rows = static_cast<int>(std::max<long long>(kSlots, std::min<long long>(want, kRopeRows)));
+  const long long ctas = (a.rows + a.cta_rows - 1) / a.cta_rows * chunks;
+  if (ctas > 0x7fffffffLL) return fail(CC_ERR_UNSUPPORTED, "%s: too many rows of heads", what);
+  const dim3 grid(static_cast<unsigned>(ctas));
   const cudaError_t e =
       style == CC_ROT_HALVES
-          ? launch_pdl(qk_norm_rope_kernel<LPH, HC, true, APPEND>, dim3(grid), dim3(kRopeThreads), 0, stream, a)
-          : launch_pdl(qk_norm_rope_kernel<LPH, HC, false, APPEND>, dim3(grid), dim3(kRopeThreads), 0, stream, a);
+          ? launch_pdl(qk_norm_rope_kernel<LPH, HC, true, APPEND>, grid, dim3(kRopeThreads), 0, stream, a)
+          : launch_pdl(qk_norm_rope_kernel<LPH, HC, false, APPEND>, grid, dim3(kRopeThreads), 0, stream, a);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
 }
@@ -174,10 +197,10 @@ cc_status run_rope(const char* what, RopeArgs& a, int style, void* stream) {
   if (st != CC_OK) return st;
   a.err = di.err_word;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return a.vecs <= 4    ? launch_rope<4, 4, APPEND>(what, a, style, di.sm_count, cs)
-         : a.vecs <= 8  ? launch_rope<8, 4, APPEND>(what, a, style, di.sm_count, cs)
-         : a.vecs <= 16 ? launch_rope<16, 4, APPEND>(what, a, style, di.sm_count, cs)
-                        : launch_rope<32, 4, APPEND>(what, a, style, di.sm_count, cs);
+  return a.vecs <= 4    ? launch_rope<4, APPEND>(what, a, style, di.sm_count, cs)
+         : a.vecs <= 8  ? launch_rope<8, APPEND>(what, a, style, di.sm_count, cs)
+         : a.vecs <= 16 ? launch_rope<16, APPEND>(what, a, style, di.sm_count, cs)
+                        : launch_rope<32, APPEND>(what, a, style, di.sm_count, cs);
 }
 
 // The checks that both entry points share.
@@ -252,7 +275,6 @@ extern "C" cc_status cc_qk_norm_rope(const cc_bf16* q, const cc_bf16* k, const c
   RopeArgs a = rope_args(q, k, gamma_q, gamma_k, rot, pos, q_out, rows, heads, kv_heads, d, rd, positions, ld_q, ld_k,
                          ld_qo, eps);
   a.k_out = reinterpret_cast<uint4*>(k_out);
-  a.all_heads = heads + kv_heads;
   a.ko_row = ld_ko / 8;
   a.ko_head = d / 8;
   return run_rope<false>(what, a, style, stream);
@@ -289,7 +311,6 @@ extern "C" cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, 
   a.ld_v = ld_v / 8;
   a.k_out = reinterpret_cast<uint4*>(k_cache);
   a.v_out = reinterpret_cast<uint4*>(v_cache);
-  a.all_heads = heads + 2 * kv_heads;
   a.ko_page = k_page / 8;
   a.ko_row = k_token / 8;
   a.ko_head = k_head / 8;
