@@ -20,8 +20,8 @@
 namespace cc {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 256;  // most rows of a CTA
+constexpr int kRopeThreads = 128;
+constexpr int kRopeRows = 128;  // most rows of a CTA
 
 struct RopeArgs {
   const uint4 *q, *k, *v;  // v: append only
@@ -54,7 +54,7 @@ struct RopeArgs {
 //
 // Bound by memory where there are many rows: MEASURED
 template <int LPH, int HC, bool HALVES, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 9) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ long long s_out[kRopeRows];
   __shared__ int s_pos[kRopeRows];  // -1: the row is left out
   constexpr int kSlots = kRopeThreads / LPH;
@@ -176,8 +176,8 @@ cc_status launch_rope(const char* what, RopeArgs& a, int style, int sms, cudaStr
   a.k_chunks = (a.kv_heads + HC - 1) / HC;
   const long long chunks = a.q_chunks + static_cast<long long>(APPEND ? 2 : 1) * a.k_chunks;
   a.chunks = static_cast<unsigned>(chunks);
-  // rows of a CTA: as many as leave about twelve CTAs to an SM, whole rounds of its lanes
-  const long long want = a.rows * chunks / (sms * 12ll) / kSlots * kSlots;
+  // rows of a CTA: as many as leave about 24 CTAs to an SM, whole rounds of its lanes
+  const long long want = a.rows * chunks / (sms * 24ll) / kSlots * kSlots;
   a.cta_rows = static_cast<int>(std::max<long long>(kSlots, std::min<long long>(want, kRopeRows)));
   const long long ctas = (a.rows + a.cta_rows - 1) / a.cta_rows * chunks;
   if (ctas > 0x7fffffffLL) return fail(CC_ERR_UNSUPPORTED, "%s: too many rows of heads", what);
