@@ -46,8 +46,8 @@ constexpr int kAhKeys = 1 << kAhTileShift;  // keys per tile, in two halves for 
 constexpr int kAhHalf = 128;      // rows per half
 constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 channels
 constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
-constexpr int kAhOut = 1024;      // bytes through which a softmax warp's output goes
-constexpr float kAhRoom = 1048576.f;  // 2^20: how far a row's weights may pass its scale
+constexpr float kAhRoom = 1048576.f;  // 2^20: what half a tile's weights of a row may come to before its scale moves
+constexpr float kAhMove = 8.f;        // and by how many powers of two at least
 constexpr int kAhSplitCost = 4;  // measured: the partial sums' way through L2 and the joining kernel
 
 // A value that all lanes hold, said in a way that the compiler keeps it in
@@ -71,7 +71,7 @@ struct AhSmem {
   static constexpr int kTile = NB * kAhKvBlock;
   static constexpr int kQHalf = NB * kAhQBlock;
   static constexpr int kQ = 2 * kQHalf;
-  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 16 * kAhOut + 1024 + 2 * kAhHalf * 8 + 4 * kAhHalf * 4;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 8 + 4 * kAhHalf * 4;
 };
 
 template <int NB, int STAGES>
@@ -83,8 +83,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + Sm::kQ;
-  uint8_t* sO = sKV + STAGES * Sm::kTile;
-  float2* sCL = reinterpret_cast<float2*>(sO + 16 * kAhOut);  // [2][128] stream 1's (c, l) of single halves
+  float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // [2][128] stream 1's (c, l) of single halves
   float* sX = reinterpret_cast<float*>(sCL + 2 * kAhHalf);    // [4][128] what warps of the same rows exchange
   AhItem* items = reinterpret_cast<AhItem*>(sX + 4 * kAhHalf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
@@ -359,15 +358,10 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         const uint32_t bd = v0 + vs * (Sm::kTile >> 4);
         tc_fence_after();
         if (elect_one()) {
-          // P of a tile's halves: columns 0-31 and 64-95, what their rounding left: 32-63 and 96-127
+          // P of a tile's halves: columns 0-31 and 64-95
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_bf16_ta(o_tmem, s_tmem + (k >> 2) * 64 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, (j >= 2 || k) ? 1u : 0u);
-          if (!two) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_ta(o_tmem, s_tmem + (k >> 2) * 64 + 32 + (k & 3) * 8, sdesc_of(bd + k * 128), idesc_o, 1u);
-          }
           if (j + 2 >= jobs) mma_commit(smem_u32(&pv_done[s]));
           mma_commit(smem_u32(&kv_empty[vs]));
         }
@@ -430,96 +424,68 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           const int lim = limit - t * kAhKeys - hf * 64;
           const bool masked = __any_sync(0xffffffffu, lim < 64);
           uint32_t sv[64];
-          auto load = [&]() {
+          // Weights on the scale in hand, which is fine while none is far above 1; their sum tells that without a
+          // maximum. Rows without a scale, and those that outgrow theirs, get one, and the tile is done again. (The
+          // code is kept short, with the rare parts in one place: what does not fit the instruction cache costs more
+          // than it saves.)
+          for (bool again = i == 0;; again = true) {
             tmem_ld64_wait(s_col, sv);
             if (masked) {
 #pragma unroll
               for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
             }
-          };
-          // Puts the rows of `off` on the scale of their largest score in this tile, and l and O with them (O's last
-          // product was complete before these scores were). Both warps of a row come here together, and the barrier
-          // keeps their weights from scores that the other one has not read.
-          auto rescale = [&](bool off, float room) {
-            float m[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            if (again) {
+              // The scale of the tile's largest score, and l and O with it (O's last product was complete before
+              // these scores were). Both warps of a row come here together, and the barrier keeps their weights from
+              // scores that the other one has not read.
+              float m0 = kNegInf, m1 = kNegInf;
 #pragma unroll
-            for (int e = 0; e < 64; e += 8) {
+              for (int e = 0; e < 64; e += 4) {
+                m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
+                m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
+              }
+              float up = ceilf(fmaxf(m0, m1) * a.kx);
+              *my_x = up;
+              named_barrier_sync(mates, 64);
+              up = fmaxf(up, *mate_x);
+              const float top = row_ok && up > c + (i == 0 ? 0.f : kAhMove) ? up : c;
+              if (__any_sync(0xffffffffu, top != c)) {
+                const float f = pow2_diff(c, top);
+                if (i > 0) {
+                  for (int col = hf * 16; col < a.d; col += 32) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + col, o);
+                    tmem_wait16(o);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                m[j] = max3(__uint_as_float(sv[e + 2 * j]), __uint_as_float(sv[e + 2 * j + 1]), m[j]);
-            }
-            float up = ceilf(max3(m[0], m[1], fmaxf(m[2], m[3])) * a.kx);
-            *my_x = up;
-            named_barrier_sync(mates, 64);
-            up = fmaxf(up, *mate_x);
-            const float top = off && up > c + room ? up : c;
-            if (!__any_sync(0xffffffffu, top != c)) return;
-            const float f = pow2_diff(c, top);
-            if (i > 0) {
-              for (int col = hf * 16; col < a.d; col += 32) {
-                uint32_t o[16];
-                tmem_ld16(o_col + col, o);
-                tmem_wait16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(o_col + col, o);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st16(o_col + col, o);
+                  }
+                }
+                l *= f;
+                c = top;
               }
             }
-            l *= f;
-            c = top;
-          };
-          load();
-          if (two) {
-            // Weights on the scale in hand, which is fine while none is far above 1; their sum tells that without a
-            // maximum. Rows without a scale, and those that outgrow theirs, get one, and the tile is done again.
-            for (bool again = i == 0;; again = true) {
-              if (again) rescale(row_ok, i == 0 ? 0.f : 8.f);
-              const float base = c == kNegInf ? 0.f : c;
-              const f32x2 nb2 = pair(-base, -base);
-              f32x2 sum = pair(0.f, 0.f), sum1 = sum;
-              uint32_t pk[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
-                const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-                if (e & 1)
-                  sum1 = add2(sum1, pair(p0, p1));
-                else
-                  sum = add2(sum, pair(p0, p1));
-                pk[e] = pack_bf16(p0, p1);
-              }
-              sum = add2(sum, sum1);
-              const float total = lo(sum) + hi(sum);
-              if (!again && named_barrier_or(mates, 64, row_ok && (c == kNegInf || !(total < kAhRoom)))) {
-                load();
-                continue;
-              }
-              tmem_st32(s_col, pk);
-              l += total;
-              break;
-            }
-          } else {
-            // few rows: the products wait for memory, and a second one takes what the first rounding leaves
-            rescale(row_ok, i == 0 ? 0.f : 16.f);
             const float base = c == kNegInf ? 0.f : c;
             const f32x2 nb2 = pair(-base, -base);
-            f32x2 sum = pair(0.f, 0.f);
+            f32x2 sum = pair(0.f, 0.f), sum1 = sum;
+            uint32_t pk[32];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t p_hi[16], p_lo[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int at = part * 32 + 2 * e;
-                const f32x2 x = fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), kx2, nb2);
-                const float p0 = ex2_approx(lo(x)), p1 = ex2_approx(hi(x));
-                sum = add2(sum, pair(p0, p1));
-                p_hi[e] = pack_bf16(p0, p1);
-                p_lo[e] = pack_bf16(p0 - __uint_as_float(p_hi[e] << 16), p1 - __uint_as_float(p_hi[e] & 0xffff0000u));
-              }
-              tmem_st16(s_col + part * 16, p_hi);
-              tmem_st16(s_col + 32 + part * 16, p_lo);
+            for (int e = 0; e < 32; ++e) {
+              const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+              pk[e] = pack_bf16(ex2_approx(lo(x)), ex2_approx(hi(x)));
+              // the rounded weights are summed, so that they come to 1: a row that one key rules is exact
+              const f32x2 p = pair(__uint_as_float(pk[e] << 16), __uint_as_float(pk[e] & 0xffff0000u));
+              if (e & 1)
+                sum1 = add2(sum1, p);
+              else
+                sum = add2(sum, p);
             }
-            l += lo(sum) + hi(sum);
+            sum = add2(sum, sum1);
+            const float total = lo(sum) + hi(sum);
+            if (!again && named_barrier_or(mates, 64, row_ok && (c == kNegInf || !(total < kAhRoom)))) continue;
+            tmem_st32(s_col, pk);
+            l += total;
+            break;
           }
           tmem_st_wait();
           tc_fence_before();
@@ -564,65 +530,47 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         const bool sees = n > 0 && limit > 0;
         const float inv = 1.f / sum;
         const int r = (two ? s * kAhHalf : 0) + row;
-        // through shared memory, so that a warp's stores cover more than a sector of a row
-        uint8_t* stage = sO + warp * kAhOut;
         const bool whole = it.slot < 0;
         const int64_t my_row = whole ? (it.q_row + tok) * a.ld_o + static_cast<int64_t>(it.head * a.group + row_head) * a.d
                                      : (static_cast<int64_t>(it.slot) * a.slot_rows + r) * a.d;
-        const unsigned ok_rows = __ballot_sync(0xffffffffu, row_ok);
-        for (int col = hf * 32; col < a.d; col += 64) {  // the two warps of a row take turns
-          uint32_t o[32];
-          float x[32];
-          if (n > 0) tmem_ld32_wait(o_col + col, o);
+#pragma unroll 1
+        for (int col = hf * 16; col < a.d; col += 32) {  // the two warps of a row take turns
+          uint32_t o[16];
+          float x[16];
+          if (n > 0) {
+            tmem_ld16(o_col + col, o);
+            tmem_wait16(o);
+          }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+          for (int e = 0; e < 16; ++e) x[e] = n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
           if (other > 0) {
-            tmem_ld32_wait(o_col + 128 + col, o);
+            tmem_ld16(o_col + 128 + col, o);
+            tmem_wait16(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
           }
-          if (whole) {  // 64 bytes a row, 16 rows at a time
-            uint32_t pk[16];
+          uint4 v[2];
+          if (whole) {
+            uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = sees ? pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv) : 0u;
-#pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
-              if (lane >> 4 == pass) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  *reinterpret_cast<uint4*>(stage + (lane & 15) * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
-                      make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+            for (int e = 0; e < 8; ++e) pk[e] = sees ? pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv) : 0u;
+            v[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            v[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            if (row_ok) {  // 16 channels: a sector, where rows start on one
+              uint4* dst = reinterpret_cast<uint4*>(a.o + my_row + col);
+              if (a.o_sectors) {
+                st_global_v8(dst, v);
+              } else {
+                dst[0] = v[0];
+                dst[1] = v[1];
               }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int r16 = i * 8 + (lane >> 2), j = lane & 3, from = pass * 16 + r16;
-                const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 8;
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + r16 * 64 + ((j ^ (r16 >> 1 & 3)) << 4));
-                if ((ok_rows >> from & 1) && col + j * 8 < a.d) *reinterpret_cast<uint4*>(a.o + at) = v;
-              }
-              __syncwarp();
             }
-          } else {  // 128 bytes a row, eight rows at a time
+          } else if (row_ok) {
 #pragma unroll
-            for (int pass = 0; pass < 4; ++pass) {
-              if (lane >> 3 == pass) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  *reinterpret_cast<float4*>(stage + (lane & 7) * 128 + ((j ^ (lane & 7)) << 4)) =
-                      make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int r8 = i * 4 + (lane >> 3), j = lane & 7, from = pass * 8 + r8;
-                const int64_t at = __shfl_sync(0xffffffffu, my_row, from) + col + j * 4;
-                const float4 v = *reinterpret_cast<const float4*>(stage + r8 * 128 + ((j ^ r8) << 4));
-                if ((ok_rows >> from & 1) && col + j * 4 < a.d) *reinterpret_cast<float4*>(a.part + at) = v;
-              }
-              __syncwarp();
-            }
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(a.part + my_row + col + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
+          __syncwarp();
         }
         if (row_ok && it.slot >= 0 && hf == 0) {
           const bool any = limit > it.t_begin * kAhKeys;
@@ -803,6 +751,7 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   const bool few = few_rows(a.rows, a.plan.seqs, a.group);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.ld_q = ld_q;
+  a.o_sectors = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.ld_o % 16 == 0;
   a.tq = (few ? kFewRows : kAhHalf) / a.group;
   a.item_tokens = few ? a.tq : 2 * a.tq;
   a.tile_shift = few ? kFewTileShift : kAhTileShift;

@@ -38,6 +38,7 @@ struct AhArgs {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   long long ld_q, ld_o;
+  int o_sectors;    // rows of o start on 32-byte borders
   float kx;         // scale * log2(e)
   unsigned block;   // causal block, 0: none
   int may_split;
