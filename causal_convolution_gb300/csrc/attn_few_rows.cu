@@ -1,16 +1,19 @@
 // Attention with heads for few query rows to a sequence (single tokens, or a few,
-// with the query heads of a group): up to 16 rows of a key head at a time. Each
-// key and value is used for two products of 16 rows, so the cache's bytes bound
+// with the query heads of a group): up to 8 rows of a key head at a time. Each key
+// and value is used for two products with those rows, so the cache's bytes bound
 // it, and the kernel is built around reading them without a pause: warp 0 finds
 // the CTA's run (cc_heads.cuh) and streams 64 keys and their values at a time with
 // TMA, across the borders of items; warps 1-4 take 16 of the 64 keys each, with
 // row statistics and a sum of their own, so that nothing but the tiles' arrival
-// ties them together. Their sums are joined at an item's end. The products are
-// m16n8k16 from registers: a 128-row tile of tcgen05 would be filled to an eighth
-// or less, and its way through tensor memory is longer than a tile's reading.
-// Weights are taken in two bf16 parts, which costs products that have time.
+// ties them together. Their sums are joined at an item's end.
 //
-// Two CTAs to an SM, 96 KB of tiles in flight each.
+// The products are m16n8k16 from registers, keys (for k q^T) and channels (for
+// v^T p) along m and the rows along n: a 128-row tile of tcgen05 would be filled
+// to a sixteenth or less, and its way through tensor memory takes longer than a
+// tile's reading. Weights are taken in two bf16 parts, which costs products that
+// have time.
+//
+// Two CTAs to an SM, 96 KB of tiles in flight each. MEASURED
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,11 +45,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&x)[4], 
       : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
 }
 
+// An 8 x 8 matrix of bf16, two of a row to a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 template <int NB, int STAGES>
 struct FrSmem {
   static constexpr int kTile = 2 * NB * kFrBlock;  // keys and values
-  static constexpr int kSum = NB * 8 * 512;        // a warp's sums, as its lanes hold them
-  static constexpr int kBytes = 1024 + STAGES * kTile + kSum + 2 * 4 * 16 * 4 + 512;
+  static constexpr int kSum = 4 * 3 * NB * 512;    // quarters of sums on their way to the warps that add them up
+  static constexpr int kBytes = 1024 + STAGES * kTile + kSum + 4 * 8 * 8 + 512;
 };
 
 template <int NB, int STAGES>
@@ -57,9 +67,8 @@ __global__ void __launch_bounds__(kFrThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float4* sSum = reinterpret_cast<float4*>(smem + STAGES * Sm::kTile);
-  float* sC = reinterpret_cast<float*>(smem + STAGES * Sm::kTile + Sm::kSum);  // [4][16]
-  float* sL = sC + 64;
-  AhItem* items = reinterpret_cast<AhItem*>(sL + 64);
+  float2* sCL = reinterpret_cast<float2*>(smem + STAGES * Sm::kTile + Sm::kSum);  // [4][8] (c, l)
+  AhItem* items = reinterpret_cast<AhItem*>(sCL + 32);
   uint64_t* full = reinterpret_cast<uint64_t*>(items + kAhItems);
   uint64_t* empty = full + STAGES;
   uint64_t* item_full = empty + STAGES;
@@ -152,9 +161,10 @@ __global__ void __launch_bounds__(kFrThreads, 2)
     const int w = warp - 1;
     const int steps = a.d / 16;
     const int kb = w * 16;  // this warp's keys of a tile
-    // ldmatrix addresses within a tile: keys as rows of the second factor of q k^T, values transposed as that of P v
-    const int k_row = kb + (lane >> 4) * 8 + (lane & 7), k_chunk = lane >> 3 & 1;
-    const int v_row = kb + (lane >> 3 & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
+    // ldmatrix addresses within a tile: 16 keys x 16 channels as they are, and values transposed
+    const int k_row = kb + (lane >> 3 & 1) * 8 + (lane & 7), k_chunk = lane >> 4;
+    const int v_row = kb + (lane >> 4) * 8 + (lane & 7), v_chunk = lane >> 3 & 1;
+    const int col = (lane & 3) * 2;  // rows col and col + 1 of the item are this lane's columns of scores and sums
     bool ok = true;
     while (true) {
       // A warp whose wait ran out goes through the rest of its item without waiting, as the others count on it at
@@ -170,34 +180,29 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       if (it.last) break;
       const int n = it.t_end - it.t_begin;
       const int rows = it.tokens * a.group;
-      // rows lane / 4 and + 8 of the item
-      int limit[2];
-      long long at_q[2], at_o[2];
+      // row lane / 4 is the one whose query this lane holds, two channels of eight
+      const int my_row = lane >> 2, my_tok = static_cast<int>(quotient(my_row, a.inv_group));
+      const int my_head = it.head * a.group + my_row - my_tok * a.group;
+      uint32_t qf[NB * 4][2];
+      {
+        const __nv_bfloat16* q =
+            a.q + (it.q_row + my_tok) * a.ld_q + static_cast<long long>(my_head) * a.d + (lane & 3) * 2;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = (lane >> 2) + 8 * i, tok = static_cast<int>(quotient(r, a.inv_group)), h = it.head * a.group + r - tok * a.group;
-        limit[i] = r < rows ? key_limit(a, it.fresh, it.len, it.first + tok) : 0;
-        at_q[i] = (it.q_row + tok) * a.ld_q + static_cast<long long>(h) * a.d;
-        at_o[i] = (it.q_row + tok) * a.ld_o + static_cast<long long>(h) * a.d;
-      }
-      const bool in[2] = {(lane >> 2) < rows, (lane >> 2) + 8 < rows};
-      uint32_t qf[NB * 4][4];
-#pragma unroll
-      for (int k = 0; k < NB * 4; ++k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i & 1;
-          qf[k][i] = k < steps && in[r]
-                         ? *reinterpret_cast<const uint32_t*>(a.q + at_q[r] + k * 16 + (i >> 1) * 8 + (lane & 3) * 2)
-                         : 0u;
+        for (int k = 0; k < NB * 4; ++k) {
+          const bool on = k < steps && my_row < rows;
+          qf[k][0] = on ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
+          qf[k][1] = on ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
         }
       }
-      float acc[NB * 8][4];
+      int limit[2];
 #pragma unroll
-      for (int j = 0; j < NB * 8; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      for (int i = 0; i < 2; ++i) {
+        const int tok = static_cast<int>(quotient(col + i, a.inv_group));
+        limit[i] = col + i < rows ? key_limit(a, it.fresh, it.len, it.first + tok) : 0;
       }
+      float acc[NB * 4][4];  // channels 16 j + lane / 4 (0, 1) and + 8 (2, 3) of rows col and col + 1
+#pragma unroll
+      for (int j = 0; j < NB * 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
       float c[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
       for (int t = it.t_begin; t < it.t_end; ++t) {
         ok = ok && warp_wait(&full[stage], ph, a);
@@ -215,63 +220,59 @@ __global__ void __launch_bounds__(kFrThreads, 2)
         }
         if (valid > 0) {
           const uint32_t kt = smem_u32(tile) + k_row * 128, vt = smem_u32(tile) + NB * kFrBlock + v_row * 128;
-          float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          // scores of keys lane / 4 (0, 1) and + 8 (2, 3) and rows col, col + 1; two chains of products
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < NB * 4; ++k) {
             if (k < steps) {
-              uint32_t b[4];
-              ldsm4(kt + (k >> 2) * kFrBlock + ((((k & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), b);
-              mma16816(sc[0], qf[k], b[0], b[1]);
-              mma16816(sc[1], qf[k], b[2], b[3]);
+              uint32_t x[4];
+              ldsm4(kt + (k >> 2) * kFrBlock + ((((k & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), x);
+              mma16816(k & 1 ? s1 : s0, x, qf[k][0], qf[k][1]);
             }
           }
-          // scores of keys 8 * j + 2 * (lane % 4) + {0, 1}, rows lane / 4 (0, 1) and + 8 (2, 3)
-          const int lim0 = limit[0] - t * kFrKeys - kb, lim1 = limit[1] - t * kFrKeys - kb;
           float m[2] = {kNegInf, kNegInf};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int i = 0; i < 4; ++i) {
+            const int key = t * kFrKeys + kb + (lane >> 2) + (i >> 1) * 8;
+            s0[i] = key < limit[i & 1] ? (s0[i] + s1[i]) * a.kx : kNegInf;
+            m[i & 1] = fmaxf(m[i & 1], s0[i]);
+          }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = j * 8 + (lane & 3) * 2 + (i & 1);
-              sc[j][i] = key < (i < 2 ? lim0 : lim1) ? sc[j][i] * a.kx : kNegInf;
-              m[i >> 1] = fmaxf(m[i >> 1], sc[j][i]);
-            }
+          for (int o = 4; o < 32; o <<= 1) {
+            m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+            m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
-            m[i] = ceilf(fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2)));
-            m[i] = m[i] > c[i] + (c[i] == kNegInf ? 0.f : kFrRoom) ? m[i] : c[i];
+            m[i] = ceilf(m[i]);
+            m[i] = m[i] > c[i] + kFrRoom ? m[i] : c[i];
           }
           if (__any_sync(0xffffffffu, m[0] != c[0] || m[1] != c[1])) {
             const float f0 = pow2_diff(c[0], m[0]), f1 = pow2_diff(c[1], m[1]);
 #pragma unroll
-            for (int j = 0; j < NB * 8; ++j) acc[j][0] *= f0, acc[j][1] *= f0, acc[j][2] *= f1, acc[j][3] *= f1;
+            for (int j = 0; j < NB * 4; ++j) acc[j][0] *= f0, acc[j][1] *= f1, acc[j][2] *= f0, acc[j][3] *= f1;
             l[0] *= f0, l[1] *= f1;
             c[0] = m[0], c[1] = m[1];
           }
-          const float b0 = c[0] == kNegInf ? 0.f : c[0], b1 = c[1] == kNegInf ? 0.f : c[1];
-          uint32_t hi[4], lo_[4];
+          // weights, and what their rounding leaves, turned into the second factor of v^T p
+          uint32_t hi[2], rest[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float p0 = ex2_approx(sc[j][2 * i] - (i ? b1 : b0)), p1 = ex2_approx(sc[j][2 * i + 1] - (i ? b1 : b0));
-              l[i] += p0 + p1;
-              const uint32_t h = pack_bf16(p0, p1);
-              hi[2 * j + i] = h;
-              lo_[2 * j + i] = pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
-            }
+          for (int i = 0; i < 2; ++i) {
+            const float p0 = ex2_approx(s0[2 * i] - (c[0] == kNegInf ? 0.f : c[0]));
+            const float p1 = ex2_approx(s0[2 * i + 1] - (c[1] == kNegInf ? 0.f : c[1]));
+            l[0] += p0;
+            l[1] += p1;
+            hi[i] = pack_bf16(p0, p1);
+            rest[i] = transpose8(pack_bf16(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u)));
+            hi[i] = transpose8(hi[i]);
           }
 #pragma unroll
           for (int j = 0; j < NB * 4; ++j) {
             if (j < steps) {
-              uint32_t b[4];
-              ldsm4_trans(vt + (j >> 2) * kFrBlock + ((((j & 3) * 2 + v_chunk) ^ (v_row & 7)) << 4), b);
-              mma16816(acc[2 * j], hi, b[0], b[1]);
-              mma16816(acc[2 * j + 1], hi, b[2], b[3]);
-              mma16816(acc[2 * j], lo_, b[0], b[1]);
-              mma16816(acc[2 * j + 1], lo_, b[2], b[3]);
+              uint32_t x[4];
+              ldsm4_trans(vt + (j >> 2) * kFrBlock + ((((j & 3) * 2 + v_chunk) ^ (v_row & 7)) << 4), x);
+              mma16816(acc[j], x, hi[0], hi[1]);
+              mma16816(acc[j], x, rest[0], rest[1]);
             }
           }
         }
@@ -284,70 +285,74 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       }
       // the four warps' sums on one scale
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if ((lane & 3) == 0) {
-          sC[w * 16 + (lane >> 2) + 8 * i] = c[i];
-          sL[w * 16 + (lane >> 2) + 8 * i] = l[i];
-        }
+      for (int o = 4; o < 32; o <<= 1) {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+      }
+      if (lane < 4) {
+        sCL[w * 8 + col] = make_float2(c[0], l[0]);
+        sCL[w * 8 + col + 1] = make_float2(c[1], l[1]);
       }
       named_barrier_sync(1, 128);
       float top[2] = {kNegInf, kNegInf}, sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = (lane >> 2) + 8 * i;
+        float2 cl[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], sC[j * 16 + r]);
+        for (int j = 0; j < 4; ++j) cl[j] = sCL[j * 8 + col + i];
+        top[i] = fmaxf(fmaxf(cl[0].x, cl[1].x), fmaxf(cl[2].x, cl[3].x));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i] = fmaf(sL[j * 16 + r], pow2_diff(sC[j * 16 + r], top[i]), sum[i]);
+        for (int j = 0; j < 4; ++j) sum[i] = fmaf(cl[j].y, pow2_diff(cl[j].x, top[i]), sum[i]);
       }
       const float f0 = pow2_diff(c[0], top[0]), f1 = pow2_diff(c[1], top[1]);
-#pragma unroll
-      for (int j = 0; j < NB * 8; ++j) acc[j][0] *= f0, acc[j][1] *= f0, acc[j][2] *= f1, acc[j][3] *= f1;
-      // a quarter of the channels at a time; each warp adds up and writes one
-      constexpr int Q = NB * 2;
-      float4 res[Q];
+      // each warp adds up and writes a quarter of the channels; the others' shares come through shared memory
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        if (q == w) continue;
 #pragma unroll
-        for (int j = 0; j < Q; ++j)
-          sSum[(w * Q + j) * 32 + lane] =
-              make_float4(acc[q * Q + j][0], acc[q * Q + j][1], acc[q * Q + j][2], acc[q * Q + j][3]);
-        named_barrier_sync(1, 128);
-        if (w == q) {
-#pragma unroll
-          for (int j = 0; j < Q; ++j) {
-            float4 v = sSum[j * 32 + lane];
-#pragma unroll
-            for (int from = 1; from < 4; ++from) {
-              const float4 x = sSum[(from * Q + j) * 32 + lane];
-              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            }
-            res[j] = v;
-          }
-        }
-        named_barrier_sync(1, 128);
+        for (int j = 0; j < NB; ++j)
+          sSum[((q * 3 + (w < q ? w : w - 1)) * NB + j) * 32 + lane] =
+              make_float4(acc[q * NB + j][0] * f0, acc[q * NB + j][1] * f1, acc[q * NB + j][2] * f0, acc[q * NB + j][3] * f1);
       }
+      named_barrier_sync(1, 128);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!in[i]) continue;
-        const bool sees = n > 0 && limit[i] > 0;
-        const float inv = 1.f / sum[i];
-        const long long at = static_cast<long long>(it.slot) * a.slot_rows + (lane >> 2) + 8 * i;
+      for (int j = 0; j < NB; ++j) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < Q; ++j) {
-          const int col = (w * Q + j) * 8 + (lane & 3) * 2;
-          const float x0 = i ? res[j].z : res[j].x, x1 = i ? res[j].w : res[j].y;
-          if (col >= a.d) break;
-          if (it.slot < 0)
-            *reinterpret_cast<uint32_t*>(a.o + at_o[i] + col) = sees ? pack_bf16(x0 * inv, x1 * inv) : 0u;
-          else
-            *reinterpret_cast<float2*>(a.part + at * a.d + col) = make_float2(x0, x1);
+        for (int q = 0; q < 4; ++q) {
+          if (q == w) v = make_float4(acc[q * NB + j][0] * f0, acc[q * NB + j][1] * f1, acc[q * NB + j][2] * f0, acc[q * NB + j][3] * f1);
         }
-        if (it.slot >= 0 && w == 0 && (lane & 3) == 0) {
+#pragma unroll
+        for (int from = 0; from < 3; ++from) {
+          const float4 x = sSum[((w * 3 + from) * NB + j) * 32 + lane];
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        const int ch = (w * NB + j) * 16;
+        if (ch >= a.d) break;
+        if (it.slot < 0) {
+          const bool sees0 = n > 0 && limit[0] > 0, sees1 = n > 0 && limit[1] > 0;
+          const float inv0 = 1.f / sum[0], inv1 = 1.f / sum[1];
+          const uint32_t x0 = transpose8(pack_bf16(sees0 ? v.x * inv0 : 0.f, sees1 ? v.y * inv1 : 0.f));
+          const uint32_t x1 = transpose8(pack_bf16(sees0 ? v.z * inv0 : 0.f, sees1 ? v.w * inv1 : 0.f));
+          if (my_row < rows) {
+            __nv_bfloat16* o =
+                a.o + (it.q_row + my_tok) * a.ld_o + static_cast<long long>(my_head) * a.d + ch + (lane & 3) * 2;
+            *reinterpret_cast<uint32_t*>(o) = x0;
+            *reinterpret_cast<uint32_t*>(o + 8) = x1;
+          }
+        } else {
+          float* part = a.part + (static_cast<long long>(it.slot) * a.slot_rows + col) * a.d + ch + (lane >> 2);
+          if (col < rows) part[0] = v.x, part[8] = v.z;
+          if (col + 1 < rows) part[a.d] = v.y, part[a.d + 8] = v.w;
+        }
+      }
+      if (it.slot >= 0 && w == 0 && lane < 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           const bool any = limit[i] > it.t_begin * kFrKeys;
-          a.part_cl[at] = make_float2(any && top[i] == kNegInf ? kNoScore : top[i], sum[i]);
+          if (col + i < rows)
+            a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + col + i] =
+                make_float2(any && top[i] == kNegInf ? kNoScore : top[i], sum[i]);
         }
       }
     }

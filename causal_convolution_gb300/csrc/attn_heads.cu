@@ -605,25 +605,20 @@ constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __grid_constant__ AhArgs a, int ctas) {
   __shared__ float sO[8][128];
-  __shared__ float sL[8];
+  __shared__ float2 sL[8];  // (c, l)
   pdl_launch_dependents();
   pdl_wait();
   const int first = blockIdx.x;
   const int4 head = a.meta[2 * first + 1];
   if (head.x == 0) return;
   // pieces: slot 1 of `first`, then slot 0 of the CTAs behind it up to the one that ends the item
-  int pieces = 1;
-  for (int j0 = first + 1;; j0 += 32) {
-    const int j = j0 + (threadIdx.x & 31);
-    const bool ends = j >= ctas || a.meta[2 * j].x != 1;
-    const unsigned hit = __ballot_sync(0xffffffffu, ends);
-    if (hit) {
-      pieces += __ffs(hit);
-      break;
-    }
-    pieces += 32;
+  int ends = ctas;
+#pragma unroll
+  for (int i = 0; i < (kAhMaxCtas + 31) / 32; ++i) {
+    const int j = first + 1 + i * 32 + (threadIdx.x & 31);
+    if (j < ctas && a.meta[2 * j].x != 1) ends = min(ends, j);
   }
-  pieces = min(pieces, ctas - first);
+  const int pieces = min(__reduce_min_sync(0xffffffffu, ends) + 1, ctas) - first;
   const int q_row = head.y, tokens = head.z, h = head.w;
   const bool two = tokens > a.tq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -636,34 +631,50 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
     const int tok = static_cast<int>(quotient(i, a.inv_group)), g = i - tok * a.group;
     const int r = two && tok >= a.tq ? kAhHalf + (tok - a.tq) * a.group + g : i;
     auto slot_of = [&](int p) { return static_cast<long long>(p == 0 ? 2 * first + 1 : 2 * (first + p)) * a.slot_rows + r; };
-    float top = kNegInf;
-    for (int p = lane; p < pieces; p += 32) top = fmaxf(top, a.part_cl[slot_of(p)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float top = kNegInf, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
     const bool on = lane * 4 < a.d;
-#pragma unroll 4
-    for (int p = shared_rows ? warp : 0; p < pieces; p += shared_rows ? 8 : 1) {
-      const long long at = slot_of(p);
-      const float2 cl = a.part_cl[at];
-      const float4 v = on ? *reinterpret_cast<const float4*>(a.part + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float f = pow2_diff(cl.x, top);
-      l = fmaf(cl.y, f, l);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
+    const int by = shared_rows ? 8 : 1;
+    for (int p0 = shared_rows ? warp : 0; p0 < pieces; p0 += 8 * by) {  // eight pieces in flight
+      float2 cl[8];
+      float4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int p = p0 + e * by;
+        const long long at = slot_of(min(p, pieces - 1));
+        cl[e] = p < pieces ? a.part_cl[at] : make_float2(kNegInf, 0.f);
+        v[e] = p < pieces && on ? *reinterpret_cast<const float4*>(a.part + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float up = top;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) up = fmaxf(up, cl[e].x);
+      const float old = pow2_diff(top, up);
+      l *= old;
+      acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+      top = up;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = pow2_diff(cl[e].x, top);
+        l = fmaf(cl[e].y, f, l);
+        acc.x = fmaf(v[e].x, f, acc.x);
+        acc.y = fmaf(v[e].y, f, acc.y);
+        acc.z = fmaf(v[e].z, f, acc.z);
+        acc.w = fmaf(v[e].w, f, acc.w);
+      }
     }
     if (shared_rows) {
       *reinterpret_cast<float4*>(&sO[warp][lane * 4]) = acc;
-      if (lane == 0) sL[warp] = l;
+      if (lane == 0) sL[warp] = make_float2(top, l);
       __syncthreads();
       if (warp == 0) {
-        for (int w = 1; w < 8; ++w) {
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, sL[w].x);
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < 8; ++w) {
+          const float f = pow2_diff(sL[w].x, top);
           const float4 v = *reinterpret_cast<const float4*>(&sO[w][lane * 4]);
-          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-          l += sL[w];
+          acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+          l = fmaf(sL[w].y, f, l);
         }
       }
       __syncthreads();
@@ -698,7 +709,7 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
   return CC_OK;
 }
 
-constexpr int kFewRows = 16;       // query rows of an item of the few-rows kernel
+constexpr int kFewRows = 8;        // query rows of an item of the few-rows kernel
 constexpr int kFewTileShift = 6;   // its tiles: 64 keys
 constexpr int kFewSplitCost = 6;
 
