@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           of_ph ^= 1u;
         }
         used = true;
-        ok = ok && warp_wait(&p_ready[s], p_ph, a) && turn(job + firsts + j);
+        ok = ok && turn(job + firsts + j) && warp_wait(&p_ready[s], p_ph, a);
         if (!ok) break;
         p_ph ^= 1u;
         const uint32_t bd = v0 + vs * (Sm::kTile >> 4);
@@ -399,15 +399,17 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       // A warp whose wait ran out goes through the rest of its item without waiting, as its mate counts on it at the
       // barriers, and both leave together here.
       if (!named_barrier_and(mates, 64, ok && warp_wait(&item_full[slot], it_ph, a))) break;
-      const AhItem it = items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
-      if (++slot == kAhItems) {
-        slot = 0;
-        it_ph ^= 1u;
-      }
+      const AhItem& it = items[slot];
       if (it.last) break;
-      const int n = it.t_end - it.t_begin;
+      auto release = [&]() {  // of the descriptor
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
+        if (++slot == kAhItems) {
+          slot = 0;
+          it_ph ^= 1u;
+        }
+      };
+      const int t_begin = it.t_begin, n = it.t_end - t_begin;
       const bool two = it.tokens > a.tq;
       const int tok = (two ? s * a.tq : 0) + row_tok;  // of the item
       const bool row_ok = row < a.tq * a.group && tok < it.tokens;
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
       float c = kNegInf, l = 0.f;
       for (int i = 0; i < mine; ++i) {
-        const int t = it.t_begin + (two ? i : 2 * i + s);
+        const int t = t_begin + (two ? i : 2 * i + s);
         ok = ok && warp_wait(&s_ready[s], s_ph, a);
         s_ph ^= 1u;
         if (active) {
@@ -505,6 +507,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(cl_ready));
         }
+        release();
         continue;
       }
       float c1 = kNegInf, l1 = 0.f;
@@ -586,6 +589,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           if (other > 0) mbar_arrive(smem_u32(&o_free[1]));
         }
       }
+      release();
     }
   }
 
