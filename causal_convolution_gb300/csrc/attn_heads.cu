@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       if (n > 0) {
         const bool two = it.tokens > a.tq;
         const int ahead = two ? 1 : 2;  // a tile of scores ahead in each stream
-        for (int t = 0; ok && t < min(ahead, n); ++t) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t);
+        for (int t = 0; ok && t < min(ahead, n); ++t) ok = load_tile(&tmK, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
         if (!ok) break;
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_empty), q_ph ^ 1u, a.err, tlim))) {
           ok = false;
@@ -218,8 +218,9 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         }
         __syncwarp();
         for (int t = 0; ok && t < n; ++t) {
-          ok = load_tile(&tmV, it.seq, it.head, it.len, it.t_begin + t);
-          if (ok && t + ahead < n) ok = load_tile(&tmK, it.seq, it.head, it.len, it.t_begin + t + ahead);
+          ok = load_tile(&tmV, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
+          if (ok && t + ahead < n)
+            ok = load_tile(&tmK, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t + ahead));
         }
       }
       r.at += static_cast<unsigned>(max(1, n));
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     while (true) {
       if (!warp_wait(&item_full[slot], it_ph, a)) break;
       const AhItem* it = &items[slot];
-      const int last = uniform(it->last), t_begin = uniform(it->t_begin), len = uniform(it->len);
+      const int last = uniform(it->last), t_begin = uniform(it->t_begin), len = uniform(it->len), from = uniform(it->turn);
       const int n = uniform(it->t_end) - t_begin;
       const bool two = uniform(it->tokens) > a.tq;
       __syncwarp();
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         const int vs = next_tile();
         ok = vs >= 0;
         if (!ok) break;
-        const int valid = len - (t_begin + i) * kAhKeys;
+        const int valid = len - tile_of(t_begin, n, from, i) * kAhKeys;
         if (valid < kAhKeys) {
           // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
           uint8_t* base = sKV + vs * Sm::kTile;
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           it_ph ^= 1u;
         }
       };
-      const int t_begin = it.t_begin, n = it.t_end - t_begin;
+      const int t_begin = it.t_begin, n = it.t_end - t_begin, from = it.turn;
       const bool two = it.tokens > a.tq;
       const int tok = (two ? s * a.tq : 0) + row_tok;  // of the item
       const bool row_ok = row < a.tq * a.group && tok < it.tokens;
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
       float c = kNegInf, l = 0.f;
       for (int i = 0; i < mine; ++i) {
-        const int t = t_begin + (two ? i : 2 * i + s);
+        const int t = tile_of(t_begin, n, from, two ? i : 2 * i + s);
         ok = ok && warp_wait(&s_ready[s], s_ph, a);
         s_ph ^= 1u;
         if (active) {

@@ -71,6 +71,7 @@ struct __align__(16) AhItem {
   int slot;         // partial slot, -1: the whole item
   int seq;
   int last;         // no item: the CTA is done
+  int turn;         // the piece's tiles are taken from t_begin + turn on, around its end
 };
 
 struct Seq {
@@ -155,7 +156,7 @@ __device__ __forceinline__ unsigned seq_units(const AhArgs& a, const Seq& s, int
 // A CTA's run of units [at, end) and where it stands: sequence, item, head and
 // tile. All lanes of a warp hold the same values.
 struct Run {
-  unsigned at, end;
+  unsigned at, end, start;
   bool split;
   int b;
   Seq s;
@@ -205,7 +206,7 @@ __device__ __forceinline__ bool find_run(const AhArgs& a, int cta, int ctas, int
       const float whole = fmaxf(static_cast<float>(top), static_cast<float>(quotient(items + ctas - 1, a.inv_ctas)) *
                                                              __fdividef(static_cast<float>(units), static_cast<float>(items)));
       r.split = a.may_split && whole > static_cast<float>(per + a.split_cost);
-      r.at = cta * per;
+      r.at = r.start = cta * per;
       r.end = min(units, r.at + per);
       if (r.at >= units) return false;
     } else {
@@ -299,12 +300,26 @@ __device__ __forceinline__ AhItem make_item(const AhArgs& a, const Run& r, int l
   it.t_all = r.tiles;
   it.t_begin = r.t;
   it.t_end = r.split ? min(it.t_all, r.t + static_cast<int>(r.end - r.at)) : it.t_all;
+  // CTAs whose items have the same keys take the same tile at about the same time, so that it is read from memory
+  // once: each goes on from where its number of tiles so far points to.
+  it.turn = 0;
+  if (it.t_end > it.t_begin) {
+    const unsigned done = r.at - r.start, all = static_cast<unsigned>(it.t_all);
+    const int here = static_cast<int>(done % all) - it.t_begin;
+    if (here > 0 && here < it.t_end - it.t_begin) it.turn = here;
+  }
   it.slot = -1;
   if (it.t_begin > 0 || it.t_end < it.t_all) {
     it.slot = 2 * blockIdx.x + (it.t_begin > 0 ? 0 : 1);
     if (lane == 0) a.meta[it.slot] = make_int4(it.t_end < it.t_all ? 1 : 2, it.q_row, it.tokens, it.head);
   }
   return it;
+}
+
+// The tile that a piece takes as its i-th.
+__device__ __forceinline__ int tile_of(int t_begin, int n, int turn, int i) {
+  const int at = i + turn;
+  return t_begin + (at >= n ? at - n : at);
 }
 
 // Launches the kernel for few rows to a sequence (attn_few_rows.cu).
