@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       next_item(a, r);
     }
     if (!ok) {  // copies in flight land before the CTA goes
+#pragma unroll 1
       for (int i = 0; i < STAGES; ++i)
         (void)mbar_wait(smem_u32(&full[i]), (i < stage) ? ph : (ph ^ 1u), a.err, 200000000ull);
     }

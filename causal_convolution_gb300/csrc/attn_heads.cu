@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  const uint64_t tlim = a.timeout_ns;
 
   if (warp == kAhTmaWarp) {
     // -------------------------------------------- run, items and TMA loads --
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           page = a.plan.pages;  // out of the map's range: the box reads as zeros
         }
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_empty[stage]), kv_ph ^ 1u, a.err, tlim))) return false;
+      if (!warp_wait(&kv_empty[stage], kv_ph ^ 1u, a)) return false;
       const uint32_t full = smem_u32(&kv_full[stage]);
       if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * a.box * 128 * NB));
       __syncwarp();
@@ -180,7 +179,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     }
     while (ok) {
       const bool more = any && r.at < r.end && r.b < a.plan.seqs;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&item_empty[slot]), it_ph ^ 1u, a.err, tlim))) {
+      if (!warp_wait(&item_empty[slot], it_ph ^ 1u, a)) {
         ok = false;
         break;
       }
@@ -201,9 +200,11 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       if (n > 0) {
         const bool two = it.tokens > a.tq;
         const int ahead = two ? 1 : 2;  // a tile of scores ahead in each stream
-        for (int t = 0; ok && t < min(ahead, n); ++t) ok = load_tile(&tmK, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
+#pragma unroll 1
+        for (int t = 0; ok && t < min(ahead, n); ++t)
+          ok = load_tile(&tmK, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
         if (!ok) break;
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(q_empty), q_ph ^ 1u, a.err, tlim))) {
+        if (!warp_wait(q_empty, q_ph ^ 1u, a)) {
           ok = false;
           break;
         }
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
                           it.q_row + s * a.tq, 0);
         }
         __syncwarp();
+#pragma unroll 1
         for (int t = 0; ok && t < n; ++t) {
           ok = load_tile(&tmV, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
           if (ok && t + ahead < n)
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       next_item(a, r);
     }
     if (!ok) {  // copies in flight land before the CTA goes
+#pragma unroll 1
       for (int i = 0; i < STAGES; ++i)
         (void)mbar_wait(smem_u32(&kv_full[i]), (i < stage) ? kv_ph : (kv_ph ^ 1u), a.err, 200000000ull);
       (void)mbar_wait(smem_u32(q_full), q_ph ^ 1u, a.err, 200000000ull);
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       __syncwarp();
       // the tiles come as k of each stream's first, then v of each with k of the one that far ahead
       const int ahead = two ? 1 : 2;
+#pragma unroll 1
       for (int i = 0; ok && i < min(ahead, n); ++i) {
         if (!two && i != s) {
           ok = skip_tile();
@@ -323,6 +327,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         scores(half, ks, s + 2 >= jobs);
         issued(job + s);
       }
+#pragma unroll 1
       for (int i = 0; ok && i < n; ++i) {
         const bool more = i + ahead < n;
         if (!two && (i & 1) != s) {
@@ -337,6 +342,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         if (valid < kAhKeys) {
           // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
           uint8_t* base = sKV + vs * Sm::kTile;
+#pragma unroll 1
           for (int e = lane; e < (kAhKeys - valid) * 8; e += 32) {
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk)
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     }
     if (elect_one()) mma_commit(smem_u32(done));
     __syncwarp();
-    (void)mbar_wait(smem_u32(done), 0, a.err, tlim);
+    (void)warp_wait(done, 0, a);
   } else {
     // -------------------------------------------------------------- softmax --
     const int s = warp >> 3;         // stream
@@ -418,6 +424,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const bool active = __any_sync(0xffffffffu, row_ok);
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
       float c = kNegInf, l = 0.f;
+#pragma unroll 1
       for (int i = 0; i < mine; ++i) {
         const int t = tile_of(t_begin, n, from, two ? i : 2 * i + s);
         ok = ok && warp_wait(&s_ready[s], s_ph, a);
@@ -455,6 +462,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
               if (__any_sync(0xffffffffu, top != c)) {
                 const float f = pow2_diff(c, top);
                 if (i > 0) {
+#pragma unroll 1
                   for (int col = hf * 16; col < a.d; col += 32) {
                     uint32_t o[16];
                     tmem_ld16(o_col + col, o);
@@ -794,7 +802,6 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   if ((st = device_info(&di)) != CC_OK) return st;
   a.err = di.err_word;
   a.device = di.device;
-  a.timeout_ns = kWaitLimitNs;
   CUtensorMap tk = {}, tv = {};
   if (keys > 0 && ((st = encode_side(&tk, k, a)) != CC_OK || (st = encode_side(&tv, v, a)) != CC_OK)) return st;
   const int grid = std::min(kAhMaxCtas, 2 * di.sm_count) / (few ? 1 : 2);

@@ -48,7 +48,6 @@ struct AhArgs {
   int4* meta;       // [2 * ctas]: 0 unused, 1 goes on, 2 ends its item; first row, tokens, head
   unsigned int* err;
   int device;
-  unsigned long long timeout_ns;
   // ceil(2^64 / divisor) for quotient(): CTAs, tokens of an item, the causal block, heads of a group
   unsigned long long inv_ctas, inv_tokens, inv_block, inv_group;
 };
@@ -276,14 +275,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
-// mbar_wait for a whole warp, with a few tries before the first look at the
-// clock, whose latency would come on top of a wait that is nearly over.
+// A whole warp's wait for a phase of an mbarrier, of about two seconds at most.
+// There are many of these and the instruction cache is small, so it is a loop of
+// few instructions that looks at the low half of the SM's clock alone (a try
+// returns within far less than the part of its range that is left).
+constexpr uint32_t kAhWaitClocks = 0xf0000000u;
+__device__ __forceinline__ uint32_t clock_low() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, const AhArgs& a) {
-  const uint32_t at = smem_u32(bar);
-  for (int i = 0; i < 16; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+  const uint32_t at = smem_u32(bar), since = clock_low();
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_try_wait(at, parity))) {
+    if (__any_sync(0xffffffffu, clock_low() - since > kAhWaitClocks)) {
+      atomicOr(a.err, DEVERR_TIMEOUT);
+      return false;
+    }
   }
-  return __all_sync(0xffffffffu, mbar_wait(at, parity, a.err, a.timeout_ns));
+  return true;
 }
 
 // The piece of an item at the head of a run; says in the workspace's directory
