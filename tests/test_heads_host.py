@@ -116,6 +116,31 @@ def test_attention_refusals(lib, p):
     assert call(lib, "cc_attn_cross", CROSS, None, lq=0)[0] == 0
 
 
+def test_attention_workspaces(lib, p):
+    paged, cross = lib.cc_attn_paged_workspace_bytes, lib.cc_attn_cross_workspace_bytes
+    part = lambda slots, rows, d: slots * (rows * (4 * d + 8) + 16)  # sums, (c, l) and a directory entry to a slot
+    assert paged(1, 1, 8, 1, 128) == part(608, 8, 128)          # few rows: eight to a slot, two CTAs to an SM
+    assert paged(2, 1, 8, 1, 128) == part(304, 16, 128)
+    assert paged(1, 1, 9, 1, 64) == part(304, 9, 64)
+    assert paged(1000, 2, 9, 1, 64) == part(304, 256, 64)
+    assert cross(2, 9, 513, 4, 4, 48) == part(304, 9, 48)
+    assert cross(2, 9, 512, 4, 4, 48) == 0                      # nothing is cut
+    assert cross(2, 8, 385, 4, 4, 48) == part(608, 8, 48) and cross(2, 8, 384, 4, 4, 48) == 0
+    for sizes in ((0, 1, 8, 1, 64), (1, 0, 8, 1, 64), (-1, 1, 8, 1, 64), (1, 1, 3, 2, 64), (1, 1, 8, 0, 64),
+                  (1, 1, 129, 1, 64), (1, 1, 8, 1, 72), (1, 1, 8, 1, 144), (1, 1, 8, 1, 0)):
+        assert paged(*sizes) == 0
+    assert cross(0, 1, 999, 1, 1, 64) == 0 and cross(1, -1, 999, 1, 1, 64) == 0
+    need = paged(4, 2, 4, 2, 64)
+    many = dict(max_pages=25)  # 400 keys: tiles enough to cut
+    refusals(lib, p, "cc_attn_paged", PAGED, [
+        (dict(ws=None, **many), 1, "null workspace"), (dict(ws=p + 8, **many), 1, "aligned"),
+        (dict(ws_bytes=need - 1, **many), 1, "workspace of"), (dict(ws_bytes=0, **many), 1, "workspace of"),
+        (dict(rows=1 << 30, max_pages=1 << 20), 2, "2^31 tiles")])
+    refusals(lib, p, "cc_attn_cross", CROSS, [
+        (dict(ws=None, lk=385), 1, "null workspace"), (dict(ws_bytes=8, lk=385), 1, "workspace of"),
+        (dict(n=1 << 15, lq=1 << 15, lk=1 << 20), 2, "2^31 tiles"), (dict(ld_k=1 << 30, lk=1 << 10), 2, "2^38")])
+
+
 # ------------------------------------------------------------------------------------------------------- binding --
 
 def i32(*shape):
