@@ -76,6 +76,10 @@ __global__ void __launch_bounds__(kFrThreads, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    if (a.plan.page_size > 0) {  // there are keys, and maps of them
+      tma_prefetch_map(&tmK);
+      tma_prefetch_map(&tmV);
+    }
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
       mbar_init(smem_u32(&empty[i]), 4);

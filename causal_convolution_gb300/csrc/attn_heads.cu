@@ -104,6 +104,13 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if (warp == kAhTmaWarp && lane == 0) {
+    tma_prefetch_map(&tmQ);
+    if (a.plan.page_size > 0) {  // there are keys, and maps of them
+      tma_prefetch_map(&tmK);
+      tma_prefetch_map(&tmV);
+    }
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&kv_full[i]), 1);
@@ -623,14 +630,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
   pdl_wait();
   const int first = blockIdx.x;
   const int4 head = a.meta[2 * first + 1];
-  if (head.x == 0) return;
-  // pieces: slot 1 of `first`, then slot 0 of the CTAs behind it up to the one that ends the item
+  // pieces: slot 1 of `first`, then slot 0 of the CTAs behind it up to the one that ends the item (all entries are
+  // asked for at once)
   int ends = ctas;
 #pragma unroll
   for (int i = 0; i < (kAhMaxCtas + 31) / 32; ++i) {
     const int j = first + 1 + i * 32 + (threadIdx.x & 31);
     if (j < ctas && a.meta[2 * j].x != 1) ends = min(ends, j);
   }
+  if (head.x == 0) return;
   const int pieces = min(__reduce_min_sync(0xffffffffu, ends) + 1, ctas) - first;
   const int q_row = head.y, tokens = head.z, h = head.w;
   const bool two = tokens > a.tq;
@@ -730,16 +738,17 @@ constexpr int kFewSplitCost = 6;
 // cache. (The other one takes 128 rows of a key head at once.)
 bool few_rows(int64_t rows, int64_t seqs, int group) { return group <= kFewRows && rows * group <= kFewRows * seqs; }
 
-// Rows that a partial slot holds: those of a half where no item can have more.
-int slot_rows(int64_t tokens, int group) {
-  const int tq = kAhHalf / group;
-  return tokens <= tq ? static_cast<int>(tokens) * group : 2 * kAhHalf;
+// Rows that a partial slot holds: those of all tokens where an item (of the
+// kernel for few rows) or half of one has room for them.
+int slot_rows(bool few, int64_t tokens, int group) {
+  const int tq = (few ? kFewRows : kAhHalf) / group;
+  return tokens <= tq ? static_cast<int>(tokens) * group : few ? kFewRows : 2 * kAhHalf;
 }
 
 size_t part_bytes(int ctas, int rows, int d) { return (size_t)2 * ctas * rows * d * 4; }
 
 size_t workspace_bytes(bool few, int64_t tokens, int group, int d) {
-  const int ctas = few ? kAhMaxCtas : kAhMaxCtas / 2, rows = few ? kFewRows : slot_rows(tokens, group);
+  const int ctas = few ? kAhMaxCtas : kAhMaxCtas / 2, rows = slot_rows(few, tokens, group);
   return part_bytes(ctas, rows, d) + (size_t)2 * ctas * (rows * 8 + 16);
 }
 
@@ -786,7 +795,7 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   if (((a.rows / a.item_tokens + (int64_t)a.plan.seqs) * a.kv_heads) * (double)tiles >= 0x1p31)
     return fail(CC_ERR_UNSUPPORTED, "%s: rows, heads and keys make 2^31 tiles or more", what);
   a.may_split = tiles > a.split_cost;
-  a.slot_rows = few ? kFewRows : slot_rows(max_tokens, a.group);
+  a.slot_rows = slot_rows(few, max_tokens, a.group);
   DeviceInfo di;
   cc_status st;
   if (a.may_split) {
