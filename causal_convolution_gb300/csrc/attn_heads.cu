@@ -40,7 +40,8 @@ namespace {
 
 constexpr int kAhTmaWarp = 16;    // behind 16 softmax warps
 constexpr int kAhMmaWarp = 17;    // and 18, one for each stream
-constexpr int kAhThreads = 608;
+constexpr int kAhValueWarp = 19;  // the second TMA warp, for values
+constexpr int kAhThreads = 640;
 constexpr int kAhTileShift = 7;
 constexpr int kAhKeys = 1 << kAhTileShift;  // keys per tile, in two halves for the softmax
 constexpr int kAhHalf = 128;      // rows per half
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     }
     for (int i = 0; i < kAhItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_empty[i]), 18);
+      mbar_init(smem_u32(&item_empty[i]), 19);
     }
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(q_empty), 2);
@@ -144,16 +145,18 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
 
-  if (warp == kAhTmaWarp) {
+  if (warp == kAhTmaWarp || warp == kAhValueWarp) {
     // -------------------------------------------- run, items and TMA loads --
-    Run r;
-    bool ok = true, any = find_run(a, blockIdx.x, gridDim.x, lane, r);
-    if (a.may_split && lane < 2) a.meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
-    __syncwarp();
+    // One warp finds the run, publishes its items and loads q and keys, the other one loads values: a box of a small
+    // page takes a warp longer to ask for than the tensor cores need for its 16 keys.
+    const bool keys = warp == kAhTmaWarp;
+    const CUtensorMap* map = keys ? &tmK : &tmV;
+    Run r = {};
+    bool ok = true, any = false;
     int stage = 0, slot = 0;
     uint32_t kv_ph = 0, it_ph = 0, q_ph = 0;
     // one tile of keys (or values): a box per piece of a page, a lane to a box
-    auto load_tile = [&](const CUtensorMap* map, int b, int h, int len, int t) {
+    auto load_tile = [&](int b, int h, int len, int t) {
       const int boxes = (min(kAhKeys, len - t * kAhKeys) + a.box - 1) / a.box;
       int page = b, at = t * kAhKeys + lane * a.box;
       if (lane < boxes && a.plan.page_table) {
@@ -174,66 +177,73 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 #pragma unroll
         for (int i = 0; i < NB; ++i) tma_load_4d(dst + i * kAhKvBlock, map, full, i * 64, h, at, page);
       }
-      if (++stage == STAGES) {
-        stage = 0;
-        kv_ph ^= 1u;
-      }
       return true;
     };
-    if (any && !r.split && r.t > 0) {  // whole items: from the first one that starts in the run
-      r.at += max(1, r.tiles) - r.t;
-      next_item(a, r);
+    if (keys) {
+      any = find_run(a, blockIdx.x, gridDim.x, lane, r);
+      if (a.may_split && lane < 2) a.meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+      __syncwarp();
+      if (any && !r.split && r.t > 0) {  // whole items: from the first one that starts in the run
+        r.at += max(1, r.tiles) - r.t;
+        next_item(a, r);
+      }
     }
     while (ok) {
-      const bool more = any && r.at < r.end && r.b < a.plan.seqs;
-      if (!warp_wait(&item_empty[slot], it_ph ^ 1u, a)) {
-        ok = false;
-        break;
+      ok = warp_wait(keys ? &item_empty[slot] : &item_full[slot], keys ? it_ph ^ 1u : it_ph, a);
+      if (!ok) break;
+      if (keys) {
+        AhItem it = {};
+        it.last = !(any && r.at < r.end && r.b < a.plan.seqs);
+        if (!it.last) it = make_item(a, r, lane);
+        if (lane == 0) {
+          items[slot] = it;
+          mbar_arrive(smem_u32(&item_full[slot]));  // releases the descriptor
+        }
+        __syncwarp();
       }
-      AhItem it = {};
-      it.last = !more;
-      if (more) it = make_item(a, r, lane);
-      if (lane == 0) {
-        items[slot] = it;
-        mbar_arrive(smem_u32(&item_full[slot]));  // releases the descriptor
-      }
+      const int last = uniform(items[slot].last), t_begin = uniform(items[slot].t_begin), seq = uniform(items[slot].seq);
+      const int head = uniform(items[slot].head), len = uniform(items[slot].len), from = uniform(items[slot].turn);
+      const int n = uniform(items[slot].t_end) - t_begin, q_row = uniform(items[slot].q_row);
+      const bool two = uniform(items[slot].tokens) > a.tq;
       __syncwarp();
+      if (!keys && lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
       if (++slot == kAhItems) {
         slot = 0;
         it_ph ^= 1u;
       }
-      if (!more) break;
-      const int n = it.t_end - it.t_begin;
-      if (n > 0) {
-        const bool two = it.tokens > a.tq;
-        const int ahead = two ? 1 : 2;  // a tile of scores ahead in each stream
+      if (last) break;
+      // k of the first tiles, q, then v of each tile with k of the one that far ahead
+      const int ahead = two ? 1 : 2;  // a tile of scores ahead in each stream
 #pragma unroll 1
-        for (int t = 0; ok && t < min(ahead, n); ++t)
-          ok = load_tile(&tmK, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
-        if (!ok) break;
-        if (!warp_wait(q_empty, q_ph ^ 1u, a)) {
-          ok = false;
-          break;
-        }
-        q_ph ^= 1u;
-        if (lane == 0) {
-          const uint32_t full = smem_u32(q_full);
-          mbar_arrive_expect_tx(full, static_cast<uint32_t>((two ? 2 : 1) * NB * a.tq * a.group * 128));
-          for (int s = 0; s < (two ? 2 : 1); ++s)
-            for (int i = 0; i < NB; ++i)
-              tma_load_4d(smem_u32(sQ + s * Sm::kQHalf + i * kAhQBlock), &tmQ, full, i * 64, it.head * a.group,
-                          it.q_row + s * a.tq, 0);
-        }
-        __syncwarp();
+      for (int i = 0; ok && n > 0 && i < n + ahead; ++i) {
+        if (keys && i == min(ahead, n)) {
+          ok = warp_wait(q_empty, q_ph ^ 1u, a);
+          if (!ok) break;
+          q_ph ^= 1u;
+          if (lane == 0) {
+            const uint32_t full = smem_u32(q_full);
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>((two ? 2 : 1) * NB * a.tq * a.group * 128));
 #pragma unroll 1
-        for (int t = 0; ok && t < n; ++t) {
-          ok = load_tile(&tmV, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t));
-          if (ok && t + ahead < n)
-            ok = load_tile(&tmK, it.seq, it.head, it.len, tile_of(it.t_begin, n, it.turn, t + ahead));
+            for (int s = 0; s < (two ? 2 : 1); ++s)
+              for (int b = 0; b < NB; ++b)
+                tma_load_4d(smem_u32(sQ + s * Sm::kQHalf + b * kAhQBlock), &tmQ, full, b * 64, head * a.group,
+                            q_row + s * a.tq, 0);
+          }
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int kind = i >= ahead ? 0 : 1; ok && kind < (i < n ? 2 : 1); ++kind) {  // v, k
+          if ((kind != 0) == keys) ok = load_tile(seq, head, len, tile_of(t_begin, n, from, kind ? i : i - ahead));
+          if (++stage == STAGES) {
+            stage = 0;
+            kv_ph ^= 1u;
+          }
         }
       }
-      r.at += static_cast<unsigned>(max(1, n));
-      next_item(a, r);
+      if (keys) {
+        r.at += static_cast<unsigned>(max(1, n));
+        next_item(a, r);
+      }
     }
     if (!ok) {  // copies in flight land before the CTA goes
 #pragma unroll 1
