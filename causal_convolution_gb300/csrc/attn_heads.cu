@@ -628,43 +628,95 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 }
 
 // Joins the partial sums of cut items: o = sum_p 2^(c_p - c) O_p / sum_p
-// 2^(c_p - c) l_p over the pieces p of a row, c = max_p c_p. blockIdx.x: the CTA
-// whose run an item was cut out of first; its pieces go on in the slots 0 of the
-// CTAs behind it. Rows with many pieces are shared by the CTA's warps.
+// 2^(c_p - c) l_p over the pieces p of a row, c = max_p c_p. A CTA reads the
+// directory that the runs' CTAs left and shares the cut items out evenly over the
+// grid: an item cut at the end of run `first` has its first piece in that run's
+// slot 1 and goes on in the slots 0 of the runs behind it. A warp takes four rows
+// of an item of two pieces at once, else a row; where pieces are many, or CTAs
+// enough, a CTA's warps share a row.
 constexpr int kJoinThreads = 256;
+
+__device__ __forceinline__ void join_store(const AhArgs& a, int q_row, int h, int i, int lane, float top, float l, float4 v) {
+  const int tok = static_cast<int>(quotient(i, a.inv_group));
+  const float inv = 1.f / l;
+  const bool sees = top != kNegInf;
+  *reinterpret_cast<uint2*>(a.o + static_cast<long long>(q_row + tok) * a.ld_o +
+                            static_cast<long long>(h * a.group + i - tok * a.group) * a.d + lane * 4) =
+      sees ? make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)) : make_uint2(0u, 0u);
+}
 
 __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __grid_constant__ AhArgs a, int ctas) {
   __shared__ float sO[8][128];
   __shared__ float2 sL[8];  // (c, l)
+  constexpr int kWords = (kAhMaxCtas + 31) / 32;
+  __shared__ unsigned sCut[kWords], sOn[kWords];  // runs whose last item is cut; runs whose first item goes on behind them
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  const int first = blockIdx.x;
-  const int4 head = a.meta[2 * first + 1];
-  // pieces: slot 1 of `first`, then slot 0 of the CTAs behind it up to the one that ends the item (all entries are
-  // asked for at once)
-  int ends = ctas;
-#pragma unroll
-  for (int i = 0; i < (kAhMaxCtas + 31) / 32; ++i) {
-    const int j = first + 1 + i * 32 + (threadIdx.x & 31);
-    if (j < ctas && a.meta[2 * j].x != 1) ends = min(ends, j);
+  for (int w = warp; w < kWords; w += kJoinThreads / 32) {
+    const int j = w * 32 + lane;
+    const int cut_here = j < ctas ? a.meta[2 * j + 1].x : 0, on_here = j < ctas ? a.meta[2 * j].x : 0;
+    const unsigned cut = __ballot_sync(0xffffffffu, cut_here != 0), on = __ballot_sync(0xffffffffu, on_here == 1);
+    if (lane == 0) sCut[w] = cut, sOn[w] = on;
   }
-  if (head.x == 0) return;
-  const int pieces = min(__reduce_min_sync(0xffffffffu, ends) + 1, ctas) - first;
+  __syncthreads();
+  int items = 0;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) items += __popc(sCut[w]);
+  if (items == 0) return;
+  const int share = gridDim.x / items;  // CTAs of an item: at least one, as the grid has as many as there are runs
+  const int item = blockIdx.x / share, y = blockIdx.x - item * share;
+  if (item >= items) return;
+  // the item's first run, and the one that ends it
+  int at_word = 0, skip = item;
+  while (skip >= __popc(sCut[at_word])) skip -= __popc(sCut[at_word++]);
+  unsigned bits = sCut[at_word];
+  while (skip-- > 0) bits &= bits - 1;
+  const int first = at_word * 32 + __ffs(bits) - 1;
+  at_word = (first + 1) >> 5;
+  bits = at_word < kWords ? ~sOn[at_word] & ~0u << ((first + 1) & 31) : 1u;
+  while (bits == 0 && ++at_word < kWords) bits = ~sOn[at_word];
+  const int last = min(ctas - 1, at_word < kWords ? at_word * 32 + __ffs(bits) - 1 : ctas);
+  const int pieces = last - first + 1;
+  const int4 head = a.meta[2 * first + 1];
   const int q_row = head.y, tokens = head.z, h = head.w;
   const bool two = tokens > a.tq;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool shared_rows = pieces > 8;
   const int rows = tokens * a.group;
-  const int step = shared_rows ? gridDim.y : gridDim.y * 8;
-  for (int i0 = shared_rows ? blockIdx.y : blockIdx.y * 8; i0 < rows; i0 += step) {
+  // row i of an item in a piece's slot
+  auto slot_of = [&](int p, int i) {
+    const int tok = static_cast<int>(quotient(i, a.inv_group));
+    const int r = two && tok >= a.tq ? kAhHalf + i - a.tq * a.group : i;
+    return static_cast<long long>(p == 0 ? 2 * first + 1 : 2 * (first + p)) * a.slot_rows + r;
+  };
+  const bool on = lane * 4 < a.d;
+  if (pieces <= 2 && share * 8 < rows) {
+    for (int i0 = (y * 8 + warp) * 4; i0 < rows; i0 += share * 32) {
+      float2 cl[8];
+      float4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const long long at = slot_of(min(e & 1, pieces - 1), min(i0 + (e >> 1), rows - 1));
+        cl[e] = a.part_cl[at];
+        v[e] = on ? *reinterpret_cast<const float4*>(a.part + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        if (i0 + (e >> 1) >= rows || !on) continue;
+        const float top = fmaxf(cl[e].x, cl[e + 1].x);
+        const float f0 = pow2_diff(cl[e].x, top), f1 = pieces > 1 ? pow2_diff(cl[e + 1].x, top) : 0.f;
+        join_store(a, q_row, h, i0 + (e >> 1), lane, top, fmaf(cl[e].y, f0, cl[e + 1].y * f1),
+                   make_float4(fmaf(v[e].x, f0, v[e + 1].x * f1), fmaf(v[e].y, f0, v[e + 1].y * f1),
+                               fmaf(v[e].z, f0, v[e + 1].z * f1), fmaf(v[e].w, f0, v[e + 1].w * f1)));
+      }
+    }
+    return;
+  }
+  const bool shared_rows = pieces > 8 || share >= rows;
+  for (int i0 = shared_rows ? y : y * 8; i0 < rows; i0 += shared_rows ? share : share * 8) {
     const int i = shared_rows ? i0 : i0 + warp;
     if (!shared_rows && i >= rows) break;
-    const int tok = static_cast<int>(quotient(i, a.inv_group)), g = i - tok * a.group;
-    const int r = two && tok >= a.tq ? kAhHalf + (tok - a.tq) * a.group + g : i;
-    auto slot_of = [&](int p) { return static_cast<long long>(p == 0 ? 2 * first + 1 : 2 * (first + p)) * a.slot_rows + r; };
     float top = kNegInf, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool on = lane * 4 < a.d;
     const int by = shared_rows ? 8 : 1;
     for (int p0 = shared_rows ? warp : 0; p0 < pieces; p0 += 8 * by) {  // eight pieces in flight
       float2 cl[8];
@@ -672,7 +724,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int p = p0 + e * by;
-        const long long at = slot_of(min(p, pieces - 1));
+        const long long at = slot_of(min(p, pieces - 1), i);
         cl[e] = p < pieces ? a.part_cl[at] : make_float2(kNegInf, 0.f);
         v[e] = p < pieces && on ? *reinterpret_cast<const float4*>(a.part + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -710,13 +762,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
       }
       __syncthreads();
     }
-    if (on && (!shared_rows || warp == 0)) {
-      const float inv = 1.f / l;
-      const bool sees = top != kNegInf;
-      *reinterpret_cast<uint2*>(a.o + static_cast<long long>(q_row + tok) * a.ld_o +
-                                static_cast<long long>(h * a.group + g) * a.d + lane * 4) =
-          sees ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv)) : make_uint2(0u, 0u);
-    }
+    if (on && (!shared_rows || warp == 0)) join_store(a, q_row, h, i, lane, top, l, acc);
   }
 }
 
@@ -839,9 +885,9 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
     st = a.d > 64 ? launch_attn<2, 4>(what, tq, tk, tv, a, grid, cs) : launch_attn<1, 8>(what, tq, tk, tv, a, grid, cs);
   }
   if (st != CC_OK || !a.may_split) return st;
-  // the joining kernel's CTAs: a row to each where few items are cut into many pieces, else eight
-  const int join_y = a.slot_rows <= 32 ? a.slot_rows : a.slot_rows / 8;
-  const cudaError_t e = launch_pdl(attn_heads_join_kernel, dim3(grid, join_y), dim3(kJoinThreads), 0, cs, a, grid);
+  // the joining kernel's CTAs: as many as give each of their warps four rows of an item to each run
+  const int join = grid * ((a.slot_rows + 31) / 32);
+  const cudaError_t e = launch_pdl(attn_heads_join_kernel, dim3(join), dim3(kJoinThreads), 0, cs, a, grid);
   if (e != cudaSuccess) return fail(CC_ERR_CUDA, "%s: launch: %s", what, cudaGetErrorString(e));
   return launch_status(what);
 }
