@@ -49,7 +49,7 @@ constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 chann
 constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
 constexpr float kAhRoom = 1048576.f;  // 2^20: what half a tile's weights of a row may come to before its scale moves
 constexpr float kAhMove = 8.f;        // and by how many powers of two at least
-constexpr int kAhSplitCost = 4;  // measured: the partial sums' way through L2 and the joining kernel
+constexpr int kAhSplitCost = 12;
 
 // A value that all lanes hold, said in a way that the compiler keeps it in
 // uniform registers.
@@ -596,8 +596,19 @@ __global__ void __launch_bounds__(kAhThreads, 1)
             }
           } else if (row_ok) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(a.part + my_row + col + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            for (int e = 0; e < 16; e += 8) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                v[b] = make_uint4(__float_as_uint(x[e + 4 * b]), __float_as_uint(x[e + 4 * b + 1]),
+                                  __float_as_uint(x[e + 4 * b + 2]), __float_as_uint(x[e + 4 * b + 3]));
+              uint4* dst = reinterpret_cast<uint4*>(a.part + my_row + col + e);
+              if (a.part_sectors) {
+                st_global_v8(dst, v);
+              } else {
+                dst[0] = v[0];
+                dst[1] = v[1];
+              }
+            }
           }
           __syncwarp();
         }
@@ -711,7 +722,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
     }
     return;
   }
-  const bool shared_rows = pieces > 8 || share >= rows;
+  // rounds of loads that a row to a warp, and a row to a CTA take
+  const int alone = (rows + share * 8 - 1) / (share * 8) * ((pieces + 7) / 8);
+  const int together = (rows + share - 1) / share * ((pieces + 63) / 64);
+  const bool shared_rows = together <= alone;
   for (int i0 = shared_rows ? y : y * 8; i0 < rows; i0 += shared_rows ? share : share * 8) {
     const int i = shared_rows ? i0 : i0 + warp;
     if (!shared_rows && i >= rows) break;
@@ -861,6 +875,7 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
     if (ws_bytes < need) return fail(CC_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", what, ws_bytes, need);
     const int ctas = few ? kAhMaxCtas : kAhMaxCtas / 2;
     a.part = static_cast<float*>(ws);
+    a.part_sectors = reinterpret_cast<uintptr_t>(ws) % 32 == 0;
     a.part_cl = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_bytes(ctas, a.slot_rows, a.d));
     a.meta = reinterpret_cast<int4*>(a.part_cl + (size_t)2 * ctas * a.slot_rows);
   }

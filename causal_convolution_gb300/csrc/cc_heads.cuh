@@ -38,7 +38,7 @@ struct AhArgs {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   long long ld_q, ld_o;
-  int o_sectors;    // rows of o start on 32-byte borders
+  int o_sectors, part_sectors;  // rows of o, of partial sums start on 32-byte borders
   float kx;         // scale * log2(e)
   unsigned block;   // causal block, 0: none
   int may_split;
@@ -201,10 +201,15 @@ __device__ __forceinline__ bool find_run(const AhArgs& a, int cta, int ctas, int
       items = __reduce_add_sync(0xffffffffu, items);
       top = __reduce_max_sync(0xffffffffu, top);
       const unsigned per = max(2u, quotient(units + ctas - 1, a.inv_ctas));
-      // what the longest run would be with whole items (all of them of the average's size), against cut ones
-      const float whole = fmaxf(static_cast<float>(top), static_cast<float>(quotient(items + ctas - 1, a.inv_ctas)) *
-                                                             __fdividef(static_cast<float>(units), static_cast<float>(items)));
-      r.split = a.may_split && whole > static_cast<float>(per + a.split_cost);
+      // What the longest run would be with whole items: as many of the average's size as come to a CTA, at least the
+      // largest one; where sequences differ, a large item may start behind small ones. Against it cut ones, whose
+      // partial sums have to be written, read and joined; where there are as many items as CTAs, a run has two of them,
+      // both cut, to begin and to end.
+      const float avg = __fdividef(static_cast<float>(units), static_cast<float>(items)), largest = static_cast<float>(top);
+      float whole = fmaxf(largest, static_cast<float>(quotient(items + ctas - 1, a.inv_ctas)) * avg);
+      if (a.plan.seqs > 1) whole += 0.5f * (largest - avg);
+      const float cost = a.split_cost * fminf(2.f, 1.f + __fdividef(static_cast<float>(items), static_cast<float>(ctas)));
+      r.split = a.may_split && whole > static_cast<float>(per) + cost;
       r.at = r.start = cta * per;
       r.end = min(units, r.at + per);
       if (r.at >= units) return false;

@@ -123,15 +123,15 @@ def test_attention_workspaces(lib, p):
     assert paged(2, 1, 8, 1, 128) == part(304, 16, 128)
     assert paged(1, 1, 9, 1, 64) == part(304, 9, 64)
     assert paged(1000, 2, 9, 1, 64) == part(304, 256, 64)
-    assert cross(2, 9, 513, 4, 4, 48) == part(304, 9, 48)
-    assert cross(2, 9, 512, 4, 4, 48) == 0                      # nothing is cut
+    assert cross(2, 9, 1537, 4, 4, 48) == part(304, 9, 48)
+    assert cross(2, 9, 1536, 4, 4, 48) == 0                     # nothing is cut
     assert cross(2, 8, 385, 4, 4, 48) == part(608, 8, 48) and cross(2, 8, 384, 4, 4, 48) == 0
     for sizes in ((0, 1, 8, 1, 64), (1, 0, 8, 1, 64), (-1, 1, 8, 1, 64), (1, 1, 3, 2, 64), (1, 1, 8, 0, 64),
                   (1, 1, 129, 1, 64), (1, 1, 8, 1, 72), (1, 1, 8, 1, 144), (1, 1, 8, 1, 0)):
         assert paged(*sizes) == 0
     assert cross(0, 1, 999, 1, 1, 64) == 0 and cross(1, -1, 999, 1, 1, 64) == 0
     need = paged(4, 2, 4, 2, 64)
-    many = dict(max_pages=25)  # 400 keys: tiles enough to cut
+    many = dict(max_pages=97)  # 1552 keys: tiles enough to cut
     refusals(lib, p, "cc_attn_paged", PAGED, [
         (dict(ws=None, **many), 1, "null workspace"), (dict(ws=p + 8, **many), 1, "aligned"),
         (dict(ws_bytes=need - 1, **many), 1, "workspace of"), (dict(ws_bytes=0, **many), 1, "workspace of"),
