@@ -23,8 +23,6 @@ namespace cc {
 namespace {
 
 constexpr int kFrThreads = 160;
-constexpr int kFrKeys = 64;
-constexpr int kFrBlock = kFrKeys * 128;  // bytes of 64 keys x 64 channels
 constexpr float kFrRoom = 8.f;           // powers of two that weights may pass their row's scale by
 
 __device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
@@ -52,18 +50,22 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int NB, int STAGES>
+// NB: 64-channel blocks of a head; KG: groups of 16 keys that a warp takes of a tile; STAGES: tiles in flight.
+template <int NB, int KG, int STAGES>
 struct FrSmem {
-  static constexpr int kTile = 2 * NB * kFrBlock;  // keys and values
+  static constexpr int kKeys = 64 * KG;
+  static constexpr int kBlock = kKeys * 128;     // bytes of a tile's keys x 64 channels
+  static constexpr int kTile = 2 * NB * kBlock;  // keys and values
   static constexpr int kSum = 4 * 3 * NB * 512;    // quarters of sums on their way to the warps that add them up
   static constexpr int kBytes = 1024 + STAGES * kTile + kSum + 4 * 8 * 8 + 512;
 };
 
-template <int NB, int STAGES>
+template <int NB, int KG, int STAGES>
 __global__ void __launch_bounds__(kFrThreads, 2)
     attn_few_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ AhArgs a) {
-  using Sm = FrSmem<NB, STAGES>;
+  using Sm = FrSmem<NB, KG, STAGES>;
+  constexpr int kKeys = Sm::kKeys, kBlock = Sm::kBlock, kMine = 16 * KG;  // kMine: a warp's keys of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float4* sSum = reinterpret_cast<float4*>(smem + STAGES * Sm::kTile);
@@ -125,8 +127,8 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       }
       if (!more) break;
       for (int t = it.t_begin; t < it.t_end; ++t) {
-        const int boxes = (min(kFrKeys, it.len - t * kFrKeys) + a.box - 1) / a.box;
-        int page = it.seq, at = t * kFrKeys + lane * a.box;
+        const int boxes = (min(kKeys, it.len - t * kKeys) + a.box - 1) / a.box;
+        int page = it.seq, at = t * kKeys + lane * a.box;
         if (lane < boxes && a.plan.page_table) {
           const int n = at / a.plan.page_size;
           at -= n * a.plan.page_size;
@@ -145,8 +147,8 @@ __global__ void __launch_bounds__(kFrThreads, 2)
           const uint32_t dst = smem_u32(smem + stage * Sm::kTile) + static_cast<uint32_t>(lane * a.box) * 128u;
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            tma_load_4d(dst + i * kFrBlock, &tmK, bar, i * 64, it.head, at, page);
-            tma_load_4d(dst + (NB + i) * kFrBlock, &tmV, bar, i * 64, it.head, at, page);
+            tma_load_4d(dst + i * kBlock, &tmK, bar, i * 64, it.head, at, page);
+            tma_load_4d(dst + (NB + i) * kBlock, &tmV, bar, i * 64, it.head, at, page);
           }
         }
         if (++stage == STAGES) {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kFrThreads, 2)
   } else {
     const int w = warp - 1;
     const int steps = a.d / 16;
-    const int kb = w * 16;  // this warp's keys of a tile
+    const int kb = w * kMine;  // this warp's keys of a tile
     // ldmatrix addresses within a tile: 16 keys x 16 channels as they are, and values transposed
     const int k_row = kb + (lane >> 3 & 1) * 8 + (lane & 7), k_chunk = lane >> 4;
     const int v_row = kb + (lane >> 4) * 8 + (lane & 7), v_chunk = lane >> 3 & 1;
@@ -212,35 +214,46 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       for (int t = it.t_begin; t < it.t_end; ++t) {
         ok = ok && warp_wait(&full[stage], ph, a);
         uint8_t* tile = smem + stage * Sm::kTile;
-        const int valid = it.len - t * kFrKeys - kb;  // of this warp's keys
-        if (valid < 16) {
+        const int valid = it.len - t * kKeys - kb;  // of this warp's keys
+        if (valid < kMine) {
           // values behind the sequence's end count 0 times, but 0 * NaN is NaN: they become zeros
-          for (int i = max(valid, 0) * 8 + lane; i < 128; i += 32) {
+          for (int i = max(valid, 0) * 8 + lane; i < 8 * kMine; i += 32) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-              *reinterpret_cast<uint4*>(tile + (NB + b) * kFrBlock + kb * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(tile + (NB + b) * kBlock + kb * 128 + i * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
         if (valid > 0) {
-          const uint32_t kt = smem_u32(tile) + k_row * 128, vt = smem_u32(tile) + NB * kFrBlock + v_row * 128;
-          // scores of keys lane / 4 (0, 1) and + 8 (2, 3) and rows col, col + 1; two chains of products
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t kt = smem_u32(tile) + k_row * 128, vt = smem_u32(tile) + NB * kBlock + v_row * 128;
+          // scores of each group's keys lane / 4 (0, 1) and + 8 (2, 3) and rows col, col + 1; two chains of products
+          float s0[KG][4], s1[KG][4];
+#pragma unroll
+          for (int g = 0; g < KG; ++g) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s0[g][i] = s1[g][i] = 0.f;
+          }
 #pragma unroll
           for (int k = 0; k < NB * 4; ++k) {
             if (k < steps) {
-              uint32_t x[4];
-              ldsm4(kt + (k >> 2) * kFrBlock + ((((k & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), x);
-              mma16816(k & 1 ? s1 : s0, x, qf[k][0], qf[k][1]);
+#pragma unroll
+              for (int g = 0; g < KG; ++g) {
+                uint32_t x[4];
+                ldsm4(kt + g * 2048 + (k >> 2) * kBlock + ((((k & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), x);
+                mma16816(k & 1 ? s1[g] : s0[g], x, qf[k][0], qf[k][1]);
+              }
             }
           }
           float m[2] = {kNegInf, kNegInf};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = t * kFrKeys + kb + (lane >> 2) + (i >> 1) * 8;
-            s0[i] = key < limit[i & 1] ? (s0[i] + s1[i]) * a.kx : kNegInf;
-            m[i & 1] = fmaxf(m[i & 1], s0[i]);
+          for (int g = 0; g < KG; ++g) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = t * kKeys + kb + g * 16 + (lane >> 2) + (i >> 1) * 8;
+              s0[g][i] = key < limit[i & 1] ? (s0[g][i] + s1[g][i]) * a.kx : kNegInf;
+              m[i & 1] = fmaxf(m[i & 1], s0[g][i]);
+            }
           }
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
@@ -260,24 +273,30 @@ __global__ void __launch_bounds__(kFrThreads, 2)
             c[0] = m[0], c[1] = m[1];
           }
           // weights, and what their rounding leaves, turned into the second factor of v^T p
-          uint32_t hi[2], rest[2];
+          uint32_t hi[KG][2], rest[KG][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p0 = ex2_approx(s0[2 * i] - (c[0] == kNegInf ? 0.f : c[0]));
-            const float p1 = ex2_approx(s0[2 * i + 1] - (c[1] == kNegInf ? 0.f : c[1]));
-            l[0] += p0;
-            l[1] += p1;
-            hi[i] = pack_bf16(p0, p1);
-            rest[i] = transpose8(pack_bf16(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u)));
-            hi[i] = transpose8(hi[i]);
+          for (int g = 0; g < KG; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float p0 = ex2_approx(s0[g][2 * i] - (c[0] == kNegInf ? 0.f : c[0]));
+              const float p1 = ex2_approx(s0[g][2 * i + 1] - (c[1] == kNegInf ? 0.f : c[1]));
+              l[0] += p0;
+              l[1] += p1;
+              const uint32_t h = pack_bf16(p0, p1);
+              rest[g][i] = transpose8(pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+              hi[g][i] = transpose8(h);
+            }
           }
 #pragma unroll
           for (int j = 0; j < NB * 4; ++j) {
             if (j < steps) {
-              uint32_t x[4];
-              ldsm4_trans(vt + (j >> 2) * kFrBlock + ((((j & 3) * 2 + v_chunk) ^ (v_row & 7)) << 4), x);
-              mma16816(acc[j], x, hi[0], hi[1]);
-              mma16816(acc[j], x, rest[0], rest[1]);
+#pragma unroll
+              for (int g = 0; g < KG; ++g) {
+                uint32_t x[4];
+                ldsm4_trans(vt + g * 2048 + (j >> 2) * kBlock + ((((j & 3) * 2 + v_chunk) ^ (v_row & 7)) << 4), x);
+                mma16816(acc[j], x, hi[g][0], hi[g][1]);
+                mma16816(acc[j], x, rest[g][0], rest[g][1]);
+              }
             }
           }
         }
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kFrThreads, 2)
       if (it.slot >= 0 && w == 0 && lane < 4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const bool any = limit[i] > it.t_begin * kFrKeys;
+          const bool any = limit[i] > it.t_begin * kKeys;
           if (col + i < rows)
             a.part_cl[static_cast<long long>(it.slot) * a.slot_rows + col + i] =
                 make_float2(any && top[i] == kNegInf ? kNoScore : top[i], sum[i]);
@@ -364,11 +383,11 @@ __global__ void __launch_bounds__(kFrThreads, 2)
   }
 }
 
-template <int NB, int STAGES>
+template <int NB, int KG, int STAGES>
 cc_status launch(const char* what, const CUtensorMap& tk, const CUtensorMap& tv, AhArgs& a, int grid,
                  cudaStream_t stream) {
-  auto kern = attn_few_rows_kernel<NB, STAGES>;
-  constexpr int kSmem = FrSmem<NB, STAGES>::kBytes;
+  auto kern = attn_few_rows_kernel<NB, KG, STAGES>;
+  constexpr int kSmem = FrSmem<NB, KG, STAGES>::kBytes;
   static_assert(kSmem <= 115712, "two CTAs to an SM");
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, a.device, ready);
@@ -382,7 +401,7 @@ cc_status launch(const char* what, const CUtensorMap& tk, const CUtensorMap& tv,
 
 cc_status launch_few_rows(const char* what, const CUtensorMap& tk, const CUtensorMap& tv, AhArgs& a, int grid,
                           cudaStream_t stream) {
-  return a.d > 64 ? launch<2, 3>(what, tk, tv, a, grid, stream) : launch<1, 6>(what, tk, tv, a, grid, stream);
+  return a.d > 64 ? launch<2, 1, 3>(what, tk, tv, a, grid, stream) : launch<1, 2, 3>(what, tk, tv, a, grid, stream);
 }
 
 }  // namespace cc

@@ -801,8 +801,10 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
 }
 
 constexpr int kFewRows = 8;        // query rows of an item of the few-rows kernel
-constexpr int kFewTileShift = 6;   // its tiles: 64 keys
 constexpr int kFewSplitCost = 6;
+
+// Its tiles: 128 keys, 64 of heads of more than 64 channels.
+int few_tile_shift(int d) { return d > 64 ? 6 : 7; }
 
 // Few rows to a sequence on average: the kernel whose CTAs do little but read the
 // cache. (The other one takes 128 rows of a key head at once.)
@@ -857,7 +859,7 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   a.o_sectors = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.ld_o % 16 == 0;
   a.tq = (few ? kFewRows : kAhHalf) / a.group;
   a.item_tokens = few ? a.tq : 2 * a.tq;
-  a.tile_shift = few ? kFewTileShift : kAhTileShift;
+  a.tile_shift = few ? few_tile_shift(a.d) : kAhTileShift;
   a.split_cost = few ? kFewSplitCost : kAhSplitCost;
   const int tile = 1 << a.tile_shift;
   a.box = std::min(tile, a.box);
@@ -927,7 +929,7 @@ extern "C" size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads
   if (n <= 0 || lq <= 0 || !sizes_ok(heads, kv_heads, d)) return 0;
   const int group = heads / kv_heads;
   const bool few = few_rows((int64_t)n * lq, n, group);
-  if (lk <= (few ? kFewSplitCost << kFewTileShift : kAhSplitCost << kAhTileShift)) return 0;  // nothing is cut
+  if (lk <= (few ? kFewSplitCost << few_tile_shift(d) : kAhSplitCost << kAhTileShift)) return 0;  // nothing is cut
   return workspace_bytes(few, lq, group, d);
 }
 

@@ -125,7 +125,8 @@ def test_attention_workspaces(lib, p):
     assert paged(1000, 2, 9, 1, 64) == part(304, 256, 64)
     assert cross(2, 9, 1537, 4, 4, 48) == part(304, 9, 48)
     assert cross(2, 9, 1536, 4, 4, 48) == 0                     # nothing is cut
-    assert cross(2, 8, 385, 4, 4, 48) == part(608, 8, 48) and cross(2, 8, 384, 4, 4, 48) == 0
+    assert cross(2, 8, 769, 4, 4, 48) == part(608, 8, 48) and cross(2, 8, 768, 4, 4, 48) == 0
+    assert cross(2, 8, 385, 4, 4, 80) == part(608, 8, 80) and cross(2, 8, 384, 4, 4, 80) == 0
     for sizes in ((0, 1, 8, 1, 64), (1, 0, 8, 1, 64), (-1, 1, 8, 1, 64), (1, 1, 3, 2, 64), (1, 1, 8, 0, 64),
                   (1, 1, 129, 1, 64), (1, 1, 8, 1, 72), (1, 1, 8, 1, 144), (1, 1, 8, 1, 0)):
         assert paged(*sizes) == 0
@@ -137,7 +138,7 @@ def test_attention_workspaces(lib, p):
         (dict(ws_bytes=need - 1, **many), 1, "workspace of"), (dict(ws_bytes=0, **many), 1, "workspace of"),
         (dict(rows=1 << 30, max_pages=1 << 20), 2, "2^31 tiles")])
     refusals(lib, p, "cc_attn_cross", CROSS, [
-        (dict(ws=None, lk=385), 1, "null workspace"), (dict(ws_bytes=8, lk=385), 1, "workspace of"),
+        (dict(ws=None, lk=769), 1, "null workspace"), (dict(ws_bytes=8, lk=769), 1, "workspace of"),
         (dict(n=1 << 15, lq=1 << 15, lk=1 << 20), 2, "2^31 tiles"), (dict(ld_k=1 << 30, lk=1 << 10), 2, "2^38")])
 
 
