@@ -2,8 +2,8 @@
 // with the query heads of a group): up to 8 rows of a key head at a time. Each key
 // and value is used for two products with those rows, so the cache's bytes bound
 // it, and the kernel is built around reading them without a pause: warp 0 finds
-// the CTA's run (cc_heads.cuh) and streams 64 keys and their values at a time with
-// TMA, across the borders of items; warps 1-4 take 16 of the 64 keys each, with
+// the CTA's run (cc_heads.cuh) and streams a tile of keys and their values at a
+// time with TMA, across the borders of items; warps 1-4 take a quarter of it each, with
 // row statistics and a sum of their own, so that nothing but the tiles' arrival
 // ties them together. Their sums are joined at an item's end.
 //
@@ -13,7 +13,12 @@
 // tile's reading. Weights are taken in two bf16 parts, which costs products that
 // have time.
 //
-// Two CTAs to an SM, 96 KB of tiles in flight each. MEASURED
+// Two CTAs to an SM, 96 KB of tiles in flight each; a tile is 64 keys of 65 to 128
+// channels or 128 of up to 64 (so that waits and maxima come half as often there:
+// 64 streams over 4096 keys of 8 heads of 64 channels 137 -> 121 us, of 32
+// 108 -> 82; 94 and 60 since L2 fetches no more than a head's row). Measured: single tokens of 64 streams, 100 to 8192 keys each, 32
+// heads over 8 of 128 channels: 178 us, 6.1 TB/s or 0.92 of a copy's rate, pages of
+// 16 or 128 alike; with the rows along m (16 at least, the keys along n) it was 192.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -7,24 +7,43 @@
 // halves of 128 rows, a row being a (token, query head of the group) pair, so
 // that grouped heads share the keys they read -- and all the 128-key tiles that
 // any of its rows sees. The items' tiles, laid end to end (sequence, rows, head),
-// are cut into equal runs, one for each CTA of a persistent grid: single tokens
-// over long caches, ragged batches and causal chunks all spread evenly over the
-// SMs. An item cut by a run's end leaves partial sums in the workspace, which a
-// second kernel joins; where whole items spread well enough nothing is cut.
-// The lengths are read on the device, so every CTA finds its run by itself.
+// are cut into equal runs, one for each CTA of a persistent grid. An item cut by
+// a run's end leaves partial sums in the workspace, which a second kernel joins;
+// where whole items spread well enough nothing is cut (cc_heads.cuh). The lengths
+// are read on the device, so every CTA finds its run by itself. Few rows to a
+// sequence go to another kernel (attn_few_rows.cu).
 //
-// Kernel. Warp 8 finds the run and streams q, k and v tiles with TMA (a box per
-// page piece); warp 9 issues the MMAs: S = q k^T (128 x 128, K = D) into tensor
-// memory, then O += P v with P read from tensor memory, where it takes the place
-// of S. Warps 0-3 and 4-7 are two softmax streams: they turn a tile of S into
-// P = bf16(exp2(kx S - c)), one row to a thread. Items of two halves give each
-// stream a half and both the same keys; items of one half give the streams every
-// other tile, and their sums are joined at the end. While a stream works on its
-// S, the tensor cores run the other's products.
+// Kernel. Warps 16 and 19 stream q and k, and v, with TMA (a box per page piece,
+// so a page of 16 tokens costs eight boxes and 64 channels; one warp for both took
+// 201 us for 2432 rows of 16 heads over 8192 keys in such pages, two take 144, as
+// do pages of 128). Warps 17 and 18 issue the products of a stream each: S = q k^T
+// (128 x 128, K = D) into tensor memory, then O += P v with P read from tensor
+// memory, where it takes the place of S. Warps 0-7 and 8-15 are two softmax
+// streams: they turn a tile of S into P = bf16(exp2(kx S - c)), half a row to a
+// thread. Items of two halves give each stream a half and both the same keys;
+// items of one half give the streams every other tile, and their sums are joined
+// at the end. While a stream works on its S, the tensor cores run the other's
+// products.
 //
-// c, the row's scale, moves in steps of 16 (powers of two: 2^16) and only up, so
-// all but a few tiles leave it where it is; when it moves, the stream itself
-// multiplies its O and sum by the exact power of two.
+// c, the row's scale, is a whole power of two: where it moves, and where streams
+// and pieces are joined, sums are multiplied exactly. It moves when a row's weights
+// of half a tile come to 2^20, which their sum tells: no maximum is looked for but
+// where that happens and in an item's first tile. fp32 sums of weights up to 2^20
+// lose nothing that weights up to 1 would keep, and neither does bf16.
+//
+// Bound: long chunks by the streams' chain -- 1024 clocks of products, 2000 of
+// softmax with its trips through tensor memory and barriers, where two streams
+// would need 2048 in all for the tensor cores alone; tensor memory (512 columns)
+// holds no third S beside the sums of 128 channels. 13728 rows of 16 heads of 128
+// over 27456 keys in blocks of 3432: 1.66 ms alone (1.51 PFLOP/s, tensor pipe 66 %
+// busy), 1.84 ms back to back, under the power limit (1.37 PFLOP/s; the library
+// product's own rate under it is 1.73). Texts of 512 keys: 70 us for 29 of
+// products; an item's four tiles take 6 us and its beginning and end, one after the
+// other for both streams, 4.6. What led here, for the chunk: one row to a thread
+// with eight softmax warps 2.12 ms; a maximum for every tile 2.17; products of
+// both streams issued by two warps as they come 2.24, by one in turns 1.94, by two
+// in turns 1.90; 64-key tiles with two S to a stream 2.26; CTAs with the same
+// keys in step 1.87 (5.5 -> 3.1 GB from memory).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,6 +68,9 @@ constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 chann
 constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
 constexpr float kAhRoom = 1048576.f;  // 2^20: what half a tile's weights of a row may come to before its scale moves
 constexpr float kAhMove = 8.f;        // and by how many powers of two at least
+// What cutting items costs, in tiles, for a run of one item; see find_run. Measured with 6, 12, 16, 24 and 48: 128 rows
+// of 8 heads, one key head, over 3000 keys 33 us cut and 45 whole (22 tiles apart), 512 of 16 over 2500 39 and 43 (16),
+// over 600 to 1200 28 and 24 (5).
 constexpr int kAhSplitCost = 12;
 
 // A value that all lanes hold, said in a way that the compiler keeps it in
@@ -147,8 +169,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
 
   if (warp == kAhTmaWarp || warp == kAhValueWarp) {
     // -------------------------------------------- run, items and TMA loads --
-    // One warp finds the run, publishes its items and loads q and keys, the other one loads values: a box of a small
-    // page takes a warp longer to ask for than the tensor cores need for its 16 keys.
+    // One warp finds the run, publishes its items and loads q and keys, the other one loads values.
     const bool keys = warp == kAhTmaWarp;
     const CUtensorMap* map = keys ? &tmK : &tmV;
     Run r = {};
@@ -256,9 +277,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
     // A product and the stream's next scores are a job. Jobs are issued one after
     // the other, streams in turn, so that a stream is back at its softmax while
     // the other's job runs; the queue holds next to nothing, so a warp that has
-    // its turn has done its waiting before. In clocks for a tile of two halves
-    // (2048 of products): one warp for both streams 3500, two without turns, which
-    // mix the streams and finish both late, 4100.
+    // its turn has done its waiting before. Without turns the streams' products
+    // mix and both finish late.
     const int s = uniform(warp - kAhMmaWarp);
     const uint32_t idesc_s = idesc_bf16_f32(kAhHalf, kAhKeys, false);
     const uint32_t idesc_o = idesc_bf16_f32(kAhHalf, a.d, true);
@@ -800,14 +820,18 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
   return CC_OK;
 }
 
-constexpr int kFewRows = 8;        // query rows of an item of the few-rows kernel
+constexpr int kFewRows = 8;        // query rows of an item of the few-rows kernel: the n of its products
+// As above, in its tiles. 64 streams of 100 to 1000 keys: 15.4 us with up to 8, 19.2 with 12; 128 of 50 to 600: 47.5
+// and 46.6.
 constexpr int kFewSplitCost = 6;
 
 // Its tiles: 128 keys, 64 of heads of more than 64 channels.
 int few_tile_shift(int d) { return d > 64 ? 6 : 7; }
 
 // Few rows to a sequence on average: the kernel whose CTAs do little but read the
-// cache. (The other one takes 128 rows of a key head at once.)
+// cache. (The other one takes 128 rows of a key head at once: 246 us instead of
+// 178 for single tokens of 64 streams with four heads to a key head. With more
+// rows than fit one item the keys would be read again for each eight of them.)
 bool few_rows(int64_t rows, int64_t seqs, int group) { return group <= kFewRows && rows * group <= kFewRows * seqs; }
 
 // Rows that a partial slot holds: those of all tokens where an item (of the

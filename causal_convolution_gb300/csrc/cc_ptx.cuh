@@ -201,7 +201,6 @@ __device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t threads,
   return out != 0;
 }
 
-
 // The same with OR.
 __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t threads, bool pred) {
   uint32_t out;
@@ -304,7 +303,9 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, uint32_t (&r)[64]
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
-}// 32 consecutive columns of this thread's TMEM lane, written; complete after tmem_st_wait.
+}
+
+// 32 consecutive columns of this thread's TMEM lane, written; complete after tmem_st_wait.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -336,6 +337,7 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
 // Shared -> global tiled TMA store (rank 2); parts outside the tensor are not
 // written. Coordinates must not be negative.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {

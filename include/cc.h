@@ -486,14 +486,19 @@ cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, const cc_bf
  * tokens: with causal_block 1 those up to itself, with F those up to the end of
  * its own block of F tokens (a frame); causal_block 0: all L. (With
  * causal_block 0 L may be less than n.) Rows that see no token become zeros.
- * Scores, softmax and sums in fp32, the weights rounded to bf16 for the product
- * with v, one rounding at the end. Keys and values behind a sequence's end may
- * hold anything, NaN included; those that some of its tokens see and others do
- * not should be finite. Results do not change from run to run, but the split of
- * the sums depends on the whole plan. ws: at least
- * cc_attn_paged_workspace_bytes() (0 for sizes that the call refuses; calls
- * whose GPU work overlaps need one each; its contents need no preparation).
- * o must not overlap q or the cache. Needs D % 16 == 0, D <= 128, heads %
+ * Scores, softmax and sums in fp32, the weights rounded to bf16 for the
+ * product with v (their sum is that of the rounded ones; where rows are few,
+ * weights are taken in two bf16 parts instead), one rounding at the end. Keys
+ * and values behind a sequence's end may hold anything, NaN included; those
+ * that some of its tokens see and others do not should be finite. Results do
+ * not change from run to run, but the split of the sums depends on the whole
+ * plan. ws: at least cc_attn_paged_workspace_bytes() (0 for sizes that the
+ * call refuses; calls whose GPU work overlaps need one each; its contents need
+ * no preparation; it may be NULL where the table has too few slots for
+ * anything to be cut: up to 384). o must not overlap q or the cache. Plans of
+ * 2^31 key tiles or more (tiles of 64 or 128 keys, 8 to 256 rows of query
+ * heads, counted as if each sequence filled its pages) and calls of more than
+ * 2^30 rows are CC_ERR_UNSUPPORTED. Needs D % 16 == 0, D <= 128, heads %
  * kv_heads == 0, group <= 128, ld_q, ld_o % 8 == 0, scale finite and > 0. */
 size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d);
 cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16* v_cache, cc_bf16* o,
@@ -508,7 +513,8 @@ cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16*
  * kv_heads (row strides ld_*, instances lq and lk rows apart). kv_lens: [n], how
  * many of an instance's keys count (0 .. lk, anything else is reported by
  * cc_check_device() and taken as the nearer of the two), or NULL (all lk). The
- * others may hold anything. Otherwise as cc_attn_paged; lk may be 0. */
+ * others may hold anything. Otherwise as cc_attn_paged; lk may be 0, and the
+ * workspace 0 bytes (ws is then not read) where lk is small. */
 size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d);
 cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_bf16* v, cc_bf16* o, const int32_t* kv_lens,
                         int n, int lq, int lk, int heads, int kv_heads, int d, int64_t ld_q, int64_t ld_k,
