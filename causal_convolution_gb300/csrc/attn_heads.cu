@@ -36,7 +36,7 @@
 // would need 2048 in all for the tensor cores alone; tensor memory (512 columns)
 // holds no third S beside the sums of 128 channels. 13728 rows of 16 heads of 128
 // over 27456 keys in blocks of 3432: 1.66 ms alone (1.51 PFLOP/s, tensor pipe 66 %
-// busy), 1.84 ms back to back, under the power limit (1.37 PFLOP/s; the library
+// busy), 1.84 ms back to back, under the power limit (1.36 PFLOP/s; the library
 // product's own rate under it is 1.73). Texts of 512 keys: 70 us for 29 of
 // products; an item's four tiles take 6 us and its beginning and end, one after the
 // other for both streams, 4.6. What led here, for the chunk: one row to a thread
