@@ -62,9 +62,12 @@ def attend(q, k, v, limit, scale):
         # a score: D products summed in fp32 and scaled; a weight is off by twice the scores' error (its own and the
         # sum's), by the exponential's (2^-22), and by its rounding to bf16; length terms are summed in fp32 twice,
         # by adders that may drop bits down to 2^-22 of a term. The exponent's own rounding: |exponent| 2^-24.
+        # What is divided by is the sum of the rounded weights: sum p (1 + e_i) v / sum p (1 + e_i) with |e_i| <= 2^-8 has a
+        # numerator off by 2^-8 sum p |v| and a denominator off by 2^-8 of itself, which is 2^-8 of the result; the
+        # result's own rounding is another.
         top = (scores.masked_fill(~sees, 0.0).abs().amax(-1, keepdim=True)) * 1.5
         err = (d + 4) * 4 * FP32 * scale * (q[:, h].abs() @ kh.abs().T).amax(-1, keepdim=True) + 4 * FP32 * top
-        bound[:, h] = STEP * want[:, h].abs() * (1 + 2 ** -6) + size * (
+        bound[:, h] = STEP * want[:, h].abs() * (2 + 2 ** -6) + size * (
             STEP + 2 * err + 2.0 ** -20 + 2 * length * 2.0 ** -22)
     return want, bound + 1e-37
 
