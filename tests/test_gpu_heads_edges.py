@@ -232,3 +232,38 @@ def test_the_largest_heads_and_groups():
     assert qo.bands_intact() and ko.bands_intact()
     ref.assert_close(qo.t, *ref.rotated(x[:, :2048], None, rot, [0, 1, 2], 1e-6, "pairs"), "q")
     ref.assert_close(ko.t, *ref.rotated(x[:, 2048:], None, rot, [0, 1, 2], 1e-6, "pairs"), "k")
+
+
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 33)], [(200, 700), (9, 33)]])
+def test_keys_and_values_of_different_layouts(lens):
+    c = Cache(lens, 48, 2, 96, "plain", seed=140)
+    q = rnd((c.rows, 4, 96), 141, 2.0)
+    want = paged(c, q, None, 1)
+    c.v = c.v.transpose(1, 2).contiguous().transpose(1, 2)     # a head's tokens side by side
+    wide = rnd((*c.k.shape[:3], 200), 142)
+    wide[..., 16:112] = c.k
+    c.k = wide[..., 16:112]                                    # channels of wider rows
+    assert same_bits(paged(c, q, None, 1), want)
+
+
+@pytest.mark.parametrize("page", [16 * 37, 4096])
+def test_large_pages(page):
+    for lens in ([(1, 5000), (1, 4096), (1, 1)], [(300, 5000), (130, 4097)]):
+        c = Cache(lens, page, 1, 48, "heads", seed=143)
+        q = rnd((c.rows, 3, 48), 144, 2.0)
+        check_paged(c, q, paged(c, q, None, 1), None, 1, "large pages")
+
+
+@pytest.mark.parametrize("new", [2, 150])
+def test_queries_that_are_not_numbers_stay_alone(new):
+    c = Cache([(new, 600), (1, 600)], 16, 2, 64, seed=145)
+    q = rnd((c.rows, 4, 64), 146, 2.0)
+    q[0, 1, 7], q[1, 2, 3] = float("nan"), float("inf")
+    o = paged(c, q, None, 1)
+    assert bool(o[0, 1].isnan().all()) and bool(o[1, 2].isnan().all())
+    k, v = c.seq(0)
+    want, bound = ref.attend(q[:new].nan_to_num(0, 0, 0), k, v, ref.limits(new, 600, 1, DEV), 0.125)
+    keep = torch.ones((new, 4), dtype=torch.bool, device=DEV)
+    keep[0, 1] = keep[1, 2] = False
+    ref.assert_close(o[:new][keep], want[keep], bound[keep], "the others")
+    ref.assert_close(o[new:], *ref.attend(q[new:], *c.seq(1), ref.limits(1, 600, 1, DEV), 0.125), "another sequence")
