@@ -470,26 +470,29 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           tc_fence_after();
           const int lim = limit - t * kAhKeys - hf * 64;
           const bool masked = __any_sync(0xffffffffu, lim < 64);
-          uint32_t sv[64];
           // Weights on the scale in hand, which is fine while none is far above 1; their sum tells that without a
           // maximum. Rows without a scale, and those that outgrow theirs, get one, and the tile is done again. (The
           // code is kept short, with the rare parts in one place: what does not fit the instruction cache costs more
           // than it saves.)
           for (bool again = i == 0;; again = true) {
-            tmem_ld64_wait(s_col, sv);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
-            }
+            uint32_t sv[32];
             if (again) {
               // The scale of the tile's largest score, and l and O with it (O's last product was complete before
               // these scores were). Both warps of a row come here together, and the barrier keeps their weights from
               // scores that the other one has not read.
               float m0 = kNegInf, m1 = kNegInf;
+#pragma unroll 1
+              for (int h = 0; h < 64; h += 32) {
+                tmem_ld32_wait(s_col + h, sv);
+                if (masked) {
 #pragma unroll
-              for (int e = 0; e < 64; e += 4) {
-                m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
-                m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
+                  for (int e = 0; e < 32; ++e) sv[e] = e + h < lim ? sv[e] : 0xff800000u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  m0 = max3(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), m0);
+                  m1 = max3(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), m1);
+                }
               }
               float up = ceilf(fmaxf(m0, m1) * a.kx);
               *my_x = up;
@@ -517,17 +520,28 @@ __global__ void __launch_bounds__(kAhThreads, 1)
             const f32x2 nb2 = pair(-base, -base);
             f32x2 sum = pair(0.f, 0.f), sum1 = sum;
             uint32_t pk[32];
+            auto weights = [&](int h) {
+              if (masked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
-              pk[e] = pack_bf16(ex2_approx(lo(x)), ex2_approx(hi(x)));
-              // the rounded weights are summed, so that they come to 1: a row that one key rules is exact
-              const f32x2 p = pair(__uint_as_float(pk[e] << 16), __uint_as_float(pk[e] & 0xffff0000u));
-              if (e & 1)
-                sum1 = add2(sum1, p);
-              else
-                sum = add2(sum, p);
-            }
+                for (int e = 0; e < 32; ++e) sv[e] = e + h < lim ? sv[e] : 0xff800000u;
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const f32x2 x = fma2(pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), kx2, nb2);
+                const uint32_t w = pack_bf16(ex2_approx(lo(x)), ex2_approx(hi(x)));
+                pk[h / 2 + e] = w;
+                // the rounded weights are summed, so that they come to 1: a row that one key rules is exact
+                const f32x2 p = pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                if (e & 1)
+                  sum1 = add2(sum1, p);
+                else
+                  sum = add2(sum, p);
+              }
+            };
+            tmem_ld32_wait(s_col, sv);
+            weights(0);
+            tmem_ld32_wait(s_col + 32, sv);
+            weights(32);
             sum = add2(sum, sum1);
             const float total = lo(sum) + hi(sum);
             if (!again && named_barrier_or(mates, 64, row_ok && (c == kNegInf || !(total < kAhRoom)))) continue;
