@@ -26,10 +26,12 @@
 // products.
 //
 // c, the row's scale, is a whole power of two: where it moves, and where streams
-// and pieces are joined, sums are multiplied exactly. It moves when a row's weights
-// of half a tile come to 2^20, which their sum tells: no maximum is looked for but
-// where that happens and in an item's first tile. fp32 sums of weights up to 2^20
-// lose nothing that weights up to 1 would keep, and neither does bf16.
+// and pieces are joined, sums are multiplied exactly. It begins as 2^0 and moves
+// when a row's weights of half a tile come to 2^20, or those of the first keys that
+// it sees to less than 2^-10, which their sum tells: no maximum is looked for but
+// where that happens (short texts 13.2 -> 11.9 us against a maximum of each item's
+// first tile). fp32 sums of weights up to 2^20 lose nothing that weights up to 1
+// would keep, and neither does bf16.
 //
 // Bound: long chunks by the streams' chain -- 1024 clocks of products, 2000 of
 // softmax with its trips through tensor memory and barriers, where two streams
@@ -67,6 +69,7 @@ constexpr int kAhHalf = 128;      // rows per half
 constexpr int kAhQBlock = kAhHalf * 128;   // bytes of 128 query rows x 64 channels
 constexpr int kAhKvBlock = kAhKeys * 128;  // bytes of 128 keys (or values) x 64 channels
 constexpr float kAhRoom = 1048576.f;  // 2^20: what half a tile's weights of a row may come to before its scale moves
+constexpr float kAhLeast = 1.f / 1024;  // and to at least, on the scale that a row tries first
 constexpr float kAhMove = 8.f;        // and by how many powers of two at least
 // What cutting items costs, in tiles, for a run of one item; see find_run. Measured with 6, 12, 16, 24 and 48: 128 rows
 // of 8 heads, one key head, over 3000 keys 33 us cut and 45 whole (22 tiles apart), 512 of 16 over 2500 39 and 43 (16),
@@ -94,7 +97,7 @@ struct AhSmem {
   static constexpr int kTile = NB * kAhKvBlock;
   static constexpr int kQHalf = NB * kAhQBlock;
   static constexpr int kQ = 2 * kQHalf;
-  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 8 + 4 * kAhHalf * 4;
+  static constexpr int kBytes = 1024 + kQ + STAGES * kTile + 1024 + 2 * kAhHalf * 8 + 8 * kAhHalf * 4;
 };
 
 template <int NB, int STAGES>
@@ -107,8 +110,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + Sm::kQ;
   float2* sCL = reinterpret_cast<float2*>(sKV + STAGES * Sm::kTile);  // [2][128] stream 1's (c, l) of single halves
-  float* sX = reinterpret_cast<float*>(sCL + 2 * kAhHalf);    // [4][128] what warps of the same rows exchange
-  AhItem* items = reinterpret_cast<AhItem*>(sX + 4 * kAhHalf);
+  float* sX = reinterpret_cast<float*>(sCL + 2 * kAhHalf);    // [2][4][128] what warps of the same rows exchange: maxima, sums
+  AhItem* items = reinterpret_cast<AhItem*>(sX + 8 * kAhHalf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kAhItems);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + STAGES;
@@ -460,7 +463,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
       const int limit = row_ok ? key_limit(a, it.fresh, it.len, it.first + tok) : 0x7fffffff;
       const bool active = __any_sync(0xffffffffu, row_ok);
       const int mine = two ? n : (n + 1 - s) >> 1;  // tiles of this stream
-      float c = kNegInf, l = 0.f;
+      float c = 0.f, l = 0.f;
+      float least = kAhLeast;  // below 0: the row's scale c is settled
 #pragma unroll 1
       for (int i = 0; i < mine; ++i) {
         const int t = tile_of(t_begin, n, from, two ? i : 2 * i + s);
@@ -471,10 +475,9 @@ __global__ void __launch_bounds__(kAhThreads, 1)
           const int lim = limit - t * kAhKeys - hf * 64;
           const bool masked = __any_sync(0xffffffffu, lim < 64);
           // Weights on the scale in hand, which is fine while none is far above 1; their sum tells that without a
-          // maximum. Rows without a scale, and those that outgrow theirs, get one, and the tile is done again. (The
-          // code is kept short, with the rare parts in one place: what does not fit the instruction cache costs more
-          // than it saves.)
-          for (bool again = i == 0;; again = true) {
+          // maximum. Where a row outgrew its scale, or begins far below it, it gets one, and the tile is done again.
+          // Scores come in two halves, so that nothing is spilled (chunk 1818 -> 1764 us, texts 69 -> 60.5).
+          for (bool again = false;; again = true) {
             uint32_t sv[32];
             if (again) {
               // The scale of the tile's largest score, and l and O with it (O's last product was complete before
@@ -498,9 +501,11 @@ __global__ void __launch_bounds__(kAhThreads, 1)
               *my_x = up;
               named_barrier_sync(mates, 64);
               up = fmaxf(up, *mate_x);
-              const float top = row_ok && up > c + (i == 0 ? 0.f : kAhMove) ? up : c;
+              const bool first = least > 0.f;  // l and O are 0 still
+              const float top = row_ok && up > (first ? kNegInf : c + kAhMove) ? up : c;
+              if (up > kNegInf) least = -1.f;
               if (__any_sync(0xffffffffu, top != c)) {
-                const float f = pow2_diff(c, top);
+                const float f = first ? 1.f : pow2_diff(c, top);
                 if (i > 0) {
 #pragma unroll 1
                   for (int col = hf * 16; col < a.d; col += 32) {
@@ -516,8 +521,7 @@ __global__ void __launch_bounds__(kAhThreads, 1)
                 c = top;
               }
             }
-            const float base = c == kNegInf ? 0.f : c;
-            const f32x2 nb2 = pair(-base, -base);
+            const f32x2 nb2 = pair(-c, -c);
             f32x2 sum = pair(0.f, 0.f), sum1 = sum;
             uint32_t pk[32];
             auto weights = [&](int h) {
@@ -544,7 +548,11 @@ __global__ void __launch_bounds__(kAhThreads, 1)
             weights(32);
             sum = add2(sum, sum1);
             const float total = lo(sum) + hi(sum);
-            if (!again && named_barrier_or(mates, 64, row_ok && (c == kNegInf || !(total < kAhRoom)))) continue;
+            if (!again) {
+              const float need = masked && lim <= 0 ? -1.f : least;
+              if (named_barrier_or(mates, 64, row_ok && !(total < kAhRoom && total > need))) continue;
+              if (!masked || lim + hf * 64 > 0) least = -1.f;
+            }
             tmem_st32(s_col, pk);
             l += total;
             break;
@@ -555,14 +563,13 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_ready[s]));
       }
+      if (least > 0.f) c = kNegInf;  // the row has seen nothing
       const int other = two ? 0 : n >> 1;  // stream 1's tiles, where stream 0 joins both
-      if (mine > 0) {
-        ok = ok && warp_wait(&pv_done[s], pv_ph, a);
-        pv_ph ^= 1u;
-      }
       if (!two && s == 1) {
         // hand (c, l) over to stream 0, which reads both sums
         if (mine > 0) {
+          ok = ok && warp_wait(&pv_done[s], pv_ph, a);
+          pv_ph ^= 1u;
           sCL[hf * kAhHalf + row] = make_float2(c, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(cl_ready));
@@ -570,25 +577,26 @@ __global__ void __launch_bounds__(kAhThreads, 1)
         release();
         continue;
       }
-      float c1 = kNegInf, l1 = 0.f;
+      float top = c, f0 = 1.f, f1 = 0.f;
       if (n > 0) {
+        // the row's whole sum, while the last product runs
+        my_x[4 * kAhHalf] = l;
+        named_barrier_sync(mates, 64);
+        l += mate_x[4 * kAhHalf];
         if (other > 0) {
           // stream 1 arrives after its own last product, so that O of both is complete
           ok = ok && warp_wait(cl_ready, cl_ph, a);
           cl_ph ^= 1u;
-          c1 = sCL[row].x;
-          l1 = sCL[row].y + sCL[kAhHalf + row].y;
+          const float c1 = sCL[row].x;
+          top = fmaxf(c, c1);
+          f0 = pow2_diff(c, top), f1 = pow2_diff(c1, top);
+          l = l * f0 + (sCL[row].y + sCL[kAhHalf + row].y) * f1;
         }
+        ok = ok && warp_wait(&pv_done[s], pv_ph, a);
+        pv_ph ^= 1u;
         tc_fence_after();
-        // the row's whole sum; the second barrier keeps the next item's maxima from what is read here
-        *my_x = l;
-        named_barrier_sync(mates, 64);
-        l += *mate_x;
-        named_barrier_sync(mates, 64);
       }
-      const float top = fmaxf(c, c1);
-      const float f0 = pow2_diff(c, top), f1 = pow2_diff(c1, top);
-      const float sum = l * f0 + l1 * f1;
+      const float sum = l;
       if (active) {
         const bool sees = n > 0 && limit > 0;
         const float inv = 1.f / sum;
