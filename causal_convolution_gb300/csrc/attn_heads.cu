@@ -33,19 +33,20 @@
 // first tile). fp32 sums of weights up to 2^20 lose nothing that weights up to 1
 // would keep, and neither does bf16.
 //
-// Bound: long chunks by the streams' chain -- 1024 clocks of products, 2000 of
+// Bound: long chunks by the streams' chain -- 1024 clocks of products, 1900 of
 // softmax with its trips through tensor memory and barriers, where two streams
 // would need 2048 in all for the tensor cores alone; tensor memory (512 columns)
 // holds no third S beside the sums of 128 channels. 13728 rows of 16 heads of 128
-// over 27456 keys in blocks of 3432: 1.66 ms alone (1.51 PFLOP/s, tensor pipe 66 %
-// busy), 1.84 ms back to back, under the power limit (1.36 PFLOP/s; the library
-// product's own rate under it is 1.73). Texts of 512 keys: 70 us for 29 of
-// products; an item's four tiles take 6 us and its beginning and end, one after the
-// other for both streams, 4.6. What led here, for the chunk: one row to a thread
+// over 27456 keys in blocks of 3432: 1.58 ms alone (1.59 PFLOP/s, tensor pipe 70 %
+// busy), 1.78 ms back to back, under the power limit (1.41 PFLOP/s; the library
+// product's own rate under it is 1.73). Texts of 512 keys: 60 us for 29 of
+// products, as an item's beginning and end come one after the other for both
+// streams. What led here, for the chunk back to back: one row to a thread
 // with eight softmax warps 2.12 ms; a maximum for every tile 2.17; products of
 // both streams issued by two warps as they come 2.24, by one in turns 1.94, by two
 // in turns 1.90; 64-key tiles with two S to a stream 2.26; CTAs with the same
-// keys in step 1.87 (5.5 -> 3.1 GB from memory).
+// keys in step 1.87 (5.5 -> 3.1 GB from memory); shorter waits 1.84; a tile's
+// scores in two halves, so that registers suffice, 1.77.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
