@@ -823,6 +823,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
   }
 }
 
+constexpr int kAhMaxHeads = 65536;
+constexpr int kAhMaxRows = 1 << 30;
+constexpr double kAhMaxSpan = 0x1p38;  // elements from an instance's keys to the next one's stay below
+
 cc_status check_attn(const char* what, const void* q, const void* k, const void* v, const void* o, int heads,
                      int kv_heads, int d, int64_t ld_q, int64_t ld_o, float scale) {
   if (!q || !o || !k || !v) return fail(CC_ERR_INVALID, "%s: null pointer", what);
@@ -833,7 +837,7 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
                 kv_heads);
   if (d % 16 != 0 || d > 128)
     return fail(CC_ERR_UNSUPPORTED, "%s: D must be a multiple of 16 up to 128 (got %d)", what, d);
-  if (heads > 65536 || heads / kv_heads > 128)
+  if (heads > kAhMaxHeads || heads / kv_heads > kAhHalf)
     return fail(CC_ERR_UNSUPPORTED, "%s: at most 65536 heads, 128 to a key head", what);
   if (ld_q < (int64_t)heads * d || ld_o < (int64_t)heads * d || ld_q % 8 || ld_o % 8)
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
@@ -862,6 +866,14 @@ bool few_rows(int64_t rows, int64_t seqs, int group) { return group <= kFewRows 
 int slot_rows(bool few, int64_t tokens, int group) {
   const int tq = (few ? kFewRows : kAhHalf) / group;
   return tokens <= tq ? static_cast<int>(tokens) * group : few ? kFewRows : 2 * kAhHalf;
+}
+
+// Tokens of an item, see AhArgs.
+int item_tokens(bool few, int group) { return few ? kFewRows / group : 2 * (kAhHalf / group); }
+
+// Tiles are counted in 31 bits. tiles: of a sequence, at most
+bool too_many_tiles(int64_t rows, int64_t seqs, int item_tokens, int64_t kv_heads, int64_t tiles) {
+  return ((rows / item_tokens + seqs) * kv_heads) * (double)tiles >= 0x1p31;
 }
 
 size_t part_bytes(int ctas, int rows, int d) { return (size_t)2 * ctas * rows * d * 4; }
@@ -905,13 +917,13 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   a.ld_q = ld_q;
   a.o_sectors = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.ld_o % 16 == 0;
   a.tq = (few ? kFewRows : kAhHalf) / a.group;
-  a.item_tokens = few ? a.tq : 2 * a.tq;
+  a.item_tokens = item_tokens(few, a.group);
   a.tile_shift = few ? few_tile_shift(a.d) : kAhTileShift;
   a.split_cost = few ? kFewSplitCost : kAhSplitCost;
   const int tile = 1 << a.tile_shift;
   a.box = std::min(tile, a.box);
   const int64_t tiles = std::max<int64_t>(1, (keys + tile - 1) / tile);
-  if (((a.rows / a.item_tokens + (int64_t)a.plan.seqs) * a.kv_heads) * (double)tiles >= 0x1p31)
+  if (too_many_tiles(a.rows, a.plan.seqs, a.item_tokens, a.kv_heads, tiles))
     return fail(CC_ERR_UNSUPPORTED, "%s: rows, heads and keys make 2^31 tiles or more", what);
   a.may_split = tiles > a.split_cost;
   a.slot_rows = slot_rows(few, max_tokens, a.group);
@@ -956,9 +968,10 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
   return launch_status(what);
 }
 
-bool sizes_ok(int64_t heads, int64_t kv_heads, int64_t d) {
-  return heads > 0 && kv_heads > 0 && heads % kv_heads == 0 && heads / kv_heads <= kAhHalf && d > 0 && d % 16 == 0 &&
-         d <= 128;
+// Sizes that the calls take, as far as a workspace's size depends on them.
+bool sizes_ok(int64_t rows, int64_t heads, int64_t kv_heads, int64_t d) {
+  return rows <= kAhMaxRows && heads > 0 && heads <= kAhMaxHeads && kv_heads > 0 && heads % kv_heads == 0 &&
+         heads / kv_heads <= kAhHalf && d > 0 && d % 16 == 0 && d <= 128;
 }
 
 }  // namespace
@@ -967,16 +980,20 @@ bool sizes_ok(int64_t heads, int64_t kv_heads, int64_t d) {
 using namespace cc;
 
 extern "C" size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d) {
-  if (rows <= 0 || seqs <= 0 || !sizes_ok(heads, kv_heads, d)) return 0;
+  if (rows <= 0 || seqs <= 0 || !sizes_ok(rows, heads, kv_heads, d)) return 0;
   const int group = heads / kv_heads;
   return workspace_bytes(few_rows(rows, seqs, group), rows, group, d);
 }
 
 extern "C" size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d) {
-  if (n <= 0 || lq <= 0 || !sizes_ok(heads, kv_heads, d)) return 0;
+  if (n <= 0 || lq <= 0 || !sizes_ok((int64_t)n * lq, heads, kv_heads, d)) return 0;
   const int group = heads / kv_heads;
   const bool few = few_rows((int64_t)n * lq, n, group);
-  if (lk <= (few ? kFewSplitCost << few_tile_shift(d) : kAhSplitCost << kAhTileShift)) return 0;  // nothing is cut
+  const int shift = few ? few_tile_shift(d) : kAhTileShift;
+  if (lk <= (few ? kFewSplitCost : kAhSplitCost) << shift) return 0;  // nothing is cut
+  const int64_t tiles = ((int64_t)lk + (1 << shift) - 1) >> shift;
+  if (too_many_tiles((int64_t)n * lq, n, item_tokens(few, group), kv_heads, tiles)) return 0;
+  if ((double)kv_heads * d * lk >= kAhMaxSpan) return 0;
   return workspace_bytes(few, lq, group, d);
 }
 
@@ -994,7 +1011,7 @@ extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, con
   if ((st = check_cache_strides(what, k_page, k_token, k_head, d)) != CC_OK ||
       (st = check_cache_strides(what, v_page, v_token, v_head, d)) != CC_OK)
     return st;
-  if (rows > 1 << 30) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
+  if (rows > kAhMaxRows) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
   if (causal_block < 0) return fail(CC_ERR_INVALID, "%s: the causal block must not be negative", what);
   AhArgs a = {};
   a.plan = {q_offsets, kv_lens, page_table, seqs, max_pages, pages, page_size};
@@ -1023,8 +1040,8 @@ extern "C" cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_
   if (!aligned16(kv_lens)) return fail(CC_ERR_INVALID, "%s: pointers must be 16-byte aligned", what);
   if (ld_k < (int64_t)kv_heads * d || ld_v < (int64_t)kv_heads * d || ld_k % 8 || ld_v % 8)
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
-  if ((int64_t)n * lq > 1 << 30) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
-  if ((double)ld_k * lk >= 0x1p38 || (double)ld_v * lk >= 0x1p38)
+  if ((int64_t)n * lq > kAhMaxRows) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
+  if ((double)ld_k * lk >= kAhMaxSpan || (double)ld_v * lk >= kAhMaxSpan)
     return fail(CC_ERR_UNSUPPORTED, "%s: an instance's keys must lie within 2^38 elements", what);
   AhArgs a = {};
   a.plan = {nullptr, kv_lens, nullptr, n, 1, n, lk};

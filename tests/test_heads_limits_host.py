@@ -1,0 +1,22 @@
+"""Argument checks of the operators with heads at the largest sizes and the loosest strides, on the host."""
+
+from test_heads_host import CROSS, PAGED, call, calls, lib, p  # noqa: F401 (fixtures)
+
+
+def test_workspaces_of_refused_sizes_are_none(lib, p):
+    """0 bytes for every size that the call refuses, and for the largest that it takes a workspace."""
+    paged, cross = lib.cc_attn_paged_workspace_bytes, lib.cc_attn_cross_workspace_bytes
+    heads = dict(heads=131072, kv_heads=1024, d=16, ld_q=1 << 21, ld_o=1 << 21, ld_k=1 << 14, ld_v=1 << 14)
+    assert call(lib, "cc_attn_paged", PAGED, p, **heads)[0] == 2 and paged(4, 2, 131072, 1024, 16) == 0
+    assert call(lib, "cc_attn_cross", CROSS, p, **heads)[0] == 2 and cross(2, 2, 5000, 131072, 1024, 16) == 0
+    assert paged(4, 2, 65536, 512, 16) > 0 and cross(2, 2, 5000, 65536, 512, 16) > 0
+    rows = (1 << 30) + 1
+    assert call(lib, "cc_attn_paged", PAGED, p, rows=rows)[0] == 2 and paged(rows, 2, 4, 2, 64) == 0
+    assert paged(1 << 30, 2, 4, 2, 64) > 0
+    assert call(lib, "cc_attn_cross", CROSS, p, n=3, lq=1 << 29)[0] == 2 and cross(3, 1 << 29, 5000, 4, 2, 64) == 0
+    assert cross(2, 1 << 29, 5000, 4, 2, 64) > 0
+    assert call(lib, "cc_attn_cross", CROSS, p, n=1 << 15, lq=1 << 15, lk=1 << 20)[0] == 2
+    assert cross(1 << 15, 1 << 15, 1 << 20, 4, 2, 64) == 0 and cross(1 << 15, 1 << 9, 1 << 12, 4, 2, 64) > 0
+    span = dict(n=1, lq=1, lk=1 << 30, heads=2, kv_heads=2, d=128)
+    assert call(lib, "cc_attn_cross", CROSS, p, ld_k=256, ld_v=256, **span)[0] == 2
+    assert cross(1, 1, 1 << 30, 2, 2, 128) == 0 and cross(1, 1, (1 << 30) - 1, 2, 2, 128) > 0
