@@ -825,6 +825,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
 
 constexpr int kAhMaxHeads = 65536;
 constexpr int kAhMaxRows = 1 << 30;
+// Every CTA counts all sequences before its first item, while its other warps' waits of two seconds run: so many take
+// 0.03 s of one row each, 0.28 of two items each other one, 0.15 where nearly all are empty and one CTA skips them one by
+// one, 0.54 of three rows of 128 heads.
+constexpr int kAhMaxSeqs = 1 << 20;
 constexpr double kAhMaxSpan = 0x1p38;  // elements from an instance's keys to the next one's stay below
 
 cc_status check_attn(const char* what, const void* q, const void* k, const void* v, const void* o, int heads,
@@ -969,8 +973,8 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
 }
 
 // Sizes that the calls take, as far as a workspace's size depends on them.
-bool sizes_ok(int64_t rows, int64_t heads, int64_t kv_heads, int64_t d) {
-  return rows <= kAhMaxRows && heads > 0 && heads <= kAhMaxHeads && kv_heads > 0 && heads % kv_heads == 0 &&
+bool sizes_ok(int64_t rows, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t d) {
+  return rows <= kAhMaxRows && seqs <= kAhMaxSeqs && heads > 0 && heads <= kAhMaxHeads && kv_heads > 0 && heads % kv_heads == 0 &&
          heads / kv_heads <= kAhHalf && d > 0 && d % 16 == 0 && d <= 128;
 }
 
@@ -980,13 +984,13 @@ bool sizes_ok(int64_t rows, int64_t heads, int64_t kv_heads, int64_t d) {
 using namespace cc;
 
 extern "C" size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d) {
-  if (rows <= 0 || seqs <= 0 || !sizes_ok(rows, heads, kv_heads, d)) return 0;
+  if (rows <= 0 || seqs <= 0 || !sizes_ok(rows, seqs, heads, kv_heads, d)) return 0;
   const int group = heads / kv_heads;
   return workspace_bytes(few_rows(rows, seqs, group), rows, group, d);
 }
 
 extern "C" size_t cc_attn_cross_workspace_bytes(int n, int lq, int lk, int heads, int kv_heads, int d) {
-  if (n <= 0 || lq <= 0 || !sizes_ok((int64_t)n * lq, heads, kv_heads, d)) return 0;
+  if (n <= 0 || lq <= 0 || !sizes_ok((int64_t)n * lq, n, heads, kv_heads, d)) return 0;
   const int group = heads / kv_heads;
   const bool few = few_rows((int64_t)n * lq, n, group);
   const int shift = few ? few_tile_shift(d) : kAhTileShift;
@@ -1012,6 +1016,7 @@ extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, con
       (st = check_cache_strides(what, v_page, v_token, v_head, d)) != CC_OK)
     return st;
   if (rows > kAhMaxRows) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
+  if (seqs > kAhMaxSeqs) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^20 sequences", what);
   if (causal_block < 0) return fail(CC_ERR_INVALID, "%s: the causal block must not be negative", what);
   AhArgs a = {};
   a.plan = {q_offsets, kv_lens, page_table, seqs, max_pages, pages, page_size};
@@ -1041,6 +1046,7 @@ extern "C" cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_
   if (ld_k < (int64_t)kv_heads * d || ld_v < (int64_t)kv_heads * d || ld_k % 8 || ld_v % 8)
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
   if ((int64_t)n * lq > kAhMaxRows) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
+  if (n > kAhMaxSeqs) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^20 instances", what);
   if ((double)ld_k * lk >= kAhMaxSpan || (double)ld_v * lk >= kAhMaxSpan)
     return fail(CC_ERR_UNSUPPORTED, "%s: an instance's keys must lie within 2^38 elements", what);
   AhArgs a = {};

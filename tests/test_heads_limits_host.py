@@ -20,3 +20,13 @@ def test_workspaces_of_refused_sizes_are_none(lib, p):
     span = dict(n=1, lq=1, lk=1 << 30, heads=2, kv_heads=2, d=128)
     assert call(lib, "cc_attn_cross", CROSS, p, ld_k=256, ld_v=256, **span)[0] == 2
     assert cross(1, 1, 1 << 30, 2, 2, 128) == 0 and cross(1, 1, (1 << 30) - 1, 2, 2, 128) > 0
+
+
+def test_sequences_beyond_what_a_cta_can_count_in_time_are_refused(lib, p):
+    paged, cross = lib.cc_attn_paged_workspace_bytes, lib.cc_attn_cross_workspace_bytes
+    most = 1 << 20
+    for name, names, key in (("cc_attn_paged", PAGED, "seqs"), ("cc_attn_cross", CROSS, "n")):
+        st, msg = call(lib, name, names, p, lq=1, **{key: most + 1})
+        assert st == 2 and "2^20" in msg, (name, st, msg)
+    assert paged(4, most, 4, 2, 64) > 0 and paged(4, most + 1, 4, 2, 64) == 0
+    assert cross(most, 1, 5000, 4, 2, 64) > 0 and cross(most + 1, 1, 5000, 4, 2, 64) == 0
