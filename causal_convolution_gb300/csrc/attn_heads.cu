@@ -1012,8 +1012,8 @@ extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, con
   if (empty_request(what, {rows, seqs}, &st)) return st;
   if ((st = check_attn(what, q, k_cache, v_cache, o, heads, kv_heads, d, ld_q, ld_o, scale)) != CC_OK) return st;
   if ((st = check_plan(what, q_offsets, kv_lens, page_table, max_pages, pages, page_size)) != CC_OK) return st;
-  if ((st = check_cache_strides(what, k_page, k_token, k_head, d)) != CC_OK ||
-      (st = check_cache_strides(what, v_page, v_token, v_head, d)) != CC_OK)
+  if ((st = check_cache_strides(what, k_page, k_token, k_head, pages, kv_heads, d)) != CC_OK ||
+      (st = check_cache_strides(what, v_page, v_token, v_head, pages, kv_heads, d)) != CC_OK)
     return st;
   if (rows > kAhMaxRows) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^30 rows", what);
   if (seqs > kAhMaxSeqs) return fail(CC_ERR_UNSUPPORTED, "%s: at most 2^20 sequences", what);

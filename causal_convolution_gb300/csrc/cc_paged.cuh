@@ -57,8 +57,13 @@ inline cc_status check_plan(const char* what, const int32_t* q_offsets, const in
 }
 
 // A cache's strides in elements. Slots that overlap are the caller's mistake, but
-// within its memory as long as the strides are true.
-inline cc_status check_cache_strides(const char* what, int64_t page, int64_t token, int64_t head, int d) {
+// within its memory as long as the strides are true. A size of one is never
+// stepped over: whatever its stride is (0 in an expanded tensor), it becomes D,
+// which a tensor map takes.
+inline cc_status check_cache_strides(const char* what, int64_t& page, int64_t token, int64_t& head, int pages,
+                                     int kv_heads, int d) {
+  if (pages == 1) page = d;
+  if (kv_heads == 1) head = d;
   if (page < d || token < d || head < d || page % 8 || token % 8 || head % 8)
     return fail(CC_ERR_INVALID, "%s: cache strides must be at least D and multiples of 8", what);
   if (page >= (1ll << 38) || token >= (1ll << 38) || head >= (1ll << 38))

@@ -308,8 +308,8 @@ extern "C" cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, 
   if (ld_v < (int64_t)kv_heads * d || ld_v % 8)
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
   if ((st = check_plan(what, q_offsets, kv_lens, page_table, max_pages, pages, page_size)) != CC_OK) return st;
-  if ((st = check_cache_strides(what, k_page, k_token, k_head, d)) != CC_OK ||
-      (st = check_cache_strides(what, v_page, v_token, v_head, d)) != CC_OK)
+  if ((st = check_cache_strides(what, k_page, k_token, k_head, pages, kv_heads, d)) != CC_OK ||
+      (st = check_cache_strides(what, v_page, v_token, v_head, pages, kv_heads, d)) != CC_OK)
     return st;
   RopeArgs a = rope_args(q, k, gamma_q, gamma_k, rot, pos, q_out, rows, heads, kv_heads, d, rd, positions, ld_q, ld_k,
                          ld_qo, eps);

@@ -443,8 +443,9 @@ cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8* wq, const 
  * is not defined.
  *
  * The cache: page g, slot s, head h at g * page + s * token + h * head elements
- * (strides of k and of v, multiples of 8 and at least D), `pages` pages of
- * page_size slots. Needs page_size % 16 == 0. */
+ * (strides of k and of v, multiples of 8 and at least D; the page stride of a
+ * single page and the head stride of a single head do not count), `pages` pages
+ * of page_size slots. Needs page_size % 16 == 0. */
 
 /* How channels pair up for a rotation of rd of them: neighbours (2i, 2i + 1), or
  * halves (i, i + rd / 2). */

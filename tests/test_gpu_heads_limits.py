@@ -1,11 +1,11 @@
-"""The attentions with heads at the most sequences that they take."""
+"""The operators with heads at the limits of what they take: the most sequences, strides that do not count."""
 
 import pytest
 import torch
 
 from causal_convolution_gb300 import api
 from gpu_util import ensure_built
-from test_gpu_heads import BF16, DEV, I32, rnd, same_bits
+from test_gpu_heads import BF16, DEV, I32, Cache, paged, rnd, same_bits
 
 pytestmark = pytest.mark.gpu
 MOST = 1 << 20  # sequences
@@ -50,3 +50,37 @@ def test_the_most_sequences_half_of_them_of_two_items():
     api.cc_attn_paged(q, k, v, o, offsets, lens, table, ws)
     api.cc_check_device()
     assert same_bits(o, v[0, 0].expand(MOST, 8, 16))
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads,d,spare", [
+    ([(1, 300)], 4, 1, 64, 0), ([(40, 300), (3, 90)], 4, 1, 80, 2), ([(1, 40)], 6, 3, 128, 0), ([(100, 176)], 2, 1, 32, 0),
+])
+def test_strides_of_a_single_head_or_page_do_not_count(lens, heads, kv_heads, d, spare):
+    c = Cache(lens, 176, kv_heads, d, seed=230, spare=spare)
+    if len(lens) == 1 and lens[0][1] <= 176:
+        assert c.k.shape[0] == 1
+    q = rnd((c.rows, heads, d), 231, 2.0)
+    x = rnd((c.rows, heads + 2 * kv_heads, d), 232)
+
+    def append(k, v):
+        qo = torch.empty_like(q)
+        api.cc_qk_norm_rope_append(x[:, :heads], x[:, heads:heads + kv_heads], x[:, heads + kv_heads:], None, None, None,
+                                   None, qo, k, v, *c.plan)
+        api.cc_check_device()
+
+    def strided(t, stride):
+        # the same memory with another stride where there is one page or head
+        return t.as_strided(t.shape, (stride if t.shape[0] == 1 else t.stride(0), t.stride(1),
+                                      stride if t.shape[2] == 1 else t.stride(2), 1))
+
+    append(c.k, c.v)
+    want, k, v = paged(c, q, None, 1), c.k, c.v
+    want_k, want_v = k.clone(), v.clone()
+    for stride in (0, 3, 1 << 40):
+        for b, (new, kv) in enumerate(lens):
+            at = c.slots(b, kv - new, kv)
+            k[at], v[at] = 0, 0
+        c.k, c.v = strided(k, stride), strided(v, stride)
+        append(c.k, c.v)
+        assert same_bits(k, want_k) and same_bits(v, want_v)
+        assert same_bits(paged(c, q, None, 1), want)

@@ -1,6 +1,8 @@
 """Argument checks of the operators with heads at the largest sizes and the loosest strides, on the host."""
 
-from test_heads_host import CROSS, PAGED, call, calls, lib, p  # noqa: F401 (fixtures)
+import pytest
+
+from test_heads_host import APPEND, CROSS, PAGED, call, lib, p  # noqa: F401 (fixtures)
 
 
 def test_workspaces_of_refused_sizes_are_none(lib, p):
@@ -30,3 +32,20 @@ def test_sequences_beyond_what_a_cta_can_count_in_time_are_refused(lib, p):
         assert st == 2 and "2^20" in msg, (name, st, msg)
     assert paged(4, most, 4, 2, 64) > 0 and paged(4, most + 1, 4, 2, 64) == 0
     assert cross(most, 1, 5000, 4, 2, 64) > 0 and cross(most + 1, 1, 5000, 4, 2, 64) == 0
+
+
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_strides_of_sizes_of_one_are_not_looked_at(lib, p, side):
+    """A page or a head that is the only one has no neighbour, so its stride may be anything (0 in an expanded tensor).
+    The refusal behind that of strides, of the rows, tells that they were accepted."""
+    one_head = dict(heads=4, kv_heads=1, k_token=64, v_token=64)
+    for stride in (0, 1, 8, -64, 1 << 50):
+        for sizes in ({**one_head, side + "_head": stride}, {"pages": 1, side + "_page": stride}):
+            st, msg = call(lib, "cc_attn_paged", PAGED, p, rows=(1 << 30) + 1, **sizes)
+            assert st == 2 and "2^30 rows" in msg, (sizes, st, msg)
+        for sizes in ({side + "_head": stride}, {side + "_page": stride}, {"pages": 1, side + "_head": stride},
+                      {**one_head, side + "_page": stride}, {**one_head, "pages": 1, side + "_token": stride}):
+            st, msg = call(lib, "cc_attn_paged", PAGED, p, rows=(1 << 30) + 1, **sizes)
+            assert st in (1, 2) and "strides" in msg, (sizes, st, msg)
+            st, msg = call(lib, "cc_qk_norm_rope_append", APPEND, p, **sizes)
+            assert st in (1, 2) and "strides" in msg, (sizes, st, msg)
