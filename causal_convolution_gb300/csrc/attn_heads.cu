@@ -14,9 +14,9 @@
 // sequence go to another kernel (attn_few_rows.cu).
 //
 // Kernel. Warps 16 and 19 stream q and k, and v, with TMA (a box per page piece,
-// so a page of 16 tokens costs eight boxes and 64 channels; one warp for both took
-// 201 us for 2432 rows of 16 heads over 8192 keys in such pages, two take 144, as
-// do pages of 128). Warps 17 and 18 issue the products of a stream each: S = q k^T
+// so a page of 16 tokens costs eight boxes and 64 channels; with one warp for both,
+// 2432 rows of 16 heads over 8192 keys in such pages went from 157 to 201 us, in pages
+// of 128 they took 156 either way). Warps 17 and 18 issue the products of a stream each: S = q k^T
 // (128 x 128, K = D) into tensor memory, then O += P v with P read from tensor
 // memory, where it takes the place of S. Warps 0-7 and 8-15 are two softmax
 // streams: they turn a tile of S into P = bf16(exp2(kx S - c)), half a row to a
@@ -29,18 +29,27 @@
 // and pieces are joined, sums are multiplied exactly. It begins as 2^0 and moves
 // when a row's weights of half a tile come to 2^20, or those of the first keys that
 // it sees to less than 2^-10, which their sum tells: no maximum is looked for but
-// where that happens (short texts 13.2 -> 11.9 us against a maximum of each item's
-// first tile). fp32 sums of weights up to 2^20 lose nothing that weights up to 1
-// would keep, and neither does bf16.
+// where that happens (short texts 13.2 -> 11.6 us against a maximum of each item's
+// first tile, together with the exchange of a row's sums during its last product).
+// fp32 sums of weights up to 2^20 lose nothing that weights up to 1 would keep.
+//
+// Weights are rounded to bf16, the type of the values that the tensor cores multiply
+// them with: off by up to 2^-8 of themselves, on whatever scale. What is divided by is
+// the sum of the rounded ones, so only the spread of the roundings is left; against 64
+// bits results are off by 0.0020 to 0.0023 (L2, relative) where their own rounding
+// alone makes 0.0017. A second part for what is left, as in the kernel for few rows,
+// would cost a second product with v, half as much again for the tensor cores. Which
+// kernel a row gets, and with it which of the two, follows from the whole call
+// (few_rows below).
 //
 // Bound: long chunks by the streams' chain -- 1024 clocks of products, 1900 of
 // softmax with its trips through tensor memory and barriers, where two streams
 // would need 2048 in all for the tensor cores alone; tensor memory (512 columns)
 // holds no third S beside the sums of 128 channels. 13728 rows of 16 heads of 128
-// over 27456 keys in blocks of 3432: 1.58 ms alone (1.59 PFLOP/s, tensor pipe 70 %
-// busy), 1.78 ms back to back, under the power limit (1.41 PFLOP/s; the library
-// product's own rate under it is 1.73). Texts of 512 keys: 60 us for 29 of
-// products, as an item's beginning and end come one after the other for both
+// over 27456 keys in blocks of 3432: 1.58 ms for a single launch (1.59 PFLOP/s, tensor
+// pipe 70 % busy), 1.78 to 1.82 ms back to back, under the power limit (1.38 to 1.41
+// PFLOP/s; the library product's own rate under it is 1.73). Texts of 512 keys: 60 us
+// for 29 of products, as an item's beginning and end come one after the other for both
 // streams. What led here, for the chunk back to back: one row to a thread
 // with eight softmax warps 2.12 ms; a maximum for every tile 2.17; products of
 // both streams issued by two warps as they come 2.24, by one in turns 1.94, by two
@@ -482,8 +491,8 @@ __global__ void __launch_bounds__(kAhThreads, 1)
             uint32_t sv[32];
             if (again) {
               // The scale of the tile's largest score, and l and O with it (O's last product was complete before
-              // these scores were). Both warps of a row come here together, and the barrier keeps their weights from
-              // scores that the other one has not read.
+              // these scores were). Both warps of a row come here together, and the barrier makes each one's maximum
+              // visible to the other. Their scores need none: a warp reads and overwrites its own half's columns only.
               float m0 = kNegInf, m1 = kNegInf;
 #pragma unroll 1
               for (int h = 0; h < 64; h += 32) {
@@ -861,8 +870,17 @@ int few_tile_shift(int d) { return d > 64 ? 6 : 7; }
 
 // Few rows to a sequence on average: the kernel whose CTAs do little but read the
 // cache. (The other one takes 128 rows of a key head at once: 246 us instead of
-// 178 for single tokens of 64 streams with four heads to a key head. With more
-// rows than fit one item the keys would be read again for each eight of them.)
+// 180 for single tokens of 64 streams with four heads to a key head. With more
+// rows than fit one item the keys are read again for each eight of them.)
+//
+// The lengths of a plan are on the device, so the host knows the average alone and a
+// call is one kernel's. That holds for steps whose sequences are alike; a prompt beside
+// single tokens makes one of the two wait for a kernel that is not its own. Heads of
+// 128, in us: 64 tokens over 4096 keys each 170 and 400 rows over 4096 32, together 188;
+// 255 tokens over 2048 327 and 1793 rows over 8192 69, together 681 here and 448 with one
+// row more in the other kernel; with four heads to a key head 32 tokens over 4096 84 and
+// 2000 rows 76, together 199; 64 tokens 172 and 400 rows over 4096 48, together 234. A
+// caller that has both kinds can make a call for each.
 bool few_rows(int64_t rows, int64_t seqs, int group) { return group <= kFewRows && rows * group <= kFewRows * seqs; }
 
 // Rows that a partial slot holds: those of all tokens where an item (of the

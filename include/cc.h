@@ -53,10 +53,11 @@
  *  [NORM], [FP8] no page: the norms in front of the convolutions and the
  *         attention, and the 1x1x1 products around the attention and in the
  *         shortcuts, in 8 bits.
- *  [HEADS] no page: the operators of a transformer that makes the decoder's
- *         latents chunk by chunk, between the 8-bit products: head norms with
+ *  [HEADS] no page: operators of transformers that make a decoder's latents
+ *         chunk by chunk, between the 8-bit products: norms over each head with
  *         rotation, a paged cache of keys and values and the attention over it,
- *         attention to an encoder's states.
+ *         attention to an encoder's states. A norm over all heads of a row, or
+ *         a rotation without a norm, is not among them.
  *  [HOST] no page: a transfer helper for the chunk-by-chunk decode loop.
  */
 #ifndef CC_H_
@@ -433,8 +434,10 @@ cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8* wq, const 
  * while a call runs: sequence b of `seqs` owns the rows q_offsets[b] ..
  * q_offsets[b + 1] - 1 (q_offsets has seqs + 1 values that do not fall), which
  * are its newest tokens; kv_lens[b] counts its tokens with them; token p lies in
- * page page_table[b * max_pages + p / page_size], slot p % page_size. Entries of
- * the table behind a sequence's last page are not read. Rows in front of the
+ * page page_table[b * max_pages + p / page_size], slot p % page_size. Like every
+ * pointer the arrays are 16-byte aligned: parts of one buffer begin at multiples
+ * of four entries. Entries of the table behind a sequence's last page are not
+ * read. Rows in front of the
  * first and behind the last sequence are left as they are. A plan that points
  * outside of the cache or the table (kv_lens below the number of new tokens or
  * above max_pages * page_size, a page below 0 or from `pages` on), or a position
@@ -455,10 +458,11 @@ typedef enum cc_rot { CC_ROT_PAIRS = 0, CC_ROT_HALVES = 1 } cc_rot;
  * position, in fp32, rounded once:
  *   y = x / sqrt(mean_c x[c]^2 + eps) * gamma[c],  over the head's D channels;
  *   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos) for each pair i,
- * (cos, sin) = rot[pos[r]][i]; channels from rd on are not rotated. gamma_q,
- * gamma_k: [D] or NULL (ones); rot: [positions][rd / 2] pairs of floats (NULL
- * where rd is 0); pos: [rows] or NULL (row r has position r). q_out may be q and
- * k_out may be k when their strides are the same; otherwise they do not overlap.
+ * (cos, sin) = rot[pos[r]][i]; channels from rd on are not rotated. Every head is
+ * normed by itself and with the same gamma. gamma_q, gamma_k: [D] or NULL (ones;
+ * the norm stays); rot: [positions][rd / 2] pairs of floats (NULL where rd is 0);
+ * pos: [rows] or NULL (row r has position r). q_out may be q and k_out may be k
+ * when their strides are the same; otherwise they do not overlap.
  * heads or kv_heads may be 0 (those pointers are then not read). Needs
  * D % 16 == 0, D <= 256, rd % 16 == 0, rd <= D, row strides % 8 == 0, eps > 0. */
 cc_status cc_qk_norm_rope(const cc_bf16* q, const cc_bf16* k, const cc_bf16* gamma_q, const cc_bf16* gamma_k,
@@ -488,12 +492,15 @@ cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, const cc_bf
  * its own block of F tokens (a frame); causal_block 0: all L. (With
  * causal_block 0 L may be less than n.) Rows that see no token become zeros.
  * Scores, softmax and sums in fp32, the weights rounded to bf16 for the
- * product with v (their sum is that of the rounded ones; where rows are few,
- * weights are taken in two bf16 parts instead), one rounding at the end. Keys
- * and values behind a sequence's end may hold anything, NaN included; those
- * that some of its tokens see and others do not should be finite. Results do
- * not change from run to run, but the split of the sums depends on the whole
- * plan. ws: at least cc_attn_paged_workspace_bytes() (0 for sizes that the
+ * product with v (their sum is that of the rounded ones), one rounding at the
+ * end. Calls of few rows, rows * group <= 8 * seqs and group <= 8, take the
+ * weights in two bf16 parts instead. Keys and values behind a sequence's end may
+ * hold anything, NaN included; those that some of its tokens see and others do
+ * not should be finite. Results do not change from run to run, but the split of
+ * the sums depends on the whole plan, and the weights' rounding on rows and
+ * seqs: the same token may come to other bits in other company. (One kernel
+ * serves a call. Where single tokens and long chunks come together, two calls,
+ * one for each kind, can be faster.) ws: at least cc_attn_paged_workspace_bytes() (0 for sizes that the
  * call refuses; calls whose GPU work overlaps need one each; its contents need
  * no preparation; it may be NULL where the table has too few slots for
  * anything to be cut: up to 384). o must not overlap q or the cache. Plans of
