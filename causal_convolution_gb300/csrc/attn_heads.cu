@@ -832,6 +832,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_heads_join_kernel(const __g
   }
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kAhMaxHeads = 65536;
 constexpr int kAhMaxRows = 1 << 30;
 // Every CTA counts all sequences before its first item, while its other warps' waits of two seconds run: so many take
@@ -856,7 +857,8 @@ cc_status check_attn(const char* what, const void* q, const void* k, const void*
     return fail(CC_ERR_INVALID, "%s: row strides must hold the heads and be multiples of 8", what);
   if (ld_q >= (1ll << 38) || ld_o >= (1ll << 38))
     return fail(CC_ERR_UNSUPPORTED, "%s: row strides must be below 2^38 elements", what);
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(CC_ERR_INVALID, "%s: scale must be finite and > 0", what);
+  if (!(scale > 0.f) || !std::isfinite(scale * kLog2e))
+    return fail(CC_ERR_INVALID, "%s: scale must be > 0, and finite times log2(e)", what);
   return CC_OK;
 }
 
@@ -1045,7 +1047,7 @@ extern "C" cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, con
   a.box = page_size & -page_size;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
-  a.kx = scale * 1.4426950408889634f;
+  a.kx = scale * kLog2e;
   a.block = std::min(causal_block, 1 << 30);
   return run_attn(what, a, q, ld_q, {k_cache, k_page, k_token, k_head}, {v_cache, v_page, v_token, v_head},
                   (int64_t)max_pages * page_size, rows, ws, ws_bytes, stream);
@@ -1077,6 +1079,6 @@ extern "C" cc_status cc_attn_cross(const cc_bf16* q, const cc_bf16* k, const cc_
   a.box = 1 << 30;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
-  a.kx = scale * 1.4426950408889634f;
+  a.kx = scale * kLog2e;
   return run_attn(what, a, q, ld_q, {k, ld_k * lk, ld_k, d}, {v, ld_v * lk, ld_v, d}, lk, lq, ws, ws_bytes, stream);
 }

@@ -507,8 +507,8 @@ cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, const cc_bf
  * 2^31 key tiles or more (tiles of 64 or 128 keys, 8 to 256 rows of query
  * heads, counted as if each sequence filled its pages) and calls of more than
  * 2^30 rows or 2^20 sequences are CC_ERR_UNSUPPORTED. Needs D % 16 == 0,
- * D <= 128, heads % kv_heads == 0, group <= 128, ld_q, ld_o % 8 == 0, scale
- * finite and > 0. */
+ * D <= 128, heads % kv_heads == 0, group <= 128, ld_q, ld_o % 8 == 0, scale > 0,
+ * and finite times log2(e). */
 size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d);
 cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16* v_cache, cc_bf16* o,
                         const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table, int rows,

@@ -49,3 +49,11 @@ def test_strides_of_sizes_of_one_are_not_looked_at(lib, p, side):
             assert st in (1, 2) and "strides" in msg, (sizes, st, msg)
             st, msg = call(lib, "cc_qk_norm_rope_append", APPEND, p, **sizes)
             assert st in (1, 2) and "strides" in msg, (sizes, st, msg)
+
+
+def test_scales_that_pass_fp32_as_powers_of_two_are_refused(lib, p):
+    """Scores are taken times scale * log2(e) in fp32: as infinity it would turn a score of 0 into NaN."""
+    for name, names, key in (("cc_attn_paged", PAGED, "seqs"), ("cc_attn_cross", CROSS, "n")):
+        for scale, text in ((2.4e38, "scale"), (3.4e38, "scale"), (2.3e38, "2^20"), (1e-45, "2^20")):
+            st, msg = call(lib, name, names, p, scale=scale, lq=1, **{key: (1 << 20) + 1})
+            assert st == (1 if text == "scale" else 2) and text in msg, (name, scale, st, msg)
