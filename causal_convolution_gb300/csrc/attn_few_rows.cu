@@ -14,13 +14,13 @@
 // have time (results are then off from 64 bits by 0.0015 to 0.0017, L2, relative:
 // their own rounding).
 //
-// Two CTAs to an SM, 96 KB of tiles in flight each; a tile is 64 keys of 65 to 128
-// channels or 128 of up to 64 (so that waits and maxima come half as often there:
-// 64 streams over 4096 keys of 8 heads of 64 channels 137 -> 121 us, of 32
+// Two CTAs to an SM, 96 KB of tiles in flight each; a tile is 64 keys of 65 to
+// 128 channels or 128 of up to 64 (so that waits and maxima come half as often
+// there: 64 streams over 4096 keys of 8 heads of 64 channels 137 -> 121 us, of 32
 // 108 -> 82; 94 and 60 since L2 fetches no more than a head's row). Measured:
 // single tokens of 64 streams, 100 to 8192 keys each, 32 heads over 8 of 128
-// channels: 180 us, 6.0 TB/s or 0.91 of a copy's rate, pages of
-// 16 or 128 alike; with the rows along m (16 at least, the keys along n) it was 192.
+// channels: 180 us, 6.0 TB/s or 0.91 of a copy's rate, pages of 16 or 128 alike;
+// with the rows along m (16 at least, the keys along n) it was 192.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

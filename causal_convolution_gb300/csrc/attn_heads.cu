@@ -14,16 +14,16 @@
 // sequence go to another kernel (attn_few_rows.cu).
 //
 // Kernel. Warps 16 and 19 stream q and k, and v, with TMA (a box per page piece,
-// so a page of 16 tokens costs eight boxes and 64 channels; with one warp for both,
-// 2432 rows of 16 heads over 8192 keys in such pages went from 157 to 201 us, in pages
-// of 128 they took 156 either way). Warps 17 and 18 issue the products of a stream each: S = q k^T
-// (128 x 128, K = D) into tensor memory, then O += P v with P read from tensor
-// memory, where it takes the place of S. Warps 0-7 and 8-15 are two softmax
-// streams: they turn a tile of S into P = bf16(exp2(kx S - c)), half a row to a
-// thread. Items of two halves give each stream a half and both the same keys;
-// items of one half give the streams every other tile, and their sums are joined
-// at the end. While a stream works on its S, the tensor cores run the other's
-// products.
+// so a page of 16 tokens costs eight boxes and 64 channels; with one warp for
+// both, 2432 rows of 16 heads over 8192 keys in such pages went from 157 to 201
+// us, in pages of 128 they took 156 either way). Warps 17 and 18 issue the
+// products of a stream each: S = q k^T (128 x 128, K = D) into tensor memory,
+// then O += P v with P read from tensor memory, where it takes the place of S.
+// Warps 0-7 and 8-15 are two softmax streams: they turn a tile of S into P =
+// bf16(exp2(kx S - c)), half a row to a thread. Items of two halves give each
+// stream a half and both the same keys; items of one half give the streams every
+// other tile, and their sums are joined at the end. While a stream works on its
+// S, the tensor cores run the other's products.
 //
 // c, the row's scale, is a whole power of two: where it moves, and where streams
 // and pieces are joined, sums are multiplied exactly. It begins as 2^0 and moves
@@ -994,8 +994,8 @@ cc_status run_attn(const char* what, AhArgs& a, const cc_bf16* q, int64_t ld_q, 
 
 // Sizes that the calls take, as far as a workspace's size depends on them.
 bool sizes_ok(int64_t rows, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t d) {
-  return rows <= kAhMaxRows && seqs <= kAhMaxSeqs && heads > 0 && heads <= kAhMaxHeads && kv_heads > 0 && heads % kv_heads == 0 &&
-         heads / kv_heads <= kAhHalf && d > 0 && d % 16 == 0 && d <= 128;
+  return rows <= kAhMaxRows && seqs <= kAhMaxSeqs && heads > 0 && heads <= kAhMaxHeads && kv_heads > 0 &&
+         heads % kv_heads == 0 && heads / kv_heads <= kAhHalf && d > 0 && d % 16 == 0 && d <= 128;
 }
 
 }  // namespace

@@ -54,17 +54,19 @@ struct RopeArgs {
 //
 // Bound by memory where there are many rows: 13728 rows of 16 + 16 heads of 128
 // channels take 40 us with pairs, 5.8 TB/s or 0.86 of a copy's rate. On the way
-// there, from 56: places looked up for a CTA's rows at once and the next row's heads loaded
-// before this one is worked on 47, CTAs of 128 threads (more of them, so that
-// their beginnings and ends overlap) 42, two heads to a thread and nine CTAs to an
-// SM 40. All of that was measured with pairs. Halves take 59 us (0.59 of a copy's
-// rate), and 19.4 instead of 14.8 for three appended chunks of 77 to 4001 rows of 10
-// heads of 96: every channel is exchanged between lanes, so that the load-store
-// unit's data pipe is busy for 80 % of the time (pairs 53 %) and four times as many
-// warps wait for it, and with eight factors of each kind instead of four the 56
-// registers of nine CTAs do not do (32 to 40 bytes a thread are spilled and 40 to 48
-// read back, with a cache 68 to 76 and 100 to 124; pairs spill none). Single tokens are bound by the host's call (11 to 15 us; on the device
-// 2.2, and 3.8 with a cache, whose place hangs on three loads in a row).
+// there, from 56: places looked up for a CTA's rows at once and the next row's
+// heads loaded before this one is worked on 47, CTAs of 128 threads (more of
+// them, so that their beginnings and ends overlap) 42, two heads to a thread and
+// nine CTAs to an SM 40. All of that was measured with pairs. Halves take 59 us
+// (0.59 of a copy's rate), and 19.4 instead of 14.8 for three appended chunks of
+// 77 to 4001 rows of 10 heads of 96: every channel is exchanged between lanes, so
+// that the load-store unit's data pipe is busy for 80 % of the time (pairs 53 %)
+// and four times as many warps wait for it, and with eight factors of each kind
+// instead of four the 56 registers of nine CTAs do not do (32 to 40 bytes a
+// thread are spilled and 40 to 48 read back, with a cache 68 to 76 and 100 to
+// 124; pairs spill none). Single tokens are bound by the host's call (11 to 15
+// us; on the device 2.2, and 3.8 with a cache, whose place hangs on three loads
+// in a row).
 template <int LPH, int HC, bool HALVES, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, 9) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ long long s_out[kRopeRows];

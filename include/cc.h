@@ -437,13 +437,12 @@ cc_status cc_gemm_fp8(const cc_fp8* a, const float* sa, const cc_fp8* wq, const 
  * page page_table[b * max_pages + p / page_size], slot p % page_size. Like every
  * pointer the arrays are 16-byte aligned: parts of one buffer begin at multiples
  * of four entries. Entries of the table behind a sequence's last page are not
- * read. Rows in front of the
- * first and behind the last sequence are left as they are. A plan that points
- * outside of the cache or the table (kv_lens below the number of new tokens or
- * above max_pages * page_size, a page below 0 or from `pages` on), or a position
- * outside of the rotation's table, makes cc_check_device() report CC_ERR_DEVICE;
- * no access leaves the caller's memory then, and what the rows concerned come to
- * is not defined.
+ * read. Rows in front of the first and behind the last sequence are left as they
+ * are. A plan that points outside of the cache or the table (kv_lens below the
+ * number of new tokens or above max_pages * page_size, a page below 0 or from
+ * `pages` on), or a position outside of the rotation's table, makes
+ * cc_check_device() report CC_ERR_DEVICE; no access leaves the caller's memory
+ * then, and what the rows concerned come to is not defined.
  *
  * The cache: page g, slot s, head h at g * page + s * token + h * head elements
  * (strides of k and of v, multiples of 8 and at least D; the page stride of a
@@ -491,24 +490,24 @@ cc_status cc_qk_norm_rope_append(const cc_bf16* q, const cc_bf16* k, const cc_bf
  * tokens: with causal_block 1 those up to itself, with F those up to the end of
  * its own block of F tokens (a frame); causal_block 0: all L. (With
  * causal_block 0 L may be less than n.) Rows that see no token become zeros.
- * Scores, softmax and sums in fp32, the weights rounded to bf16 for the
- * product with v (their sum is that of the rounded ones), one rounding at the
- * end. Calls of few rows, rows * group <= 8 * seqs and group <= 8, take the
- * weights in two bf16 parts instead. Keys and values behind a sequence's end may
- * hold anything, NaN included; those that some of its tokens see and others do
- * not should be finite. Results do not change from run to run, but the split of
- * the sums depends on the whole plan, and the weights' rounding on rows and
- * seqs: the same token may come to other bits in other company. (One kernel
- * serves a call. Where single tokens and long chunks come together, two calls,
- * one for each kind, can be faster.) ws: at least cc_attn_paged_workspace_bytes() (0 for sizes that the
- * call refuses; calls whose GPU work overlaps need one each; its contents need
- * no preparation; it may be NULL where the table has too few slots for
- * anything to be cut: up to 384). o must not overlap q or the cache. Plans of
- * 2^31 key tiles or more (tiles of 64 or 128 keys, 8 to 256 rows of query
+ * Scores, softmax and sums in fp32, the weights rounded to bf16 for the product
+ * with v (their sum is that of the rounded ones), one rounding at the end. Calls
+ * of few rows, rows * group <= 8 * seqs and group <= 8, take the weights in two
+ * bf16 parts instead. Keys and values behind a sequence's end may hold anything,
+ * NaN included; those that some of its tokens see and others do not should be
+ * finite. Results do not change from run to run, but the split of the sums
+ * depends on the whole plan, and the weights' rounding on rows and seqs: the
+ * same token may come to other bits in other company. (One kernel serves a call.
+ * Where single tokens and long chunks come together, two calls, one for each
+ * kind, can be faster.) ws: at least cc_attn_paged_workspace_bytes() (0 for
+ * sizes that the call refuses; calls whose GPU work overlaps need one each; its
+ * contents need no preparation; it may be NULL where the table has too few slots
+ * for anything to be cut: up to 384). o must not overlap q or the cache. Plans
+ * of 2^31 key tiles or more (tiles of 64 or 128 keys, 8 to 256 rows of query
  * heads, counted as if each sequence filled its pages) and calls of more than
- * 2^30 rows or 2^20 sequences are CC_ERR_UNSUPPORTED. Needs D % 16 == 0,
- * D <= 128, heads % kv_heads == 0, group <= 128, ld_q, ld_o % 8 == 0, scale > 0,
- * and finite times log2(e). */
+ * 2^30 rows or 2^20 sequences are CC_ERR_UNSUPPORTED. Needs D % 16 == 0, D <=
+ * 128, heads % kv_heads == 0, group <= 128, ld_q, ld_o % 8 == 0, scale > 0, and
+ * finite times log2(e). */
 size_t cc_attn_paged_workspace_bytes(int rows, int seqs, int heads, int kv_heads, int d);
 cc_status cc_attn_paged(const cc_bf16* q, const cc_bf16* k_cache, const cc_bf16* v_cache, cc_bf16* o,
                         const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table, int rows,
